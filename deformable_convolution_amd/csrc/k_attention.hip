@@ -1,0 +1,428 @@
+// k_attention.hip -- attention's forward pass in one sweep over the keys,
+// with the running maximum and sum of the softmax.
+//
+// A workgroup takes rows of one key head (the query rows of all the query
+// heads that share it) and walks the keys that they see in tiles staged
+// through LDS.  Scores are formed transposed, S^T = K Q^T, so that a lane's
+// 16 scores of a tile belong to one row: its maximum and sum need one
+// exchange with lane ^ 32, and the probabilities stand where the next
+// product, O^T = V^T P^T, wants its operand.
+//
+//   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
+//   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j     (s in units of log 2)
+//
+// out = o / l, lse = m + log l.  A row that sees no key keeps l = 0: out 0,
+// lse -infinity.
+#include "attn_tile.h"
+
+namespace dc1d {
+
+namespace {
+
+// Rows of the softmax that a lane carries (row lane % 32 of its wave; the
+// two halves hold the same maximum and each its own part of the sum).
+struct Softmax {
+    float m, l;  // maximum in units of log 2 (-inf: nothing seen), part of the sum
+};
+
+// One tile of 32 * NT keys (first key k0) against 32 rows: scores, running
+// softmax, o^T += V^T P^T.  kt, vt: the tiles in LDS.  masked: some lane's
+// range cuts the tile.
+template <typename T, int DP, int NT>
+__device__ __forceinline__ void attend(const typename T::T *kt, const typename T::T *vt, const typename Tile<T>::Frag *q,
+                                       f32x16 *o, Softmax &sm, float c, bool masked, int k0, KeyRange kr, int lane) {
+    using M = Tile<T>;
+    constexpr int PK = DP + M::PADR, PV = DP + M::PADC, NS = DP / 16, ND = DP / 32;
+    const int half = lane >> 5;
+    f32x16 s[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        s[t] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            s[t] = M::mma(M::row_frag(kt + (t * 32 + (lane & 31)) * PK + i * 16 + half * 8), q[i], s[t]);
+    }
+    if (masked) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int j = k0 + t * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
+                if (j < kr.lo || j >= kr.hi) s[t][r] = -INFINITY;
+            }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+    top = half_max(top) * c;
+    // The reference that the exponents are taken from moves only when the
+    // maximum has outgrown it by a factor of 2^8: sums of that size lose
+    // nothing in 32 bits, and rescaling o is rare.
+    if (__any(top > sm.m + 8.0f)) {
+        const float m = fmaxf(sm.m, top);
+        const float alpha = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm.m - m);
+        sm.m = m;
+        sm.l *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] *= alpha;
+    }
+    const float m = sm.m == -INFINITY ? 0.0f : sm.m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], c, -m));
+            sum += s[t][r];
+        }
+    sm.l += sum;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const typename M::Frag p0 = M::template pack<0>(s[t]), p1 = M::template pack<1>(s[t]);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            o[d] = M::mma(M::col_frag(vt, PV, t * 32, d * 32, lane), p0, o[d]);
+            o[d] = M::mma(M::col_frag(vt, PV, t * 32 + 16, d * 32, lane), p1, o[d]);
+        }
+    }
+}
+
+// 16 elements of a row's 32 d's in a result's order, times f.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_row(typename T::T *row, const f32x16 &o, float f, int d0, int half, int D) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int d = d0 + 8 * g + 4 * half;
+        const f32x4 v = {o[4 * g] * f, o[4 * g + 1] * f, o[4 * g + 2] * f, o[4 * g + 3] * f};
+        if constexpr (VEC) {
+            if (d < D) Tile<T>::store4(row + d, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < D) T::st(row, d + e, v[e]);
+        }
+    }
+}
+
+template <typename T, int DP, bool VEC>
+__device__ __forceinline__ void load_q(const AttnArgs &a, typename Tile<T>::Frag *q, int b, int hk, int64_t row, int half) {
+    constexpr int CH = Tile<T>::CH;
+    const int pos = (int)((uint32_t)row / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)row % (uint32_t)a.G);
+    const typename T::T *p = (const typename T::T *)a.q + b * a.qs.b + pos * a.qs.l + h * a.qs.h;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+        u32x4 w[8 / CH];
+#pragma unroll
+        for (int j = 0; j < 8 / CH; ++j) {
+            const int col = i * 16 + half * 8 + j * CH;
+            w[j] = load_piece<T, VEC>(p, col, a.D);
+            if (VEC && col >= a.D) w[j] = u32x4{0, 0, 0, 0};
+        }
+        __builtin_memcpy(&q[i], w, sizeof(w));
+    }
+}
+
+// ---- rows split among the waves ---------------------------------------------
+//
+// 128 rows a workgroup, 32 a wave; tiles of KT keys, double-buffered, the
+// next one on its way in registers while this one is used.
+template <typename T, int DP>
+struct RowsShape {
+    static constexpr int KT = sizeof(typename T::T) == 2 ? 64 : 32;
+    static constexpr int PK = DP + Tile<T>::PADR, PV = DP + Tile<T>::PADC;
+    static constexpr size_t lds = (size_t)2 * KT * (PK + PV) * sizeof(typename T::T);
+};
+
+template <typename T, int DP, bool VEC>
+__global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
+    using E = typename T::T;
+    using S = RowsShape<T, DP>;
+    constexpr int KT = S::KT, ND = DP / 32;
+    extern __shared__ __align__(16) char smem[];
+    E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * KT * S::PK;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+
+    const int64_t tiles = (a.rows + 127) / 128;
+    const int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t tile = tiles - 1 - id % tiles;  // causal: the longest first
+    const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
+    const int64_t row0 = tile * 128;
+    const int64_t last = min(row0 + 127, a.rows - 1);
+    const int64_t row = row0 + wave * 32 + (lane & 31), rc = min(row, a.rows - 1);
+
+    const KeyRule rule = key_rule(a, b);
+    const KeyRange kr = rule.at((int)((uint32_t)rc / (uint32_t)a.G));
+    // the ranges' ends grow with the position, so the first and last row bound them
+    const int lo = rule.at((int)((uint32_t)row0 / (uint32_t)a.G)).lo;
+    const int hi = rule.at((int)((uint32_t)last / (uint32_t)a.G)).hi;
+    const KeyRange first = {__builtin_amdgcn_readfirstlane(kr.lo), __builtin_amdgcn_readfirstlane(kr.hi)};
+    const KeyRange final = {__builtin_amdgcn_readlane(kr.lo, 31), __builtin_amdgcn_readlane(kr.hi, 31)};
+
+    typename Tile<T>::Frag q[DP / 16];
+    load_q<T, DP, VEC>(a, q, b, hk, rc, half);
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f32x16{};
+    Softmax sm = {-INFINITY, 0.0f};
+    const float c = a.scale * kLog2e;
+
+    const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
+    Stage<T, KT, DP, 256, VEC> ks, vs;
+    int k0 = lo / KT * KT;
+    if (k0 < hi) {
+        ks.load(kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
+        vs.load(vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
+        ks.store(kbuf, S::PK, hi - k0, a.D, t);
+        vs.store(vbuf, S::PV, hi - k0, a.D, t);
+    }
+    for (int at = 0; k0 < hi; k0 += KT, at ^= 1) {
+        __syncthreads();
+        const int next = k0 + KT;
+        if (next < hi) {
+            ks.load(kp + next * a.ks.l, a.ks.l, hi - next, a.D, t);
+            vs.load(vp + next * a.vs.l, a.vs.l, hi - next, a.D, t);
+        }
+        if (k0 < final.hi && k0 + KT > first.lo)
+            attend<T, DP, KT / 32>(kbuf + at * KT * S::PK, vbuf + at * KT * S::PV, q, o, sm, c,
+                                   final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+        if (next < hi) {
+            ks.store(kbuf + (at ^ 1) * KT * S::PK, S::PK, hi - next, a.D, t);
+            vs.store(vbuf + (at ^ 1) * KT * S::PV, S::PV, hi - next, a.D, t);
+        }
+    }
+
+    const float l = half_sum(sm.l);
+    if (row >= a.rows) return;
+    const int pos = (int)((uint32_t)row / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)row % (uint32_t)a.G);
+    E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
+    const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a NaN stays one
+#pragma unroll
+    for (int d = 0; d < ND; ++d) store_row<T, VEC>(op, o[d], f, d * 32, half, a.D);
+    if (a.lse && half == 0)
+        a.lse[((int64_t)b * a.Hq + h) * a.Lq + pos] = l == 0.0f ? -INFINITY : sm.m * kLn2 + __logf(l);
+}
+
+// ---- keys split among the waves -----------------------------------------------
+//
+// 32 rows a workgroup (one or a few positions of every query head of the key
+// head); each wave stages and uses its own tiles of 32 keys, every fourth one
+// of the workgroup's part of the keys, with no barrier between them, so the
+// keys and values stream.  The waves' results are joined through LDS; where
+// the keys are also split among workgroups (`splits`) each part leaves its
+// maximum, sum and unscaled o, and k_attn_join adds the parts in order.
+template <typename T, int DP>
+struct KeysShape {
+    static constexpr int KT = 32;
+    static constexpr int PK = DP + Tile<T>::PADR, PV = DP + Tile<T>::PADC, PO = DP + 4;
+    static constexpr size_t wave_lds = (size_t)KT * (PK + PV) * sizeof(typename T::T);
+    static constexpr size_t join_lds = (size_t)4 * 32 * (PO + 2) * sizeof(float);
+    static constexpr size_t lds = 4 * wave_lds > join_lds ? 4 * wave_lds : join_lds;
+};
+
+template <typename T, int DP, bool VEC>
+__global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) void k_attn_keys(AttnArgs a) {
+    using E = typename T::T;
+    using S = KeysShape<T, DP>;
+    constexpr int KT = S::KT, ND = DP / 32;
+    extern __shared__ __align__(16) char smem[];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+    E *const kbuf = (E *)(smem + wave * S::wave_lds), *const vbuf = kbuf + KT * S::PK;
+
+    const int64_t tiles = (a.rows + 31) / 32;
+    int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    const int split = (int)(id % a.splits);
+    id /= a.splits;
+    const int64_t row0 = id % tiles * 32;
+    const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
+    const int64_t last = min(row0 + 31, a.rows - 1);
+    const int64_t row = row0 + (lane & 31), rc = min(row, a.rows - 1);
+
+    const KeyRule rule = key_rule(a, b);
+    const KeyRange kr = rule.at((int)((uint32_t)rc / (uint32_t)a.G));
+    const KeyRange first = rule.at((int)((uint32_t)row0 / (uint32_t)a.G));
+    const KeyRange final = rule.at((int)((uint32_t)last / (uint32_t)a.G));
+
+    typename Tile<T>::Frag q[DP / 16];
+    load_q<T, DP, VEC>(a, q, b, hk, rc, half);
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f32x16{};
+    Softmax sm = {-INFINITY, 0.0f};
+    const float c = a.scale * kLog2e;
+
+    // this part's run of the tiles [t0, t1) that the rows see
+    const int t0 = first.lo / KT, t1 = final.hi > first.lo ? (final.hi + KT - 1) / KT : t0;
+    const int per = ((t1 - t0 + a.splits - 1) / a.splits + 3) / 4 * 4;
+    const int s0 = t0 + min((int64_t)per * split, (int64_t)(t1 - t0)), s1 = min(s0 + per, t1);
+
+    const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
+    Stage<T, KT, DP, 64, VEC> ks, vs;
+    int n = s0 + wave;
+    if (n < s1) {
+        ks.load(kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane);
+        vs.load(vp + (int64_t)n * KT * a.vs.l, a.vs.l, final.hi - n * KT, a.D, lane);
+    }
+    for (; n < s1; n += 4) {
+        const int k0 = n * KT, next = n + 4;
+        ks.store(kbuf, S::PK, final.hi - k0, a.D, lane);
+        vs.store(vbuf, S::PV, final.hi - k0, a.D, lane);
+        if (next < s1) {
+            ks.load(kp + (int64_t)next * KT * a.ks.l, a.ks.l, final.hi - next * KT, a.D, lane);
+            vs.load(vp + (int64_t)next * KT * a.vs.l, a.vs.l, final.hi - next * KT, a.D, lane);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        attend<T, DP, 1>(kbuf, vbuf, q, o, sm, c, final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+
+    // join the four waves: each leaves o, m, l; thread (row, slice) adds them in wave order
+    __syncthreads();
+    float *const of = (float *)smem, *const ml = of + 4 * 32 * S::PO;
+    const float l = half_sum(sm.l);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *(f32x4 *)(of + (wave * 32 + (lane & 31)) * S::PO + d * 32 + 8 * g + 4 * half) =
+                f32x4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+    if (half == 0) {
+        ml[(wave * 32 + lane) * 2] = sm.m;
+        ml[(wave * 32 + lane) * 2 + 1] = l;
+    }
+    __syncthreads();
+    const int r = t >> 3, slice = t & 7;  // eight threads a row
+    const int64_t n_row = row0 + r;
+    if (n_row >= a.rows) return;
+    float m = -INFINITY, w[4], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, ml[(i * 32 + r) * 2]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float mi = ml[(i * 32 + r) * 2];
+        w[i] = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
+        sum += w[i] * ml[(i * 32 + r) * 2 + 1];
+    }
+    const int pos = (int)((uint32_t)n_row / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)n_row % (uint32_t)a.G);
+    const float f = a.splits > 1 ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
+    const int64_t at = ((int64_t)b * a.Hkv + hk) * a.rows + n_row, all = (int64_t)a.B * a.Hkv * a.rows;
+    float *const pp = a.splits > 1 ? a.part + ((int64_t)split * all + at) * (DP + 2) : nullptr;
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j) {
+        const int d = j * 32 + slice * 4;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v += w[i] * *(const f32x4 *)(of + (i * 32 + r) * S::PO + d);
+        v *= f;
+        if (pp) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pp[2 + d + e] = v[e];
+        } else if constexpr (VEC) {
+            if (d < a.D) Tile<T>::store4(op + d, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < a.D) T::st(op, d + e, v[e]);
+        }
+    }
+    if (slice == 0) {
+        if (pp) {
+            pp[0] = m;
+            pp[1] = sum;
+        } else if (a.lse) {
+            a.lse[((int64_t)b * a.Hq + h) * a.Lq + pos] = sum == 0.0f ? -INFINITY : m * kLn2 + __logf(sum);
+        }
+    }
+}
+
+// The parts of a row joined in order; a wave a row.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    using E = typename T::T;
+    const int lane = threadIdx.x & 63;
+    const int64_t all = (int64_t)a.B * a.Hkv * a.rows, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (at >= all) return;
+    const float *const p = a.part + at * (DP + 2);
+    float m = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, p[(int64_t)s * all * (DP + 2)]);
+    float sum = 0.0f, v[(DP + 63) / 64] = {};
+    for (int s = 0; s < a.splits; ++s) {
+        const float *const ps = p + (int64_t)s * all * (DP + 2);
+        const float w = ps[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ps[0] - m);
+        sum += w * ps[1];
+#pragma unroll
+        for (int i = 0; i < (DP + 63) / 64; ++i)
+            if (i * 64 + lane < DP) v[i] += w * ps[2 + i * 64 + lane];
+    }
+    const int64_t bh = at / a.rows;
+    const uint32_t n = (uint32_t)(at % a.rows);
+    const int b = (int)(bh / a.Hkv), pos = (int)(n / (uint32_t)a.G), h = (int)(bh % a.Hkv) * a.G + (int)(n % (uint32_t)a.G);
+    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
+#pragma unroll
+    for (int i = 0; i < (DP + 63) / 64; ++i)
+        if (i * 64 + lane < a.D) T::st(op, i * 64 + lane, v[i] * f);
+    if (a.lse && lane == 0)
+        a.lse[((int64_t)b * a.Hq + h) * a.Lq + pos] = sum == 0.0f ? -INFINITY : m * kLn2 + __logf(sum);
+}
+
+int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+
+template <typename T, int DP, bool VEC>
+hipError_t launch(const AttnArgs &a, const AttnPlan &pl, hipStream_t stream) {
+    if (!pl.by_keys) {
+        constexpr size_t lds = RowsShape<T, DP>::lds;
+        hipLaunchKernelGGL((k_attn_rows<T, DP, VEC>), dim3((uint32_t)pl.blocks), dim3(256), lds, stream, a);
+        return hipGetLastError();
+    }
+    constexpr size_t lds = KeysShape<T, DP>::lds;
+    hipLaunchKernelGGL((k_attn_keys<T, DP, VEC>), dim3((uint32_t)pl.blocks), dim3(256), lds, stream, a);
+    if (a.splits > 1)
+        hipLaunchKernelGGL((k_attn_join<T, DP>), dim3((uint32_t)(((int64_t)a.B * a.Hkv * a.rows + 3) / 4)), dim3(256), 0,
+                           stream, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_typed(const AttnArgs &a, const AttnPlan &pl, hipStream_t stream) {
+    const int DP = padded(a.D);
+    if (DP == 32) return a.vec ? launch<T, 32, true>(a, pl, stream) : launch<T, 32, false>(a, pl, stream);
+    if (DP == 64) return a.vec ? launch<T, 64, true>(a, pl, stream) : launch<T, 64, false>(a, pl, stream);
+    return a.vec ? launch<T, 128, true>(a, pl, stream) : launch<T, 128, false>(a, pl, stream);
+}
+
+}  // namespace
+
+AttnPlan plan_attention(const AttnArgs &a, int num_cus) {
+    AttnPlan pl = {};
+    const int64_t heads = (int64_t)a.B * a.Hkv, row_blocks = heads * ((a.rows + 127) / 128);
+    pl.by_keys = a.rows <= 32;
+    pl.splits = 1;
+    if (!pl.by_keys) {
+        pl.name = "attention_rows";
+        pl.blocks = row_blocks;
+        return pl;
+    }
+    pl.name = "attention_keys";
+    const int64_t blocks = heads * ((a.rows + 31) / 32);
+    if (blocks == 0) return pl;
+    // enough workgroups for two on every CU, none with fewer than 256 keys
+    const int64_t most = (a.Lk + 255) / 256;
+    int64_t splits = (2 * (int64_t)num_cus + blocks - 1) / blocks;
+    splits = splits < 1 ? 1 : splits > most ? most : splits;
+    pl.splits = (int)(splits < 1 ? 1 : splits > 256 ? 256 : splits);
+    pl.blocks = blocks * pl.splits;
+    if (pl.splits > 1) pl.ws_bytes = (size_t)pl.splits * heads * a.rows * (padded(a.D) + 2) * sizeof(float);
+    return pl;
+}
+
+hipError_t launch_attention(AttnArgs a, const AttnPlan &pl, void *ws, hipStream_t stream) {
+    a.splits = pl.splits;
+    a.part = (float *)ws;
+    if (pl.blocks == 0) return hipSuccess;
+    return a.dtype == kF32 ? launch_typed<F32>(a, pl, stream) : launch_typed<BF16>(a, pl, stream);
+}
+
+}  // namespace dc1d

@@ -71,7 +71,8 @@ extern "C" {
 /* Storage dtypes. */
 typedef enum dc1d_dtype {
     DC1D_F32 = 0,  /* IEEE binary32 */
-    DC1D_BF16 = 1  /* bfloat16 (upper half of a binary32) */
+    DC1D_BF16 = 1, /* bfloat16 (upper half of a binary32) */
+    DC1D_I32 = 2   /* 32-bit integers: positions and lengths of the sequence operators only */
 } dc1d_dtype;
 
 typedef enum dc1d_status {
@@ -437,6 +438,162 @@ int dc1d_plan(const dc1d_tensor *x, const dc1d_tensor *offsets, const dc1d_tenso
               int64_t padding, int64_t dilation, int64_t groups, int64_t offset_groups,
               const char **kernel_name, int64_t *grid_blocks, int32_t *block_threads,
               int32_t *splits);
+
+/* ---- sequence operators ------------------------------------------------------
+ *
+ * What a sequence or image model puts next to a deformable convolution:
+ * layer norm over the channels, rotary positions with several axes, and
+ * attention, each with its gradient.  fp32 or bf16 storage (one dtype per
+ * call for the data tensors); sums, statistics and softmax are held in fp32
+ * and each result is rounded once, to nearest even; probabilities and score
+ * gradients of bf16 calls are rounded to bf16 as operands of the matrix
+ * instructions.  Every result is summed in a fixed order without atomics:
+ * the same call gives the same bits.  Ownership, streams, workspaces,
+ * logging and errors are those of the calls above.
+ */
+
+/* A tensor in device memory with a stride (in elements) for each dimension.
+ * Strides are not negative and the last dimension is contiguous (stride 1,
+ * any where its size is 1); a stride of 0 repeats an input.  An output's
+ * elements must not share memory. */
+typedef struct dc1d_strided {
+    void *data;
+    int32_t dtype; /* a dc1d_dtype */
+    int32_t ndim;
+    int64_t shape[4];
+    int64_t stride[4];
+} dc1d_strided;
+
+/*
+ * Layer norm over axis 1:
+ *
+ *   mean = mean_c x,  rstd = 1 / sqrt(mean_c (x - mean)^2 + eps)
+ *   y    = (x - mean) * rstd * weight + bias
+ *
+ *   x, y       [N, C], [B, C, L] or [B, C, H, W]   (axis 1 normalised)
+ *   weight, bias  [C], x's dtype, or NULL (ones, zeros)
+ *   mean, rstd  x's shape without axis 1, fp32, or NULL (not wanted)
+ *
+ * y may be x itself (in place); otherwise outputs must not overlap the
+ * inputs or each other.  eps is finite and not negative.  C >= 1; an empty
+ * x is a no-op.  Limits: C <= 2^24, fewer than 2^31 positions.
+ */
+int dc1d_layer_norm(const dc1d_tensor *x, const dc1d_tensor *weight_or_null, const dc1d_tensor *bias_or_null,
+                    const dc1d_tensor *y, const dc1d_tensor *mean_or_null, const dc1d_tensor *rstd_or_null, double eps,
+                    void *stream);
+
+/*
+ * Gradients of sum(grad_out * y) with respect to x, weight and bias, from
+ * the forward's x, mean and rstd (NULL: not computed):
+ *
+ *   grad_x = rstd * (u - mean_c u - xh * mean_c(u * xh)),
+ *            u = grad_out * weight,  xh = (x - mean) * rstd
+ *   grad_weight[c] = sum grad_out * xh,   grad_bias[c] = sum grad_out
+ *
+ * in their inputs' shapes and dtype.  grad_x may be grad_out itself.  An
+ * empty x gives zero grad_weight and grad_bias.  workspace: at least
+ * dc1d_layer_norm_backward_workspace_bytes() bytes, 256-byte aligned, when
+ * that is not 0 (the parameter gradients' partial sums).
+ */
+int dc1d_layer_norm_backward_workspace_bytes(const dc1d_tensor *x, int want_params, size_t *bytes_out);
+
+int dc1d_layer_norm_backward(const dc1d_tensor *x, const dc1d_tensor *weight_or_null, const dc1d_tensor *grad_out,
+                             const dc1d_tensor *mean, const dc1d_tensor *rstd, const dc1d_tensor *grad_x_or_null,
+                             const dc1d_tensor *grad_weight_or_null, const dc1d_tensor *grad_bias_or_null,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions with up to four axes (one for sequences, rows and columns
+ * for images, time, rows and columns for video).  Every head of D elements
+ * holds R pairs, 2 R <= D; pair i belongs to the axis whose section it is in
+ * (axis 0 the first sections[0] pairs, and so on; the sections add up to R)
+ * and turns by the tables' angle of that axis' position:
+ *
+ *   (a, b) -> (a c - b s, a s + b c),  c = cos[p][i], s = sin[p][i],
+ *   p = positions[b][l][axis(i)]
+ *
+ * The pair is elements (i, R + i) of the head, or (2i, 2i + 1) where
+ * interleaved is not 0; elements past 2 R are copied.  inverse not 0 turns
+ * the other way: the backward pass (apply it to the output's gradient).
+ *
+ *   q, q_out   [B, L, Hq, D], k, k_out [B, L, Hkv, D] (both NULL: queries only)
+ *   cos, sin   [P, R] fp32
+ *   positions  [B, L, A] or [1, L, A] (shared) int32, A = n_axes
+ *   sections   n_axes host integers, each >= 0, R = their sum >= 1
+ *
+ * Positions outside [0, P) are taken as the nearest end of the tables.  An
+ * output may be its own input (in place); otherwise it must not overlap any
+ * input or the other output, except that two tensors may be disjoint head
+ * slices of one buffer.  Limits: B * L < 2^31, B * L * (Hq + Hkv) * D < 2^40.
+ */
+int dc1d_rotary(const dc1d_strided *q, const dc1d_strided *k_or_null, const dc1d_tensor *cos, const dc1d_tensor *sin,
+                const dc1d_tensor *positions, const dc1d_strided *q_out, const dc1d_strided *k_out_or_null,
+                const int64_t *sections, int32_t n_axes, int interleaved, int inverse, void *stream);
+
+/*
+ * Attention.  Query i of batch b stands at position p = q_start[b] + i and
+ * sees the keys j with
+ *
+ *   j < kv_lens[b],   j <= p where causal,   |p - j| < window where window > 0
+ *
+ *   out[b,i,h] = sum_j P_ij v[b,j,h'],   P_ij = exp(s_ij - lse[b,h,i]),
+ *   s_ij = scale * q[b,i,h] . k[b,j,h'],   lse = log sum_j exp s_ij,
+ *
+ * h' = h / (Hq / Hkv): neighbouring query heads share a key head.  A query
+ * that sees no key gives out 0 and lse -infinity.  Keys and values at and
+ * past kv_lens[b] are never used, whatever they hold; those before it should
+ * be finite even where causal or window hide them.
+ *
+ *   q, out    [B, Lq, Hq, D], k, v [B, Lk, Hkv, D], Hkv dividing Hq, D <= 128
+ *   kv_lens   [B] int32, clamped to [0, Lk], or NULL (Lk)
+ *   q_start   [B] int32, or NULL (Lk - Lq: the last query at the last key);
+ *             for a cache of ragged lengths, kv_lens - Lq
+ *   lse       [B, Hq, Lq] fp32, or NULL (not wanted)
+ *   scale     finite, > 0 (usually 1 / sqrt(D));  window >= 0, 0: none
+ *
+ * Strides are free, so q, k, v and out may be slices of larger buffers; out
+ * must not overlap the inputs unless as a disjoint head slice of one buffer.
+ * |q_start| and window are clamped to 2^29.  workspace: at least
+ * dc1d_attention_workspace_bytes() bytes, 256-byte aligned, when that is not
+ * 0 (few queries over many keys: the partial results of parts of the keys).
+ * Limits: Lq, Lk <= 2^29, B * Hkv < 2^24, B * Lq * Hq < 2^29, B * Lk * Hkv < 2^31.
+ */
+int dc1d_attention_workspace_bytes(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v,
+                                   size_t *bytes_out);
+
+int dc1d_attention(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v,
+                   const dc1d_tensor *kv_lens_or_null, const dc1d_tensor *q_start_or_null, const dc1d_strided *out,
+                   const dc1d_tensor *lse_or_null, int causal, int64_t window, double scale, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Which kernel dc1d_attention would use ("attention_rows", "attention_keys"),
+ * its workgroups, and into how many parts it splits the keys. */
+int dc1d_attention_plan(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v, const char **kernel_name,
+                        int64_t *grid_blocks, int32_t *splits);
+
+/*
+ * Gradients of sum(grad_out * out) with respect to q, k and v, from the
+ * forward's inputs, out and lse (the probabilities are formed again):
+ *
+ *   dS = P * (grad_out . v - grad_out . out),
+ *   grad_q = scale * dS k,  grad_k = scale * dS^T q,  grad_v = P^T grad_out,
+ *
+ * grad_k and grad_v summed over the query heads that share a key head.
+ * Keys that no query sees get zeros.  NULL gradients are not computed.  The
+ * other arguments are the forward's; gradients must not overlap the inputs or
+ * each other unless as disjoint head slices of one buffer.  workspace: at
+ * least dc1d_attention_backward_workspace_bytes() bytes, 256-byte aligned,
+ * when that is not 0.
+ */
+int dc1d_attention_backward_workspace_bytes(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v,
+                                            size_t *bytes_out);
+
+int dc1d_attention_backward(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v,
+                            const dc1d_tensor *kv_lens_or_null, const dc1d_tensor *q_start_or_null,
+                            const dc1d_strided *out, const dc1d_tensor *lse, const dc1d_strided *grad_out,
+                            const dc1d_strided *grad_q_or_null, const dc1d_strided *grad_k_or_null,
+                            const dc1d_strided *grad_v_or_null, int causal, int64_t window, double scale,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /* A static, NUL-terminated description of a status code. */
 const char *dc1d_status_string(int status);
