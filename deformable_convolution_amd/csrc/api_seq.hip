@@ -231,6 +231,7 @@ int attn_shape(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided 
     a->dtype = q->dtype;
     a->B = (int)B, a->Lq = (int)Lq, a->Lk = (int)Lk, a->Hq = (int)Hq, a->Hkv = (int)Hkv, a->G = (int)G, a->D = (int)D;
     a->rows = Lq * G;
+    a->by_G = make_fastdiv((uint32_t)G);
     return DC1D_OK;
 }
 
@@ -336,6 +337,7 @@ int dc1d_layer_norm(const dc1d_tensor *x, const dc1d_tensor *weight_or_null, con
     a.rstd = rstd_or_null ? (float *)rstd_or_null->data : nullptr;
     a.dtype = x->dtype;
     a.B = B, a.C = (int)C, a.L = L;
+    a.inv_c = 1.0f / (float)C;
     a.eps = (float)eps;
     return launched(launch_layer_norm(a, cus, (hipStream_t)stream));
 }
@@ -395,6 +397,7 @@ int dc1d_layer_norm_backward(const dc1d_tensor *x, const dc1d_tensor *weight_or_
     a.gb = grad_bias_or_null ? grad_bias_or_null->data : nullptr;
     a.dtype = x->dtype;
     a.B = B, a.C = (int)C, a.L = L;
+    a.inv_c = 1.0f / (float)C;
     a.ws = (float *)workspace;
     if (!a.y && !params) return DC1D_OK;
     return launched(launch_layer_norm_backward(a, cus, (hipStream_t)stream));
@@ -421,7 +424,7 @@ int dc1d_rotary(const dc1d_strided *q, const dc1d_strided *k_or_null, const dc1d
         if (!distinct(out[i])) return DC1D_ERR_ALIAS;
     }
     if (D < 2 || D > (1 << 24) || B >= kLim31 || L >= kLim31 || B * L >= kLim31) return DC1D_ERR_BAD_SHAPE;
-    if (B * L > 0 && heads * D >= ((int64_t)1 << 40) / (B * L)) return DC1D_ERR_BAD_SHAPE;
+    if (heads * D >= (1 << 30) || heads * D * (B * L) >= (int64_t)1 << 40) return DC1D_ERR_BAD_SHAPE;
     int64_t R = 0;
     int first[4];
     for (int i = 0; i < 4; ++i) {

@@ -24,6 +24,7 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -136,33 +137,82 @@ __device__ __forceinline__ u32x4 load_piece(const typename T::T *row, int col, i
     }
 }
 
+// Row n of a key head's queries: position n / G, head n % G of its G heads.
+struct RowAt {
+    int pos, head;
+};
+__device__ __forceinline__ RowAt row_at(const AttnArgs &a, int64_t n) {
+    const uint32_t pos = fdiv((uint32_t)n, a.by_G);
+    return {(int)pos, (int)((uint32_t)n - pos * (uint32_t)a.G)};
+}
+
 // A tile of ROWS rows of DP elements carried by NT threads, from global
 // memory through registers into LDS.  Rows at and past `limit` and elements
 // at and past D become zero, whatever memory holds there.
+//
+// Whole tiles of aligned rows are read at the tile's base, which the whole
+// workgroup shares, plus 32-bit offsets that each thread forms once (`near`:
+// they fit); other tiles form their addresses as they go.
 template <typename T, int ROWS, int DP, int NT, bool VEC>
 struct Stage {
     using E = typename T::T;
     static constexpr int CH = Tile<T>::CH, PER = DP / CH, N = (ROWS * PER + NT - 1) / NT;
     static_assert(ROWS * PER % NT == 0 || ROWS * PER < NT, "the tile divides among the threads, or needs only some");
+    static constexpr int64_t kNear = 1 << 23;  // elements between rows: 64 rows of 4 bytes stay below 2^31
     u32x4 r[N];
+    uint32_t off[N];
+    bool near;
 
-    // base: the tile's row 0 (limit >= 1 rows of it may be read), stride in elements
-    __device__ __forceinline__ void load(const E *base, int64_t stride, int limit, int D, int t) {
+    // rows `stride` elements apart
+    __device__ __forceinline__ void init(int64_t stride, int D, int t) {
+        near = VEC && stride < kNear;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = t + i * NT, row = c / PER, col = c % PER * CH;
-            r[i] = load_piece<T, VEC>(base + (int64_t)min(row, limit - 1) * stride, col, D);
+            for (int i = 0; i < N; ++i) {
+                const int c = t + i * NT, row = min(c / PER, ROWS - 1), col = c % PER * CH;
+                off[i] = (uint32_t)(row * (uint32_t)stride + (col < D ? col : 0)) * sizeof(E);
+            }
         }
     }
-    // rows of a key head's queries: row n is position n / G, head n % G
-    __device__ __forceinline__ void load_rows(const E *base, const Strides3 &s, int64_t row0, int64_t rows, int G, int D,
-                                              int t) {
+    // rows of a key head's queries: whole tiles start at the same head where
+    // G divides their rows
+    __device__ __forceinline__ void init_rows(const AttnArgs &a, const Strides3 &s, int t) {
+        near = VEC && ROWS % a.G == 0 && s.l < kNear && s.h < kNear;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = t + i * NT, col = c % PER * CH;
-            const int64_t n = row0 + c / PER < rows ? row0 + c / PER : rows - 1;
-            const int pos = (int)((uint32_t)n / (uint32_t)G), h = (int)((uint32_t)n % (uint32_t)G);
-            r[i] = load_piece<T, VEC>(base + pos * s.l + h * s.h, col, D);
+            for (int i = 0; i < N; ++i) {
+                const int c = t + i * NT, col = c % PER * CH;
+                const RowAt at = row_at(a, min(c / PER, ROWS - 1));
+                off[i] = ((uint32_t)at.pos * (uint32_t)s.l + (uint32_t)at.head * (uint32_t)s.h + (col < a.D ? col : 0)) * (uint32_t)sizeof(E);
+            }
+        }
+    }
+    // base: the tile's row 0 (limit >= 1 rows of it may be read)
+    __device__ __forceinline__ void load(const E *base, int64_t stride, int limit, int D, int t) {
+        if (near && limit >= ROWS) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] = *(const u32x4 *)((const char *)base + off[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = t + i * NT, row = c / PER, col = c % PER * CH;
+                r[i] = load_piece<T, VEC>(base + (int64_t)min(row, limit - 1) * stride, col, D);
+            }
+        }
+    }
+    // base: the key head's first query head, position 0; row0: a multiple of ROWS
+    __device__ __forceinline__ void load_rows(const E *base, const AttnArgs &a, const Strides3 &s, int64_t row0, int t) {
+        if (near && row0 + ROWS <= a.rows) {
+            const char *const p = (const char *)(base + (int64_t)fdiv((uint32_t)row0, a.by_G) * s.l);
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] = *(const u32x4 *)(p + off[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = t + i * NT, col = c % PER * CH;
+                const RowAt at = row_at(a, row0 + c / PER < a.rows ? row0 + c / PER : a.rows - 1);
+                r[i] = load_piece<T, VEC>(base + at.pos * s.l + at.head * s.h, col, a.D);
+            }
         }
     }
     __device__ __forceinline__ void store(E *lds, int pitch, int limit, int D, int t) {

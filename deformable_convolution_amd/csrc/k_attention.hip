@@ -109,7 +109,7 @@ __device__ __forceinline__ void store_row(typename T::T *row, const f32x16 &o, f
 template <typename T, int DP, bool VEC>
 __device__ __forceinline__ void load_q(const AttnArgs &a, typename Tile<T>::Frag *q, int b, int hk, int64_t row, int half) {
     constexpr int CH = Tile<T>::CH;
-    const int pos = (int)((uint32_t)row / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)row % (uint32_t)a.G);
+    const int pos = row_at(a, row).pos, h = hk * a.G + row_at(a, row).head;
     const typename T::T *p = (const typename T::T *)a.q + b * a.qs.b + pos * a.qs.l + h * a.qs.h;
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
@@ -153,10 +153,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
     const int64_t row = row0 + wave * 32 + (lane & 31), rc = min(row, a.rows - 1);
 
     const KeyRule rule = key_rule(a, b);
-    const KeyRange kr = rule.at((int)((uint32_t)rc / (uint32_t)a.G));
+    const KeyRange kr = rule.at(row_at(a, rc).pos);
     // the ranges' ends grow with the position, so the first and last row bound them
-    const int lo = rule.at((int)((uint32_t)row0 / (uint32_t)a.G)).lo;
-    const int hi = rule.at((int)((uint32_t)last / (uint32_t)a.G)).hi;
+    const int lo = rule.at(row_at(a, row0).pos).lo;
+    const int hi = rule.at(row_at(a, last).pos).hi;
     const KeyRange first = {__builtin_amdgcn_readfirstlane(kr.lo), __builtin_amdgcn_readfirstlane(kr.hi)};
     const KeyRange final = {__builtin_amdgcn_readlane(kr.lo, 31), __builtin_amdgcn_readlane(kr.hi, 31)};
 
@@ -170,6 +170,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 256, VEC> ks, vs;
+    ks.init(a.ks.l, a.D, t);
+    vs.init(a.vs.l, a.D, t);
     int k0 = lo / KT * KT;
     if (k0 < hi) {
         ks.load(kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
 
     const float l = half_sum(sm.l);
     if (row >= a.rows) return;
-    const int pos = (int)((uint32_t)row / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)row % (uint32_t)a.G);
+    const int pos = row_at(a, row).pos, h = hk * a.G + row_at(a, row).head;
     E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
     const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // a NaN stays one
 #pragma unroll
@@ -240,9 +242,9 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     const int64_t row = row0 + (lane & 31), rc = min(row, a.rows - 1);
 
     const KeyRule rule = key_rule(a, b);
-    const KeyRange kr = rule.at((int)((uint32_t)rc / (uint32_t)a.G));
-    const KeyRange first = rule.at((int)((uint32_t)row0 / (uint32_t)a.G));
-    const KeyRange final = rule.at((int)((uint32_t)last / (uint32_t)a.G));
+    const KeyRange kr = rule.at(row_at(a, rc).pos);
+    const KeyRange first = rule.at(row_at(a, row0).pos);
+    const KeyRange final = rule.at(row_at(a, last).pos);
 
     typename Tile<T>::Frag q[DP / 16];
     load_q<T, DP, VEC>(a, q, b, hk, rc, half);
@@ -259,6 +261,8 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 64, VEC> ks, vs;
+    ks.init(a.ks.l, a.D, lane);
+    vs.init(a.vs.l, a.D, lane);
     int n = s0 + wave;
     if (n < s1) {
         ks.load(kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane);
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
         w[i] = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - m);
         sum += w[i] * ml[(i * 32 + r) * 2 + 1];
     }
-    const int pos = (int)((uint32_t)n_row / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)n_row % (uint32_t)a.G);
+    const int pos = row_at(a, n_row).pos, h = hk * a.G + row_at(a, n_row).head;
     const float f = a.splits > 1 ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
     const int64_t at = ((int64_t)b * a.Hkv + hk) * a.rows + n_row, all = (int64_t)a.B * a.Hkv * a.rows;
@@ -358,7 +362,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     }
     const int64_t bh = at / a.rows;
     const uint32_t n = (uint32_t)(at % a.rows);
-    const int b = (int)(bh / a.Hkv), pos = (int)(n / (uint32_t)a.G), h = (int)(bh % a.Hkv) * a.G + (int)(n % (uint32_t)a.G);
+    const int b = (int)(bh / a.Hkv), pos = row_at(a, n).pos, h = (int)(bh % a.Hkv) * a.G + row_at(a, n).head;
     const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
 #pragma unroll

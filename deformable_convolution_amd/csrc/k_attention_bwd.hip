@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a) {
     const int64_t all = (int64_t)a.B * a.Hkv * a.rows, m = n < all ? n : all - 1;
     const int64_t bh = m / a.rows;
     const uint32_t r = (uint32_t)(m % a.rows);
-    const int b = (int)(bh / a.Hkv), pos = (int)(r / (uint32_t)a.G), h = (int)(bh % a.Hkv) * a.G + (int)(r % (uint32_t)a.G);
+    const int b = (int)(bh / a.Hkv), pos = row_at(a, r).pos, h = (int)(bh % a.Hkv) * a.G + row_at(a, r).head;
     const E *const g = (const E *)a.g + b * a.gs.b + pos * a.gs.l + h * a.gs.h;
     const E *const o = (const E *)a.o + b * a.os.b + pos * a.os.l + h * a.os.h;
     float s = 0.0f;
@@ -106,7 +106,8 @@ __device__ __forceinline__ void load_frags(typename Tile<T>::Frag *f, const type
 
 // ---- dK, dV ----------------------------------------------------------------------
 //
-// 128 keys a workgroup, 32 a wave with k and v in registers; tiles of 32 rows
+// 128 keys a workgroup, 32 a wave with k in registers and v there too, or in
+// LDS where two waves a SIMD would not find the registers; tiles of 32 rows
 // (q, g, lse, delta) through LDS, double-buffered.  S and dP are formed with
 // a lane's elements along the rows and its column a key, so that P and dS are
 // operands of dV^T = g^T P and dK^T = q^T dS where they stand.
@@ -115,10 +116,13 @@ struct KvShape {
     static constexpr int RT = 32;
     static constexpr int P = DP + Tile<T>::PADC;
     static constexpr size_t tile = (size_t)RT * P;
-    static constexpr size_t loop_lds = 2 * (2 * tile * sizeof(typename T::T) + 4 * RT * sizeof(float));
+    static constexpr bool v_lds = sizeof(typename T::T) * DP >= 256;
+    static constexpr int PV = DP + Tile<T>::PADR;
+    static constexpr size_t loop_lds = 2 * (2 * tile * sizeof(typename T::T) + 4 * RT * sizeof(float)) +
+                                       (v_lds ? (size_t)128 * PV * sizeof(typename T::T) : 0);
     static constexpr size_t drain_lds = (size_t)4 * 32 * (DP + 4) * sizeof(float);
     static constexpr size_t lds = loop_lds > drain_lds ? loop_lds : drain_lds;
-    static constexpr int blocks = sizeof(typename T::T) * DP > 128 ? 1 : 2;  // k, v, dk, dv of a wave: registers
+    static constexpr int blocks = sizeof(typename T::T) * DP > 256 ? 1 : 2;
 };
 
 template <typename T, int DP, bool VEC>
@@ -132,6 +136,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
     float *const lbuf = (float *)(gbuf + 2 * S::tile), *const dbuf = lbuf + 2 * RT;
     int *const from = (int *)(dbuf + 2 * RT), *const upto = from + 2 * RT;  // the keys that each row sees
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
+    E *const vrow = (E *)(upto + 2 * RT) + (wave * 32 + (lane & 31)) * S::PV + half * 8;  // this lane's key in LDS
 
     const int64_t tiles = (a.Lk + 127) / 128;
     int64_t id = xcd_order(blockIdx.x, gridDim.x);
@@ -158,11 +163,18 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
     r0 += min(per * split, n_tiles) * RT;
     r1 = min(r1, r0 + per * RT);
 
-    typename M::Frag kf[NS], vf[NS];
+    typename M::Frag kf[NS], vf[S::v_lds ? 1 : NS];
     {
         const int kc = min(key, a.Lk - 1);
+        const E *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h + kc * a.vs.l;
+        if constexpr (S::v_lds) {  // each lane leaves what it will read itself
+            load_frags<T, DP, VEC>(kf, vp, a.D, half, key < rule.len);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) *(typename M::Frag *)(vrow + i * 16) = kf[i];
+        } else {
+            load_frags<T, DP, VEC>(vf, vp, a.D, half, key < rule.len);
+        }
         load_frags<T, DP, VEC>(kf, (const E *)a.k + b * a.ks.b + hk * a.ks.h + kc * a.ks.l, a.D, half, key < rule.len);
-        load_frags<T, DP, VEC>(vf, (const E *)a.v + b * a.vs.b + hk * a.vs.h + kc * a.vs.l, a.D, half, key < rule.len);
     }
     f32x16 dk[ND], dv[ND];
 #pragma unroll
@@ -172,13 +184,15 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
     const E *const qp = (const E *)a.q + b * a.qs.b + hk * a.G * a.qs.h, *const gp = (const E *)a.g + b * a.gs.b + hk * a.G * a.gs.h;
     const float *const dp = a.delta + ((int64_t)b * a.Hkv + hk) * a.rows, *const lp = a.lse + ((int64_t)b * a.Hq + hk * a.G) * a.Lq;
     Stage<T, RT, DP, 256, VEC> qs, gs;
+    qs.init_rows(a, a.qs, t);
+    gs.init_rows(a, a.gs, t);
     float lse = 0.0f, del = 0.0f;
     auto load = [&](int64_t r) {
-        qs.load_rows(qp, a.qs, r, a.rows, a.G, a.D, t);
-        gs.load_rows(gp, a.gs, r, a.rows, a.G, a.D, t);
+        qs.load_rows(qp, a, a.qs, r, t);
+        gs.load_rows(gp, a, a.gs, r, t);
         if (t < RT) {
-            const uint32_t n = (uint32_t)min(r + t, a.rows - 1);
-            lse = lp[(int64_t)(n % (uint32_t)a.G) * a.Lq + n / (uint32_t)a.G];
+            const int64_t n = min(r + t, a.rows - 1);
+            lse = lp[(int64_t)row_at(a, n).head * a.Lq + row_at(a, n).pos];
             del = dp[n];
         }
     };
@@ -190,7 +204,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
             // rows that saw nothing, or are not there, get probability 0
             lbuf[at * RT + t] = t < limit && lse != -INFINITY ? lse * kLog2e : INFINITY;
             dbuf[at * RT + t] = t < limit ? del : 0.0f;
-            const KeyRange kr = rule.at((int)((uint32_t)min(r + t, a.rows - 1) / (uint32_t)a.G));
+            const KeyRange kr = rule.at(row_at(a, min(r + t, a.rows - 1)).pos);
             from[at * RT + t] = kr.lo;
             upto[at * RT + t] = kr.hi;
         }
@@ -209,7 +223,13 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
 #pragma unroll
         for (int i = 0; i < NS; ++i) s = M::mma(M::row_frag(qt + (lane & 31) * S::P + i * 16 + half * 8), kf[i], s);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) p = M::mma(M::row_frag(gt + (lane & 31) * S::P + i * 16 + half * 8), vf[i], p);
+        for (int i = 0; i < NS; ++i) {
+            const typename M::Frag gr = M::row_frag(gt + (lane & 31) * S::P + i * 16 + half * 8);
+            if constexpr (S::v_lds)
+                p = M::mma(gr, M::row_frag(vrow + i * 16), p);
+            else
+                p = M::mma(gr, vf[i], p);
+        }
         // does every row of the tile see every key of the wave?
         const int w0 = key0 + wave * 32;
         const bool masked = __builtin_amdgcn_readfirstlane(from[at * RT + RT - 1]) > w0 ||
@@ -220,13 +240,21 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int k = 4 * g + e;
-                float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], c, -l4[e])), ds = pr * (p[k] - d4[e]);
-                if (masked) {
-                    const int n = at * RT + 8 * g + 4 * half + e;
-                    if (key < from[n] || key >= upto[n]) pr = ds = 0.0f;
+                s[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k], c, -l4[e]));
+                p[k] = s[k] * (p[k] - d4[e]);
+            }
+        }
+        if (masked) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const i32x4 lo = *(const i32x4 *)(from + at * RT + 8 * g + 4 * half);
+                const i32x4 hi = *(const i32x4 *)(upto + at * RT + 8 * g + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool sees = key >= lo[e] && key < hi[e];
+                    s[4 * g + e] = sees ? s[4 * g + e] : 0.0f;
+                    p[4 * g + e] = sees ? p[4 * g + e] : 0.0f;
                 }
-                s[k] = pr;
-                p[k] = ds;
             }
         }
         const typename M::Frag p0 = M::template pack<0>(s), p1 = M::template pack<1>(s);
@@ -319,12 +347,12 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
     const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
     const int64_t row0 = tile * 128, last = min(row0 + 127, a.rows - 1);
     const int64_t row = row0 + wave * 32 + (lane & 31), rc = min(row, a.rows - 1);
-    const int pos = (int)((uint32_t)rc / (uint32_t)a.G), h = hk * a.G + (int)((uint32_t)rc % (uint32_t)a.G);
+    const int pos = row_at(a, rc).pos, h = hk * a.G + row_at(a, rc).head;
 
     const KeyRule rule = key_rule(a, b);
     const KeyRange kr = rule.at(pos);
-    const int lo = rule.at((int)((uint32_t)row0 / (uint32_t)a.G)).lo;
-    const int hi = rule.at((int)((uint32_t)last / (uint32_t)a.G)).hi;
+    const int lo = rule.at(row_at(a, row0).pos).lo;
+    const int hi = rule.at(row_at(a, last).pos).hi;
     const KeyRange first = {__builtin_amdgcn_readfirstlane(kr.lo), __builtin_amdgcn_readfirstlane(kr.hi)};
     const KeyRange final = {__builtin_amdgcn_readlane(kr.lo, 31), __builtin_amdgcn_readlane(kr.hi, 31)};
 
@@ -341,6 +369,8 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 256, VEC> ks, vs;
+    ks.init(a.ks.l, a.D, t);
+    vs.init(a.vs.l, a.D, t);
     int k0 = lo / KT * KT;
     if (k0 < hi) {
         ks.load(kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
@@ -364,11 +394,12 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
             for (int i = 0; i < NS; ++i) p = M::mma(M::row_frag(vt + (lane & 31) * S::P + i * 16 + half * 8), gf[i], p);
             const bool masked = final.lo > k0 || first.hi < k0 + KT;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lse)) * (p[r] - delta);
-                if (masked) {
+            for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lse)) * (p[r] - delta);
+            if (masked) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
                     const int j = k0 + 8 * (r >> 2) + 4 * half + (r & 3);
-                    if (j < kr.lo || j >= kr.hi) p[r] = 0.0f;
+                    p[r] = j >= kr.lo && j < kr.hi ? p[r] : 0.0f;
                 }
             }
             const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
@@ -388,7 +419,7 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
     drain<DP>((float *)smem + wave * 32 * (DP + 4), dq, a.scale, lane, [&](int r, int col, f32x4 v) {
         const int64_t n = row0 + wave * 32 + r;
         if (n >= a.rows) return;
-        const int i = (int)((uint32_t)n / (uint32_t)a.G), hq = hk * a.G + (int)((uint32_t)n % (uint32_t)a.G);
+        const int i = row_at(a, n).pos, hq = hk * a.G + row_at(a, n).head;
         store_piece<T, VEC>(out + i * a.gqs.l + hq * a.gqs.h, col, v, a.D);
     });
 }

@@ -16,6 +16,8 @@
 // The parameter gradients are summed per workgroup over all the positions
 // that it visits, left in the workspace and added in workgroup order: no
 // atomics, the same bits every time.
+#include <type_traits>
+
 #include "attn_tile.h"
 
 namespace dc1d {
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(256) void k_ln_rows(LayerNormArgs a) {
 #pragma unroll
                 for (int e = 0; e < V::N; ++e) s += f[i][e];
         }
-        const float mean = row_sum<WPR>(s, red, 0) / a.C;
+        const float mean = row_sum<WPR>(s, red, 0) * a.inv_c;
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -122,7 +124,7 @@ __global__ __launch_bounds__(256) void k_ln_rows(LayerNormArgs a) {
                 if (in) s += f[i][e] * f[i][e];
             }
         }
-        const float rstd = rsqrtf(row_sum<WPR>(s, red, 1) / a.C + a.eps);
+        const float rstd = rsqrtf(row_sum<WPR>(s, red, 1) * a.inv_c + a.eps);
         if (!on) continue;
         E *const y = (E *)a.y + n * a.C;
 #pragma unroll
@@ -157,13 +159,13 @@ __global__ __launch_bounds__(256) void k_ln_rows_any(LayerNormArgs a) {
         const E *const x = (const E *)a.x + n * a.C;
         float s = 0.0f;
         for (int c = threadIdx.x; c < a.C; c += 256) s += T::ld(x, c);
-        const float mean = row_sum<4>(s, red, 0) / a.C;
+        const float mean = row_sum<4>(s, red, 0) * a.inv_c;
         s = 0.0f;
         for (int c = threadIdx.x; c < a.C; c += 256) {
             const float d = T::ld(x, c) - mean;
             s += d * d;
         }
-        const float rstd = rsqrtf(row_sum<4>(s, red, 1) / a.C + a.eps);
+        const float rstd = rsqrtf(row_sum<4>(s, red, 1) * a.inv_c + a.eps);
         E *const y = (E *)a.y + n * a.C;
         for (int c = threadIdx.x; c < a.C; c += 256) {
             float v = (T::ld(x, c) - mean) * rstd;
@@ -231,8 +233,8 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd(LayerNormArgs a) {
             }
         }
         if (a.y) {
-            s1 = row_sum<WPR>(s1, red, slot) / a.C;
-            s2 = row_sum<WPR>(s2, red, slot + 1) / a.C;
+            s1 = row_sum<WPR>(s1, red, slot) * a.inv_c;
+            s2 = row_sum<WPR>(s2, red, slot + 1) * a.inv_c;
             slot ^= 2;
             if (n < a.B) {
                 E *const y = (E *)a.y + n * a.C;
@@ -301,8 +303,8 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd_any(LayerNormArgs a) {
         }
         fresh = false;
         if (!a.y) continue;
-        s1 = row_sum<4>(s1, red, slot) / a.C;
-        s2 = row_sum<4>(s2, red, slot + 1) / a.C;
+        s1 = row_sum<4>(s1, red, slot) * a.inv_c;
+        s2 = row_sum<4>(s2, red, slot + 1) * a.inv_c;
         slot ^= 2;
         E *const y = (E *)a.y + n * a.C;
         for (int c = threadIdx.x; c < a.C; c += 256) {
@@ -318,11 +320,13 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd_any(LayerNormArgs a) {
 // A tile is TL neighbouring positions of one batch and all C channels.  A
 // thread holds EPT neighbouring positions (16 bytes, or one element where
 // rows are not aligned) of every RP-th channel: NP of them in registers, or,
-// NP = 0, read again for each pass.
-template <typename T, int EPT, int NT>
+// NP = 0, read again for each pass.  TPR threads stand across a tile's row:
+// 8 (whole 128-byte lines), fewer where C channels would not fit otherwise.
+// Neighbouring tiles go to one XCD: where rows are not whole lines they share
+// the lines at their edges.
+template <int EPT, int TPR_, int NT>
 struct ColShape {
-    static constexpr int TPR = EPT > 1 ? 8 : 64;  // threads across a tile's row
-    static constexpr int TL = TPR * EPT, RP = NT / TPR;
+    static constexpr int TPR = TPR_, TL = TPR * EPT, RP = NT / TPR;
 };
 
 template <typename T, int EPT>
@@ -371,121 +375,157 @@ __device__ __forceinline__ void col_sum(float (*s)[EPT], float *red) {
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             float v = 0.0f;
-#pragma unroll
+#pragma unroll 2
             for (int w = 0; w < W; ++w) v += red[(k * W + w) * TL + tl * EPT + e];
             s[k][e] = v;
         }
 }
 
-template <typename T, int EPT, int NP, int NT>
-__global__ __launch_bounds__(NT) void k_ln_cols(LayerNormArgs a) {
+// The pieces of a tile that a thread holds: channels c0 + i RP.  Each is read
+// at a base that the whole workgroup shares plus this thread's 32-bit offset;
+// a channel past C reads row i RP in its place and is left out of the sums.
+template <typename T, int EPT>
+struct ColPiece {
     using E = typename T::T;
-    using S = ColShape<T, EPT, NT>;
+    using Raw = typename std::conditional<(EPT > 1), u32x4, E>::type;
+    static __device__ __forceinline__ Raw load(const E *base, uint32_t off) { return *(const Raw *)((const char *)base + off); }
+    // Between two uses of a held piece: the compiler otherwise keeps the
+    // widened and centred values of the first use for the second, in more
+    // registers than the pieces take.
+    static __device__ __forceinline__ void again(Raw &r) {
+        if constexpr (EPT > 1) {
+            asm volatile("" : "+v"(r));
+        } else {
+            uint32_t v;
+            if constexpr (sizeof(E) == 4)
+                v = __float_as_uint(r);
+            else
+                v = r;
+            asm volatile("" : "+v"(v));
+            if constexpr (sizeof(E) == 4)
+                r = __uint_as_float(v);
+            else
+                r = (E)v;
+        }
+    }
+    static __device__ __forceinline__ void widen(Raw r, float *f) {
+        if constexpr (EPT > 1)
+            Vec<T>::widen(r, f);
+        else
+            f[0] = T::ld(&r, 0);
+    }
+};
+
+template <typename T, int EPT, int TPR, int NP, int NT>
+__global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
+    using E = typename T::T;
+    using S = ColShape<EPT, TPR, NT>;
+    using P = ColPiece<T, EPT>;
     __shared__ float red[NT / 64 * S::TL];
     const int64_t tiles = (a.L + S::TL - 1) / S::TL;
     const int c0 = threadIdx.x / S::TPR;
-    for (int64_t tile = blockIdx.x; tile < tiles * a.B; tile += gridDim.x) {
-        const int64_t b = tile / tiles, l = tile % tiles * S::TL + threadIdx.x % S::TPR * EPT;
-        const bool on = l < a.L;
-        const int64_t at = b * a.C * a.L + (on ? l : 0);
-        const E *const x = (const E *)a.x + at;
-        E *const y = (E *)a.y + at;
-        float f[NP > 0 ? NP : 1][EPT], s[1][EPT] = {};
+    for (int64_t tile = xcd_order(blockIdx.x, gridDim.x); tile < tiles * a.B; tile += gridDim.x) {
+        const int64_t b = tile / tiles, l0 = tile % tiles * S::TL;
+        const int tl = threadIdx.x % S::TPR * EPT;
+        const bool on = l0 + tl < a.L;
+        const E *const x = (const E *)a.x + b * a.C * a.L + l0;
+        E *const y = (E *)a.y + b * a.C * a.L + l0;
+        const uint32_t row0 = (on ? tl : 0) * sizeof(E), off = row0 + (uint32_t)c0 * (uint32_t)a.L * sizeof(E);
+        typename P::Raw raw[NP > 0 ? NP : 1];
+        float f[EPT], s[1][EPT] = {};
         if constexpr (NP > 0) {
-            u32x4 raw[NP];
-            if constexpr (EPT > 1) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int c = c0 + i * S::RP;
-                    raw[i] = *(const u32x4 *)(x + (int64_t)(c < a.C ? c : 0) * a.L);
-                }
+            for (int i = 0; i < NP; ++i) {
+                const int ci = i * S::RP < a.C ? i * S::RP : 0;
+                raw[i] = P::load(x + (int64_t)ci * a.L, c0 + ci < a.C ? off : row0);
             }
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int c = c0 + i * S::RP;
-                if constexpr (EPT > 1) {
-                    Vec<T>::widen(raw[i], f[i]);
-                } else {
-                    f[i][0] = T::ld(x, (int64_t)(c < a.C ? c : 0) * a.L);
-                }
-                if (c < a.C)
+                P::widen(raw[i], f);
+                if (c0 + i * S::RP < a.C)
 #pragma unroll
-                    for (int e = 0; e < EPT; ++e) s[0][e] += f[i][e];
+                    for (int e = 0; e < EPT; ++e) s[0][e] += f[e];
             }
         } else {
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, on, f[0]);
+                col_load<T, EPT>(x + (int64_t)c * a.L + tl, on, f);
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) s[0][e] += f[0][e];
+                for (int e = 0; e < EPT; ++e) s[0][e] += f[e];
             }
         }
         col_sum<EPT, S::TPR, NT, 1>(s, red);
         float mean[EPT], rstd[EPT];
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) mean[e] = s[0][e] / a.C, s[0][e] = 0.0f;
+        for (int e = 0; e < EPT; ++e) mean[e] = s[0][e] * a.inv_c, s[0][e] = 0.0f;
         if constexpr (NP > 0) {
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
+            for (int i = 0; i < NP; ++i) {
+                P::again(raw[i]);
+                P::widen(raw[i], f);
+                if (c0 + i * S::RP < a.C)
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) {
-                    f[i][e] -= mean[e];
-                    if (c0 + i * S::RP < a.C) s[0][e] += f[i][e] * f[i][e];
-                }
+                    for (int e = 0; e < EPT; ++e) s[0][e] += (f[e] - mean[e]) * (f[e] - mean[e]);
+            }
         } else {
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, on, f[0]);
+                col_load<T, EPT>(x + (int64_t)c * a.L + tl, on, f);
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) s[0][e] += (f[0][e] - mean[e]) * (f[0][e] - mean[e]);
+                for (int e = 0; e < EPT; ++e) s[0][e] += (f[e] - mean[e]) * (f[e] - mean[e]);
             }
         }
         col_sum<EPT, S::TPR, NT, 1>(s, red);
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) rstd[e] = rsqrtf(s[0][e] / a.C + a.eps);
+        for (int e = 0; e < EPT; ++e) rstd[e] = rsqrtf(s[0][e] * a.inv_c + a.eps);
         if (!on) continue;
-        auto put = [&](int c, float *v, bool centred) {
+        auto put = [&](int c) {
             const float w = a.w ? T::ld((const E *)a.w, c) : 1.0f, bias = a.b ? T::ld((const E *)a.b, c) : 0.0f;
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                v[e] = (centred ? v[e] : v[e] - mean[e]) * rstd[e];
-                if (a.w) v[e] *= w;
-                if (a.b) v[e] += bias;
+                f[e] = (f[e] - mean[e]) * rstd[e];
+                if (a.w) f[e] *= w;
+                if (a.b) f[e] += bias;
             }
-            col_store<T, EPT>(y + (int64_t)c * a.L, v);
+            col_store<T, EPT>(y + (int64_t)c * a.L + tl, f);
         };
         if constexpr (NP > 0) {
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (c0 + i * S::RP < a.C) put(c0 + i * S::RP, f[i], true);
+            for (int i = 0; i < NP; ++i) {
+                P::again(raw[i]);
+                P::widen(raw[i], f);
+                if (c0 + i * S::RP < a.C) put(c0 + i * S::RP);
+            }
         } else {
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, true, f[0]);
-                put(c, f[0], false);
+                col_load<T, EPT>(x + (int64_t)c * a.L + tl, true, f);
+                put(c);
             }
         }
         if (c0 == 0) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                if (a.mean) a.mean[b * a.L + l + e] = mean[e];
-                if (a.rstd) a.rstd[b * a.L + l + e] = rstd[e];
+                if (a.mean) a.mean[b * a.L + l0 + tl + e] = mean[e];
+                if (a.rstd) a.rstd[b * a.L + l0 + tl + e] = rstd[e];
             }
         }
     }
 }
 
-// Backward, channels first.  Workgroups stride over the tiles.  With the
-// channels in registers (NP > 0) so are their parameter sums; otherwise they
-// are kept in the workgroup's part of the workspace, a thread row (TPR
-// neighbouring lanes) owning its channels.
-template <typename T, int EPT, int NP, int NT>
-__global__ __launch_bounds__(NT) void k_ln_cols_bwd(LayerNormArgs a) {
+// Backward, channels first.  Workgroups, as many as fit the GPU at once,
+// stride over the tiles, and a tile's pieces are on their way from HBM while
+// the one before it is worked on.  With the channels in registers (NP > 0) so
+// are their parameter sums; otherwise they are kept in the workgroup's part
+// of the workspace, a thread row (TPR neighbouring lanes) owning its channels.
+template <typename T, int EPT, int TPR, int NP, int NT>
+__global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(LayerNormArgs a) {
     using E = typename T::T;
-    using S = ColShape<T, EPT, NT>;
+    using S = ColShape<EPT, TPR, NT>;
+    using P = ColPiece<T, EPT>;
     constexpr int NR = NP > 0 ? NP : 1;
     __shared__ float red[2 * (NT / 64) * S::TL];
     const int64_t tiles = (a.L + S::TL - 1) / S::TL;
-    const int c0 = threadIdx.x / S::TPR, tr = threadIdx.x % S::TPR;
+    const int c0 = threadIdx.x / S::TPR, tr = threadIdx.x % S::TPR, tl = tr * EPT;
     const bool params = a.gw || a.gb;
-    float *const pw = params ? a.ws + (int64_t)blockIdx.x * 2 * a.C : nullptr, *const pb = pw + a.C;
+    float *const pw = a.ws + (params ? (int64_t)blockIdx.x * 2 * a.C : 0), *const pb = pw + a.C;
     float gw[NR] = {}, gb[NR] = {};
     bool fresh = true;
     auto across = [](float v) {  // over the lanes of a thread row
@@ -493,69 +533,72 @@ __global__ __launch_bounds__(NT) void k_ln_cols_bwd(LayerNormArgs a) {
         for (int d = 1; d < S::TPR; d <<= 1) v += __shfl_xor(v, d);
         return v;
     };
-    for (int64_t tile = blockIdx.x; tile < tiles * a.B; tile += gridDim.x) {
-        const int64_t b = tile / tiles, l = tile % tiles * S::TL + tr * EPT;
-        const bool on = l < a.L;
-        const int64_t at = b * a.C * a.L + (on ? l : 0);
-        const E *const x = (const E *)a.x + at, *const g = (const E *)a.g + at;
-        E *const y = (E *)a.y + at;
-        float mean[EPT], rstd[EPT], s[2][EPT] = {};
+    struct Held {
+        typename P::Raw x[NR], g[NR];
+        float mean[EPT], rstd[EPT];
+    };
+    auto fetch = [&](int64_t tile, Held &h) {
+        const int64_t b = tile / tiles, l0 = tile % tiles * S::TL, at = b * a.C * a.L + l0;
+        const bool on = l0 + tl < a.L;
+        if constexpr (NP > 0) {
+            const E *const x = (const E *)a.x + at, *const g = (const E *)a.g + at;
+            const uint32_t row0 = (on ? tl : 0) * sizeof(E), off = row0 + (uint32_t)c0 * (uint32_t)a.L * sizeof(E);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int ci = i * S::RP < a.C ? i * S::RP : 0;
+                const uint32_t o = c0 + ci < a.C ? off : row0;
+                h.x[i] = P::load(x + (int64_t)ci * a.L, o);
+                h.g[i] = P::load(g + (int64_t)ci * a.L, o);
+            }
+        }
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            mean[e] = a.mean[b * a.L + (on ? l + e : 0)];
-            rstd[e] = a.rstd[b * a.L + (on ? l + e : 0)];
+            h.mean[e] = a.mean[b * a.L + l0 + (on ? tl + e : 0)];
+            h.rstd[e] = a.rstd[b * a.L + l0 + (on ? tl + e : 0)];
         }
-        float xh[NR][EPT], u[NR][EPT];
-        // the normalised x and the weighted gradient of channel c, and what they add to the sums
-        auto take = [&](int c, bool in, float *xv, float *uv, float &w_sum, float &b_sum) {
-            const float w = a.w ? T::ld((const E *)a.w, c) : 1.0f;
+    };
+    const int64_t all = tiles * a.B;
+    // held, not read in the loop: loads return in order, and one issued after
+    // the next tile's would wait for all of it
+    float wv[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) wv[i] = NP > 0 && a.w && c0 + i * S::RP < a.C ? T::ld((const E *)a.w, c0 + i * S::RP) : 1.0f;
+    Held next;
+    const int64_t tile0 = xcd_order(blockIdx.x, gridDim.x);
+    fetch(tile0, next);  // there are at least as many tiles as workgroups
+    for (int64_t tile = tile0; tile < all; tile += gridDim.x) {
+        Held h = next;
+        if (tile + gridDim.x < all) fetch(tile + gridDim.x, next);
+        const int64_t b = tile / tiles, l0 = tile % tiles * S::TL, at = b * a.C * a.L + l0;
+        const bool on = l0 + tl < a.L;
+        float s[2][EPT] = {}, xh[EPT], u[EPT];
+        // what a channel of weight w adds to the sums over the channels and to its parameters' gradients
+        auto take = [&](float w, float &w_sum, float &b_sum) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                xv[e] = (xv[e] - mean[e]) * rstd[e];
-                if (in) {
-                    w_sum += uv[e] * xv[e];
-                    b_sum += uv[e];
-                }
-                uv[e] *= w;
-                if (in) {
-                    s[0][e] += uv[e];
-                    s[1][e] += uv[e] * xv[e];
-                }
+                xh[e] = (xh[e] - h.mean[e]) * h.rstd[e];
+                w_sum += u[e] * xh[e];
+                b_sum += u[e];
+                u[e] *= w;
+                s[0][e] += u[e];
+                s[1][e] += u[e] * xh[e];
             }
         };
         if constexpr (NP > 0) {
-            if constexpr (EPT > 1) {
-                u32x4 xr[NP], gr[NP];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int64_t c = c0 + i * S::RP < a.C ? c0 + i * S::RP : 0;
-                    xr[i] = *(const u32x4 *)(x + c * a.L);
-                    gr[i] = *(const u32x4 *)(g + c * a.L);
-                }
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    Vec<T>::widen(xr[i], xh[i]);
-                    Vec<T>::widen(gr[i], u[i]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int64_t c = c0 + i * S::RP < a.C ? c0 + i * S::RP : 0;
-                    xh[i][0] = T::ld(x, c * a.L);
-                    u[i][0] = T::ld(g, c * a.L);
-                }
-            }
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const int c = c0 + i * S::RP;
-                take(c < a.C ? c : 0, on && c < a.C, xh[i], u[i], gw[i], gb[i]);
+                P::widen(h.x[i], xh);
+                P::widen(h.g[i], u);
+                if (on && c < a.C) take(wv[i], gw[i], gb[i]);
             }
         } else {
+            const E *const x = (const E *)a.x + at + tl, *const g = (const E *)a.g + at + tl;
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, on, xh[0]);
-                col_load<T, EPT>(g + (int64_t)c * a.L, on, u[0]);
+                col_load<T, EPT>(x + (int64_t)c * a.L, on, xh);
+                col_load<T, EPT>(g + (int64_t)c * a.L, on, u);
                 float w_sum = 0.0f, b_sum = 0.0f;
-                take(c, on, xh[0], u[0], w_sum, b_sum);
+                if (on) take(a.w ? T::ld((const E *)a.w, c) : 1.0f, w_sum, b_sum);
                 if (params) {
                     w_sum = across(w_sum);
                     b_sum = across(b_sum);
@@ -570,26 +613,32 @@ __global__ __launch_bounds__(NT) void k_ln_cols_bwd(LayerNormArgs a) {
         if (!a.y) continue;
         col_sum<EPT, S::TPR, NT, 2>(s, red);
         if (!on) continue;
-        auto put = [&](int c, const float *xv, float *uv) {
+        E *const y = (E *)a.y + at + tl;
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) uv[e] = rstd[e] * (uv[e] - s[0][e] / a.C - xv[e] * (s[1][e] / a.C));
-            col_store<T, EPT>(y + (int64_t)c * a.L, uv);
+        for (int e = 0; e < EPT; ++e) s[0][e] *= a.inv_c, s[1][e] *= a.inv_c;
+        auto put = [&](int c, float w) {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                xh[e] = (xh[e] - h.mean[e]) * h.rstd[e];
+                u[e] = h.rstd[e] * (u[e] * w - s[0][e] - xh[e] * s[1][e]);
+            }
+            col_store<T, EPT>(y + (int64_t)c * a.L, u);
         };
         if constexpr (NP > 0) {
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (c0 + i * S::RP < a.C) put(c0 + i * S::RP, xh[i], u[i]);
+            for (int i = 0; i < NP; ++i) {
+                P::again(h.x[i]);
+                P::again(h.g[i]);
+                P::widen(h.x[i], xh);
+                P::widen(h.g[i], u);
+                if (c0 + i * S::RP < a.C) put(c0 + i * S::RP, wv[i]);
+            }
         } else {
+            const E *const x = (const E *)a.x + at + tl, *const g = (const E *)a.g + at + tl;
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, true, xh[0]);
-                col_load<T, EPT>(g + (int64_t)c * a.L, true, u[0]);
-                const float w = a.w ? T::ld((const E *)a.w, c) : 1.0f;
-#pragma unroll
-                for (int e = 0; e < EPT; ++e) {
-                    xh[0][e] = (xh[0][e] - mean[e]) * rstd[e];
-                    u[0][e] *= w;
-                }
-                put(c, xh[0], u[0]);
+                col_load<T, EPT>(x + (int64_t)c * a.L, true, xh);
+                col_load<T, EPT>(g + (int64_t)c * a.L, true, u);
+                put(c, a.w ? T::ld((const E *)a.w, c) : 1.0f);
             }
         }
     }
@@ -607,24 +656,27 @@ __global__ __launch_bounds__(NT) void k_ln_cols_bwd(LayerNormArgs a) {
     }
 }
 
-// gw, gb: the workgroups' parts [parts][2][C] in order.  16 channels by 16
-// runs of the parts a workgroup; the runs are added in order.
+// gw, gb: the workgroups' parts [parts][2][C] in order.  16 channels by 64
+// runs of the parts a workgroup, so that few loads follow one another; the
+// runs are added in order.
 template <typename T>
-__global__ __launch_bounds__(256) void k_ln_params(LayerNormArgs a, int parts) {
+__global__ __launch_bounds__(1024) void k_ln_params(LayerNormArgs a, int parts) {
     using E = typename T::T;
-    __shared__ float red[16][17];
+    __shared__ float red[64][17];
     const int j = threadIdx.x & 15, run = threadIdx.x >> 4;
-    const int64_t n = (int64_t)blockIdx.x * 16 + j;  // of 2 C
-    const int per = (parts + 15) / 16, p0 = run * per, p1 = min(p0 + per, parts);
+    const int64_t n = (int64_t)blockIdx.x * 16 + j, all = 2 * (int64_t)a.C;
+    const int per = (parts + 63) / 64, p0 = run * per, p1 = min(p0 + per, parts);
     float s = 0.0f;
-    if (n < 2 * (int64_t)a.C)
-        for (int p = p0; p < p1; ++p) s += a.ws[(int64_t)p * 2 * a.C + n];
+    if (n < all) {
+#pragma unroll 8
+        for (int p = p0; p < p1; ++p) s += a.ws[p * all + n];
+    }
     red[run][j] = s;
     __syncthreads();
-    if (run != 0 || n >= 2 * (int64_t)a.C) return;
+    if (run != 0 || n >= all) return;
     s = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s += red[r][j];
+    for (int r = 0; r < 64; ++r) s += red[r][j];
     if (n < a.C) {
         if (a.gw) T::st((E *)a.gw, n, s);
     } else if (a.gb) {
@@ -652,20 +704,20 @@ RowChoice choose_rows(int C, int per, bool vec) {
     return {0, 0};
 }
 
-// Threads and channels held per thread, channels first; np 0: read again.
+// Which kernel serves channels first: threads across a row, channels held per
+// thread (0: read again), threads.
 struct ColChoice {
-    int nt, np;
+    int tpr, np, nt;
 };
-ColChoice choose_cols(int C, bool vec) {
+ColChoice choose_cols(int C, int64_t L, bool vec) {
+    const bool far = L >= 1 << 23;  // a tile's channels lie past 32-bit offsets
     if (vec) {
-        if (C <= 256) return {256, 8};
-        if (C <= 512) return {512, 8};
-        if (C <= 1024) return {1024, 8};
-        return {1024, 0};
+        if (far || C > 2048) return {8, 0, 1024};
+        if (C <= 256) return {8, 8, 256};
+        return {C <= 512 ? 8 : C <= 1024 ? 4 : 2, 8, 512};
     }
-    if (C <= 128) return {1024, 8};
-    if (C <= 512) return {1024, 32};
-    return {1024, 0};
+    if (far || C > 512) return {32, 0, 1024};
+    return {16, 16, 512};
 }
 
 template <typename T>
@@ -676,6 +728,20 @@ bool vec_ok(const LayerNormArgs &a, bool backward) {
     if (a.L == 1) ok = ok && aligned16(a.w) && aligned16(a.b);
     return ok;
 }
+
+// Every combination that choose_cols gives.
+#define DC1D_COLS_SWITCH                                        \
+    if (vec) {                                                  \
+        constexpr int V = Vec<T>::N;                            \
+        if (c.np == 0) DC1D_COLS(V, 8, 0, 1024);                \
+        else if (c.nt == 256) DC1D_COLS(V, 8, 8, 256);          \
+        else if (c.tpr == 8) DC1D_COLS(V, 8, 8, 512);           \
+        else if (c.tpr == 4) DC1D_COLS(V, 4, 8, 512);           \
+        else DC1D_COLS(V, 2, 8, 512);                           \
+    } else {                                                    \
+        if (c.np == 0) DC1D_COLS(1, 32, 0, 1024);               \
+        else DC1D_COLS(1, 16, 16, 512);                         \
+    }
 
 template <typename T>
 hipError_t forward_typed(const LayerNormArgs &a, hipStream_t st) {
@@ -694,31 +760,19 @@ hipError_t forward_typed(const LayerNormArgs &a, hipStream_t st) {
 #undef DC1D_ROWS
         return hipGetLastError();
     }
-    const ColChoice c = choose_cols(a.C, vec);
-#define DC1D_COLS(E, P, N)                                                                                             \
-    hipLaunchKernelGGL((k_ln_cols<T, E, P, N>),                                                                        \
-                       grid_of(a.B * ((a.L + ColShape<T, E, N>::TL - 1) / ColShape<T, E, N>::TL)), dim3(N), 0, \
-                       st, a)
-    constexpr int V = Vec<T>::N;
-    if (vec) {
-        if (c.nt == 256) DC1D_COLS(V, 8, 256);
-        else if (c.nt == 512) DC1D_COLS(V, 8, 512);
-        else if (c.np) DC1D_COLS(V, 8, 1024);
-        else DC1D_COLS(V, 0, 1024);
-    } else {
-        if (c.np == 8) DC1D_COLS(1, 8, 1024);
-        else if (c.np) DC1D_COLS(1, 32, 1024);
-        else DC1D_COLS(1, 0, 1024);
-    }
+    const ColChoice c = choose_cols(a.C, a.L, vec);
+#define DC1D_COLS(E, R, P, N)                                                                                       \
+    hipLaunchKernelGGL((k_ln_cols<T, E, R, P, N>), grid_of(a.B * ((a.L + R * E - 1) / (R * E))), dim3(N), 0, st, a)
+    DC1D_COLS_SWITCH
 #undef DC1D_COLS
     return hipGetLastError();
 }
 
-// Workgroups of a backward call: few enough that the parts stay small next
-// to x, enough to fill the GPU.
+// The most workgroups (parts of the parameter gradients) of a backward call:
+// those that fit the GPU at once.
 int64_t backward_blocks(int64_t B, int64_t L, int num_cus) {
-    // the smallest unit that any of the kernels takes at a time: a row, or 32 positions
-    const int64_t units = L == 1 ? B : B * ((L + 31) / 32);
+    // no more than the smallest unit that any of the kernels takes at a time: a row, or 8 positions
+    const int64_t units = L == 1 ? B : B * ((L + 7) / 8);
     const int64_t most = (int64_t)num_cus * (L == 1 ? 4 : 2);
     return units < most ? units : most;
 }
@@ -727,7 +781,7 @@ template <typename T>
 hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
     if (a.B == 0 || a.L == 0) {  // no parts: the parameter gradients are zero
         if (a.gw || a.gb)
-            hipLaunchKernelGGL((k_ln_params<T>), dim3((uint32_t)((2 * (int64_t)a.C + 15) / 16)), dim3(256), 0, st, a, 0);
+            hipLaunchKernelGGL((k_ln_params<T>), dim3((uint32_t)((2 * (int64_t)a.C + 15) / 16)), dim3(1024), 0, st, a, 0);
         return hipGetLastError();
     }
     const bool vec = vec_ok<T>(a, true);
@@ -748,26 +802,17 @@ hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
         else hipLaunchKernelGGL((k_ln_rows_bwd_any<T>), dim3(blocks), blk, 0, st, a);
 #undef DC1D_ROWS
     } else {
-        const ColChoice c = choose_cols(a.C, vec);
-        constexpr int V = Vec<T>::N;
-        const int TL = vec ? 8 * V : 64;
-        const int64_t need = a.B * ((a.L + TL - 1) / TL);
-        blocks = (uint32_t)(need < most ? need : most);
-#define DC1D_COLS(E, P, N) hipLaunchKernelGGL((k_ln_cols_bwd<T, E, P, N>), dim3(blocks), dim3(N), 0, st, a)
-        if (vec) {
-            if (c.nt == 256) DC1D_COLS(V, 8, 256);
-            else if (c.nt == 512) DC1D_COLS(V, 8, 512);
-            else if (c.np) DC1D_COLS(V, 8, 1024);
-            else DC1D_COLS(V, 0, 1024);
-        } else {
-            if (c.np == 8) DC1D_COLS(1, 8, 1024);
-            else DC1D_COLS(1, 0, 1024);
-        }
+        const ColChoice c = choose_cols(a.C, a.L, vec);
+        const int TL = c.tpr * (vec ? Vec<T>::N : 1);
+        const int64_t need = a.B * ((a.L + TL - 1) / TL), fit = (int64_t)num_cus * (c.nt < 512 ? 512 / c.nt : 1);
+        blocks = (uint32_t)(need < fit ? need : fit);
+#define DC1D_COLS(E, R, P, N) hipLaunchKernelGGL((k_ln_cols_bwd<T, E, R, P, N>), dim3(blocks), dim3(N), 0, st, a)
+        DC1D_COLS_SWITCH
 #undef DC1D_COLS
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.gw || a.gb)) return e;
-    hipLaunchKernelGGL((k_ln_params<T>), dim3((uint32_t)((2 * (int64_t)a.C + 15) / 16)), dim3(256), 0, st, a, (int)blocks);
+    hipLaunchKernelGGL((k_ln_params<T>), dim3((uint32_t)((2 * (int64_t)a.C + 15) / 16)), dim3(1024), 0, st, a, (int)blocks);
     return hipGetLastError();
 }
 

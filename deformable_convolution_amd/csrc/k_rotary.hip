@@ -45,23 +45,32 @@ struct Piece {  // N neighbouring elements, moved as one access where N > 1
     }
 };
 
-// VP pairs and HT heads a thread.  Threads run over [units] of a position
-// (units: pair pieces, then pieces of the carried elements), head runs, and
-// positions.
+// VP pairs and HT heads a thread.  A position has `units` pieces (of pairs,
+// then of the carried elements) in each of `runs` runs of HT heads; a
+// workgroup takes `ppb` positions.
+struct RotaryGrid {
+    int units, runs, ppb;
+    int64_t positions;
+    FastDiv by_units, by_runs, by_L;
+    int rows16;  // the tables' rows of VP entries are 16-byte aligned
+};
+
 template <typename T, int VP, int HT>
-__global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int units, int runs, int64_t total) {
+__global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, RotaryGrid gr) {
     using E = typename T::T;
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
-        const int unit = (int)(id % units);
-        const int64_t rest = id / units;
-        int h0 = (int)(rest % runs) * HT;
-        const int64_t n = rest / runs;
-        const int b = (int)(n / a.L), l = (int)(n % a.L);
+    const int64_t n0 = (int64_t)blockIdx.x * gr.ppb;
+    const int work = (int)min((int64_t)gr.ppb, gr.positions - n0) * gr.units * gr.runs;
+    for (int w = threadIdx.x; w < work; w += 256) {
+        const uint32_t rest = fdiv(w, gr.by_units), local = fdiv(rest, gr.by_runs);
+        const int unit = w - (int)rest * gr.units;
+        int h0 = (int)(rest - local * gr.runs) * HT;
+        const uint32_t n = (uint32_t)n0 + local;
+        const int b = (int)fdiv(n, gr.by_L), l = (int)n - b * a.L;
         // runs cover the queries' heads, then the keys'
-        const int q_runs = (a.t[0].H + HT - 1) / HT;
-        const int which = h0 >= q_runs * HT;
+        const int q_heads = (a.t[0].H + HT - 1) / HT * HT;
+        const int which = h0 >= q_heads;
         const RotaryTensor &t = a.t[which];
-        if (which) h0 -= q_runs * HT;
+        if (which) h0 -= q_heads;
         const E *const x = (const E *)t.x + b * t.xs.b + l * t.xs.l;
         E *const y = (E *)t.y + b * t.ys.b + l * t.ys.l;
         const int i = unit * VP;
@@ -70,15 +79,6 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int units, int run
             for (int h = h0; h < min(h0 + HT, t.H); ++h)
                 for (int d = d0; d < min(d0 + 2 * VP, a.D); ++d) y[h * t.ys.h + d] = x[h * t.xs.h + d];
             continue;
-        }
-        const int *const pos = a.pos + b * a.pos_b + (int64_t)l * a.A;
-        float c[VP], s[VP];
-#pragma unroll
-        for (int j = 0; j < VP; ++j) {
-            const int axis = (i + j >= a.first[1]) + (i + j >= a.first[2]) + (i + j >= a.first[3]);
-            const int p = min(max(pos[axis], 0), a.P - 1);
-            c[j] = a.cos[(int64_t)p * a.R + i + j];
-            s[j] = a.sin[(int64_t)p * a.R + i + j] * a.sign;
         }
         float u[HT][2 * VP];
 #pragma unroll
@@ -92,6 +92,28 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int units, int run
                 Piece<T, VP>::load(xh + a.R + i, u[k] + VP);
             }
         }
+        const int *const pos = a.pos + b * a.pos_b + (int64_t)l * a.A;
+        auto axis_of = [&](int j) { return (j >= a.first[1]) + (j >= a.first[2]) + (j >= a.first[3]); };
+        auto row_of = [&](int axis) { return (int64_t)min(max(pos[axis], 0), a.P - 1) * a.R + i; };
+        float c[VP], s[VP];
+        const int axis = axis_of(i);
+        if (VP > 1 && gr.rows16 && axis == axis_of(i + VP - 1)) {  // the piece lies in one section
+            const int64_t at = row_of(axis);
+#pragma unroll
+            for (int j = 0; j < VP; j += 4) {
+                Piece<F32, VP < 4 ? VP : 4>::load(a.cos + at + j, c + j);
+                Piece<F32, VP < 4 ? VP : 4>::load(a.sin + at + j, s + j);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VP; ++j) {
+                const int64_t at = row_of(axis_of(i + j)) + j;
+                c[j] = a.cos[at];
+                s[j] = a.sin[at];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VP; ++j) s[j] *= a.sign;
 #pragma unroll
         for (int k = 0; k < HT; ++k) {
             if (h0 + k >= t.H) break;
@@ -133,23 +155,31 @@ bool pieces_ok(const RotaryArgs &a, int VP) {
     return true;
 }
 
+template <typename T, int VP, int HT>
+hipError_t launch_heads(const RotaryArgs &a, hipStream_t stream) {
+    RotaryGrid g;
+    g.units = (a.R + VP - 1) / VP + (a.D - 2 * a.R + 2 * VP - 1) / (2 * VP);
+    g.runs = (a.t[0].H + HT - 1) / HT + (a.t[1].H + HT - 1) / HT;
+    g.positions = (int64_t)a.B * a.L;
+    const int64_t per = (int64_t)g.units * g.runs;
+    // one piece a thread, and few enough workgroups for one launch
+    int64_t ppb = per >= 256 ? 1 : 256 / per;
+    const int64_t least = (g.positions + (1 << 22) - 1) >> 22;
+    if (ppb < least) ppb = least;
+    g.ppb = (int)ppb;
+    g.by_units = make_fastdiv((uint32_t)g.units);
+    g.by_runs = make_fastdiv((uint32_t)g.runs);
+    g.by_L = make_fastdiv((uint32_t)a.L);
+    g.rows16 = a.R % 4 == 0 && ((uintptr_t)a.cos & 15) == 0 && ((uintptr_t)a.sin & 15) == 0;
+    hipLaunchKernelGGL((k_rotary<T, VP, HT>), dim3((uint32_t)((g.positions + ppb - 1) / ppb)), dim3(256), 0, stream, a, g);
+    return hipGetLastError();
+}
+
 template <typename T, int VP>
 hipError_t launch(const RotaryArgs &a, hipStream_t stream) {
-    const int units = (a.R + VP - 1) / VP + (a.D - 2 * a.R + 2 * VP - 1) / (2 * VP);
-    const int64_t n = (int64_t)a.B * a.L;
-    auto runs_of = [&](int ht) { return (a.t[0].H + ht - 1) / ht + (a.t[1].H + ht - 1) / ht; };
     // one head a thread while that leaves the GPU unfilled (latency counts), else four
-    const int64_t one = n * units * runs_of(1);
-    if (one <= 256 * 256) {
-        hipLaunchKernelGGL((k_rotary<T, VP, 1>), dim3((uint32_t)((one + 255) / 256)), dim3(256), 0, stream, a, units,
-                           runs_of(1), one);
-    } else {
-        const int64_t total = n * units * runs_of(4);
-        const int64_t blocks = (total + 255) / 256;
-        hipLaunchKernelGGL((k_rotary<T, VP, 4>), dim3((uint32_t)(blocks < 1 << 20 ? blocks : 1 << 20)), dim3(256), 0, stream, a, units,
-                           runs_of(4), total);
-    }
-    return hipGetLastError();
+    const int64_t one = (int64_t)a.B * a.L * ((a.R + VP - 1) / VP) * (a.t[0].H + a.t[1].H);
+    return one <= 256 * 256 ? launch_heads<T, VP, 1>(a, stream) : launch_heads<T, VP, (sizeof(typename T::T) == 2 ? 2 : 4)>(a, stream);
 }
 
 }  // namespace

@@ -17,7 +17,7 @@ struct LayerNormArgs {
     int dtype;
     int64_t B, L;
     int C;
-    float eps;
+    float eps, inv_c;           // inv_c: 1 / C
     float *ws;                  // backward: the parameter gradients' partial sums
 };
 hipError_t launch_layer_norm(const LayerNormArgs &a, int num_cus, hipStream_t stream);
@@ -62,6 +62,7 @@ struct AttnArgs {
     const int *kv_lens, *q_start;  // [B] or null
     int dtype, B, Lq, Lk, Hq, Hkv, G, D;
     int64_t rows;               // Lq * G
+    FastDiv by_G;
     int causal, window;         // window 0: none
     float scale;
     bool vec;                   // 16-byte pieces of every row are aligned

@@ -10,20 +10,21 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
 from . import dc1d
-from .dc1d import _check, _contig, _device_ctx, _ref, _Tensor, _workspace
+from .dc1d import _check, _contig, _nullctx, _workspace
 
 DC1D_I32 = 2
 _DTYPES = {torch.float32: dc1d.DC1D_F32, torch.bfloat16: dc1d.DC1D_BF16, torch.int32: DC1D_I32}
 
-
-class _Strided(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
-                ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
-
+# Descriptors are packed bytes in the layout of the C structures (small calls
+# are bound by the host; filling ctypes structures takes several times as
+# long): dc1d_tensor by rank, the unused shape entries zero, and dc1d_strided.
+_TENSOR = [struct.Struct("Pii%dq%dx" % (n, 8 * (4 - n))).pack for n in range(5)]
+_STRIDED = struct.Struct("Pii8q").pack
 
 _declared = None
 
@@ -32,19 +33,17 @@ def _library():
     global _declared
     if _declared is None:
         lib = dc1d.load_library()
-        T, S, p, n = ctypes.POINTER(_Tensor), ctypes.POINTER(_Strided), ctypes.c_void_p, ctypes.c_size_t
-        i32, i64, f64, out = ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)
+        p, n, i32, i64, f64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, ctypes.c_double
         for name, args in {
-                "dc1d_layer_norm": [T] * 6 + [f64, p],
-                "dc1d_layer_norm_backward_workspace_bytes": [T, i32, out],
-                "dc1d_layer_norm_backward": [T] * 8 + [p, n, p],
-                "dc1d_rotary": [S, S, T, T, T, S, S, ctypes.POINTER(i64), ctypes.c_int32, i32, i32, p],
-                "dc1d_attention_workspace_bytes": [S] * 3 + [out],
-                "dc1d_attention_plan": [S] * 3 + [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(i64),
-                                                  ctypes.POINTER(ctypes.c_int32)],
-                "dc1d_attention": [S] * 3 + [T, T, S, T, i32, i64, f64, p, n, p],
-                "dc1d_attention_backward_workspace_bytes": [S] * 3 + [out],
-                "dc1d_attention_backward": [S] * 3 + [T, T, S, T] + [S] * 4 + [i32, i64, f64, p, n, p]}.items():
+                "dc1d_layer_norm": [p] * 6 + [f64, p],
+                "dc1d_layer_norm_backward_workspace_bytes": [p, i32, p],
+                "dc1d_layer_norm_backward": [p] * 8 + [p, n, p],
+                "dc1d_rotary": [p] * 8 + [ctypes.c_int32, i32, i32, p],
+                "dc1d_attention_workspace_bytes": [p] * 3 + [p],
+                "dc1d_attention_plan": [p] * 3 + [p] * 3,
+                "dc1d_attention": [p] * 7 + [i32, i64, f64, p, n, p],
+                "dc1d_attention_backward_workspace_bytes": [p] * 3 + [p],
+                "dc1d_attention_backward": [p] * 11 + [i32, i64, f64, p, n, p]}.items():
             fn = getattr(lib, name)
             fn.restype = ctypes.c_int
             fn.argtypes = args
@@ -56,13 +55,13 @@ def _desc(t, name):
     """A contiguous tensor's descriptor."""
     if t is None:
         return None
-    _contig(t, name)
-    d = _Tensor()
-    d.data = t.data_ptr() or None
-    d.dtype = _DTYPES.get(t.dtype, -1)
-    d.ndim = t.dim()
-    d.shape[:min(d.ndim, 4)] = t.shape[:4]
-    return d
+    if not t.is_contiguous():
+        _contig(t, name)
+    shape = t.shape
+    n = len(shape)
+    if n > 4:  # the rank alone decides: refused
+        return _TENSOR[4](t.data_ptr(), _DTYPES.get(t.dtype, -1), n, *shape[:4])
+    return _TENSOR[n](t.data_ptr(), _DTYPES.get(t.dtype, -1), n, *shape)
 
 
 def _strided(t, name):
@@ -71,21 +70,29 @@ def _strided(t, name):
         return None
     if t.dim() != 4:
         raise ValueError("%s must have four dimensions" % name)
-    d = _Strided()
-    d.data = t.data_ptr() or None
-    d.dtype = _DTYPES.get(t.dtype, -1)
-    d.ndim = 4
-    d.shape[:] = t.shape
-    d.stride[:] = t.stride()
-    return d
+    return _STRIDED(t.data_ptr(), _DTYPES.get(t.dtype, -1), 4, *t.shape, *t.stride())
 
 
-def _one_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must be on one device")
-    if first.device.type != "cuda":
+def _device_of(first, *rest):
+    """The index of the GPU that all the tensors (or Nones) are on."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("tensors must be on the GPU")
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors must be on one device")
+    return index
+
+
+_here = _nullctx()
+
+
+def _on(index):
+    return _here if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _sized(query, *args):
@@ -97,9 +104,9 @@ def _sized(query, *args):
 def _scratch(nbytes, workspace, device):
     """(pointer, bytes) of the caller's workspace or of this stream's cached one."""
     if workspace is None:
+        if nbytes == 0:
+            return None, 0
         workspace = _workspace(nbytes, device)
-    if workspace is None:
-        return None, 0
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -109,18 +116,16 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, with_stats=False, out=None):
     Returns y (allocated unless given as ``out``, which may be x), or with
     with_stats (y, mean, rstd), float32 tensors of x's shape without axis 1."""
     lib = _library()
-    _one_device(x, weight, bias, out)
+    index = _device_of(x, weight, bias, out)
     y = torch.empty_like(x) if out is None else out
     mean = rstd = None
     if with_stats:
-        shape = x.shape[:1] + x.shape[2:]
-        mean = torch.empty(shape, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(shape, dtype=torch.float32, device=x.device)
+        mean = x.new_empty(x.shape[:1] + x.shape[2:], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
     d = (_desc(x, "x"), _desc(weight, "weight"), _desc(bias, "bias"), _desc(y, "out"), _desc(mean, "mean"),
          _desc(rstd, "rstd"))
-    with _device_ctx(x.device):
-        _check(lib.dc1d_layer_norm(*map(_ref, d), eps, torch.cuda.current_stream(x.device).cuda_stream),
-               "dc1d_layer_norm")
+    with _on(index):
+        _check(lib.dc1d_layer_norm(*d, eps, _stream(index)), "dc1d_layer_norm")
     return (y, mean, rstd) if with_stats else y
 
 
@@ -129,16 +134,16 @@ def layer_norm_backward(x, grad_out, mean, rstd, weight=None, need=("x", "weight
     forward's mean and rstd: a dict with the requested keys, each gradient in
     x's dtype."""
     lib = _library()
-    _one_device(x, grad_out, mean, rstd, weight)
-    grads = {k: torch.empty_like(x) if k == "x" else torch.empty(x.shape[1], dtype=x.dtype, device=x.device) for k in need}
+    index = _device_of(x, grad_out, mean, rstd, weight)
+    grads = {k: torch.empty_like(x) if k == "x" else x.new_empty(x.shape[1]) for k in need}
     gx, gw, gb = (grads.get(k) for k in ("x", "weight", "bias"))
     d = (_desc(x, "x"), _desc(weight, "weight"), _desc(grad_out, "grad_out"), _desc(mean, "mean"), _desc(rstd, "rstd"),
          _desc(gx, "grad_x"), _desc(gw, "grad_weight"), _desc(gb, "grad_bias"))
-    with _device_ctx(x.device):
+    with _on(index):
         params = int(gw is not None or gb is not None)
-        nbytes = _sized(lib.dc1d_layer_norm_backward_workspace_bytes, _ref(d[0]), params) if params else 0
-        _check(lib.dc1d_layer_norm_backward(*map(_ref, d), *_scratch(nbytes, workspace, x.device),
-                                            torch.cuda.current_stream(x.device).cuda_stream), "dc1d_layer_norm_backward")
+        nbytes = _sized(lib.dc1d_layer_norm_backward_workspace_bytes, d[0], params) if params else 0
+        _check(lib.dc1d_layer_norm_backward(*d, *_scratch(nbytes, workspace, x.device), _stream(index)),
+               "dc1d_layer_norm_backward")
     return grads
 
 
@@ -154,19 +159,19 @@ def rotary(q, k, cos, sin, positions, sections, interleaved=False, inverse=False
     which may be (q, k)."""
     lib = _library()
     q_out, k_out = out if out is not None else (None, None)
-    _one_device(q, k, cos, sin, positions, q_out, k_out)
+    index = _device_of(q, k, cos, sin, positions, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = q.new_empty(q.shape)
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = k.new_empty(k.shape)
     n = len(sections)
     s = (_strided(q, "q"), _strided(k, "k"), _desc(cos, "cos"), _desc(sin, "sin"), _desc(positions, "positions"),
          _strided(q_out, "out"), _strided(k_out, "out"))
-    with _device_ctx(q.device):
-        _check(lib.dc1d_rotary(*map(_ref, s), (ctypes.c_int64 * max(n, 1))(*sections), n, int(interleaved), int(inverse),
-                               torch.cuda.current_stream(q.device).cuda_stream), "dc1d_rotary")
+    with _on(index):
+        _check(lib.dc1d_rotary(*s, struct.pack("%dq" % n, *sections), n, int(interleaved), int(inverse),
+                               _stream(index)), "dc1d_rotary")
     return q_out, k_out
 
 
@@ -180,19 +185,17 @@ def attention(q, k, v, causal=False, window=0, scale=None, kv_lens=None, q_start
     -inf).  scale defaults to 1 / sqrt(D).  Returns out (allocated unless
     given), or with with_lse (out, lse), lse float32 [B, Hq, Lq]."""
     lib = _library()
-    _one_device(q, k, v, kv_lens, q_start, out)
+    index = _device_of(q, k, v, kv_lens, q_start, out)
     s = (_strided(q, "q"), _strided(k, "k"), _strided(v, "v"))
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
     B, Lq, Hq, D = q.shape
-    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device) if with_lse else None
-    r = tuple(map(_ref, s))
+    lse = q.new_empty((B, Hq, Lq), dtype=torch.float32) if with_lse else None
     more = (_desc(kv_lens, "kv_lens"), _desc(q_start, "q_start"), _strided(out, "out"), _desc(lse, "lse"))
-    with _device_ctx(q.device):
-        nbytes = _sized(lib.dc1d_attention_workspace_bytes, *r)
-        _check(lib.dc1d_attention(*r, *map(_ref, more), int(causal), window, _scale(scale, D),
-                                  *_scratch(nbytes, workspace, q.device),
-                                  torch.cuda.current_stream(q.device).cuda_stream), "dc1d_attention")
+    with _on(index):
+        nbytes = _sized(lib.dc1d_attention_workspace_bytes, *s)
+        _check(lib.dc1d_attention(*s, *more, int(causal), window, _scale(scale, D),
+                                  *_scratch(nbytes, workspace, q.device), _stream(index)), "dc1d_attention")
     return (out, lse) if with_lse else out
 
 
@@ -200,10 +203,11 @@ def attention_plan(q, k, v) -> dict:
     """Which kernel an attention call with these tensors uses, its workgroups
     and into how many parts the keys are split."""
     lib = _library()
+    index = _device_of(q, k, v)
     s = (_strided(q, "q"), _strided(k, "k"), _strided(v, "v"))
     name, grid, splits = ctypes.c_char_p(), ctypes.c_int64(), ctypes.c_int32()
-    with _device_ctx(q.device):
-        _check(lib.dc1d_attention_plan(*map(_ref, s), ctypes.byref(name), ctypes.byref(grid), ctypes.byref(splits)),
+    with _on(index):
+        _check(lib.dc1d_attention_plan(*s, ctypes.byref(name), ctypes.byref(grid), ctypes.byref(splits)),
                "dc1d_attention_plan")
     return {"kernel": name.value.decode(), "grid": grid.value, "splits": splits.value}
 
@@ -217,18 +221,17 @@ def attention_backward(q, k, v, out, lse, grad_out, causal=False, window=0, scal
     lib = _library()
     like = {"q": q, "k": k, "v": v}
     given = grads or {}
-    grads = {n: given[n] if given.get(n) is not None else torch.empty(like[n].shape, dtype=q.dtype, device=q.device)
+    grads = {n: given[n] if given.get(n) is not None else q.new_empty(like[n].shape)
              for n in need}
-    _one_device(q, k, v, out, lse, grad_out, kv_lens, q_start, *grads.values())
+    index = _device_of(q, k, v, out, lse, grad_out, kv_lens, q_start, *grads.values())
     s = (_strided(q, "q"), _strided(k, "k"), _strided(v, "v"))
-    r = tuple(map(_ref, s))
     more = (_desc(kv_lens, "kv_lens"), _desc(q_start, "q_start"), _strided(out, "out"), _desc(lse, "lse"),
             _strided(grad_out, "grad_out"), *(_strided(grads.get(n), "grads") for n in ("q", "k", "v")))
-    with _device_ctx(q.device):
-        nbytes = _sized(lib.dc1d_attention_backward_workspace_bytes, *r)
-        _check(lib.dc1d_attention_backward(*r, *map(_ref, more), int(causal), window, _scale(scale, q.shape[3]),
-                                           *_scratch(nbytes, workspace, q.device),
-                                           torch.cuda.current_stream(q.device).cuda_stream), "dc1d_attention_backward")
+    with _on(index):
+        nbytes = _sized(lib.dc1d_attention_backward_workspace_bytes, *s)
+        _check(lib.dc1d_attention_backward(*s, *more, int(causal), window, _scale(scale, q.shape[3]),
+                                           *_scratch(nbytes, workspace, q.device), _stream(index)),
+               "dc1d_attention_backward")
     return grads
 
 

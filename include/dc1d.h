@@ -524,7 +524,8 @@ int dc1d_layer_norm_backward(const dc1d_tensor *x, const dc1d_tensor *weight_or_
  * Positions outside [0, P) are taken as the nearest end of the tables.  An
  * output may be its own input (in place); otherwise it must not overlap any
  * input or the other output, except that two tensors may be disjoint head
- * slices of one buffer.  Limits: B * L < 2^31, B * L * (Hq + Hkv) * D < 2^40.
+ * slices of one buffer.  Limits: B * L < 2^31, (Hq + Hkv) * D < 2^30,
+ * B * L * (Hq + Hkv) * D < 2^40.
  */
 int dc1d_rotary(const dc1d_strided *q, const dc1d_strided *k_or_null, const dc1d_tensor *cos, const dc1d_tensor *sin,
                 const dc1d_tensor *positions, const dc1d_strided *q_out, const dc1d_strided *k_out_or_null,

@@ -14,6 +14,11 @@ F32, BF16, I32 = 0, 1, 2
 BIG = 1 << 62
 
 
+class Strided(ctypes.Structure):  # dc1d_strided
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
+                ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     return sequence._library()
@@ -28,7 +33,7 @@ def T(shape, slot, dtype=F32, addr=None):
 
 
 def S(shape, slot, dtype=F32, stride=None, addr=None):
-    d = sequence._Strided()
+    d = Strided()
     d.data = BASE + slot * STEP if addr is None else (addr or None)
     d.dtype, d.ndim = dtype, 4
     if stride is None:
