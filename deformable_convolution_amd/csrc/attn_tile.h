@@ -33,9 +33,24 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kMaxLen = 1 << 29;  // limit of every length, and of window and |q_start|
 
-// PADR: elements added to a tile row that is read along the row in 16-byte
-// pieces (rows then start 16 bytes apart modulo the banks); PADC: to one that
-// is read down the columns (four rows of 32 bytes at a time).
+// ---- tiles in LDS -------------------------------------------------------------
+//
+// A tile is rows of DP elements, row after row, in 16-byte pieces whose index
+// is exchanged with the row's: piece c of row r stands at (r * PER + c) ^
+// mix(r), PER = DP elements in pieces.  LDS has 64 banks of 4 bytes; without
+// the exchange rows of 256 bytes all start in the same bank (a row read by
+// 32 lanes then took 64 clocks for its 1 KiB, measured on a wave's reads),
+// with it both ways of reading a tile run at the LDS's rate: along the rows
+// 4.2 clocks for 1 KiB, down the columns 2.5 for 512 bytes.  Padding the rows
+// by 16 or 32 bytes instead served one way at full rate and the other at half.
+template <int PER>
+__host__ __device__ constexpr int mix(int row) {
+    static_assert(PER == 4 || PER == 8 || PER == 16 || PER == 32, "64 to 512 bytes a row");
+    if constexpr (PER == 4) return (row >> 2) & 3;
+    if constexpr (PER == 8) return ((row & 2) << 1) | ((row >> 2) & 3);
+    return ((row & 3) << 2) | ((row >> 2) & 3);
+}
+
 template <typename T>
 struct Tile;
 
@@ -43,23 +58,27 @@ template <>
 struct Tile<BF16> {
     using E = uint16_t;
     using Frag = bf16x8;
-    static constexpr int CH = 8, PADR = 8, PADC = 16;
+    static constexpr int CH = 8;
 
     static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
-    // eight consecutive elements of a row
-    static __device__ __forceinline__ Frag row_frag(const E *p) { return *(const Frag *)p; }
+    // Elements c0 .. c0+7 of a tile's row (c0 a multiple of 8)
+    template <int DP>
+    static __device__ __forceinline__ Frag row_frag(const E *tile, int row, int c0) {
+        return *(const Frag *)(tile + (((row * (DP / CH) + c0 / CH) ^ mix<DP / CH>(row)) * CH));
+    }
     // Eight elements of column c0 + lane%32, rows k0 + 8*(j/4) + 4*(lane/32) +
     // j%4 (k0: a multiple of 16): each transposing read takes a 4 x 16 block
     // whose lane 4*i + c addresses elements 4c .. 4c+3 of row i, and gives
     // lane i of the 16 the block's column i.
-    static __device__ __forceinline__ Frag col_frag(const E *tile, int pitch, int k0, int c0, int lane) {
+    template <int DP>
+    static __device__ __forceinline__ Frag col_frag(const E *tile, int k0, int c0, int lane) {
         typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-        const int i = lane & 15;
-        const E *p = tile + (k0 + 4 * (lane >> 5) + (i >> 2)) * pitch + c0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
-        const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p);
-        const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + 8 * pitch));
+        const int i = lane & 15, row = k0 + 4 * (lane >> 5) + (i >> 2), c = c0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
+        auto at = [&](int r) { return tile + (((r * (DP / CH) + c / CH) ^ mix<DP / CH>(r)) * CH + c % CH); };
+        const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)at(row));
+        const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)at(row + 8));
         typedef short i16x8 __attribute__((ext_vector_type(8)));
         return __builtin_bit_cast(Frag, (i16x8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
@@ -73,36 +92,34 @@ struct Tile<BF16> {
     static __device__ __forceinline__ void store4(E *p, f32x4 v) {
         *(bf16x4 *)p = __builtin_convertvector(v, bf16x4);
     }
-    static __device__ __forceinline__ void widen8(const E *p, float *f) {
-        const u32x4 u = *(const u32x4 *)p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    }
 };
 
 template <>
 struct Tile<F32> {
     using E = float;
     using Frag = f32x8;
-    static constexpr int CH = 4, PADR = 4, PADC = 4;
+    static constexpr int CH = 4;
 
     static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ Frag row_frag(const E *p) {
-        const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+    template <int DP>
+    static __device__ __forceinline__ Frag row_frag(const E *tile, int row, int c0) {
+        auto at = [&](int c) { return *(const f32x4 *)(tile + (((row * (DP / CH) + c / CH) ^ mix<DP / CH>(row)) * CH)); };
+        const f32x4 a = at(c0), b = at(c0 + 4);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    static __device__ __forceinline__ Frag col_frag(const E *tile, int pitch, int k0, int c0, int lane) {
-        const E *p = tile + (k0 + 4 * (lane >> 5)) * pitch + c0 + (lane & 31);
+    template <int DP>
+    static __device__ __forceinline__ Frag col_frag(const E *tile, int k0, int c0, int lane) {
+        const int c = c0 + (lane & 31);
         Frag f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = p[(8 * (j >> 2) + (j & 3)) * pitch];
+        for (int j = 0; j < 8; ++j) {
+            const int row = k0 + 4 * (lane >> 5) + 8 * (j >> 2) + (j & 3);
+            f[j] = tile[((row * (DP / CH) + c / CH) ^ mix<DP / CH>(row)) * CH + c % CH];
+        }
         return f;
     }
     template <int S>
@@ -111,11 +128,6 @@ struct Tile<F32> {
                                        8 * S + 7);
     }
     static __device__ __forceinline__ void store4(E *p, f32x4 v) { *(f32x4 *)p = v; }
-    static __device__ __forceinline__ void widen8(const E *p, float *f) {
-        const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
-    }
 };
 
 // One 16-byte piece of a row of D elements, from element col on; elements at
@@ -146,91 +158,115 @@ __device__ __forceinline__ RowAt row_at(const AttnArgs &a, int64_t n) {
     return {(int)pos, (int)((uint32_t)n - pos * (uint32_t)a.G)};
 }
 
-// A tile of ROWS rows of DP elements carried by NT threads, from global
-// memory through registers into LDS.  Rows at and past `limit` and elements
-// at and past D become zero, whatever memory holds there.
+// A tile of ROWS rows of DP elements brought into LDS by NT threads (whole
+// waves).  Rows at and past `limit` and elements at and past D become zero,
+// whatever memory holds there.
 //
-// Whole tiles of aligned rows are read at the tile's base, which the whole
-// workgroup shares, plus 32-bit offsets that each thread forms once (`near`:
-// they fit); other tiles form their addresses as they go.
+// Aligned rows (VEC) go from memory to LDS without passing through registers:
+// a load of the wave writes 64 consecutive pieces of LDS, each lane's from an
+// address of its own, and a lane whose offset lies outside the buffer's range
+// writes zeros.  Such loads are in flight until landed().  Rows that are not
+// aligned, or so far apart that a tile passes 32-bit offsets (not `near`),
+// are read element by element (or piece by piece) and stored at once.
+//
+// A thread's i-th piece stands at place t + i NT, i.e. row t / PER + i STEP,
+// and mix() is linear in the row's bits: its column is the first piece's with
+// a constant exchanged in.
 template <typename T, int ROWS, int DP, int NT, bool VEC>
 struct Stage {
     using E = typename T::T;
     static constexpr int CH = Tile<T>::CH, PER = DP / CH, N = (ROWS * PER + NT - 1) / NT;
-    static_assert(ROWS * PER % NT == 0 || ROWS * PER < NT, "the tile divides among the threads, or needs only some");
-    static constexpr int64_t kNear = 1 << 23;  // elements between rows: 64 rows of 4 bytes stay below 2^31
-    u32x4 r[N];
-    uint32_t off[N];
+    static constexpr int STEP = NT / PER;
+    static constexpr bool PART = ROWS * PER < NT;  // fewer pieces than threads
+    static_assert(NT % PER == 0, "a thread's pieces are of one column, but for the exchange");
+    static_assert(PART ? ROWS * PER % 64 == 0 : ROWS * PER % NT == 0, "whole waves carry the tile");
+    static constexpr int64_t kNear = 1 << 22;       // elements between rows: 64 rows of 4 bytes stay below 2^30
+    static constexpr uint32_t kRange = 0x7fffffff, kOut = 0x80000000u;
+    uint32_t row, col, rows_at;  // the first piece's row and first element; the row's offset in bytes
     bool near;
 
     // rows `stride` elements apart
-    __device__ __forceinline__ void init(int64_t stride, int D, int t) {
+    __device__ __forceinline__ void init(int64_t stride, int t) {
+        row = t / PER;
+        col = ((t % PER) ^ mix<PER>(row)) * CH;
         near = VEC && stride < kNear;
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = t + i * NT, row = min(c / PER, ROWS - 1), col = c % PER * CH;
-                off[i] = (uint32_t)(row * (uint32_t)stride + (col < D ? col : 0)) * sizeof(E);
-            }
-        }
+        rows_at = row * (uint32_t)stride * (uint32_t)sizeof(E);
     }
-    // rows of a key head's queries: whole tiles start at the same head where
-    // G divides their rows
-    __device__ __forceinline__ void init_rows(const AttnArgs &a, const Strides3 &s, int t) {
-        near = VEC && ROWS % a.G == 0 && s.l < kNear && s.h < kNear;
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = t + i * NT, col = c % PER * CH;
-                const RowAt at = row_at(a, min(c / PER, ROWS - 1));
-                off[i] = ((uint32_t)at.pos * (uint32_t)s.l + (uint32_t)at.head * (uint32_t)s.h + (col < a.D ? col : 0)) * (uint32_t)sizeof(E);
-            }
-        }
+    // rows of a key head's queries: all of a thread's pieces are of one head
+    // where G divides the rows between them
+    __device__ __forceinline__ void init_rows(const AttnArgs &a, const Strides3 &st, int t) {
+        row = t / PER;
+        col = ((t % PER) ^ mix<PER>(row)) * CH;
+        near = VEC && ROWS % a.G == 0 && (N == 1 || STEP % a.G == 0) && st.l < kNear && st.h < kNear;
+        const RowAt at = row_at(a, row);
+        rows_at = ((uint32_t)at.pos * (uint32_t)st.l + (uint32_t)at.head * (uint32_t)st.h) * (uint32_t)sizeof(E);
     }
-    // base: the tile's row 0 (limit >= 1 rows of it may be read)
-    __device__ __forceinline__ void load(const E *base, int64_t stride, int limit, int D, int t) {
-        if (near && limit >= ROWS) {
+    static constexpr int col_flip(int i) { return mix<PER>(i * STEP) * CH; }
+
+    // base and lds are the same for the whole wave
+    static __device__ __forceinline__ void to_lds(const E *base, uint32_t off, E *lds) {
+        const uint64_t p = (uint64_t)base;
+        const uint64_t u = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p) |
+                           (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32)) << 32;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)u, 0, kRange, 0x00027000);
+        typedef __attribute__((address_space(3))) void lds_void;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, off, 0, 0, 0);
+    }
+    // pieces whose rows are `step` elements apart from base on
+    __device__ __forceinline__ void fetch(E *lds, const E *base, int64_t step, int limit, int D, int t) const {
+        E *const to = lds + __builtin_amdgcn_readfirstlane(t >> 6) * 64 * CH;
+        if (limit >= ROWS && D == DP) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) r[i] = *(const u32x4 *)((const char *)base + off[i]);
+            for (int i = 0; i < N; ++i)
+                to_lds(base + i * step, rows_at + (col ^ col_flip(i)) * (uint32_t)sizeof(E), to + i * NT * CH);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = t + i * NT, row = c / PER, col = c % PER * CH;
-                r[i] = load_piece<T, VEC>(base + (int64_t)min(row, limit - 1) * stride, col, D);
+                const int c = col ^ col_flip(i);
+                const bool in = (int)row + i * STEP < limit && c < D;
+                to_lds(base + i * step, in ? rows_at + c * (uint32_t)sizeof(E) : kOut, to + i * NT * CH);
             }
         }
     }
-    // base: the key head's first query head, position 0; row0: a multiple of ROWS
-    __device__ __forceinline__ void load_rows(const E *base, const AttnArgs &a, const Strides3 &s, int64_t row0, int t) {
-        if (near && row0 + ROWS <= a.rows) {
-            const char *const p = (const char *)(base + (int64_t)fdiv((uint32_t)row0, a.by_G) * s.l);
-#pragma unroll
-            for (int i = 0; i < N; ++i) r[i] = *(const u32x4 *)(p + off[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = t + i * NT, col = c % PER * CH;
-                const RowAt at = row_at(a, row0 + c / PER < a.rows ? row0 + c / PER : a.rows - 1);
-                r[i] = load_piece<T, VEC>(base + at.pos * s.l + at.head * s.h, col, a.D);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(E *lds, int pitch, int limit, int D, int t) {
-        if (limit < ROWS || D < DP) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = t + i * NT, row = c / PER, col = c % PER * CH;
-                if (row >= limit || col >= D) r[i] = u32x4{0, 0, 0, 0};
-            }
-        }
-#pragma unroll
+
+    // base: the tile's row 0, `limit` (at least 1) rows may be read
+    __device__ __forceinline__ void load(E *lds, const E *base, int64_t stride, int limit, int D, int t) const {
+        if (PART && t >= ROWS * PER) return;  // whole waves
+        if (VEC && near) return fetch(lds, base, STEP * stride, limit, D, t);
+#pragma unroll 1
         for (int i = 0; i < N; ++i) {
-            const int c = t + i * NT;
-            if (ROWS * PER < NT && c >= ROWS * PER) continue;
-            *(u32x4 *)(lds + c / PER * pitch + c % PER * CH) = r[i];
+            const int r = row + i * STEP, c = col ^ (mix<PER>(i * STEP) * CH);
+            u32x4 v = load_piece<T, VEC>(base + (int64_t)min(r, limit - 1) * stride, c, D);
+            if (r >= limit || (VEC && c >= D)) v = u32x4{0, 0, 0, 0};
+            *(u32x4 *)(lds + (t + i * NT) * CH) = v;
+        }
+    }
+    // The rows from row0 (a multiple of ROWS) on of a key head's queries; base: its
+    // first query head, position 0
+    __device__ __forceinline__ void load_rows(E *lds, const E *base, const AttnArgs &a, const Strides3 &st, int64_t row0,
+                                              int limit, int t) const {
+        if (PART && t >= ROWS * PER) return;
+        if (VEC && near)
+            return fetch(lds, base + (int64_t)fdiv((uint32_t)row0, a.by_G) * st.l, (int64_t)fdiv(STEP, a.by_G) * st.l, limit,
+                         a.D, t);
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+            const int r = row + i * STEP, c = col ^ (mix<PER>(i * STEP) * CH);
+            const RowAt at = row_at(a, row0 + min(r, limit - 1));
+            u32x4 v = load_piece<T, VEC>(base + at.pos * st.l + at.head * st.h, c, a.D);
+            if (r >= limit || (VEC && c >= a.D)) v = u32x4{0, 0, 0, 0};
+            *(u32x4 *)(lds + (t + i * NT) * CH) = v;
         }
     }
 };
+
+// Waits until all but the latest N of the wave's loads into LDS have landed.
+template <int N>
+__device__ __forceinline__ void landed() {
+    static_assert(N < 64, "the counter's range");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
+    asm volatile("" ::: "memory");
+}
 
 // The keys [lo, hi) that position i of batch b sees: always an interval.
 // hi <= lo: none.

@@ -32,7 +32,7 @@ template <typename T, int DP, int NT>
 __device__ __forceinline__ void attend(const typename T::T *kt, const typename T::T *vt, const typename Tile<T>::Frag *q,
                                        f32x16 *o, Softmax &sm, float c, bool masked, int k0, KeyRange kr, int lane) {
     using M = Tile<T>;
-    constexpr int PK = DP + M::PADR, PV = DP + M::PADC, NS = DP / 16, ND = DP / 32;
+    constexpr int NS = DP / 16, ND = DP / 32;
     const int half = lane >> 5;
     f32x16 s[NT];
 #pragma unroll
@@ -40,7 +40,7 @@ __device__ __forceinline__ void attend(const typename T::T *kt, const typename T
         s[t] = f32x16{};
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-            s[t] = M::mma(M::row_frag(kt + (t * 32 + (lane & 31)) * PK + i * 16 + half * 8), q[i], s[t]);
+            s[t] = M::mma(M::template row_frag<DP>(kt, t * 32 + (lane & 31), i * 16 + half * 8), q[i], s[t]);
     }
     if (masked) {
 #pragma unroll
@@ -83,8 +83,8 @@ __device__ __forceinline__ void attend(const typename T::T *kt, const typename T
         const typename M::Frag p0 = M::template pack<0>(s[t]), p1 = M::template pack<1>(s[t]);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            o[d] = M::mma(M::col_frag(vt, PV, t * 32, d * 32, lane), p0, o[d]);
-            o[d] = M::mma(M::col_frag(vt, PV, t * 32 + 16, d * 32, lane), p1, o[d]);
+            o[d] = M::mma(M::template col_frag<DP>(vt, t * 32, d * 32, lane), p0, o[d]);
+            o[d] = M::mma(M::template col_frag<DP>(vt, t * 32 + 16, d * 32, lane), p1, o[d]);
         }
     }
 }
@@ -127,12 +127,12 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, typename Tile<T>::Frag
 // ---- rows split among the waves ---------------------------------------------
 //
 // 128 rows a workgroup, 32 a wave; tiles of KT keys, double-buffered, the
-// next one on its way in registers while this one is used.
+// next one on its way while this one is used.
 template <typename T, int DP>
 struct RowsShape {
     static constexpr int KT = sizeof(typename T::T) == 2 ? 64 : 32;
-    static constexpr int PK = DP + Tile<T>::PADR, PV = DP + Tile<T>::PADC;
-    static constexpr size_t lds = (size_t)2 * KT * (PK + PV) * sizeof(typename T::T);
+    static constexpr int tile = KT * DP;
+    static constexpr size_t lds = (size_t)4 * tile * sizeof(typename T::T);
 };
 
 template <typename T, int DP, bool VEC>
@@ -140,8 +140,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
     using E = typename T::T;
     using S = RowsShape<T, DP>;
     constexpr int KT = S::KT, ND = DP / 32;
-    extern __shared__ __align__(16) char smem[];
-    E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * KT * S::PK;
+    extern __shared__ __align__(512) char smem[];
+    E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * S::tile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
 
     const int64_t tiles = (a.rows + 127) / 128;
@@ -170,29 +170,22 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 256, VEC> ks, vs;
-    ks.init(a.ks.l, a.D, t);
-    vs.init(a.vs.l, a.D, t);
+    ks.init(a.ks.l, t);
+    vs.init(a.vs.l, t);
+    ks.near = vs.near = ks.near && vs.near;
+    auto load = [&](int at, int k0) {
+        ks.load(kbuf + at * S::tile, kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
+        vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
+    };
     int k0 = lo / KT * KT;
-    if (k0 < hi) {
-        ks.load(kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
-        vs.load(vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
-        ks.store(kbuf, S::PK, hi - k0, a.D, t);
-        vs.store(vbuf, S::PV, hi - k0, a.D, t);
-    }
+    if (k0 < hi) load(0, k0);
     for (int at = 0; k0 < hi; k0 += KT, at ^= 1) {
+        landed<0>();
         __syncthreads();
-        const int next = k0 + KT;
-        if (next < hi) {
-            ks.load(kp + next * a.ks.l, a.ks.l, hi - next, a.D, t);
-            vs.load(vp + next * a.vs.l, a.vs.l, hi - next, a.D, t);
-        }
+        if (k0 + KT < hi) load(at ^ 1, k0 + KT);
         if (k0 < final.hi && k0 + KT > first.lo)
-            attend<T, DP, KT / 32>(kbuf + at * KT * S::PK, vbuf + at * KT * S::PV, q, o, sm, c,
+            attend<T, DP, KT / 32>(kbuf + at * S::tile, vbuf + at * S::tile, q, o, sm, c,
                                    final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
-        if (next < hi) {
-            ks.store(kbuf + (at ^ 1) * KT * S::PK, S::PK, hi - next, a.D, t);
-            vs.store(vbuf + (at ^ 1) * KT * S::PV, S::PV, hi - next, a.D, t);
-        }
     }
 
     const float l = half_sum(sm.l);
@@ -217,8 +210,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
 template <typename T, int DP>
 struct KeysShape {
     static constexpr int KT = 32;
-    static constexpr int PK = DP + Tile<T>::PADR, PV = DP + Tile<T>::PADC, PO = DP + 4;
-    static constexpr size_t wave_lds = (size_t)KT * (PK + PV) * sizeof(typename T::T);
+    static constexpr int tile = KT * DP, PO = DP + 4;
+    // a wave's tiles twice, where the LDS holds that for four waves
+    static constexpr int NB = (size_t)16 * tile * sizeof(typename T::T) <= 128 << 10 ? 2 : 1;
+    static constexpr size_t wave_lds = (size_t)2 * NB * tile * sizeof(typename T::T);
     static constexpr size_t join_lds = (size_t)4 * 32 * (PO + 2) * sizeof(float);
     static constexpr size_t lds = 4 * wave_lds > join_lds ? 4 * wave_lds : join_lds;
 };
@@ -228,9 +223,9 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     using E = typename T::T;
     using S = KeysShape<T, DP>;
     constexpr int KT = S::KT, ND = DP / 32;
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(512) char smem[];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
-    E *const kbuf = (E *)(smem + wave * S::wave_lds), *const vbuf = kbuf + KT * S::PK;
+    E *const kbuf = (E *)(smem + wave * S::wave_lds), *const vbuf = kbuf + S::NB * S::tile;
 
     const int64_t tiles = (a.rows + 31) / 32;
     int64_t id = xcd_order(blockIdx.x, gridDim.x);
@@ -261,24 +256,29 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 64, VEC> ks, vs;
-    ks.init(a.ks.l, a.D, lane);
-    vs.init(a.vs.l, a.D, lane);
+    ks.init(a.ks.l, lane);
+    vs.init(a.vs.l, lane);
+    ks.near = vs.near = ks.near && vs.near;
+    auto load = [&](int at, int n) {
+        ks.load(kbuf + at * S::tile, kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane);
+        vs.load(vbuf + at * S::tile, vp + (int64_t)n * KT * a.vs.l, a.vs.l, final.hi - n * KT, a.D, lane);
+    };
     int n = s0 + wave;
-    if (n < s1) {
-        ks.load(kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane);
-        vs.load(vp + (int64_t)n * KT * a.vs.l, a.vs.l, final.hi - n * KT, a.D, lane);
-    }
-    for (; n < s1; n += 4) {
-        const int k0 = n * KT, next = n + 4;
-        ks.store(kbuf, S::PK, final.hi - k0, a.D, lane);
-        vs.store(vbuf, S::PV, final.hi - k0, a.D, lane);
-        if (next < s1) {
-            ks.load(kp + (int64_t)next * KT * a.ks.l, a.ks.l, final.hi - next * KT, a.D, lane);
-            vs.load(vp + (int64_t)next * KT * a.vs.l, a.vs.l, final.hi - next * KT, a.D, lane);
+    if (n < s1) load(0, n);
+    for (int at = 0; n < s1; n += 4, at ^= S::NB - 1) {
+        const int k0 = n * KT;
+        // the next tile takes the other buffer's place, whose reads are done
+        if (S::NB > 1 && n + 4 < s1) {
+            load(at ^ 1, n + 4);
+            landed<2 * decltype(ks)::N>();
+        } else {
+            landed<0>();
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        attend<T, DP, 1>(kbuf, vbuf, q, o, sm, c, final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+        attend<T, DP, 1>(kbuf + at * S::tile, vbuf + at * S::tile, q, o, sm, c, final.lo > k0 || first.hi < k0 + KT, k0, kr,
+                         lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (S::NB == 1 && n + 4 < s1) load(0, n + 4);
     }
 
     // join the four waves: each leaves o, m, l; thread (row, slice) adds them in wave order

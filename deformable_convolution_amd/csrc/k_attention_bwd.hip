@@ -114,10 +114,9 @@ __device__ __forceinline__ void load_frags(typename Tile<T>::Frag *f, const type
 template <typename T, int DP>
 struct KvShape {
     static constexpr int RT = 32;
-    static constexpr int P = DP + Tile<T>::PADC;
-    static constexpr size_t tile = (size_t)RT * P;
+    static constexpr size_t tile = (size_t)RT * DP;
     static constexpr bool v_lds = sizeof(typename T::T) * DP >= 256;
-    static constexpr int PV = DP + Tile<T>::PADR;
+    static constexpr int PV = DP + Tile<T>::CH;  // rows 16 bytes apart modulo the banks
     static constexpr size_t loop_lds = 2 * (2 * tile * sizeof(typename T::T) + 4 * RT * sizeof(float)) +
                                        (v_lds ? (size_t)128 * PV * sizeof(typename T::T) : 0);
     static constexpr size_t drain_lds = (size_t)4 * 32 * (DP + 4) * sizeof(float);
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
     using M = Tile<T>;
     using S = KvShape<T, DP>;
     constexpr int RT = S::RT, NS = DP / 16, ND = DP / 32;
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(512) char smem[];
     E *const qbuf = (E *)smem, *const gbuf = qbuf + 2 * S::tile;
     float *const lbuf = (float *)(gbuf + 2 * S::tile), *const dbuf = lbuf + 2 * RT;
     int *const from = (int *)(dbuf + 2 * RT), *const upto = from + 2 * RT;  // the keys that each row sees
@@ -187,19 +186,18 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
     qs.init_rows(a, a.qs, t);
     gs.init_rows(a, a.gs, t);
     float lse = 0.0f, del = 0.0f;
-    auto load = [&](int64_t r) {
-        qs.load_rows(qp, a, a.qs, r, t);
-        gs.load_rows(gp, a, a.gs, r, t);
+    auto load = [&](int64_t r, int at) {
         if (t < RT) {
             const int64_t n = min(r + t, a.rows - 1);
             lse = lp[(int64_t)row_at(a, n).head * a.Lq + row_at(a, n).pos];
             del = dp[n];
         }
+        const int limit = (int)min(r1 - r, (int64_t)RT);
+        qs.load_rows(qbuf + at * S::tile, qp, a, a.qs, r, limit, t);
+        gs.load_rows(gbuf + at * S::tile, gp, a, a.gs, r, limit, t);
     };
     auto store = [&](int64_t r, int at) {
         const int limit = (int)min(r1 - r, (int64_t)RT);
-        qs.store(qbuf + at * S::tile, S::P, limit, a.D, t);
-        gs.store(gbuf + at * S::tile, S::P, limit, a.D, t);
         if (t < RT) {
             // rows that saw nothing, or are not there, get probability 0
             lbuf[at * RT + t] = t < limit && lse != -INFINITY ? lse * kLog2e : INFINITY;
@@ -210,23 +208,24 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
         }
     };
     if (r0 < r1) {
-        load(r0);
+        load(r0, 0);
         store(r0, 0);
     }
     int at = 0;
     for (int64_t r = r0; r < r1; r += RT, at ^= 1) {
+        landed<0>();
         __syncthreads();
-        if (r + RT < r1) load(r + RT);
+        if (r + RT < r1) load(r + RT, at ^ 1);
         const E *const qt = qbuf + at * S::tile, *const gt = gbuf + at * S::tile;
         const float *const lt = lbuf + at * RT, *const dt = dbuf + at * RT;
         f32x16 s = {}, p = {};
 #pragma unroll
-        for (int i = 0; i < NS; ++i) s = M::mma(M::row_frag(qt + (lane & 31) * S::P + i * 16 + half * 8), kf[i], s);
+        for (int i = 0; i < NS; ++i) s = M::mma(M::template row_frag<DP>(qt, lane & 31, i * 16 + half * 8), kf[i], s);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const typename M::Frag gr = M::row_frag(gt + (lane & 31) * S::P + i * 16 + half * 8);
+            const typename M::Frag gr = M::template row_frag<DP>(gt, lane & 31, i * 16 + half * 8);
             if constexpr (S::v_lds)
-                p = M::mma(gr, M::row_frag(vrow + i * 16), p);
+                p = M::mma(gr, *(const typename M::Frag *)(vrow + i * 16), p);
             else
                 p = M::mma(gr, vf[i], p);
         }
@@ -261,13 +260,13 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
         const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            dv[d] = M::mma(M::col_frag(gt, S::P, 0, d * 32, lane), p0, dv[d]);
-            dv[d] = M::mma(M::col_frag(gt, S::P, 16, d * 32, lane), p1, dv[d]);
+            dv[d] = M::mma(M::template col_frag<DP>(gt, 0, d * 32, lane), p0, dv[d]);
+            dv[d] = M::mma(M::template col_frag<DP>(gt, 16, d * 32, lane), p1, dv[d]);
         }
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            dk[d] = M::mma(M::col_frag(qt, S::P, 0, d * 32, lane), s0, dk[d]);
-            dk[d] = M::mma(M::col_frag(qt, S::P, 16, d * 32, lane), s1, dk[d]);
+            dk[d] = M::mma(M::template col_frag<DP>(qt, 0, d * 32, lane), s0, dk[d]);
+            dk[d] = M::mma(M::template col_frag<DP>(qt, 16, d * 32, lane), s1, dk[d]);
         }
         if (r + RT < r1) store(r + RT, at ^ 1);
     }
@@ -323,8 +322,7 @@ __global__ __launch_bounds__(256) void k_attn_bwd_sum(AttnArgs a) {
 template <typename T, int DP>
 struct QShape {
     static constexpr int KT = 32;
-    static constexpr int P = DP + Tile<T>::PADC;
-    static constexpr size_t tile = (size_t)KT * P;
+    static constexpr size_t tile = (size_t)KT * DP;
     static constexpr size_t loop_lds = 4 * tile * sizeof(typename T::T);
     static constexpr size_t drain_lds = (size_t)4 * 32 * (DP + 4) * sizeof(float);
     static constexpr size_t lds = loop_lds > drain_lds ? loop_lds : drain_lds;
@@ -337,7 +335,7 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
     using M = Tile<T>;
     using S = QShape<T, DP>;
     constexpr int KT = S::KT, NS = DP / 16, ND = DP / 32;
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(512) char smem[];
     E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * S::tile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
 
@@ -369,29 +367,26 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 256, VEC> ks, vs;
-    ks.init(a.ks.l, a.D, t);
-    vs.init(a.vs.l, a.D, t);
+    ks.init(a.ks.l, t);
+    vs.init(a.vs.l, t);
+    ks.near = vs.near = ks.near && vs.near;
+    auto load = [&](int at, int k0) {
+        ks.load(kbuf + at * S::tile, kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
+        vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
+    };
     int k0 = lo / KT * KT;
-    if (k0 < hi) {
-        ks.load(kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
-        vs.load(vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
-        ks.store(kbuf, S::P, hi - k0, a.D, t);
-        vs.store(vbuf, S::P, hi - k0, a.D, t);
-    }
+    if (k0 < hi) load(0, k0);
     for (int at = 0; k0 < hi; k0 += KT, at ^= 1) {
+        landed<0>();
         __syncthreads();
-        const int next = k0 + KT;
-        if (next < hi) {
-            ks.load(kp + next * a.ks.l, a.ks.l, hi - next, a.D, t);
-            vs.load(vp + next * a.vs.l, a.vs.l, hi - next, a.D, t);
-        }
+        if (k0 + KT < hi) load(at ^ 1, k0 + KT);
         if (k0 < final.hi && k0 + KT > first.lo) {
             const E *const kt = kbuf + at * S::tile, *const vt = vbuf + at * S::tile;
             f32x16 s = {}, p = {};
 #pragma unroll
-            for (int i = 0; i < NS; ++i) s = M::mma(M::row_frag(kt + (lane & 31) * S::P + i * 16 + half * 8), qf[i], s);
+            for (int i = 0; i < NS; ++i) s = M::mma(M::template row_frag<DP>(kt, lane & 31, i * 16 + half * 8), qf[i], s);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) p = M::mma(M::row_frag(vt + (lane & 31) * S::P + i * 16 + half * 8), gf[i], p);
+            for (int i = 0; i < NS; ++i) p = M::mma(M::template row_frag<DP>(vt, lane & 31, i * 16 + half * 8), gf[i], p);
             const bool masked = final.lo > k0 || first.hi < k0 + KT;
 #pragma unroll
             for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lse)) * (p[r] - delta);
@@ -405,13 +400,9 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
             const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                dq[d] = M::mma(M::col_frag(kt, S::P, 0, d * 32, lane), s0, dq[d]);
-                dq[d] = M::mma(M::col_frag(kt, S::P, 16, d * 32, lane), s1, dq[d]);
+                dq[d] = M::mma(M::template col_frag<DP>(kt, 0, d * 32, lane), s0, dq[d]);
+                dq[d] = M::mma(M::template col_frag<DP>(kt, 16, d * 32, lane), s1, dq[d]);
             }
-        }
-        if (next < hi) {
-            ks.store(kbuf + (at ^ 1) * S::tile, S::P, hi - next, a.D, t);
-            vs.store(vbuf + (at ^ 1) * S::tile, S::P, hi - next, a.D, t);
         }
     }
     __syncthreads();
