@@ -268,6 +268,37 @@ __device__ __forceinline__ void landed() {
     asm volatile("" ::: "memory");
 }
 
+// Between the reads of the next product's operands and this product: the
+// scheduler otherwise puts each read of LDS right before its use, and its
+// latency is waited out every time.  (fp32's matrix instructions are long
+// enough to cover it, and its operands too many to hold twice.)
+template <typename T>
+__device__ __forceinline__ void reads_first() {
+    if constexpr (sizeof(typename T::T) == 2) __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc[d] += A_d P for the 32-column slices d of a tile, A_d its rows k0 ..
+// k0+31 read down the columns, P the two operands p0, p1.
+template <typename T, int DP>
+__device__ __forceinline__ void add_columns(f32x16 *acc, const typename T::T *tile, int k0, typename Tile<T>::Frag p0,
+                                            typename Tile<T>::Frag p1, int lane) {
+    using M = Tile<T>;
+    constexpr int ND = DP / 32;
+    typename M::Frag a0 = M::template col_frag<DP>(tile, k0, 0, lane), a1 = M::template col_frag<DP>(tile, k0 + 16, 0, lane);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        typename M::Frag n0 = a0, n1 = a1;
+        if (d + 1 < ND) {
+            n0 = M::template col_frag<DP>(tile, k0, (d + 1) * 32, lane);
+            n1 = M::template col_frag<DP>(tile, k0 + 16, (d + 1) * 32, lane);
+        }
+        reads_first<T>();
+        acc[d] = M::mma(a0, p0, acc[d]);
+        acc[d] = M::mma(a1, p1, acc[d]);
+        a0 = n0, a1 = n1;
+    }
+}
+
 // The keys [lo, hi) that position i of batch b sees: always an interval.
 // hi <= lo: none.
 struct KeyRange {

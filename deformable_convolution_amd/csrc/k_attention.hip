@@ -35,12 +35,21 @@ __device__ __forceinline__ void attend(const typename T::T *kt, const typename T
     constexpr int NS = DP / 16, ND = DP / 32;
     const int half = lane >> 5;
     f32x16 s[NT];
+    typename M::Frag ka = M::template row_frag<DP>(kt, lane & 31, half * 8);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         s[t] = f32x16{};
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-            s[t] = M::mma(M::template row_frag<DP>(kt, t * 32 + (lane & 31), i * 16 + half * 8), q[i], s[t]);
+        for (int i = 0; i < NS; ++i) {
+            typename M::Frag kn = ka;
+            if (i + 1 < NS)
+                kn = M::template row_frag<DP>(kt, t * 32 + (lane & 31), (i + 1) * 16 + half * 8);
+            else if (t + 1 < NT)
+                kn = M::template row_frag<DP>(kt, (t + 1) * 32 + (lane & 31), half * 8);
+            reads_first<T>();
+            s[t] = M::mma(ka, q[i], s[t]);
+            ka = kn;
+        }
     }
     if (masked) {
 #pragma unroll
@@ -80,12 +89,7 @@ __device__ __forceinline__ void attend(const typename T::T *kt, const typename T
     sm.l += sum;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const typename M::Frag p0 = M::template pack<0>(s[t]), p1 = M::template pack<1>(s[t]);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            o[d] = M::mma(M::template col_frag<DP>(vt, t * 32, d * 32, lane), p0, o[d]);
-            o[d] = M::mma(M::template col_frag<DP>(vt, t * 32 + 16, d * 32, lane), p1, o[d]);
-        }
+        add_columns<T, DP>(o, vt, t * 32, M::template pack<0>(s[t]), M::template pack<1>(s[t]), lane);
     }
 }
 

@@ -5,8 +5,8 @@
 //   dS = P (dP - delta),  delta = sum_d g out,
 //   dQ = scale dS k,  dK = scale dS^T q
 //
-// Two kernels, each with its result's rows to itself, so that nothing is
-// added atomically and every call gives the same bits: one walks the query
+// Two kinds of workgroups, each with its result's rows to itself, so that nothing is
+// added atomically and every call gives the same bits: one kind walks the query
 // rows for a tile of keys (dK, dV; the rows are those of every query head
 // that shares the key head, so their gradients add up in registers), one the
 // keys for a tile of rows (dQ).  That forms S and dP twice, seven products
@@ -125,12 +125,11 @@ struct KvShape {
 };
 
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(AttnArgs a) {
+__device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, int64_t block, int64_t blocks) {
     using E = typename T::T;
     using M = Tile<T>;
     using S = KvShape<T, DP>;
     constexpr int RT = S::RT, NS = DP / 16, ND = DP / 32;
-    extern __shared__ __align__(512) char smem[];
     E *const qbuf = (E *)smem, *const gbuf = qbuf + 2 * S::tile;
     float *const lbuf = (float *)(gbuf + 2 * S::tile), *const dbuf = lbuf + 2 * RT;
     int *const from = (int *)(dbuf + 2 * RT), *const upto = from + 2 * RT;  // the keys that each row sees
@@ -138,7 +137,7 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
     E *const vrow = (E *)(upto + 2 * RT) + (wave * 32 + (lane & 31)) * S::PV + half * 8;  // this lane's key in LDS
 
     const int64_t tiles = (a.Lk + 127) / 128;
-    int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    int64_t id = xcd_order(block, blocks);
     const int split = (int)(id % a.splits);
     id /= a.splits;
     const int key0 = (int)(id % tiles) * 128;  // causal: the longest first
@@ -219,15 +218,26 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
         const E *const qt = qbuf + at * S::tile, *const gt = gbuf + at * S::tile;
         const float *const lt = lbuf + at * RT, *const dt = dbuf + at * RT;
         f32x16 s = {}, p = {};
-#pragma unroll
-        for (int i = 0; i < NS; ++i) s = M::mma(M::template row_frag<DP>(qt, lane & 31, i * 16 + half * 8), kf[i], s);
+        auto v_frag = [&](int i) {
+            if constexpr (S::v_lds)
+                return *(const typename M::Frag *)(vrow + i * 16);
+            else
+                return vf[i];
+        };
+        typename M::Frag qa = M::template row_frag<DP>(qt, lane & 31, half * 8), ga = M::template row_frag<DP>(gt, lane & 31, half * 8);
+        typename M::Frag va = v_frag(0);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const typename M::Frag gr = M::template row_frag<DP>(gt, lane & 31, i * 16 + half * 8);
-            if constexpr (S::v_lds)
-                p = M::mma(gr, *(const typename M::Frag *)(vrow + i * 16), p);
-            else
-                p = M::mma(gr, vf[i], p);
+            typename M::Frag qn = qa, gn = ga, vn = va;
+            if (i + 1 < NS) {
+                qn = M::template row_frag<DP>(qt, lane & 31, (i + 1) * 16 + half * 8);
+                gn = M::template row_frag<DP>(gt, lane & 31, (i + 1) * 16 + half * 8);
+                vn = v_frag(i + 1);
+            }
+            reads_first<T>();
+            s = M::mma(qa, kf[i], s);
+            p = M::mma(ga, va, p);
+            qa = qn, ga = gn, va = vn;
         }
         // does every row of the tile see every key of the wave?
         const int w0 = key0 + wave * 32;
@@ -258,16 +268,8 @@ __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks)) void k_attn_bwd_kv(A
         }
         const typename M::Frag p0 = M::template pack<0>(s), p1 = M::template pack<1>(s);
         const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            dv[d] = M::mma(M::template col_frag<DP>(gt, 0, d * 32, lane), p0, dv[d]);
-            dv[d] = M::mma(M::template col_frag<DP>(gt, 16, d * 32, lane), p1, dv[d]);
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            dk[d] = M::mma(M::template col_frag<DP>(qt, 0, d * 32, lane), s0, dk[d]);
-            dk[d] = M::mma(M::template col_frag<DP>(qt, 16, d * 32, lane), s1, dk[d]);
-        }
+        add_columns<T, DP>(dv, gt, 0, p0, p1, lane);
+        add_columns<T, DP>(dk, qt, 0, s0, s1, lane);
         if (r + RT < r1) store(r + RT, at ^ 1);
     }
     __syncthreads();
@@ -330,17 +332,16 @@ struct QShape {
 };
 
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(AttnArgs a) {
+__device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, int64_t block, int64_t blocks) {
     using E = typename T::T;
     using M = Tile<T>;
     using S = QShape<T, DP>;
     constexpr int KT = S::KT, NS = DP / 16, ND = DP / 32;
-    extern __shared__ __align__(512) char smem[];
     E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * S::tile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
 
     const int64_t tiles = (a.rows + 127) / 128;
-    const int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t id = xcd_order(block, blocks);
     const int64_t tile = tiles - 1 - id % tiles;  // causal: the longest first
     const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
     const int64_t row0 = tile * 128, last = min(row0 + 127, a.rows - 1);
@@ -383,10 +384,19 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
         if (k0 < final.hi && k0 + KT > first.lo) {
             const E *const kt = kbuf + at * S::tile, *const vt = vbuf + at * S::tile;
             f32x16 s = {}, p = {};
+            typename M::Frag ka = M::template row_frag<DP>(kt, lane & 31, half * 8), va = M::template row_frag<DP>(vt, lane & 31, half * 8);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) s = M::mma(M::template row_frag<DP>(kt, lane & 31, i * 16 + half * 8), qf[i], s);
-#pragma unroll
-            for (int i = 0; i < NS; ++i) p = M::mma(M::template row_frag<DP>(vt, lane & 31, i * 16 + half * 8), gf[i], p);
+            for (int i = 0; i < NS; ++i) {
+                typename M::Frag kn = ka, vn = va;
+                if (i + 1 < NS) {
+                    kn = M::template row_frag<DP>(kt, lane & 31, (i + 1) * 16 + half * 8);
+                    vn = M::template row_frag<DP>(vt, lane & 31, (i + 1) * 16 + half * 8);
+                }
+                reads_first<T>();
+                s = M::mma(ka, qf[i], s);
+                p = M::mma(va, gf[i], p);
+                ka = kn, va = vn;
+            }
             const bool masked = final.lo > k0 || first.hi < k0 + KT;
 #pragma unroll
             for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lse)) * (p[r] - delta);
@@ -398,11 +408,7 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
                 }
             }
             const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                dq[d] = M::mma(M::template col_frag<DP>(kt, 0, d * 32, lane), s0, dq[d]);
-                dq[d] = M::mma(M::template col_frag<DP>(kt, 16, d * 32, lane), s1, dq[d]);
-            }
+            add_columns<T, DP>(dq, kt, 0, s0, s1, lane);
         }
     }
     __syncthreads();
@@ -415,26 +421,36 @@ __global__ __launch_bounds__(256, (QShape<T, DP>::blocks)) void k_attn_bwd_q(Att
     });
 }
 
+// Both in one launch: neither needs the other's result, together they fill the
+// GPU where each alone would leave part of it idle (16 x 128 positions, 8
+// heads of 64, fp32: 128 workgroups each on 256 CUs, 49 us one after the
+// other and 28 at once), and the shorter one fills the longer one's end.
+template <typename T, int DP, bool VEC>
+__global__ __launch_bounds__(256, (KvShape<T, DP>::blocks < QShape<T, DP>::blocks ? KvShape<T, DP>::blocks : QShape<T, DP>::blocks))
+void k_attn_bwd(AttnArgs a, uint32_t kv_blocks) {
+    extern __shared__ __align__(512) char smem[];
+    if (blockIdx.x < kv_blocks)
+        key_gradients<T, DP, VEC>(a, smem, blockIdx.x, kv_blocks);
+    else
+        query_gradients<T, DP, VEC>(a, smem, blockIdx.x - kv_blocks, gridDim.x - kv_blocks);
+}
+
 int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 
 template <typename T, int DP, bool VEC>
 hipError_t launch(const AttnArgs &a, hipStream_t stream) {
     constexpr size_t q_lds = QShape<T, DP>::lds, kv_lds = KvShape<T, DP>::lds;
     const int64_t heads = (int64_t)a.B * a.Hkv;
-    if (a.rows > 0) {
+    const int64_t kv_blocks = a.gk || a.gv ? heads * ((a.Lk + 127) / 128) * a.splits : 0;
+    const int64_t q_blocks = a.gq ? heads * ((a.rows + 127) / 128) : 0;
+    if (kv_blocks + q_blocks == 0) return hipSuccess;
+    if (a.rows > 0)
         hipLaunchKernelGGL((k_attn_delta<T, VEC>), dim3((uint32_t)((heads * a.rows + 31) / 32)), dim3(256), 0, stream, a);
-        if (a.gq) {
-            hipLaunchKernelGGL((k_attn_bwd_q<T, DP, VEC>), dim3((uint32_t)(heads * ((a.rows + 127) / 128))), dim3(256),
-                               q_lds, stream, a);
-        }
-    }
-    if ((a.gk || a.gv) && a.Lk > 0) {
-        hipLaunchKernelGGL((k_attn_bwd_kv<T, DP, VEC>), dim3((uint32_t)(heads * ((a.Lk + 127) / 128) * a.splits)), dim3(256),
-                           kv_lds, stream, a);
-        if (a.splits > 1)
-            hipLaunchKernelGGL((k_attn_bwd_sum<T, DP, VEC>), dim3((uint32_t)((2 * heads * a.Lk * (DP / 4) + 255) / 256)),
-                               dim3(256), 0, stream, a);
-    }
+    hipLaunchKernelGGL((k_attn_bwd<T, DP, VEC>), dim3((uint32_t)(kv_blocks + q_blocks)), dim3(256),
+                       q_lds > kv_lds ? q_lds : kv_lds, stream, a, (uint32_t)kv_blocks);
+    if (kv_blocks > 0 && a.splits > 1)
+        hipLaunchKernelGGL((k_attn_bwd_sum<T, DP, VEC>), dim3((uint32_t)((2 * heads * a.Lk * (DP / 4) + 255) / 256)),
+                           dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
