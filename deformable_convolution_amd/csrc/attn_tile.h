@@ -68,19 +68,51 @@ struct Tile<BF16> {
     static __device__ __forceinline__ Frag row_frag(const E *tile, int row, int c0) {
         return *(const Frag *)(tile + (((row * (DP / CH) + c0 / CH) ^ mix<DP / CH>(row)) * CH));
     }
-    // Eight elements of column c0 + lane%32, rows k0 + 8*(j/4) + 4*(lane/32) +
-    // j%4 (k0: a multiple of 16): each transposing read takes a 4 x 16 block
-    // whose lane 4*i + c addresses elements 4c .. 4c+3 of row i, and gives
-    // lane i of the 16 the block's column i.
-    template <int DP>
-    static __device__ __forceinline__ Frag col_frag(const E *tile, int k0, int c0, int lane) {
-        typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-        const int i = lane & 15, row = k0 + 4 * (lane >> 5) + (i >> 2), c = c0 + ((lane >> 4) & 1) * 16 + (i & 3) * 4;
-        auto at = [&](int r) { return tile + (((r * (DP / CH) + c / CH) ^ mix<DP / CH>(r)) * CH + c % CH); };
-        const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)at(row));
-        const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)at(row + 8));
+    // Rows k0 .. k0+31 of the columns c0 + 32 d + lane%32, d < N, as the operands
+    // f[d][0] (the first 16 rows) and f[d][1]: eight elements each, rows 8*(j/4)
+    // + 4*(lane/32) + j%4.  A transposing read takes a 4 x 16 block whose lane
+    // 4*i + c addresses elements 4c .. 4c+3 of row i, and gives lane i of the 16
+    // the block's column i.  The reads are written out with their own wait: as
+    // builtins each would first wait for the loads into LDS that are in flight
+    // for the tiles to come.
+    template <int DP, int N>
+    static __device__ __forceinline__ void col_frags(const E *tile, int k0, int c0, int lane, Frag (*f)[2]) {
+        static_assert(N == 1 || N == 2, "one or two slices");
+        const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2), c = ((lane >> 4) & 1) * 16 + (i & 3) * 4;
+        auto at = [&](int r, int d) {
+            const E *const p = tile + (k0 * DP + ((r * (DP / CH) + (c0 + 32 * d + c) / CH) ^ mix<DP / CH>(r)) * CH + c % CH);
+            return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const E *)p;
+        };
+        constexpr int next = 16 * DP * sizeof(E);  // mix() repeats after 16 rows
+        i16x4 v[2 * N][2];
+        if constexpr (N == 1) {
+            asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                         "ds_read_b64_tr_b16 %1, %5\n\t"
+                         "ds_read_b64_tr_b16 %2, %4 offset:%6\n\t"
+                         "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
+                         : "v"(at(row, 0)), "v"(at(row + 8, 0)), "n"(next)
+                         : "memory");
+        } else {
+            asm volatile("ds_read_b64_tr_b16 %0, %8\n\t"
+                         "ds_read_b64_tr_b16 %1, %9\n\t"
+                         "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %4, %10\n\t"
+                         "ds_read_b64_tr_b16 %5, %11\n\t"
+                         "ds_read_b64_tr_b16 %6, %10 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1]), "=&v"(v[2][0]), "=&v"(v[2][1]),
+                           "=&v"(v[3][0]), "=&v"(v[3][1])
+                         : "v"(at(row, 0)), "v"(at(row + 8, 0)), "v"(at(row, 1)), "v"(at(row + 8, 1)), "n"(next)
+                         : "memory");
+        }
         typedef short i16x8 __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(Frag, (i16x8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int k = 0; k < 2 * N; ++k)
+            f[k >> 1][k & 1] = __builtin_bit_cast(Frag, (i16x8)__builtin_shufflevector(v[k][0], v[k][1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
     // Elements 8s .. 8s+7 of a result as an operand, rounded to nearest even.
     template <int S>
@@ -111,16 +143,17 @@ struct Tile<F32> {
         const f32x4 a = at(c0), b = at(c0 + 4);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    template <int DP>
-    static __device__ __forceinline__ Frag col_frag(const E *tile, int k0, int c0, int lane) {
-        const int c = c0 + (lane & 31);
-        Frag f;
+    template <int DP, int N>
+    static __device__ __forceinline__ void col_frags(const E *tile, int k0, int c0, int lane, Frag (*f)[2]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = k0 + 4 * (lane >> 5) + 8 * (j >> 2) + (j & 3);
-            f[j] = tile[((row * (DP / CH) + c / CH) ^ mix<DP / CH>(row)) * CH + c % CH];
+        for (int k = 0; k < 2 * N; ++k) {
+            const int c = c0 + 32 * (k >> 1) + (lane & 31);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = 16 * (k & 1) + 4 * (lane >> 5) + 8 * (j >> 2) + (j & 3);
+                f[k >> 1][k & 1][j] = tile[k0 * DP + ((row * (DP / CH) + c / CH) ^ mix<DP / CH>(row)) * CH + c % CH];
+            }
         }
-        return f;
     }
     template <int S>
     static __device__ __forceinline__ Frag pack(const f32x16 &c) {
@@ -278,24 +311,21 @@ __device__ __forceinline__ void reads_first() {
 }
 
 // acc[d] += A_d P for the 32-column slices d of a tile, A_d its rows k0 ..
-// k0+31 read down the columns, P the two operands p0, p1.
+// k0+31 (k0 a multiple of 32) read down the columns, P the two operands p0, p1.
 template <typename T, int DP>
 __device__ __forceinline__ void add_columns(f32x16 *acc, const typename T::T *tile, int k0, typename Tile<T>::Frag p0,
                                             typename Tile<T>::Frag p1, int lane) {
     using M = Tile<T>;
-    constexpr int ND = DP / 32;
-    typename M::Frag a0 = M::template col_frag<DP>(tile, k0, 0, lane), a1 = M::template col_frag<DP>(tile, k0 + 16, 0, lane);
+    constexpr int ND = DP / 32, N = ND > 1 && sizeof(typename T::T) == 2 ? 2 : 1;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-        typename M::Frag n0 = a0, n1 = a1;
-        if (d + 1 < ND) {
-            n0 = M::template col_frag<DP>(tile, k0, (d + 1) * 32, lane);
-            n1 = M::template col_frag<DP>(tile, k0 + 16, (d + 1) * 32, lane);
+    for (int d = 0; d < ND; d += N) {
+        typename M::Frag f[N][2];
+        M::template col_frags<DP, N>(tile, k0, d * 32, lane, f);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            acc[d + n] = M::mma(f[n][0], p0, acc[d + n]);
+            acc[d + n] = M::mma(f[n][1], p1, acc[d + n]);
         }
-        reads_first<T>();
-        acc[d] = M::mma(a0, p0, acc[d]);
-        acc[d] = M::mma(a1, p1, acc[d]);
-        a0 = n0, a1 = n1;
     }
 }
 

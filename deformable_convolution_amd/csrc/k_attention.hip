@@ -19,22 +19,23 @@ namespace dc1d {
 
 namespace {
 
+constexpr int kMaxParts = 128;  // of the keys: lanes of k_attn_join times two
+
 // Rows of the softmax that a lane carries (row lane % 32 of its wave; the
 // two halves hold the same maximum and each its own part of the sum).
 struct Softmax {
     float m, l;  // maximum in units of log 2 (-inf: nothing seen), part of the sum
 };
 
-// One tile of 32 * NT keys (first key k0) against 32 rows: scores, running
-// softmax, o^T += V^T P^T.  kt, vt: the tiles in LDS.  masked: some lane's
-// range cuts the tile.
+// The scores S^T = K Q^T of 32 * NT keys (first key k0), in place of those
+// that a lane's row does not see -infinity.  masked: some lane's range cuts
+// the tile.
 template <typename T, int DP, int NT>
-__device__ __forceinline__ void attend(const typename T::T *kt, const typename T::T *vt, const typename Tile<T>::Frag *q,
-                                       f32x16 *o, Softmax &sm, float c, bool masked, int k0, KeyRange kr, int lane) {
+__device__ __forceinline__ void scores(f32x16 *s, const typename T::T *kt, const typename Tile<T>::Frag *q, bool masked, int k0,
+                                       KeyRange kr, int lane) {
     using M = Tile<T>;
-    constexpr int NS = DP / 16, ND = DP / 32;
+    constexpr int NS = DP / 16;
     const int half = lane >> 5;
-    f32x16 s[NT];
     typename M::Frag ka = M::template row_frag<DP>(kt, lane & 31, half * 8);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -57,9 +58,15 @@ __device__ __forceinline__ void attend(const typename T::T *kt, const typename T
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int j = k0 + t * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
-                if (j < kr.lo || j >= kr.hi) s[t][r] = -INFINITY;
+                s[t][r] = j >= kr.lo && j < kr.hi ? s[t][r] : -INFINITY;
             }
     }
+}
+
+// Scores into probabilities against the running maximum, which they may move.
+template <int DP, int NT>
+__device__ __forceinline__ void soften(f32x16 *s, f32x16 *o, Softmax &sm, float c) {
+    constexpr int ND = DP / 32;
     float top = s[0][0];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -87,10 +94,15 @@ __device__ __forceinline__ void attend(const typename T::T *kt, const typename T
             sum += s[t][r];
         }
     sm.l += sum;
+}
+
+// o^T += V^T P^T
+template <typename T, int DP, int NT>
+__device__ __forceinline__ void add_values(f32x16 *o, const typename T::T *vt, const f32x16 *s, int lane) {
+    using M = Tile<T>;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
         add_columns<T, DP>(o, vt, t * 32, M::template pack<0>(s[t]), M::template pack<1>(s[t]), lane);
-    }
 }
 
 // 16 elements of a row's 32 d's in a result's order, times f.
@@ -187,9 +199,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
         landed<0>();
         __syncthreads();
         if (k0 + KT < hi) load(at ^ 1, k0 + KT);
-        if (k0 < final.hi && k0 + KT > first.lo)
-            attend<T, DP, KT / 32>(kbuf + at * S::tile, vbuf + at * S::tile, q, o, sm, c,
-                                   final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+        if (k0 < final.hi && k0 + KT > first.lo) {
+            f32x16 s[KT / 32];
+            scores<T, DP, KT / 32>(s, kbuf + at * S::tile, q, final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+            soften<DP, KT / 32>(s, o, sm, c);
+            add_values<T, DP, KT / 32>(o, vbuf + at * S::tile, s, lane);
+        }
     }
 
     const float l = half_sum(sm.l);
@@ -215,9 +230,7 @@ template <typename T, int DP>
 struct KeysShape {
     static constexpr int KT = 32;
     static constexpr int tile = KT * DP, PO = DP + 4;
-    // a wave's tiles twice, where the LDS holds that for four waves
-    static constexpr int NB = (size_t)16 * tile * sizeof(typename T::T) <= 128 << 10 ? 2 : 1;
-    static constexpr size_t wave_lds = (size_t)2 * NB * tile * sizeof(typename T::T);
+    static constexpr size_t wave_lds = (size_t)2 * tile * sizeof(typename T::T);
     static constexpr size_t join_lds = (size_t)4 * 32 * (PO + 2) * sizeof(float);
     static constexpr size_t lds = 4 * wave_lds > join_lds ? 4 * wave_lds : join_lds;
 };
@@ -229,10 +242,12 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     constexpr int KT = S::KT, ND = DP / 32;
     extern __shared__ __align__(512) char smem[];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
-    E *const kbuf = (E *)(smem + wave * S::wave_lds), *const vbuf = kbuf + S::NB * S::tile;
+    E *const kbuf = (E *)(smem + wave * S::wave_lds), *const vbuf = kbuf + S::tile;
 
     const int64_t tiles = (a.rows + 31) / 32;
-    int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    // several tiles of rows read the same keys, and share an L2; with one the
+    // workgroups are spread, so that no XCD gets only long sequences
+    int64_t id = tiles > 1 ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x;
     const int split = (int)(id % a.splits);
     id /= a.splits;
     const int64_t row0 = id % tiles * 32;
@@ -253,36 +268,42 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     Softmax sm = {-INFINITY, 0.0f};
     const float c = a.scale * kLog2e;
 
-    // this part's run of the tiles [t0, t1) that the rows see
+    // this part's run of the tiles [t0, t1) that the rows see: parts are of one
+    // length, so that a short sequence's later parts end at once
     const int t0 = first.lo / KT, t1 = final.hi > first.lo ? (final.hi + KT - 1) / KT : t0;
-    const int per = ((t1 - t0 + a.splits - 1) / a.splits + 3) / 4 * 4;
-    const int s0 = t0 + min((int64_t)per * split, (int64_t)(t1 - t0)), s1 = min(s0 + per, t1);
+    const int s0 = (int)min(t0 + (int64_t)a.part_tiles * split, (int64_t)t1), s1 = (int)min(s0 + (int64_t)a.part_tiles, (int64_t)t1);
 
     const E *const kp = (const E *)a.k + b * a.ks.b + hk * a.ks.h, *const vp = (const E *)a.v + b * a.vs.b + hk * a.vs.h;
     Stage<T, KT, DP, 64, VEC> ks, vs;
     ks.init(a.ks.l, lane);
     vs.init(a.vs.l, lane);
     ks.near = vs.near = ks.near && vs.near;
-    auto load = [&](int at, int n) {
-        ks.load(kbuf + at * S::tile, kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane);
-        vs.load(vbuf + at * S::tile, vp + (int64_t)n * KT * a.vs.l, a.vs.l, final.hi - n * KT, a.D, lane);
-    };
+    auto load_k = [&](int n) { ks.load(kbuf, kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane); };
+    auto load_v = [&](int n) { vs.load(vbuf, vp + (int64_t)n * KT * a.vs.l, a.vs.l, final.hi - n * KT, a.D, lane); };
+    constexpr int LOADS = decltype(ks)::N;  // of one tile, in flight where the rows are near
     int n = s0 + wave;
-    if (n < s1) load(0, n);
-    for (int at = 0; n < s1; n += 4, at ^= S::NB - 1) {
+    if (n < s1) {
+        load_k(n);
+        load_v(n);
+    }
+    for (; n < s1; n += 4) {
         const int k0 = n * KT;
-        // the next tile takes the other buffer's place, whose reads are done
-        if (S::NB > 1 && n + 4 < s1) {
-            load(at ^ 1, n + 4);
-            landed<2 * decltype(ks)::N>();
-        } else {
+        const bool more = n + 4 < s1;
+        f32x16 s[1];
+        landed<LOADS>();  // the keys; the values follow
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        scores<T, DP, 1>(s, kbuf, q, final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (more) load_k(n + 4);  // over the keys just used
+        soften<DP, 1>(s, o, sm, c);
+        if (more)
+            landed<LOADS>();  // the values; the next keys follow
+        else
             landed<0>();
-        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        attend<T, DP, 1>(kbuf + at * S::tile, vbuf + at * S::tile, q, o, sm, c, final.lo > k0 || first.hi < k0 + KT, k0, kr,
-                         lane);
+        add_values<T, DP, 1>(o, vbuf, s, lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (S::NB == 1 && n + 4 < s1) load(0, n + 4);
+        if (more) load_v(n + 4);
     }
 
     // join the four waves: each leaves o, m, l; thread (row, slice) adds them in wave order
@@ -345,35 +366,58 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     }
 }
 
-// The parts of a row joined in order; a wave a row.
+// The parts of a row joined, a workgroup a row: every wave forms the parts'
+// weights (a lane a part), adds up every fourth part, and the waves' sums are
+// added in wave order.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     using E = typename T::T;
-    const int lane = threadIdx.x & 63;
-    const int64_t all = (int64_t)a.B * a.Hkv * a.rows, at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (at >= all) return;
+    constexpr int NV = (DP + 63) / 64, PL = kMaxParts / 64;
+    __shared__ float sums[4][DP], weight[kMaxParts];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t all = (int64_t)a.B * a.Hkv * a.rows, at = blockIdx.x, step = all * (DP + 2);
     const float *const p = a.part + at * (DP + 2);
-    float m = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, p[(int64_t)s * all * (DP + 2)]);
-    float sum = 0.0f, v[(DP + 63) / 64] = {};
-    for (int s = 0; s < a.splits; ++s) {
-        const float *const ps = p + (int64_t)s * all * (DP + 2);
-        const float w = ps[0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ps[0] - m);
-        sum += w * ps[1];
+    float w[PL], l[PL], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < (DP + 63) / 64; ++i)
-            if (i * 64 + lane < DP) v[i] += w * ps[2 + i * 64 + lane];
+    for (int i = 0; i < PL; ++i) {
+        const int s = i * 64 + lane;
+        w[i] = s < a.splits ? p[s * step] : -INFINITY;
+        l[i] = s < a.splits ? p[s * step + 1] : 0.0f;
+        m = fmaxf(m, w[i]);
     }
-    const int64_t bh = at / a.rows;
-    const uint32_t n = (uint32_t)(at % a.rows);
-    const int b = (int)(bh / a.Hkv), pos = row_at(a, n).pos, h = (int)(bh % a.Hkv) * a.G + row_at(a, n).head;
-    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    E *const op = (E *)a.out + b * a.os.b + pos * a.os.l + h * a.os.h;
 #pragma unroll
-    for (int i = 0; i < (DP + 63) / 64; ++i)
-        if (i * 64 + lane < a.D) T::st(op, i * 64 + lane, v[i] * f);
-    if (a.lse && lane == 0)
-        a.lse[((int64_t)b * a.Hq + h) * a.Lq + pos] = sum == 0.0f ? -INFINITY : m * kLn2 + __logf(sum);
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        w[i] = w[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(w[i] - m);
+        sum += w[i] * l[i];
+        if (wave == 0) weight[i * 64 + lane] = w[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    float v[NV] = {};
+#pragma unroll 4
+    for (int s = wave; s < a.splits; s += 4) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j * 64 + lane < DP) v[j] += weight[s] * p[s * step + 2 + j * 64 + lane];
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (j * 64 + lane < DP) sums[wave][j * 64 + lane] = v[j];
+    __syncthreads();
+    const int64_t bh = at / a.rows, n = at % a.rows;
+    const RowAt r = row_at(a, n);
+    const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv) * a.G + r.head;
+    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    if ((int)threadIdx.x < a.D) {
+        const int d = threadIdx.x;
+        const float o = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+        T::st((E *)a.out + b * a.os.b + r.pos * a.os.l + h * a.os.h, d, o * f);
+    }
+    if (a.lse && threadIdx.x == 0)
+        a.lse[((int64_t)b * a.Hq + h) * a.Lq + r.pos] = sum == 0.0f ? -INFINITY : m * kLn2 + __logf(sum);
 }
 
 int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
@@ -388,8 +432,7 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &pl, hipStream_t stream) {
     constexpr size_t lds = KeysShape<T, DP>::lds;
     hipLaunchKernelGGL((k_attn_keys<T, DP, VEC>), dim3((uint32_t)pl.blocks), dim3(256), lds, stream, a);
     if (a.splits > 1)
-        hipLaunchKernelGGL((k_attn_join<T, DP>), dim3((uint32_t)(((int64_t)a.B * a.Hkv * a.rows + 3) / 4)), dim3(256), 0,
-                           stream, a);
+        hipLaunchKernelGGL((k_attn_join<T, DP>), dim3((uint32_t)((int64_t)a.B * a.Hkv * a.rows)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -416,18 +459,33 @@ AttnPlan plan_attention(const AttnArgs &a, int num_cus) {
     pl.name = "attention_keys";
     const int64_t blocks = heads * ((a.rows + 31) / 32);
     if (blocks == 0) return pl;
-    // enough workgroups for two on every CU, none with fewer than 256 keys
-    const int64_t most = (a.Lk + 255) / 256;
-    int64_t splits = (2 * (int64_t)num_cus + blocks - 1) / blocks;
-    splits = splits < 1 ? 1 : splits > most ? most : splits;
-    pl.splits = (int)(splits < 1 ? 1 : splits > 256 ? 256 : splits);
+    // the most tiles of 32 keys that a tile of rows can see: its rows are of at
+    // most 31 / G + 2 neighbouring positions
+    int64_t tiles = ((int64_t)a.Lk + 31) / 32;
+    if (a.window) {
+        const int64_t seen = a.window + (a.causal ? 0 : a.window) + 31 / a.G + 2, few = (seen + 31) / 32 + 1;
+        tiles = tiles < few ? tiles : few;
+    }
+    // where there are fewer than CUs, enough for two on each, none with fewer
+    // than 8 tiles
+    const int64_t most = tiles / 8 > 1 ? tiles / 8 : 1;
+    int64_t splits = blocks >= num_cus ? 1 : (2 * (int64_t)num_cus + blocks - 1) / blocks;
+    splits = splits > most ? most : splits;
+    splits = splits < 1 ? 1 : splits > kMaxParts ? kMaxParts : splits;
+    // the workspace is sized before the parts are made a multiple of the four
+    // waves' tiles: it then never grows where a window leaves fewer tiles, and
+    // can be asked for without one
+    if (splits > 1) pl.ws_bytes = (size_t)splits * heads * a.rows * (padded(a.D) + 2) * sizeof(float);
+    pl.part_tiles = (int)(((tiles + splits - 1) / splits + 3) / 4 * 4);
+    pl.splits = (int)((tiles + pl.part_tiles - 1) / pl.part_tiles);
+    if (pl.splits < 1) pl.splits = 1;
     pl.blocks = blocks * pl.splits;
-    if (pl.splits > 1) pl.ws_bytes = (size_t)pl.splits * heads * a.rows * (padded(a.D) + 2) * sizeof(float);
     return pl;
 }
 
 hipError_t launch_attention(AttnArgs a, const AttnPlan &pl, void *ws, hipStream_t stream) {
     a.splits = pl.splits;
+    a.part_tiles = pl.part_tiles;
     a.part = (float *)ws;
     if (pl.blocks == 0) return hipSuccess;
     return a.dtype == kF32 ? launch_typed<F32>(a, pl, stream) : launch_typed<BF16>(a, pl, stream);

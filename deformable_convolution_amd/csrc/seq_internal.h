@@ -67,6 +67,7 @@ struct AttnArgs {
     float scale;
     bool vec;                   // 16-byte pieces of every row are aligned
     int splits;                 // forward: parts of the keys; backward: parts of the rows
+    int part_tiles;             // forward: tiles of 32 keys in a part
     float *part;                // the parts' partial sums
     float *delta;               // backward: sum_d g out, [B][Hkv][rows]
 };
@@ -74,7 +75,7 @@ struct AttnArgs {
 struct AttnPlan {
     const char *name;
     bool by_keys;  // the waves of a workgroup share its rows and split its keys
-    int splits;
+    int splits, part_tiles;
     int64_t blocks;
     size_t ws_bytes;
 };

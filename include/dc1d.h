@@ -568,7 +568,8 @@ int dc1d_attention(const dc1d_strided *q, const dc1d_strided *k, const dc1d_stri
                    size_t workspace_bytes, void *stream);
 
 /* Which kernel dc1d_attention would use ("attention_rows", "attention_keys"),
- * its workgroups, and into how many parts it splits the keys. */
+ * its workgroups, and into how many parts it splits the keys, where no window
+ * narrows them. */
 int dc1d_attention_plan(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v, const char **kernel_name,
                         int64_t *grid_blocks, int32_t *splits);
 
