@@ -68,45 +68,46 @@ struct Tile<BF16> {
     static __device__ __forceinline__ Frag row_frag(const E *tile, int row, int c0) {
         return *(const Frag *)(tile + (((row * (DP / CH) + c0 / CH) ^ mix<DP / CH>(row)) * CH));
     }
-    // Rows k0 .. k0+31 of the columns c0 + 32 d + lane%32, d < N, as the operands
-    // f[d][0] (the first 16 rows) and f[d][1]: eight elements each, rows 8*(j/4)
-    // + 4*(lane/32) + j%4.  A transposing read takes a 4 x 16 block whose lane
+    // Rows K0 .. K0+31 of the columns c0 + 32 d + lane%32, d < N, of the tile OFF
+    // elements on, as the operands f[d][0] (the first 16 rows) and f[d][1]: eight
+    // elements each, rows 8*(j/4) + 4*(lane/32) + j%4.  A transposing read takes a 4 x 16 block whose lane
     // 4*i + c addresses elements 4c .. 4c+3 of row i, and gives lane i of the 16
     // the block's column i.  The reads are written out with their own wait: as
     // builtins each would first wait for the loads into LDS that are in flight
     // for the tiles to come.
-    template <int DP, int N>
-    static __device__ __forceinline__ void col_frags(const E *tile, int k0, int c0, int lane, Frag (*f)[2]) {
+    template <int DP, int N, int OFF, int K0>
+    static __device__ __forceinline__ void col_frags(const E *tile, int c0, int lane, Frag (*f)[2]) {
         static_assert(N == 1 || N == 2, "one or two slices");
         const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2), c = ((lane >> 4) & 1) * 16 + (i & 3) * 4;
         auto at = [&](int r, int d) {
-            const E *const p = tile + (k0 * DP + ((r * (DP / CH) + (c0 + 32 * d + c) / CH) ^ mix<DP / CH>(r)) * CH + c % CH);
+            const E *const p = tile + (((r * (DP / CH) + (c0 + 32 * d + c) / CH) ^ mix<DP / CH>(r)) * CH + c % CH);
             return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const E *)p;
         };
-        constexpr int next = 16 * DP * sizeof(E);  // mix() repeats after 16 rows
+        constexpr int here = (OFF + K0 * DP) * sizeof(E), next = here + 16 * DP * sizeof(E);  // mix() repeats after 16 rows
+        static_assert(next < 1 << 16, "the offset's range");
         i16x4 v[2 * N][2];
         if constexpr (N == 1) {
-            asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
-                         "ds_read_b64_tr_b16 %1, %5\n\t"
-                         "ds_read_b64_tr_b16 %2, %4 offset:%6\n\t"
-                         "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+            asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+                         "ds_read_b64_tr_b16 %1, %5 offset:%6\n\t"
+                         "ds_read_b64_tr_b16 %2, %4 offset:%7\n\t"
+                         "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
                          "s_waitcnt lgkmcnt(0)"
                          : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
-                         : "v"(at(row, 0)), "v"(at(row + 8, 0)), "n"(next)
+                         : "v"(at(row, 0)), "v"(at(row + 8, 0)), "n"(here), "n"(next)
                          : "memory");
         } else {
-            asm volatile("ds_read_b64_tr_b16 %0, %8\n\t"
-                         "ds_read_b64_tr_b16 %1, %9\n\t"
-                         "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %4, %10\n\t"
-                         "ds_read_b64_tr_b16 %5, %11\n\t"
-                         "ds_read_b64_tr_b16 %6, %10 offset:%12\n\t"
-                         "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+            asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %2, %8 offset:%13\n\t"
+                         "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+                         "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %5, %11 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %6, %10 offset:%13\n\t"
+                         "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
                          "s_waitcnt lgkmcnt(0)"
                          : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1]), "=&v"(v[2][0]), "=&v"(v[2][1]),
                            "=&v"(v[3][0]), "=&v"(v[3][1])
-                         : "v"(at(row, 0)), "v"(at(row + 8, 0)), "v"(at(row, 1)), "v"(at(row + 8, 1)), "n"(next)
+                         : "v"(at(row, 0)), "v"(at(row + 8, 0)), "v"(at(row, 1)), "v"(at(row + 8, 1)), "n"(here), "n"(next)
                          : "memory");
         }
         typedef short i16x8 __attribute__((ext_vector_type(8)));
@@ -143,15 +144,15 @@ struct Tile<F32> {
         const f32x4 a = at(c0), b = at(c0 + 4);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    template <int DP, int N>
-    static __device__ __forceinline__ void col_frags(const E *tile, int k0, int c0, int lane, Frag (*f)[2]) {
+    template <int DP, int N, int OFF, int K0>
+    static __device__ __forceinline__ void col_frags(const E *tile, int c0, int lane, Frag (*f)[2]) {
 #pragma unroll
         for (int k = 0; k < 2 * N; ++k) {
             const int c = c0 + 32 * (k >> 1) + (lane & 31);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int row = 16 * (k & 1) + 4 * (lane >> 5) + 8 * (j >> 2) + (j & 3);
-                f[k >> 1][k & 1][j] = tile[k0 * DP + ((row * (DP / CH) + c / CH) ^ mix<DP / CH>(row)) * CH + c % CH];
+                f[k >> 1][k & 1][j] = tile[OFF + K0 * DP + ((row * (DP / CH) + c / CH) ^ mix<DP / CH>(row)) * CH + c % CH];
             }
         }
     }
@@ -310,17 +311,17 @@ __device__ __forceinline__ void reads_first() {
     if constexpr (sizeof(typename T::T) == 2) __builtin_amdgcn_sched_barrier(0);
 }
 
-// acc[d] += A_d P for the 32-column slices d of a tile, A_d its rows k0 ..
-// k0+31 (k0 a multiple of 32) read down the columns, P the two operands p0, p1.
-template <typename T, int DP>
-__device__ __forceinline__ void add_columns(f32x16 *acc, const typename T::T *tile, int k0, typename Tile<T>::Frag p0,
+// acc[d] += A_d P for the 32-column slices d of the tile OFF elements on, A_d its
+// rows K0 .. K0+31 read down the columns, P the two operands p0, p1.
+template <typename T, int DP, int OFF = 0, int K0 = 0>
+__device__ __forceinline__ void add_columns(f32x16 *acc, const typename T::T *tile, typename Tile<T>::Frag p0,
                                             typename Tile<T>::Frag p1, int lane) {
     using M = Tile<T>;
     constexpr int ND = DP / 32, N = ND > 1 && sizeof(typename T::T) == 2 ? 2 : 1;
 #pragma unroll
     for (int d = 0; d < ND; d += N) {
         typename M::Frag f[N][2];
-        M::template col_frags<DP, N>(tile, k0, d * 32, lane, f);
+        M::template col_frags<DP, N, OFF, K0>(tile, d * 32, lane, f);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             acc[d + n] = M::mma(f[n][0], p0, acc[d + n]);

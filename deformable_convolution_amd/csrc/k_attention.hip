@@ -13,6 +13,8 @@
 //
 // out = o / l, lse = m + log l.  A row that sees no key keeps l = 0: out 0,
 // lse -infinity.
+#include <type_traits>
+
 #include "attn_tile.h"
 
 namespace dc1d {
@@ -96,13 +98,13 @@ __device__ __forceinline__ void soften(f32x16 *s, f32x16 *o, Softmax &sm, float 
     sm.l += sum;
 }
 
-// o^T += V^T P^T
-template <typename T, int DP, int NT>
+// o^T += V^T P^T, V the tile OFF elements on
+template <typename T, int DP, int NT, int OFF>
 __device__ __forceinline__ void add_values(f32x16 *o, const typename T::T *vt, const f32x16 *s, int lane) {
     using M = Tile<T>;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-        add_columns<T, DP>(o, vt, t * 32, M::template pack<0>(s[t]), M::template pack<1>(s[t]), lane);
+    static_assert(NT <= 2, "up to 64 keys");
+    add_columns<T, DP, OFF, 0>(o, vt, M::template pack<0>(s[0]), M::template pack<1>(s[0]), lane);
+    if constexpr (NT > 1) add_columns<T, DP, OFF, 32>(o, vt, M::template pack<0>(s[1]), M::template pack<1>(s[1]), lane);
 }
 
 // 16 elements of a row's 32 d's in a result's order, times f.
@@ -149,10 +151,11 @@ struct RowsShape {
     static constexpr int KT = sizeof(typename T::T) == 2 ? 64 : 32;
     static constexpr int tile = KT * DP;
     static constexpr size_t lds = (size_t)4 * tile * sizeof(typename T::T);
+    static constexpr int blocks = sizeof(typename T::T) * DP == 128 ? 4 : 2;  // a CU; bf16, D 64: 312 -> 307 us for four
 };
 
 template <typename T, int DP, bool VEC>
-__global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
+__global__ __launch_bounds__(256, (RowsShape<T, DP>::blocks)) void k_attn_rows(AttnArgs a) {
     using E = typename T::T;
     using S = RowsShape<T, DP>;
     constexpr int KT = S::KT, ND = DP / 32;
@@ -194,17 +197,30 @@ __global__ __launch_bounds__(256, 2) void k_attn_rows(AttnArgs a) {
         vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
     };
     int k0 = lo / KT * KT;
-    if (k0 < hi) load(0, k0);
-    for (int at = 0; k0 < hi; k0 += KT, at ^= 1) {
+    // one tile: the buffer it stands in is a constant, so that every read's
+    // address is one that the lane keeps plus a constant
+    auto step = [&](auto at) {
+        constexpr int AT = decltype(at)::value;
         landed<0>();
         __syncthreads();
-        if (k0 + KT < hi) load(at ^ 1, k0 + KT);
+        if (k0 + KT < hi) load(AT ^ 1, k0 + KT);
         if (k0 < final.hi && k0 + KT > first.lo) {
             f32x16 s[KT / 32];
-            scores<T, DP, KT / 32>(s, kbuf + at * S::tile, q, final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
+            scores<T, DP, KT / 32>(s, kbuf + AT * S::tile, q, final.lo > k0 || first.hi < k0 + KT, k0, kr, lane);
             soften<DP, KT / 32>(s, o, sm, c);
-            add_values<T, DP, KT / 32>(o, vbuf + at * S::tile, s, lane);
+            // this wave's products before another's exponentials: the matrix unit
+            // is the one to keep busy (D 128: 274 -> 263 us)
+            __builtin_amdgcn_s_setprio(1);
+            add_values<T, DP, KT / 32, AT * S::tile>(o, vbuf, s, lane);
+            __builtin_amdgcn_s_setprio(0);
         }
+        k0 += KT;
+    };
+    if (k0 < hi) load(0, k0);
+    while (k0 < hi) {
+        step(std::integral_constant<int, 0>{});
+        if (k0 >= hi) break;
+        step(std::integral_constant<int, 1>{});
     }
 
     const float l = half_sum(sm.l);
@@ -301,7 +317,7 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
         else
             landed<0>();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        add_values<T, DP, 1>(o, vbuf, s, lane);
+        add_values<T, DP, 1, 0>(o, vbuf, s, lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (more) load_v(n + 4);
     }
@@ -449,7 +465,12 @@ hipError_t launch_typed(const AttnArgs &a, const AttnPlan &pl, hipStream_t strea
 AttnPlan plan_attention(const AttnArgs &a, int num_cus) {
     AttnPlan pl = {};
     const int64_t heads = (int64_t)a.B * a.Hkv, row_blocks = heads * ((a.rows + 127) / 128);
-    pl.by_keys = a.rows <= 32;
+    // While workgroups of 128 rows leave CUs empty, four times as many of 32
+    // rows finish sooner though each reads all the keys: 8 heads of 64 over 2048
+    // positions, bf16, 128 and 512 workgroups: 36 and 25 us (fp32, 1024
+    // positions: 87 and 28).  From one workgroup a CU on the wider ones win:
+    // two such sequences, 256 and 1024 workgroups: 38 and 42 us.
+    pl.by_keys = a.rows <= 32 || row_blocks < num_cus;
     pl.splits = 1;
     if (!pl.by_keys) {
         pl.name = "attention_rows";
@@ -461,7 +482,7 @@ AttnPlan plan_attention(const AttnArgs &a, int num_cus) {
     if (blocks == 0) return pl;
     // the most tiles of 32 keys that a tile of rows can see: its rows are of at
     // most 31 / G + 2 neighbouring positions
-    int64_t tiles = ((int64_t)a.Lk + 31) / 32;
+    int64_t tiles = a.Lk > 0 ? ((int64_t)a.Lk + 31) / 32 : 1;
     if (a.window) {
         const int64_t seen = a.window + (a.causal ? 0 : a.window) + 31 / a.G + 2, few = (seen + 31) / 32 + 1;
         tiles = tiles < few ? tiles : few;
@@ -478,7 +499,6 @@ AttnPlan plan_attention(const AttnArgs &a, int num_cus) {
     if (splits > 1) pl.ws_bytes = (size_t)splits * heads * a.rows * (padded(a.D) + 2) * sizeof(float);
     pl.part_tiles = (int)(((tiles + splits - 1) / splits + 3) / 4 * 4);
     pl.splits = (int)((tiles + pl.part_tiles - 1) / pl.part_tiles);
-    if (pl.splits < 1) pl.splits = 1;
     pl.blocks = blocks * pl.splits;
     return pl;
 }

@@ -268,8 +268,8 @@ __device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, int
         }
         const typename M::Frag p0 = M::template pack<0>(s), p1 = M::template pack<1>(s);
         const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
-        add_columns<T, DP>(dv, gt, 0, p0, p1, lane);
-        add_columns<T, DP>(dk, qt, 0, s0, s1, lane);
+        add_columns<T, DP>(dv, gt, p0, p1, lane);
+        add_columns<T, DP>(dk, qt, s0, s1, lane);
         if (r + RT < r1) store(r + RT, at ^ 1);
     }
     __syncthreads();
@@ -408,7 +408,7 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, i
                 }
             }
             const typename M::Frag s0 = M::template pack<0>(p), s1 = M::template pack<1>(p);
-            add_columns<T, DP>(dq, kt, 0, s0, s1, lane);
+            add_columns<T, DP>(dq, kt, s0, s1, lane);
         }
     }
     __syncthreads();
