@@ -4,13 +4,15 @@
 
 Every source is compiled for gfx950 only, with packed-fp32 instruction
 selection disabled (scalar fp32 arithmetic only), and linked into
-``deformable_convolution_amd/libdc1d.so``.
+``deformable_convolution_amd/libdc1d.so``.  The sequence operators' Python
+binding (host code only) becomes ``deformable_convolution_amd/_seq.so``.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -28,6 +30,29 @@ FLAGS = [
 ]
 
 
+BIND = os.path.join(PKG, "_seq.so")
+
+
+def build_binding(verbose: bool = False) -> str:
+    """_seq.so: bind_seq.cpp against this interpreter and torch."""
+    import torch
+    from torch.utils import cpp_extension
+    tmp = BIND + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", os.path.join(ROOT, "include"),
+           "-I", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(HERE, "bind_seq.cpp"), "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for bind_seq.cpp:\n%s" % r.stderr)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(verbose: bool = False) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -42,8 +67,10 @@ def build(verbose: bool = False) -> str:
             raise RuntimeError("hipcc failed for %s:\n%s" % (src, r.stderr))
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = OUT + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -21,7 +21,20 @@ class Strided(ctypes.Structure):  # dc1d_strided
 
 @pytest.fixture(scope="module")
 def lib():
-    return sequence._library()
+    lib = dc1d.load_library()
+    p, n, i32, i64, f64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, ctypes.c_double
+    for name, args in {
+            "dc1d_layer_norm": [p] * 6 + [f64, p],
+            "dc1d_layer_norm_backward_workspace_bytes": [p, i32, p],
+            "dc1d_layer_norm_backward": [p] * 8 + [p, n, p],
+            "dc1d_rotary": [p] * 8 + [ctypes.c_int32, i32, i32, p],
+            "dc1d_attention_workspace_bytes": [p] * 4,
+            "dc1d_attention_plan": [p] * 6,
+            "dc1d_attention": [p] * 7 + [i32, i64, f64, p, n, p],
+            "dc1d_attention_backward_workspace_bytes": [p] * 4,
+            "dc1d_attention_backward": [p] * 11 + [i32, i64, f64, p, n, p]}.items():
+        getattr(lib, name).argtypes = args
+    return lib
 
 
 def T(shape, slot, dtype=F32, addr=None):
