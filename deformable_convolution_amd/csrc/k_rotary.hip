@@ -7,9 +7,11 @@
 // 2R are carried over.  Queries and keys go in one launch.
 //
 // Bound by HBM: every element is read and written once.  A thread takes VP
-// neighbouring pairs of one position (16-byte pieces of both halves) and
-// turns them in several heads, so that the table, which the L2 holds, is
-// read once for those heads.
+// neighbouring pairs (16-byte pieces of both halves) of one head; the tables'
+// rows come from the L2 for every head anew.  Turning two or four heads a
+// thread, the row read once for them, left fewer loads in flight and was
+// slower: 8 x 4096 positions, 16 heads of 64, fp32: 49 us (5.5 TB/s) with one
+// head, 62 with four.
 #include "attn_tile.h"
 
 namespace dc1d {
@@ -45,53 +47,41 @@ struct Piece {  // N neighbouring elements, moved as one access where N > 1
     }
 };
 
-// VP pairs and HT heads a thread.  A position has `units` pieces (of pairs,
-// then of the carried elements) in each of `runs` runs of HT heads; a
-// workgroup takes `ppb` positions.
+// VP pairs of a head a thread.  A position has `units` pieces (of pairs, then
+// of the carried elements) in each of its `heads` heads, the queries' and then
+// the keys'; a workgroup takes `ppb` positions.
 struct RotaryGrid {
-    int units, runs, ppb;
+    int units, heads, ppb;
     int64_t positions;
-    FastDiv by_units, by_runs, by_L;
+    FastDiv by_units, by_heads, by_L;
     int rows16;  // the tables' rows of VP entries are 16-byte aligned
 };
 
-template <typename T, int VP, int HT>
+template <typename T, int VP>
 __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, RotaryGrid gr) {
     using E = typename T::T;
     const int64_t n0 = (int64_t)blockIdx.x * gr.ppb;
-    const int work = (int)min((int64_t)gr.ppb, gr.positions - n0) * gr.units * gr.runs;
+    const int work = (int)min((int64_t)gr.ppb, gr.positions - n0) * gr.units * gr.heads;
     for (int w = threadIdx.x; w < work; w += 256) {
-        const uint32_t rest = fdiv(w, gr.by_units), local = fdiv(rest, gr.by_runs);
+        const uint32_t rest = fdiv(w, gr.by_units), local = fdiv(rest, gr.by_heads);
         const int unit = w - (int)rest * gr.units;
-        int h0 = (int)(rest - local * gr.runs) * HT;
+        int h = (int)(rest - local * gr.heads);
         const uint32_t n = (uint32_t)n0 + local;
         const int b = (int)fdiv(n, gr.by_L), l = (int)n - b * a.L;
-        // runs cover the queries' heads, then the keys'
-        const int q_heads = (a.t[0].H + HT - 1) / HT * HT;
-        const int which = h0 >= q_heads;
+        const int which = h >= a.t[0].H;
         const RotaryTensor &t = a.t[which];
-        if (which) h0 -= q_heads;
-        const E *const x = (const E *)t.x + b * t.xs.b + l * t.xs.l;
-        E *const y = (E *)t.y + b * t.ys.b + l * t.ys.l;
+        if (which) h -= a.t[0].H;
+        const E *const x = (const E *)t.x + b * t.xs.b + l * t.xs.l + h * t.xs.h;
+        E *const y = (E *)t.y + b * t.ys.b + l * t.ys.l + h * t.ys.h;
         const int i = unit * VP;
         if (i >= a.R) {  // carried over
             const int d0 = 2 * a.R + (i - (a.R + VP - 1) / VP * VP) * 2;
-            for (int h = h0; h < min(h0 + HT, t.H); ++h)
-                for (int d = d0; d < min(d0 + 2 * VP, a.D); ++d) y[h * t.ys.h + d] = x[h * t.xs.h + d];
+            for (int d = d0; d < min(d0 + 2 * VP, a.D); ++d) y[d] = x[d];
             continue;
         }
-        float u[HT][2 * VP];
-#pragma unroll
-        for (int k = 0; k < HT; ++k) {
-            const E *const xh = x + min(h0 + k, t.H - 1) * t.xs.h;
-            if (a.interleaved) {
-                Piece<T, VP>::load(xh + 2 * i, u[k]);
-                Piece<T, VP>::load(xh + 2 * i + VP, u[k] + VP);
-            } else {
-                Piece<T, VP>::load(xh + i, u[k]);
-                Piece<T, VP>::load(xh + a.R + i, u[k] + VP);
-            }
-        }
+        float u[2 * VP], v[2 * VP];
+        Piece<T, VP>::load(x + (a.interleaved ? 2 * i : i), u);
+        Piece<T, VP>::load(x + (a.interleaved ? 2 * i + VP : a.R + i), u + VP);
         const int *const pos = a.pos + b * a.pos_b + (int64_t)l * a.A;
         auto axis_of = [&](int j) { return (j >= a.first[1]) + (j >= a.first[2]) + (j >= a.first[3]); };
         auto row_of = [&](int axis) { return (int64_t)min(max(pos[axis], 0), a.P - 1) * a.R + i; };
@@ -114,29 +104,21 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, RotaryGrid gr) {
         }
 #pragma unroll
         for (int j = 0; j < VP; ++j) s[j] *= a.sign;
+        if (a.interleaved) {
 #pragma unroll
-        for (int k = 0; k < HT; ++k) {
-            if (h0 + k >= t.H) break;
-            E *const yh = y + (h0 + k) * t.ys.h;
-            float v[2 * VP];
-            if (a.interleaved) {
+            for (int j = 0; j < VP; ++j) {
+                v[2 * j] = u[2 * j] * c[j] - u[2 * j + 1] * s[j];
+                v[2 * j + 1] = u[2 * j] * s[j] + u[2 * j + 1] * c[j];
+            }
+        } else {
 #pragma unroll
-                for (int j = 0; j < VP; ++j) {
-                    v[2 * j] = u[k][2 * j] * c[j] - u[k][2 * j + 1] * s[j];
-                    v[2 * j + 1] = u[k][2 * j] * s[j] + u[k][2 * j + 1] * c[j];
-                }
-                Piece<T, VP>::store(yh + 2 * i, v);
-                Piece<T, VP>::store(yh + 2 * i + VP, v + VP);
-            } else {
-#pragma unroll
-                for (int j = 0; j < VP; ++j) {
-                    v[j] = u[k][j] * c[j] - u[k][VP + j] * s[j];
-                    v[VP + j] = u[k][j] * s[j] + u[k][VP + j] * c[j];
-                }
-                Piece<T, VP>::store(yh + i, v);
-                Piece<T, VP>::store(yh + a.R + i, v + VP);
+            for (int j = 0; j < VP; ++j) {
+                v[j] = u[j] * c[j] - u[VP + j] * s[j];
+                v[VP + j] = u[j] * s[j] + u[VP + j] * c[j];
             }
         }
+        Piece<T, VP>::store(y + (a.interleaved ? 2 * i : i), v);
+        Piece<T, VP>::store(y + (a.interleaved ? 2 * i + VP : a.R + i), v + VP);
     }
 }
 
@@ -155,31 +137,24 @@ bool pieces_ok(const RotaryArgs &a, int VP) {
     return true;
 }
 
-template <typename T, int VP, int HT>
-hipError_t launch_heads(const RotaryArgs &a, hipStream_t stream) {
+template <typename T, int VP>
+hipError_t launch(const RotaryArgs &a, hipStream_t stream) {
     RotaryGrid g;
     g.units = (a.R + VP - 1) / VP + (a.D - 2 * a.R + 2 * VP - 1) / (2 * VP);
-    g.runs = (a.t[0].H + HT - 1) / HT + (a.t[1].H + HT - 1) / HT;
+    g.heads = a.t[0].H + a.t[1].H;
     g.positions = (int64_t)a.B * a.L;
-    const int64_t per = (int64_t)g.units * g.runs;
+    const int64_t per = (int64_t)g.units * g.heads;
     // one piece a thread, and few enough workgroups for one launch
     int64_t ppb = per >= 256 ? 1 : 256 / per;
     const int64_t least = (g.positions + (1 << 22) - 1) >> 22;
     if (ppb < least) ppb = least;
     g.ppb = (int)ppb;
     g.by_units = make_fastdiv((uint32_t)g.units);
-    g.by_runs = make_fastdiv((uint32_t)g.runs);
+    g.by_heads = make_fastdiv((uint32_t)g.heads);
     g.by_L = make_fastdiv((uint32_t)a.L);
     g.rows16 = a.R % 4 == 0 && ((uintptr_t)a.cos & 15) == 0 && ((uintptr_t)a.sin & 15) == 0;
-    hipLaunchKernelGGL((k_rotary<T, VP, HT>), dim3((uint32_t)((g.positions + ppb - 1) / ppb)), dim3(256), 0, stream, a, g);
+    hipLaunchKernelGGL((k_rotary<T, VP>), dim3((uint32_t)((g.positions + ppb - 1) / ppb)), dim3(256), 0, stream, a, g);
     return hipGetLastError();
-}
-
-template <typename T, int VP>
-hipError_t launch(const RotaryArgs &a, hipStream_t stream) {
-    // one head a thread while that leaves the GPU unfilled (latency counts), else four
-    const int64_t one = (int64_t)a.B * a.L * ((a.R + VP - 1) / VP) * (a.t[0].H + a.t[1].H);
-    return one <= 256 * 256 ? launch_heads<T, VP, 1>(a, stream) : launch_heads<T, VP, (sizeof(typename T::T) == 2 ? 2 : 4)>(a, stream);
 }
 
 }  // namespace
