@@ -370,8 +370,8 @@ __device__ __forceinline__ float half_sum(float v) {
 // Workgroups are dealt to the 8 XCDs in turn; this gives each XCD a
 // contiguous run of the logical order, so that the workgroups that read the
 // same keys share an L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t n) {
-    const int64_t per = n / 8, extra = n % 8, x = id % 8, k = id / 8;
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
+    const uint32_t per = n / 8, extra = n % 8, x = id % 8, k = id / 8;
     return x * per + (x < extra ? x : extra) + k;
 }
 

@@ -163,11 +163,10 @@ __global__ __launch_bounds__(256, (RowsShape<T, DP>::blocks)) void k_attn_rows(A
     E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * S::tile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
 
-    const int64_t tiles = (a.rows + 127) / 128;
-    const int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t tile = tiles - 1 - id % tiles;  // causal: the longest first
-    const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
-    const int64_t row0 = tile * 128;
+    const uint32_t tiles = (uint32_t)((a.rows + 127) / 128), id = xcd_order(blockIdx.x, gridDim.x), bh = id / tiles;
+    const uint32_t tile = tiles - 1 - (id - bh * tiles);  // causal: the longest first
+    const int b = (int)(bh / (uint32_t)a.Hkv), hk = (int)(bh % (uint32_t)a.Hkv);
+    const int64_t row0 = (int64_t)tile * 128;
     const int64_t last = min(row0 + 127, a.rows - 1);
     const int64_t row = row0 + wave * 32 + (lane & 31), rc = min(row, a.rows - 1);
 
@@ -260,14 +259,14 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
     E *const kbuf = (E *)(smem + wave * S::wave_lds), *const vbuf = kbuf + S::tile;
 
-    const int64_t tiles = (a.rows + 31) / 32;
+    const uint32_t tiles = (uint32_t)((a.rows + 31) / 32);
     // several tiles of rows read the same keys, and share an L2; with one the
     // workgroups are spread, so that no XCD gets only long sequences
-    int64_t id = tiles > 1 ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x;
-    const int split = (int)(id % a.splits);
-    id /= a.splits;
-    const int64_t row0 = id % tiles * 32;
-    const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
+    const uint32_t at_grid = tiles > 1 ? xcd_order(blockIdx.x, gridDim.x) : blockIdx.x;
+    const uint32_t id = at_grid / (uint32_t)a.splits, bh = id / tiles;
+    const int split = (int)(at_grid - id * (uint32_t)a.splits);
+    const int64_t row0 = (int64_t)(id - bh * tiles) * 32;
+    const int b = (int)(bh / (uint32_t)a.Hkv), hk = (int)(bh % (uint32_t)a.Hkv);
     const int64_t last = min(row0 + 31, a.rows - 1);
     const int64_t row = row0 + (lane & 31), rc = min(row, a.rows - 1);
 
@@ -423,9 +422,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     for (int j = 0; j < NV; ++j)
         if (j * 64 + lane < DP) sums[wave][j * 64 + lane] = v[j];
     __syncthreads();
-    const int64_t bh = at / a.rows, n = at % a.rows;
-    const RowAt r = row_at(a, n);
-    const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv) * a.G + r.head;
+    const uint32_t bh = (uint32_t)at / (uint32_t)a.rows;
+    const RowAt r = row_at(a, (uint32_t)at - bh * (uint32_t)a.rows);
+    const int b = (int)(bh / (uint32_t)a.Hkv), h = (int)(bh % (uint32_t)a.Hkv) * a.G + r.head;
     const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     if ((int)threadIdx.x < a.D) {
         const int d = threadIdx.x;

@@ -30,9 +30,8 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a) {
     const int64_t n = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
     const int part = threadIdx.x & 7;
     const int64_t all = (int64_t)a.B * a.Hkv * a.rows, m = n < all ? n : all - 1;
-    const int64_t bh = m / a.rows;
-    const uint32_t r = (uint32_t)(m % a.rows);
-    const int b = (int)(bh / a.Hkv), pos = row_at(a, r).pos, h = (int)(bh % a.Hkv) * a.G + row_at(a, r).head;
+    const uint32_t bh = (uint32_t)m / (uint32_t)a.rows, r = (uint32_t)m - bh * (uint32_t)a.rows;
+    const int b = (int)(bh / (uint32_t)a.Hkv), pos = row_at(a, r).pos, h = (int)(bh % (uint32_t)a.Hkv) * a.G + row_at(a, r).head;
     const E *const g = (const E *)a.g + b * a.gs.b + pos * a.gs.l + h * a.gs.h;
     const E *const o = (const E *)a.o + b * a.os.b + pos * a.os.l + h * a.os.h;
     float s = 0.0f;
@@ -125,7 +124,7 @@ struct KvShape {
 };
 
 template <typename T, int DP, bool VEC>
-__device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, int64_t block, int64_t blocks) {
+__device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, uint32_t block, uint32_t blocks) {
     using E = typename T::T;
     using M = Tile<T>;
     using S = KvShape<T, DP>;
@@ -136,12 +135,11 @@ __device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, int
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
     E *const vrow = (E *)(upto + 2 * RT) + (wave * 32 + (lane & 31)) * S::PV + half * 8;  // this lane's key in LDS
 
-    const int64_t tiles = (a.Lk + 127) / 128;
-    int64_t id = xcd_order(block, blocks);
-    const int split = (int)(id % a.splits);
-    id /= a.splits;
-    const int key0 = (int)(id % tiles) * 128;  // causal: the longest first
-    const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
+    const uint32_t tiles = (uint32_t)(a.Lk + 127) / 128, at_grid = xcd_order(block, blocks);
+    const uint32_t id = at_grid / (uint32_t)a.splits, bh = id / tiles;
+    const int split = (int)(at_grid - id * (uint32_t)a.splits);
+    const int key0 = (int)(id - bh * tiles) * 128;  // causal: the longest first
+    const int b = (int)(bh / (uint32_t)a.Hkv), hk = (int)(bh % (uint32_t)a.Hkv);
     const int key = key0 + wave * 32 + (lane & 31);
     const KeyRule rule = key_rule(a, b);
 
@@ -157,9 +155,9 @@ __device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, int
     }
     int64_t r0 = (int64_t)i0 * a.G / RT * RT, r1 = i1 > i0 ? (int64_t)i1 * a.G : r0;
     // this part of them
-    const int64_t n_tiles = (r1 - r0 + RT - 1) / RT, per = (n_tiles + a.splits - 1) / a.splits;
-    r0 += min(per * split, n_tiles) * RT;
-    r1 = min(r1, r0 + per * RT);
+    const uint32_t n_tiles = (uint32_t)((r1 - r0 + RT - 1) / RT), per = (n_tiles + a.splits - 1) / (uint32_t)a.splits;
+    r0 += min((int64_t)per * split, (int64_t)n_tiles) * RT;
+    r1 = min(r1, r0 + (int64_t)per * RT);
 
     typename M::Frag kf[NS], vf[S::v_lds ? 1 : NS];
     {
@@ -305,14 +303,13 @@ __global__ __launch_bounds__(256) void k_attn_bwd_sum(AttnArgs a) {
     const int col = (int)(id % (DP / 4)) * 4;
     if (n >= 2 * keys) return;
     const int which = n >= keys;
-    const int64_t m = n - (which ? keys : 0);
+    const uint32_t m = (uint32_t)(n - (which ? keys : 0)), bh = m / (uint32_t)a.Lk, b = bh / (uint32_t)a.Hkv;
     void *const out = which ? a.gv : a.gk;
     if (!out || col >= a.D) return;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < a.splits; ++s) v += *(const f32x4 *)(a.part + ((int64_t)s * 2 * keys + n) * DP + col);
     const Strides3 st = which ? a.gvs : a.gks;
-    const int64_t bh = m / a.Lk;
-    store_piece<T, VEC>((E *)out + bh / a.Hkv * st.b + bh % a.Hkv * st.h + m % a.Lk * st.l, col, v, a.D);
+    store_piece<T, VEC>((E *)out + b * st.b + (bh - b * a.Hkv) * st.h + (int64_t)(m - bh * (uint32_t)a.Lk) * st.l, col, v, a.D);
 }
 
 // ---- dQ --------------------------------------------------------------------------
@@ -332,7 +329,7 @@ struct QShape {
 };
 
 template <typename T, int DP, bool VEC>
-__device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, int64_t block, int64_t blocks) {
+__device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, uint32_t block, uint32_t blocks) {
     using E = typename T::T;
     using M = Tile<T>;
     using S = QShape<T, DP>;
@@ -340,11 +337,10 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, i
     E *const kbuf = (E *)smem, *const vbuf = kbuf + 2 * S::tile;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, half = lane >> 5;
 
-    const int64_t tiles = (a.rows + 127) / 128;
-    const int64_t id = xcd_order(block, blocks);
-    const int64_t tile = tiles - 1 - id % tiles;  // causal: the longest first
-    const int b = (int)(id / tiles / a.Hkv), hk = (int)(id / tiles % a.Hkv);
-    const int64_t row0 = tile * 128, last = min(row0 + 127, a.rows - 1);
+    const uint32_t tiles = (uint32_t)((a.rows + 127) / 128), id = xcd_order(block, blocks), bh = id / tiles;
+    const uint32_t tile = tiles - 1 - (id - bh * tiles);  // causal: the longest first
+    const int b = (int)(bh / (uint32_t)a.Hkv), hk = (int)(bh % (uint32_t)a.Hkv);
+    const int64_t row0 = (int64_t)tile * 128, last = min(row0 + 127, a.rows - 1);
     const int64_t row = row0 + wave * 32 + (lane & 31), rc = min(row, a.rows - 1);
     const int pos = row_at(a, rc).pos, h = hk * a.G + row_at(a, rc).head;
 

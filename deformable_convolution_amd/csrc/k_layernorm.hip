@@ -422,10 +422,10 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
     using S = ColShape<EPT, TPR, NT>;
     using P = ColPiece<T, EPT>;
     __shared__ float red[NT / 64 * S::TL];
-    const int64_t tiles = (a.L + S::TL - 1) / S::TL;
+    const uint32_t tiles = (uint32_t)((a.L + S::TL - 1) / S::TL);  // of a batch; all positions are fewer than 2^31
     const int c0 = threadIdx.x / S::TPR;
     for (int64_t tile = xcd_order(blockIdx.x, gridDim.x); tile < tiles * a.B; tile += gridDim.x) {
-        const int64_t b = tile / tiles, l0 = tile % tiles * S::TL;
+        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL;
         const int tl = threadIdx.x % S::TPR * EPT;
         const bool on = l0 + tl < a.L;
         const E *const x = (const E *)a.x + b * a.C * a.L + l0;
@@ -522,7 +522,7 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
     using P = ColPiece<T, EPT>;
     constexpr int NR = NP > 0 ? NP : 1;
     __shared__ float red[2 * (NT / 64) * S::TL];
-    const int64_t tiles = (a.L + S::TL - 1) / S::TL;
+    const uint32_t tiles = (uint32_t)((a.L + S::TL - 1) / S::TL);  // of a batch; all positions are fewer than 2^31
     const int c0 = threadIdx.x / S::TPR, tr = threadIdx.x % S::TPR, tl = tr * EPT;
     const bool params = a.gw || a.gb;
     float *const pw = a.ws + (params ? (int64_t)blockIdx.x * 2 * a.C : 0), *const pb = pw + a.C;
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
         float mean[EPT], rstd[EPT];
     };
     auto fetch = [&](int64_t tile, Held &h) {
-        const int64_t b = tile / tiles, l0 = tile % tiles * S::TL, at = b * a.C * a.L + l0;
+        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL, at = b * a.C * a.L + l0;
         const bool on = l0 + tl < a.L;
         if constexpr (NP > 0) {
             const E *const x = (const E *)a.x + at, *const g = (const E *)a.g + at;
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
     for (int64_t tile = tile0; tile < all; tile += gridDim.x) {
         Held h = next;
         if (tile + gridDim.x < all) fetch(tile + gridDim.x, next);
-        const int64_t b = tile / tiles, l0 = tile % tiles * S::TL, at = b * a.C * a.L + l0;
+        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL, at = b * a.C * a.L + l0;
         const bool on = l0 + tl < a.L;
         float s[2][EPT] = {}, xh[EPT], u[EPT];
         // what a channel of weight w adds to the sums over the channels and to its parameters' gradients
