@@ -423,12 +423,13 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, u
 // other and 28 at once), and the shorter one fills the longer one's end.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks < QShape<T, DP>::blocks ? KvShape<T, DP>::blocks : QShape<T, DP>::blocks))
-void k_attn_bwd(AttnArgs a, uint32_t kv_blocks) {
+void k_attn_bwd(AttnArgs a, uint32_t kv_blocks, int keys_first) {
     extern __shared__ __align__(512) char smem[];
-    if (blockIdx.x < kv_blocks)
-        key_gradients<T, DP, VEC>(a, smem, blockIdx.x, kv_blocks);
+    const uint32_t q_blocks = gridDim.x - kv_blocks, kv0 = keys_first ? 0 : q_blocks, q0 = keys_first ? kv_blocks : 0;
+    if (blockIdx.x - kv0 < kv_blocks)
+        key_gradients<T, DP, VEC>(a, smem, blockIdx.x - kv0, kv_blocks);
     else
-        query_gradients<T, DP, VEC>(a, smem, blockIdx.x - kv_blocks, gridDim.x - kv_blocks);
+        query_gradients<T, DP, VEC>(a, smem, blockIdx.x - q0, q_blocks);
 }
 
 int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
@@ -443,7 +444,8 @@ hipError_t launch(const AttnArgs &a, hipStream_t stream) {
     if (a.rows > 0)
         hipLaunchKernelGGL((k_attn_delta<T, VEC>), dim3((uint32_t)((heads * a.rows + 31) / 32)), dim3(256), 0, stream, a);
     hipLaunchKernelGGL((k_attn_bwd<T, DP, VEC>), dim3((uint32_t)(kv_blocks + q_blocks)), dim3(256),
-                       q_lds > kv_lds ? q_lds : kv_lds, stream, a, (uint32_t)kv_blocks);
+                       q_lds > kv_lds ? q_lds : kv_lds, stream, a, (uint32_t)kv_blocks,
+                       (int)(4 * (a.rows / a.splits) >= 3 * (int64_t)a.Lk));  // the longer workgroups: 4 and 3 products a tile
     if (kv_blocks > 0 && a.splits > 1)
         hipLaunchKernelGGL((k_attn_bwd_sum<T, DP, VEC>), dim3((uint32_t)((2 * heads * a.Lk * (DP / 4) + 255) / 256)),
                            dim3(256), 0, stream, a);
@@ -463,10 +465,15 @@ hipError_t launch_typed(const AttnArgs &a, hipStream_t stream) {
 AttnBwdPlan plan_attention_backward(const AttnArgs &a, int num_cus) {
     AttnBwdPlan pl = {};
     const int64_t heads = (int64_t)a.B * a.Hkv, blocks = heads * ((a.Lk + 127) / 128);
-    // parts of the rows: enough workgroups that a causal call's uneven ones
-    // even out (four to a CU), none with fewer than 512 rows
-    int64_t splits = blocks > 0 ? (4 * (int64_t)num_cus + blocks - 1) / blocks : 1;
-    const int64_t most = (a.rows + 511) / 512;
+    // Parts of the rows: enough workgroups that a causal call's uneven ones even
+    // out (two to a CU; 4 x 4096 positions, 2 key heads: 1012 us unsplit, 498 in
+    // two parts, 510 in four), none with fewer than 512 rows: the parts' sums cost
+    // more than they save where the query workgroups already share the GPU (4 x
+    // 512 positions, 8 heads of 64, fp32: 86 us whole, 97 in four parts).  Only
+    // where hardly any CU has a workgroup are parts of 128 rows better (2 x 256
+    // positions, 2 key heads of 128: 37 and 26 us).
+    int64_t splits = blocks > 0 ? (2 * (int64_t)num_cus + blocks - 1) / blocks : 1;
+    const int64_t least = 16 * blocks <= num_cus ? 128 : 512, most = (a.rows + least - 1) / least;
     splits = splits > most ? most : splits;
     pl.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
     pl.delta_bytes = ((size_t)heads * a.rows * sizeof(float) + 255) / 256 * 256;
