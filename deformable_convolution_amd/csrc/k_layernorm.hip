@@ -342,21 +342,12 @@ __device__ __forceinline__ void col_load(const typename T::T *p, bool in, float 
         f[0] = in ? T::ld(p, 0) : 0.0f;
     }
 }
-// stream: past the caches, for the forward where the tiles' rows are whole
-// lines of 128 bytes (8 x 256 x 16384 bf16: 33.5 -> 31.0 us; rows of 4092 fp32,
-// whose lines neighbouring tiles share: 65 -> 97 us, so not there; nor in the
-// backward, whose reads then find less in them: 99 -> 114 us).
 template <typename T, int EPT>
-__device__ __forceinline__ void col_store(typename T::T *p, const float *f, bool stream) {
-    if constexpr (EPT > 1) {
-        const u32x4 v = Vec<T>::narrow(f);
-        if (stream)
-            __builtin_nontemporal_store(v, (u32x4 *)p);
-        else
-            *(u32x4 *)p = v;
-    } else {
+__device__ __forceinline__ void col_store(typename T::T *p, const float *f) {
+    if constexpr (EPT > 1)
+        *(u32x4 *)p = Vec<T>::narrow(f);
+    else
         T::st(p, 0, f[0]);
-    }
 }
 
 // Sums over the channels, per position: over a wave's threads of the same
@@ -433,7 +424,6 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
     __shared__ float red[NT / 64 * S::TL];
     const uint32_t tiles = (uint32_t)((a.L + S::TL - 1) / S::TL);  // of a batch; all positions are fewer than 2^31
     const int c0 = threadIdx.x / S::TPR;
-    const bool stream = S::TL * sizeof(E) % 128 == 0 && a.L * sizeof(E) % 128 == 0 && ((uintptr_t)a.y & 127) == 0;
     for (int64_t tile = xcd_order(blockIdx.x, gridDim.x); tile < tiles * a.B; tile += gridDim.x) {
         const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL;
         const int tl = threadIdx.x % S::TPR * EPT;
@@ -495,7 +485,7 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
                 if (a.w) f[e] *= w;
                 if (a.b) f[e] += bias;
             }
-            col_store<T, EPT>(y + (int64_t)c * a.L + tl, f, stream);
+            col_store<T, EPT>(y + (int64_t)c * a.L + tl, f);
         };
         if constexpr (NP > 0) {
 #pragma unroll
@@ -632,7 +622,7 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
                 xh[e] = (xh[e] - h.mean[e]) * h.rstd[e];
                 u[e] = h.rstd[e] * (u[e] * w - s[0][e] - xh[e] * s[1][e]);
             }
-            col_store<T, EPT>(y + (int64_t)c * a.L, u, false);
+            col_store<T, EPT>(y + (int64_t)c * a.L, u);
         };
         if constexpr (NP > 0) {
 #pragma unroll
