@@ -710,7 +710,9 @@ struct ColChoice {
     int tpr, np, nt;
 };
 ColChoice choose_cols(int C, int64_t L, bool vec) {
-    const bool far = L >= 1 << 23;  // a tile's channels lie past 32-bit offsets
+    // a thread's first channel lies past 32-bit byte offsets: as many as 256
+    // thread rows of four bytes an element
+    const bool far = L >= 1 << 22;
     if (vec) {
         if (far || C > 2048) return {8, 0, 1024};
         if (C <= 256) return {8, 8, 256};

@@ -145,6 +145,27 @@ def test_layer_norm_in_place_and_unaligned():
             assert torch.equal(y, want)
 
 
+def test_layer_norm_channels_past_32_bit_offsets():
+    # 1025 channels, two threads across a row: channel 255 of 2^22 + 8 float32 positions starts past 2^32 bytes
+    C, L = 1025, (1 << 22) + 8
+    x = torch.empty((1, C, L), device=DEV)
+    for c in range(C):  # a channel at a time, so that no index passes 32 bits in what fills it
+        x[0, c].normal_(generator=gen(100 + c))
+    at = torch.tensor([0, 1, 7, 8, 1000003, L - 9, L - 1], device=DEV)
+    some = torch.stack([x[0, c][at] for c in range(C)]).unsqueeze(0)
+    y, mean, rstd = sequence.layer_norm(x, with_stats=True)
+    wy, wm, wr = ref.layer_norm(some)
+    got = torch.stack([y[0, c][at] for c in range(C)]).unsqueeze(0)
+    within(got, wy, ln_bound(some, wm, wr) + 4 * U32 * wy.abs(), "y")
+    grad = sequence.layer_norm_backward(x, x, mean, rstd, need=("x",))["x"]
+    got = torch.stack([grad[0, c][at] for c in range(C)]).unsqueeze(0)
+    # against the same positions by themselves, whose gradients are checked above
+    _, m, r = sequence.layer_norm(some, with_stats=True)
+    want = sequence.layer_norm_backward(some, some, m, r, need=("x",))["x"].double()
+    e = 16 * U32 * (1 + some.double().abs().amax(1, keepdim=True) * wr.unsqueeze(1)) ** 2
+    within(got, want, 16 * e * (1 + some.double().abs()) * (1 + wr.unsqueeze(1)), "grad_x")
+
+
 def test_layer_norm_empty():
     for shape in ((0, 8), (0, 8, 4), (2, 8, 0)):
         x = torch.empty(shape, device=DEV)
