@@ -55,6 +55,32 @@ struct Vec<BF16> {
     }
 };
 
+// 16 bytes at an address that is a multiple of 16, or (ODD) of the element's
+// size only: one load or store either way.
+typedef u32x4 u32x4_odd __attribute__((aligned(2)));
+template <bool ODD, typename E>
+__device__ __forceinline__ u32x4 load16(const E *p) {
+    if constexpr (ODD)
+        return *(const u32x4_odd *)p;
+    else
+        return *(const u32x4 *)p;
+}
+// The elements from `skip` on of a piece.
+template <typename T, bool ODD>
+__device__ __forceinline__ void store16(typename T::T *p, const float *f, int skip) {
+    if constexpr (ODD) {
+        if (skip == 0) {
+            *(u32x4_odd *)p = Vec<T>::narrow(f);
+        } else {
+#pragma unroll
+            for (int e = 1; e < Vec<T>::N; ++e)
+                if (e >= skip) T::st(p, e, f[e]);
+        }
+    } else {
+        *(u32x4 *)p = Vec<T>::narrow(f);
+    }
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
@@ -79,49 +105,71 @@ __device__ __forceinline__ float row_sum(float v, float *red, int slot) {
 
 // ---- rows ----------------------------------------------------------------------
 //
-// Four waves a workgroup; WPR of them to a row, NV 16-byte pieces to a lane
-// (C <= WPR * 64 * NV * Vec::N, C a multiple of Vec::N, 16-byte rows).
-template <typename T, int WPR, int NV>
-__global__ __launch_bounds__(256) void k_ln_rows(LayerNormArgs a) {
+// WPR waves to a row and at least four to a workgroup; NV 16-byte pieces to a
+// lane (C <= WPR * 64 * NV * Vec::N).  Where C is no multiple of a piece, or
+// the rows are not aligned (ODD), the last piece is moved back to end with the
+// row (C >= Vec::N), and the elements that it shares with the one before it
+// are left to that one: 16 bytes a load at any address take what aligned ones
+// take, element by element a row of 1022 bf16 took four times as long.
+template <typename T, int WPR, int NV, bool ODD>
+struct RowShape {
+    static constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / (64 * WPR);
+    int at[NV], skip[NV];  // where a piece is read, and how many of its elements are others' (Vec::N: it is not there)
+    __device__ __forceinline__ RowShape(int lane, int C) {
+        constexpr int N = Vec<T>::N;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * 64 * WPR + lane) * N;
+            if constexpr (ODD) {
+                at[i] = min(c, C - N);
+                skip[i] = min(c - at[i], N);
+            } else {
+                at[i] = c < C ? c : 0;
+                skip[i] = c < C ? 0 : N;
+            }
+        }
+    }
+    __device__ __forceinline__ bool own(int i, int e) const { return ODD ? e >= skip[i] : skip[i] == 0; }
+};
+
+template <typename T, int WPR, int NV, bool ODD>
+__global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows(LayerNormArgs a) {
     using V = Vec<T>;
     using E = typename T::T;
-    __shared__ float red[2 * 4];
+    using S = RowShape<T, WPR, NV, ODD>;
+    __shared__ float red[2 * WPR];
     const int lane = threadIdx.x % (64 * WPR);
-    for (int64_t n0 = (int64_t)blockIdx.x * (4 / WPR); n0 < a.B; n0 += (int64_t)gridDim.x * (4 / WPR)) {
+    const S sh(lane, a.C);
+    for (int64_t n0 = (int64_t)blockIdx.x * S::RPB; n0 < a.B; n0 += (int64_t)gridDim.x * S::RPB) {
         const int64_t n = n0 + threadIdx.x / (64 * WPR);
         const bool on = n < a.B;
         const E *const x = (const E *)a.x + (on ? n : a.B - 1) * a.C;
         u32x4 raw[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * 64 * WPR + lane) * V::N;
-            raw[i] = *(const u32x4 *)(x + (c < a.C ? c : 0));
-        }
+        for (int i = 0; i < NV; ++i) raw[i] = load16<ODD>(x + sh.at[i]);
         // the parameters are loaded before the sums are waited for
         u32x4 wr[NV], br[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * 64 * WPR + lane) * V::N, cc = c < a.C ? c : 0;
-            if (a.w) wr[i] = *(const u32x4 *)((const E *)a.w + cc);
-            if (a.b) br[i] = *(const u32x4 *)((const E *)a.b + cc);
+            if (a.w) wr[i] = load16<ODD>((const E *)a.w + sh.at[i]);
+            if (a.b) br[i] = load16<ODD>((const E *)a.b + sh.at[i]);
         }
         float f[NV][V::N], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             V::widen(raw[i], f[i]);
-            if ((i * 64 * WPR + lane) * V::N < a.C)
 #pragma unroll
-                for (int e = 0; e < V::N; ++e) s += f[i][e];
+            for (int e = 0; e < V::N; ++e)
+                if (sh.own(i, e)) s += f[i][e];
         }
         const float mean = row_sum<WPR>(s, red, 0) * a.inv_c;
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = (i * 64 * WPR + lane) * V::N < a.C;
 #pragma unroll
             for (int e = 0; e < V::N; ++e) {
                 f[i][e] -= mean;
-                if (in) s += f[i][e] * f[i][e];
+                if (sh.own(i, e)) s += f[i][e] * f[i][e];
             }
         }
         const float rstd = rsqrtf(row_sum<WPR>(s, red, 1) * a.inv_c + a.eps);
@@ -129,8 +177,7 @@ __global__ __launch_bounds__(256) void k_ln_rows(LayerNormArgs a) {
         E *const y = (E *)a.y + n * a.C;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * 64 * WPR + lane) * V::N;
-            if (c >= a.C) continue;
+            if (sh.skip[i] == V::N) continue;
             float w[V::N], b[V::N];
             if (a.w) V::widen(wr[i], w);
             if (a.b) V::widen(br[i], b);
@@ -140,7 +187,7 @@ __global__ __launch_bounds__(256) void k_ln_rows(LayerNormArgs a) {
                 if (a.w) f[i][e] *= w[e];
                 if (a.b) f[i][e] += b[e];
             }
-            *(u32x4 *)(y + c) = V::narrow(f[i]);
+            store16<T, ODD>(y + sh.at[i], f[i], sh.skip[i]);
         }
         if (lane == 0) {
             if (a.mean) a.mean[n] = mean;
@@ -149,25 +196,26 @@ __global__ __launch_bounds__(256) void k_ln_rows(LayerNormArgs a) {
     }
 }
 
-// Rows of any length and alignment: a workgroup a row, read once for each
-// sum and once more (from cache, for rows that fit it).
-template <typename T>
-__global__ __launch_bounds__(256) void k_ln_rows_any(LayerNormArgs a) {
+// Rows shorter than a piece (a wave a row) or longer than registers hold (16
+// waves): read once for each sum and once more, from cache where a row fits it.
+template <typename T, int WPR>
+__global__ __launch_bounds__(64 * WPR) void k_ln_rows_any(LayerNormArgs a) {
     using E = typename T::T;
-    __shared__ float red[2 * 4];
+    constexpr int NT = 64 * WPR;
+    __shared__ float red[2 * WPR];
     for (int64_t n = blockIdx.x; n < a.B; n += gridDim.x) {
         const E *const x = (const E *)a.x + n * a.C;
         float s = 0.0f;
-        for (int c = threadIdx.x; c < a.C; c += 256) s += T::ld(x, c);
-        const float mean = row_sum<4>(s, red, 0) * a.inv_c;
+        for (int c = threadIdx.x; c < a.C; c += NT) s += T::ld(x, c);
+        const float mean = row_sum<WPR>(s, red, 0) * a.inv_c;
         s = 0.0f;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
+        for (int c = threadIdx.x; c < a.C; c += NT) {
             const float d = T::ld(x, c) - mean;
             s += d * d;
         }
-        const float rstd = rsqrtf(row_sum<4>(s, red, 1) * a.inv_c + a.eps);
+        const float rstd = rsqrtf(row_sum<WPR>(s, red, 1) * a.inv_c + a.eps);
         E *const y = (E *)a.y + n * a.C;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
+        for (int c = threadIdx.x; c < a.C; c += NT) {
             float v = (T::ld(x, c) - mean) * rstd;
             if (a.w) v *= T::ld((const E *)a.w, c);
             if (a.b) v += T::ld((const E *)a.b, c);
@@ -182,22 +230,22 @@ __global__ __launch_bounds__(256) void k_ln_rows_any(LayerNormArgs a) {
 
 // Backward of rows.  Workgroups stride over the rows; a lane keeps its
 // channels' parameter gradients in registers until the end.
-template <typename T, int WPR, int NV>
-__global__ __launch_bounds__(256) void k_ln_rows_bwd(LayerNormArgs a) {
+template <typename T, int WPR, int NV, bool ODD>
+__global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows_bwd(LayerNormArgs a) {
     using V = Vec<T>;
     using E = typename T::T;
-    constexpr int RPB = 4 / WPR;
-    __shared__ float red[4 * 4];
+    using S = RowShape<T, WPR, NV, ODD>;
+    constexpr int RPB = S::RPB;
+    __shared__ float red[4 * WPR];
     __shared__ float acc[RPB > 1 ? 64 * NV * V::N : 1];
     const int lane = threadIdx.x % (64 * WPR), grp = threadIdx.x / (64 * WPR);
     const bool params = a.gw || a.gb;
+    const S sh(lane, a.C);
     float gw[NV][V::N] = {}, gb[NV][V::N] = {};
     u32x4 wr[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * 64 * WPR + lane) * V::N;
-        if (a.w) wr[i] = *(const u32x4 *)((const E *)a.w + (c < a.C ? c : 0));
-    }
+    for (int i = 0; i < NV; ++i)
+        if (a.w) wr[i] = load16<ODD>((const E *)a.w + sh.at[i]);
     int slot = 0;
     for (int64_t n0 = (int64_t)blockIdx.x * RPB; n0 < a.B; n0 += (int64_t)gridDim.x * RPB) {
         const int64_t n = n0 + grp, m = n < a.B ? n : a.B - 1;
@@ -206,20 +254,19 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd(LayerNormArgs a) {
         u32x4 xr[NV], gr[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * 64 * WPR + lane) * V::N, cc = c < a.C ? c : 0;
-            xr[i] = *(const u32x4 *)(x + cc);
-            gr[i] = *(const u32x4 *)(g + cc);
+            xr[i] = load16<ODD>(x + sh.at[i]);
+            gr[i] = load16<ODD>(g + sh.at[i]);
         }
         float xh[NV][V::N], u[NV][V::N], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = n < a.B && (i * 64 * WPR + lane) * V::N < a.C;
             V::widen(xr[i], xh[i]);
             V::widen(gr[i], u[i]);
             float w[V::N];
             if (a.w) V::widen(wr[i], w);
 #pragma unroll
             for (int e = 0; e < V::N; ++e) {
+                const bool in = n < a.B && sh.own(i, e);
                 xh[i][e] = (xh[i][e] - mean) * rstd;
                 if (in) {
                     gw[i][e] += u[i][e] * xh[i][e];
@@ -240,11 +287,10 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd(LayerNormArgs a) {
                 E *const y = (E *)a.y + n * a.C;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = (i * 64 * WPR + lane) * V::N;
-                    if (c >= a.C) continue;
+                    if (sh.skip[i] == V::N) continue;
 #pragma unroll
                     for (int e = 0; e < V::N; ++e) u[i][e] = rstd * (u[i][e] - s1 - xh[i][e] * s2);
-                    *(u32x4 *)(y + c) = V::narrow(u[i]);
+                    store16<T, ODD>(y + sh.at[i], u[i], sh.skip[i]);
                 }
             }
         }
@@ -263,26 +309,27 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd(LayerNormArgs a) {
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int e = 0; e < V::N; ++e) {
-                        const int j = (i * 64 * WPR + lane) * V::N + e;
                         float v = which ? gb[i][e] : gw[i][e];
                         if constexpr (RPB > 1) {
-                            if (k > 0) v += acc[j];
-                            if (k < RPB - 1) acc[j] = v;
+                            float &sum = acc[(i * 64 + lane) * V::N + e];
+                            if (k > 0) v += sum;
+                            if (k < RPB - 1) sum = v;
                         }
-                        if (k == RPB - 1 && j < a.C) p[j] = v;
+                        if (k == RPB - 1 && sh.own(i, e)) p[sh.at[i] + e] = v;
                     }
             }
         }
     }
 }
 
-// Backward of rows of any length and alignment: a workgroup strides over the
-// rows, its threads over the channels; the parameter sums are kept in the
-// workgroup's part of the workspace.
-template <typename T>
-__global__ __launch_bounds__(256) void k_ln_rows_bwd_any(LayerNormArgs a) {
+// Backward of rows shorter than a piece or longer than registers hold: a
+// workgroup strides over the rows, its threads over the channels; the
+// parameter sums are kept in the workgroup's part of the workspace.
+template <typename T, int WPR>
+__global__ __launch_bounds__(64 * WPR) void k_ln_rows_bwd_any(LayerNormArgs a) {
     using E = typename T::T;
-    __shared__ float red[4 * 4];
+    constexpr int NT = 64 * WPR;
+    __shared__ float red[4 * WPR];
     const bool params = a.gw || a.gb;
     float *const pw = params ? a.ws + (int64_t)blockIdx.x * 2 * a.C : nullptr, *const pb = pw + a.C;
     int slot = 0;
@@ -291,7 +338,7 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd_any(LayerNormArgs a) {
         const E *const x = (const E *)a.x + n * a.C, *const g = (const E *)a.g + n * a.C;
         const float mean = a.mean[n], rstd = a.rstd[n];
         float s1 = 0.0f, s2 = 0.0f;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
+        for (int c = threadIdx.x; c < a.C; c += NT) {
             const float xh = (T::ld(x, c) - mean) * rstd, gc = T::ld(g, c);
             if (params) {
                 pw[c] = (fresh ? 0.0f : pw[c]) + gc * xh;
@@ -303,11 +350,11 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd_any(LayerNormArgs a) {
         }
         fresh = false;
         if (!a.y) continue;
-        s1 = row_sum<4>(s1, red, slot) * a.inv_c;
-        s2 = row_sum<4>(s2, red, slot + 1) * a.inv_c;
+        s1 = row_sum<WPR>(s1, red, slot) * a.inv_c;
+        s2 = row_sum<WPR>(s2, red, slot + 1) * a.inv_c;
         slot ^= 2;
         E *const y = (E *)a.y + n * a.C;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
+        for (int c = threadIdx.x; c < a.C; c += NT) {
             const float xh = (T::ld(x, c) - mean) * rstd, gc = T::ld(g, c);
             const float u = a.w ? gc * T::ld((const E *)a.w, c) : gc;
             T::st(y, c, rstd * (u - s1 - xh * s2));
@@ -318,9 +365,11 @@ __global__ __launch_bounds__(256) void k_ln_rows_bwd_any(LayerNormArgs a) {
 // ---- channels first ---------------------------------------------------------------
 //
 // A tile is TL neighbouring positions of one batch and all C channels.  A
-// thread holds EPT neighbouring positions (16 bytes, or one element where
-// rows are not aligned) of every RP-th channel: NP of them in registers, or,
-// NP = 0, read again for each pass.  TPR threads stand across a tile's row:
+// thread holds EPT neighbouring positions (16 bytes, or one element where a
+// batch has fewer) of every RP-th channel: NP of them in registers, or,
+// NP = 0, read again for each pass.  Where rows are not aligned, or end inside
+// a piece (ODD), the last pieces are moved back to end with the row; what a
+// thread then reads of positions before its own it neither adds nor stores.  TPR threads stand across a tile's row:
 // 8 (whole 128-byte lines), fewer where C channels would not fit otherwise.
 // Neighbouring tiles go to one XCD: where rows are not whole lines they share
 // the lines at their edges.
@@ -329,23 +378,39 @@ struct ColShape {
     static constexpr int TPR = TPR_, TL = TPR * EPT, RP = NT / TPR;
 };
 
-template <typename T, int EPT>
-__device__ __forceinline__ void col_load(const typename T::T *p, bool in, float *f) {
-    if constexpr (EPT > 1) {
-        if (in) {
-            Vec<T>::widen(*(const u32x4 *)p, f);
+// Where this thread's positions of a tile (its first: l0) are read.  Every
+// address is inside the tensor, also of threads that have no position (!on).
+template <int EPT, bool ODD>
+struct ColPlace {
+    int64_t base;  // the workgroup's first position
+    int at, skip;  // the thread's, from base; how many of them are other threads'
+    bool on;
+    __device__ __forceinline__ ColPlace(int64_t l0, int tl, int64_t L) {
+        on = l0 + tl < L;
+        if constexpr (ODD) {
+            base = min(l0, L - EPT);
+            at = (int)(min(l0 + tl, L - EPT) - base);
+            skip = (int)(l0 + tl - base) - at;
         } else {
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) f[e] = 0.0f;
+            base = l0;
+            at = on ? tl : 0;
+            skip = 0;
         }
-    } else {
-        f[0] = in ? T::ld(p, 0) : 0.0f;
     }
-}
-template <typename T, int EPT>
-__device__ __forceinline__ void col_store(typename T::T *p, const float *f) {
+    __device__ __forceinline__ bool own(int e) const { return !ODD || e >= skip; }
+};
+
+template <typename T, int EPT, bool ODD>
+__device__ __forceinline__ void col_load(const typename T::T *p, float *f) {
     if constexpr (EPT > 1)
-        *(u32x4 *)p = Vec<T>::narrow(f);
+        Vec<T>::widen(load16<ODD>(p), f);
+    else
+        f[0] = T::ld(p, 0);
+}
+template <typename T, int EPT, bool ODD>
+__device__ __forceinline__ void col_store(typename T::T *p, const float *f, int skip) {
+    if constexpr (EPT > 1)
+        store16<T, ODD>(p, f, skip);
     else
         T::st(p, 0, f[0]);
 }
@@ -384,11 +449,17 @@ __device__ __forceinline__ void col_sum(float (*s)[EPT], float *red) {
 // The pieces of a tile that a thread holds: channels c0 + i RP.  Each is read
 // at a base that the whole workgroup shares plus this thread's 32-bit offset;
 // a channel past C reads row i RP in its place and is left out of the sums.
-template <typename T, int EPT>
+template <typename T, int EPT, bool ODD>
 struct ColPiece {
     using E = typename T::T;
     using Raw = typename std::conditional<(EPT > 1), u32x4, E>::type;
-    static __device__ __forceinline__ Raw load(const E *base, uint32_t off) { return *(const Raw *)((const char *)base + off); }
+    static __device__ __forceinline__ Raw load(const E *base, uint32_t off) {
+        const E *const p = (const E *)((const char *)base + off);
+        if constexpr (EPT > 1)
+            return load16<ODD>(p);
+        else
+            return *p;
+    }
     // Between two uses of a held piece: the compiler otherwise keeps the
     // widened and centred values of the first use for the second, in more
     // registers than the pieces take.
@@ -416,21 +487,20 @@ struct ColPiece {
     }
 };
 
-template <typename T, int EPT, int TPR, int NP, int NT>
+template <typename T, int EPT, int TPR, int NP, int NT, bool ODD>
 __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
     using E = typename T::T;
     using S = ColShape<EPT, TPR, NT>;
-    using P = ColPiece<T, EPT>;
+    using P = ColPiece<T, EPT, ODD>;
     __shared__ float red[NT / 64 * S::TL];
     const uint32_t tiles = (uint32_t)((a.L + S::TL - 1) / S::TL);  // of a batch; all positions are fewer than 2^31
     const int c0 = threadIdx.x / S::TPR;
     for (int64_t tile = xcd_order(blockIdx.x, gridDim.x); tile < tiles * a.B; tile += gridDim.x) {
         const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL;
-        const int tl = threadIdx.x % S::TPR * EPT;
-        const bool on = l0 + tl < a.L;
-        const E *const x = (const E *)a.x + b * a.C * a.L + l0;
-        E *const y = (E *)a.y + b * a.C * a.L + l0;
-        const uint32_t row0 = (on ? tl : 0) * sizeof(E), off = row0 + (uint32_t)c0 * (uint32_t)a.L * sizeof(E);
+        const ColPlace<EPT, ODD> place(l0, threadIdx.x % S::TPR * EPT, a.L);
+        const E *const x = (const E *)a.x + b * a.C * a.L + place.base;
+        E *const y = (E *)a.y + b * a.C * a.L + place.base;
+        const uint32_t row0 = place.at * sizeof(E), off = row0 + (uint32_t)c0 * (uint32_t)a.L * sizeof(E);
         typename P::Raw raw[NP > 0 ? NP : 1];
         float f[EPT], s[1][EPT] = {};
         if constexpr (NP > 0) {
@@ -448,7 +518,7 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
             }
         } else {
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L + tl, on, f);
+                col_load<T, EPT, ODD>(x + (int64_t)c * a.L + place.at, f);
 #pragma unroll
                 for (int e = 0; e < EPT; ++e) s[0][e] += f[e];
             }
@@ -468,7 +538,7 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
             }
         } else {
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L + tl, on, f);
+                col_load<T, EPT, ODD>(x + (int64_t)c * a.L + place.at, f);
 #pragma unroll
                 for (int e = 0; e < EPT; ++e) s[0][e] += (f[e] - mean[e]) * (f[e] - mean[e]);
             }
@@ -476,7 +546,7 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
         col_sum<EPT, S::TPR, NT, 1>(s, red);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) rstd[e] = rsqrtf(s[0][e] * a.inv_c + a.eps);
-        if (!on) continue;
+        if (!place.on) continue;
         auto put = [&](int c) {
             const float w = a.w ? T::ld((const E *)a.w, c) : 1.0f, bias = a.b ? T::ld((const E *)a.b, c) : 0.0f;
 #pragma unroll
@@ -485,7 +555,7 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
                 if (a.w) f[e] *= w;
                 if (a.b) f[e] += bias;
             }
-            col_store<T, EPT>(y + (int64_t)c * a.L + tl, f);
+            col_store<T, EPT, ODD>(y + (int64_t)c * a.L + place.at, f, place.skip);
         };
         if constexpr (NP > 0) {
 #pragma unroll
@@ -496,15 +566,16 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
             }
         } else {
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L + tl, true, f);
+                col_load<T, EPT, ODD>(x + (int64_t)c * a.L + place.at, f);
                 put(c);
             }
         }
         if (c0 == 0) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                if (a.mean) a.mean[b * a.L + l0 + tl + e] = mean[e];
-                if (a.rstd) a.rstd[b * a.L + l0 + tl + e] = rstd[e];
+                if (!place.own(e)) continue;
+                if (a.mean) a.mean[b * a.L + place.base + place.at + e] = mean[e];
+                if (a.rstd) a.rstd[b * a.L + place.base + place.at + e] = rstd[e];
             }
         }
     }
@@ -515,11 +586,11 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
 // the one before it is worked on.  With the channels in registers (NP > 0) so
 // are their parameter sums; otherwise they are kept in the workgroup's part
 // of the workspace, a thread row (TPR neighbouring lanes) owning its channels.
-template <typename T, int EPT, int TPR, int NP, int NT>
+template <typename T, int EPT, int TPR, int NP, int NT, bool ODD>
 __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(LayerNormArgs a) {
     using E = typename T::T;
     using S = ColShape<EPT, TPR, NT>;
-    using P = ColPiece<T, EPT>;
+    using P = ColPiece<T, EPT, ODD>;
     constexpr int NR = NP > 0 ? NP : 1;
     __shared__ float red[2 * (NT / 64) * S::TL];
     const uint32_t tiles = (uint32_t)((a.L + S::TL - 1) / S::TL);  // of a batch; all positions are fewer than 2^31
@@ -538,11 +609,12 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
         float mean[EPT], rstd[EPT];
     };
     auto fetch = [&](int64_t tile, Held &h) {
-        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL, at = b * a.C * a.L + l0;
-        const bool on = l0 + tl < a.L;
+        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL;
+        const ColPlace<EPT, ODD> place(l0, tl, a.L);
         if constexpr (NP > 0) {
+            const int64_t at = b * a.C * a.L + place.base;
             const E *const x = (const E *)a.x + at, *const g = (const E *)a.g + at;
-            const uint32_t row0 = (on ? tl : 0) * sizeof(E), off = row0 + (uint32_t)c0 * (uint32_t)a.L * sizeof(E);
+            const uint32_t row0 = place.at * sizeof(E), off = row0 + (uint32_t)c0 * (uint32_t)a.L * sizeof(E);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const int ci = i * S::RP < a.C ? i * S::RP : 0;
@@ -553,8 +625,8 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
         }
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            h.mean[e] = a.mean[b * a.L + l0 + (on ? tl + e : 0)];
-            h.rstd[e] = a.rstd[b * a.L + l0 + (on ? tl + e : 0)];
+            h.mean[e] = a.mean[b * a.L + place.base + place.at + e];
+            h.rstd[e] = a.rstd[b * a.L + place.base + place.at + e];
         }
     };
     const int64_t all = tiles * a.B;
@@ -569,13 +641,15 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
     for (int64_t tile = tile0; tile < all; tile += gridDim.x) {
         Held h = next;
         if (tile + gridDim.x < all) fetch(tile + gridDim.x, next);
-        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL, at = b * a.C * a.L + l0;
-        const bool on = l0 + tl < a.L;
+        const int64_t b = (uint32_t)tile / tiles, l0 = (int64_t)((uint32_t)tile % tiles) * S::TL;
+        const ColPlace<EPT, ODD> place(l0, tl, a.L);
+        const int64_t at = b * a.C * a.L + place.base + place.at;
         float s[2][EPT] = {}, xh[EPT], u[EPT];
         // what a channel of weight w adds to the sums over the channels and to its parameters' gradients
         auto take = [&](float w, float &w_sum, float &b_sum) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
+                if (!place.own(e)) continue;
                 xh[e] = (xh[e] - h.mean[e]) * h.rstd[e];
                 w_sum += u[e] * xh[e];
                 b_sum += u[e];
@@ -590,15 +664,15 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
                 const int c = c0 + i * S::RP;
                 P::widen(h.x[i], xh);
                 P::widen(h.g[i], u);
-                if (on && c < a.C) take(wv[i], gw[i], gb[i]);
+                if (place.on && c < a.C) take(wv[i], gw[i], gb[i]);
             }
         } else {
-            const E *const x = (const E *)a.x + at + tl, *const g = (const E *)a.g + at + tl;
+            const E *const x = (const E *)a.x + at, *const g = (const E *)a.g + at;
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, on, xh);
-                col_load<T, EPT>(g + (int64_t)c * a.L, on, u);
+                col_load<T, EPT, ODD>(x + (int64_t)c * a.L, xh);
+                col_load<T, EPT, ODD>(g + (int64_t)c * a.L, u);
                 float w_sum = 0.0f, b_sum = 0.0f;
-                if (on) take(a.w ? T::ld((const E *)a.w, c) : 1.0f, w_sum, b_sum);
+                if (place.on) take(a.w ? T::ld((const E *)a.w, c) : 1.0f, w_sum, b_sum);
                 if (params) {
                     w_sum = across(w_sum);
                     b_sum = across(b_sum);
@@ -612,8 +686,8 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
         fresh = false;
         if (!a.y) continue;
         col_sum<EPT, S::TPR, NT, 2>(s, red);
-        if (!on) continue;
-        E *const y = (E *)a.y + at + tl;
+        if (!place.on) continue;
+        E *const y = (E *)a.y + at;
 #pragma unroll
         for (int e = 0; e < EPT; ++e) s[0][e] *= a.inv_c, s[1][e] *= a.inv_c;
         auto put = [&](int c, float w) {
@@ -622,7 +696,7 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
                 xh[e] = (xh[e] - h.mean[e]) * h.rstd[e];
                 u[e] = h.rstd[e] * (u[e] * w - s[0][e] - xh[e] * s[1][e]);
             }
-            col_store<T, EPT>(y + (int64_t)c * a.L, u);
+            col_store<T, EPT, ODD>(y + (int64_t)c * a.L, u, place.skip);
         };
         if constexpr (NP > 0) {
 #pragma unroll
@@ -634,10 +708,10 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
                 if (c0 + i * S::RP < a.C) put(c0 + i * S::RP, wv[i]);
             }
         } else {
-            const E *const x = (const E *)a.x + at + tl, *const g = (const E *)a.g + at + tl;
+            const E *const x = (const E *)a.x + at, *const g = (const E *)a.g + at;
             for (int c = c0; c < a.C; c += S::RP) {
-                col_load<T, EPT>(x + (int64_t)c * a.L, true, xh);
-                col_load<T, EPT>(g + (int64_t)c * a.L, true, u);
+                col_load<T, EPT, ODD>(x + (int64_t)c * a.L, xh);
+                col_load<T, EPT, ODD>(g + (int64_t)c * a.L, u);
                 put(c, a.w ? T::ld((const E *)a.w, c) : 1.0f);
             }
         }
@@ -689,19 +763,22 @@ dim3 grid_of(int64_t blocks) { return dim3((uint32_t)(blocks < 1 << 20 ? blocks 
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// Which kernel serves the rows: pieces per lane and waves per row, 0: any.
+// Which kernel serves the rows: pieces per lane and waves per row.  nv = 0:
+// from memory for each pass, as rows of less than a piece or of more than
+// eight waves hold are.
 struct RowChoice {
     int wpr, nv;
 };
-RowChoice choose_rows(int C, int per, bool vec) {
-    if (!vec) return {0, 0};
-    const int lanes = (C / per + 63) / 64;  // 16-byte pieces a lane of one wave
+RowChoice choose_rows(int C, int per) {
+    if (C < per) return {1, 0};
+    const int lanes = ((C + per - 1) / per + 63) / 64;  // 16-byte pieces a lane of one wave
     if (lanes <= 1) return {1, 1};
     if (lanes <= 2) return {1, 2};
     if (lanes <= 4) return {1, 4};
     if (lanes <= 8) return {4, 2};
     if (lanes <= 16) return {4, 4};
-    return {0, 0};
+    if (lanes <= 32) return {8, 4};
+    return {16, 0};
 }
 
 // Which kernel serves channels first: threads across a row, channels held per
@@ -709,21 +786,19 @@ RowChoice choose_rows(int C, int per, bool vec) {
 struct ColChoice {
     int tpr, np, nt;
 };
-ColChoice choose_cols(int C, int64_t L, bool vec) {
+ColChoice choose_cols(int C, int64_t L, int per) {
+    if (L < per) return C > 1024 ? ColChoice{8, 0, 1024} : ColChoice{8, 16, 512};
     // a thread's first channel lies past 32-bit byte offsets: as many as 256
     // thread rows of four bytes an element
     const bool far = L >= 1 << 22;
-    if (vec) {
-        if (far || C > 2048) return {8, 0, 1024};
-        if (C <= 256) return {8, 8, 256};
-        return {C <= 512 ? 8 : C <= 1024 ? 4 : 2, 8, 512};
-    }
-    if (far || C > 512) return {32, 0, 1024};
-    return {16, 16, 512};
+    if (far || C > 2048) return {8, 0, 1024};
+    if (C <= 256) return {8, 8, 256};
+    return {C <= 512 ? 8 : C <= 1024 ? 4 : 2, 8, 512};
 }
 
+// Whether every 16-byte piece is aligned and inside its row.
 template <typename T>
-bool vec_ok(const LayerNormArgs &a, bool backward) {
+bool whole(const LayerNormArgs &a, bool backward) {
     const int64_t run = a.L == 1 ? a.C : a.L;
     bool ok = run % Vec<T>::N == 0 && aligned16(a.x) && aligned16(a.y);
     if (backward) ok = ok && aligned16(a.g);
@@ -731,41 +806,53 @@ bool vec_ok(const LayerNormArgs &a, bool backward) {
     return ok;
 }
 
-// Every combination that choose_cols gives.
-#define DC1D_COLS_SWITCH                                        \
-    if (vec) {                                                  \
-        constexpr int V = Vec<T>::N;                            \
-        if (c.np == 0) DC1D_COLS(V, 8, 0, 1024);                \
-        else if (c.nt == 256) DC1D_COLS(V, 8, 8, 256);          \
-        else if (c.tpr == 8) DC1D_COLS(V, 8, 8, 512);           \
-        else if (c.tpr == 4) DC1D_COLS(V, 4, 8, 512);           \
-        else DC1D_COLS(V, 2, 8, 512);                           \
-    } else {                                                    \
-        if (c.np == 0) DC1D_COLS(1, 32, 0, 1024);               \
-        else DC1D_COLS(1, 16, 16, 512);                         \
-    }
+// Every combination that choose_rows and choose_cols give.
+#define DC1D_ROWS_SWITCH(ODD)                                \
+    if (c.nv == 0 && c.wpr == 1) DC1D_ANY(1);                \
+    else if (c.nv == 0) DC1D_ANY(16);                        \
+    else if (c.wpr == 1 && c.nv == 1) DC1D_ROWS(1, 1, ODD);  \
+    else if (c.wpr == 1 && c.nv == 2) DC1D_ROWS(1, 2, ODD);  \
+    else if (c.wpr == 1) DC1D_ROWS(1, 4, ODD);               \
+    else if (c.wpr == 4 && c.nv == 2) DC1D_ROWS(4, 2, ODD);  \
+    else if (c.wpr == 4) DC1D_ROWS(4, 4, ODD);               \
+    else DC1D_ROWS(8, 4, ODD);
+#define DC1D_COLS_SWITCH(V, ODD)                             \
+    if (c.np == 0) DC1D_COLS(V, 8, 0, 1024, ODD);            \
+    else if (c.nt == 256) DC1D_COLS(V, 8, 8, 256, ODD);      \
+    else if (c.tpr == 8) DC1D_COLS(V, 8, 8, 512, ODD);       \
+    else if (c.tpr == 4) DC1D_COLS(V, 4, 8, 512, ODD);       \
+    else DC1D_COLS(V, 2, 8, 512, ODD);
 
 template <typename T>
 hipError_t forward_typed(const LayerNormArgs &a, hipStream_t st) {
-    const bool vec = vec_ok<T>(a, false);
+    const bool even = whole<T>(a, false);
     if (a.L == 1) {
-        const RowChoice c = choose_rows(a.C, Vec<T>::N, vec);
-        const dim3 blk(256);
-#define DC1D_ROWS(W, N) \
-    hipLaunchKernelGGL((k_ln_rows<T, W, N>), grid_of((a.B + 4 / W - 1) / (4 / W)), blk, 0, st, a)
-        if (c.wpr == 1 && c.nv == 1) DC1D_ROWS(1, 1);
-        else if (c.wpr == 1 && c.nv == 2) DC1D_ROWS(1, 2);
-        else if (c.wpr == 1) DC1D_ROWS(1, 4);
-        else if (c.wpr == 4 && c.nv == 2) DC1D_ROWS(4, 2);
-        else if (c.wpr == 4) DC1D_ROWS(4, 4);
-        else hipLaunchKernelGGL((k_ln_rows_any<T>), grid_of(a.B), blk, 0, st, a);
+        const RowChoice c = choose_rows(a.C, Vec<T>::N);
+#define DC1D_ROWS(W, N, O)                                                                                       \
+    hipLaunchKernelGGL((k_ln_rows<T, W, N, O>), grid_of(W < 4 ? (a.B + 3) / 4 : a.B), dim3(W > 4 ? 64 * W : 256), 0, \
+                       st, a)
+#define DC1D_ANY(W) hipLaunchKernelGGL((k_ln_rows_any<T, W>), grid_of(a.B), dim3(64 * W), 0, st, a)
+        if (even) {
+            DC1D_ROWS_SWITCH(false)
+        } else {
+            DC1D_ROWS_SWITCH(true)
+        }
 #undef DC1D_ROWS
+#undef DC1D_ANY
         return hipGetLastError();
     }
-    const ColChoice c = choose_cols(a.C, a.L, vec);
-#define DC1D_COLS(E, R, P, N)                                                                                       \
-    hipLaunchKernelGGL((k_ln_cols<T, E, R, P, N>), grid_of(a.B * ((a.L + R * E - 1) / (R * E))), dim3(N), 0, st, a)
-    DC1D_COLS_SWITCH
+    constexpr int V = Vec<T>::N;
+    const ColChoice c = choose_cols(a.C, a.L, V);
+#define DC1D_COLS(E, R, P, N, O)                                                                                     \
+    hipLaunchKernelGGL((k_ln_cols<T, E, R, P, N, O>), grid_of(a.B * ((a.L + R * E - 1) / (R * E))), dim3(N), 0, st, a)
+    if (a.L < V) {
+        if (c.np == 0) DC1D_COLS(1, 8, 0, 1024, false);
+        else DC1D_COLS(1, 8, 16, 512, false);
+    } else if (even) {
+        DC1D_COLS_SWITCH(V, false)
+    } else {
+        DC1D_COLS_SWITCH(V, true)
+    }
 #undef DC1D_COLS
     return hipGetLastError();
 }
@@ -786,30 +873,38 @@ hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
             hipLaunchKernelGGL((k_ln_params<T>), dim3((uint32_t)((2 * (int64_t)a.C + 15) / 16)), dim3(1024), 0, st, a, 0);
         return hipGetLastError();
     }
-    const bool vec = vec_ok<T>(a, true);
-    const int64_t most = backward_blocks(a.B, a.L, num_cus);
+    const bool even = whole<T>(a, true);
     uint32_t blocks;
     if (a.L == 1) {
-        const RowChoice c = choose_rows(a.C, Vec<T>::N, vec);
-        const int rpb = c.wpr == 1 ? 4 : 1;
-        const int64_t need = (a.B + rpb - 1) / rpb;
-        blocks = (uint32_t)(need < most ? need : most);
-        const dim3 blk(256);
-#define DC1D_ROWS(W, N) hipLaunchKernelGGL((k_ln_rows_bwd<T, W, N>), dim3(blocks), blk, 0, st, a)
-        if (c.wpr == 1 && c.nv == 1) DC1D_ROWS(1, 1);
-        else if (c.wpr == 1 && c.nv == 2) DC1D_ROWS(1, 2);
-        else if (c.wpr == 1) DC1D_ROWS(1, 4);
-        else if (c.wpr == 4 && c.nv == 2) DC1D_ROWS(4, 2);
-        else if (c.wpr == 4) DC1D_ROWS(4, 4);
-        else hipLaunchKernelGGL((k_ln_rows_bwd_any<T>), dim3(blocks), blk, 0, st, a);
+        const int64_t most = backward_blocks(a.B, a.L, num_cus);
+        const RowChoice c = choose_rows(a.C, Vec<T>::N);
+        const int64_t need = c.wpr == 1 && c.nv > 0 ? (a.B + 3) / 4 : a.B, fit = c.wpr > 4 ? (most + 1) / 2 : most;
+        blocks = (uint32_t)(need < fit ? need : fit);
+#define DC1D_ROWS(W, N, O) \
+    hipLaunchKernelGGL((k_ln_rows_bwd<T, W, N, O>), dim3(blocks), dim3(W > 4 ? 64 * W : 256), 0, st, a)
+#define DC1D_ANY(W) hipLaunchKernelGGL((k_ln_rows_bwd_any<T, W>), dim3(blocks), dim3(64 * W), 0, st, a)
+        if (even) {
+            DC1D_ROWS_SWITCH(false)
+        } else {
+            DC1D_ROWS_SWITCH(true)
+        }
 #undef DC1D_ROWS
+#undef DC1D_ANY
     } else {
-        const ColChoice c = choose_cols(a.C, a.L, vec);
-        const int TL = c.tpr * (vec ? Vec<T>::N : 1);
+        constexpr int V = Vec<T>::N;
+        const ColChoice c = choose_cols(a.C, a.L, V);
+        const int TL = c.tpr * (a.L < V ? 1 : V);
         const int64_t need = a.B * ((a.L + TL - 1) / TL), fit = (int64_t)num_cus * (c.nt < 512 ? 512 / c.nt : 1);
         blocks = (uint32_t)(need < fit ? need : fit);
-#define DC1D_COLS(E, R, P, N) hipLaunchKernelGGL((k_ln_cols_bwd<T, E, R, P, N>), dim3(blocks), dim3(N), 0, st, a)
-        DC1D_COLS_SWITCH
+#define DC1D_COLS(E, R, P, N, O) hipLaunchKernelGGL((k_ln_cols_bwd<T, E, R, P, N, O>), dim3(blocks), dim3(N), 0, st, a)
+        if (a.L < V) {
+            if (c.np == 0) DC1D_COLS(1, 8, 0, 1024, false);
+            else DC1D_COLS(1, 8, 16, 512, false);
+        } else if (even) {
+            DC1D_COLS_SWITCH(V, false)
+        } else {
+            DC1D_COLS_SWITCH(V, true)
+        }
 #undef DC1D_COLS
     }
     hipError_t e = hipGetLastError();

@@ -145,6 +145,54 @@ def test_layer_norm_in_place_and_unaligned():
             assert torch.equal(y, want)
 
 
+ODD_SHAPES = [
+    (9, 1), (6, 5), (5, 9), (7, 15), (3, 65), (6, 513), (5, 1022), (3, 2047), (3, 4099), (2, 8191), (2, 12345), (2, 16383), (2, 16391),
+    (3, 6, 2), (2, 9, 7), (2, 1030, 3), (2, 5, 9), (2, 64, 97), (1, 256, 131), (2, 300, 65), (1, 700, 71), (2, 1025, 19), (1, 2051, 37),
+    (1, 33, 4093), (3, 65, 641),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", ODD_SHAPES)
+def test_layer_norm_odd_sizes_between_neighbours(shape, dtype):
+    # inputs and results that start off every alignment, with other values right before and after
+    print("layer norm, odd", shape, dtype, flush=True)
+    n, C = math.prod(shape), shape[1]
+    side = (1, -1) + (1,) * (len(shape) - 2)
+
+    def amid(t):  # the same values one element off, NaN around them
+        store = torch.full((t.numel() + 32,), float("nan"), dtype=t.dtype, device=DEV)
+        store[17:17 + t.numel()] = t.reshape(-1)
+        return store[17:17 + t.numel()].view(t.shape), store
+
+    x, w, b, go = ln_inputs(shape, dtype, 11, 0.5)
+    (ox, sx), (ow, _), (ob, _), (og, _) = amid(x), amid(w), amid(b), amid(go)
+    wy, wm, wr = ref.layer_norm(x, w, b)
+    e = ln_bound(x, wm, wr)
+    bound = e * w.double().abs().view(side) + 4 * U32 * b.double().abs().view(side)
+    bound = bound + (ref.unit(dtype) if dtype == BF16 else 4 * U32) * wy.abs() * 1.01
+    y, mean, rstd = sequence.layer_norm(ox, ow, ob, with_stats=True)
+    within(y, wy, bound, "y")
+    within(mean, wm, 16 * U32 * x.double().abs().amax(1), "mean")
+    got = sequence.layer_norm_backward(ox, og, mean, rstd, ow)
+    want = ref.layer_norm_backward(x, go, w)
+    r = wr.unsqueeze(1)
+    xh = (x.double() - wm.unsqueeze(1)) * r
+    u = go.double() * w.double().view(side)
+    e = 16 * U32 * (1 + (x.double().abs().amax(1, keepdim=True) * r)) ** 2
+    ub, ux = u.abs().mean(1, keepdim=True), (u * xh).abs().mean(1, keepdim=True)
+    own = ref.unit(dtype) * 1.01
+    within(got["x"], want["x"], 4 * e * r * (u.abs() + ub + (xh.abs() + 1) * (ux + ub)) + own * want["x"].abs(), "grad_x")
+    rest = [0] + list(range(2, x.dim()))
+    s = (64 + math.sqrt(n // C)) * U32  # as above
+    within(got["weight"], want["weight"], (go.double().abs() * (e * (1 + xh.abs()) + s * xh.abs())).sum(rest) + own * want["weight"].abs(), "grad_weight")
+    within(got["bias"], want["bias"], s * go.double().abs().sum(rest) + own * want["bias"].abs(), "grad_bias")
+    # in place: the same bits, and nothing around them is touched
+    assert sequence.layer_norm(ox, ow, ob, out=ox) is ox
+    assert torch.equal(ox, y)
+    assert torch.isnan(sx[:17]).all() and torch.isnan(sx[17 + n:]).all()
+
+
 def test_layer_norm_channels_past_32_bit_offsets():
     # 1025 channels, two threads across a row: channel 255 of 2^22 + 8 float32 positions starts past 2^32 bytes
     C, L = 1025, (1 << 22) + 8
