@@ -81,18 +81,14 @@ __device__ __forceinline__ void store16(typename T::T *p, const float *f, int sk
     }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
-}
-
-// The sum over WPR waves that share a row (all of a workgroup's when WPR >
-// 1), the same value in every lane.  `slot` alternates between two arrays so
-// that one barrier per sum is enough.
-template <int WPR>
+// The sum over the LPR lanes that share a row (a part of a wave, or all of a
+// workgroup), the same value in every one.  `slot` alternates between two
+// arrays so that one barrier per sum is enough.
+template <int LPR>
 __device__ __forceinline__ float row_sum(float v, float *red, int slot) {
-    v = wave_sum(v);
+    constexpr int WPR = LPR / 64;
+#pragma unroll
+    for (int d = 1; d < (LPR < 64 ? LPR : 64); d <<= 1) v += __shfl_xor(v, d);
     if constexpr (WPR > 1) {
         if ((threadIdx.x & 63) == 0) red[slot * WPR + (threadIdx.x >> 6)] = v;
         __syncthreads();
@@ -105,21 +101,21 @@ __device__ __forceinline__ float row_sum(float v, float *red, int slot) {
 
 // ---- rows ----------------------------------------------------------------------
 //
-// WPR waves to a row and at least four to a workgroup; NV 16-byte pieces to a
-// lane (C <= WPR * 64 * NV * Vec::N).  Where C is no multiple of a piece, or
+// LPR lanes to a row, NV 16-byte pieces to a lane (C <= LPR * NV * Vec::N);
+// four waves a workgroup, or the row's.  Where C is no multiple of a piece, or
 // the rows are not aligned (ODD), the last piece is moved back to end with the
 // row (C >= Vec::N), and the elements that it shares with the one before it
 // are left to that one: 16 bytes a load at any address take what aligned ones
 // take, element by element a row of 1022 bf16 took four times as long.
-template <typename T, int WPR, int NV, bool ODD>
+template <typename T, int LPR, int NV, bool ODD>
 struct RowShape {
-    static constexpr int NT = WPR > 4 ? 64 * WPR : 256, RPB = NT / (64 * WPR);
+    static constexpr int NT = LPR > 256 ? LPR : 256, RPB = NT / LPR;
     int at[NV], skip[NV];  // where a piece is read, and how many of its elements are others' (Vec::N: it is not there)
     __device__ __forceinline__ RowShape(int lane, int C) {
         constexpr int N = Vec<T>::N;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * 64 * WPR + lane) * N;
+            const int c = (i * LPR + lane) * N;
             if constexpr (ODD) {
                 at[i] = min(c, C - N);
                 skip[i] = min(c - at[i], N);
@@ -132,16 +128,16 @@ struct RowShape {
     __device__ __forceinline__ bool own(int i, int e) const { return ODD ? e >= skip[i] : skip[i] == 0; }
 };
 
-template <typename T, int WPR, int NV, bool ODD>
-__global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows(LayerNormArgs a) {
+template <typename T, int LPR, int NV, bool ODD>
+__global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows(LayerNormArgs a) {
     using V = Vec<T>;
     using E = typename T::T;
-    using S = RowShape<T, WPR, NV, ODD>;
-    __shared__ float red[2 * WPR];
-    const int lane = threadIdx.x % (64 * WPR);
+    using S = RowShape<T, LPR, NV, ODD>;
+    __shared__ float red[LPR > 64 ? 2 * (LPR / 64) : 1];
+    const int lane = threadIdx.x % LPR;
     const S sh(lane, a.C);
     for (int64_t n0 = (int64_t)blockIdx.x * S::RPB; n0 < a.B; n0 += (int64_t)gridDim.x * S::RPB) {
-        const int64_t n = n0 + threadIdx.x / (64 * WPR);
+        const int64_t n = n0 + threadIdx.x / LPR;
         const bool on = n < a.B;
         const E *const x = (const E *)a.x + (on ? n : a.B - 1) * a.C;
         u32x4 raw[NV];
@@ -162,7 +158,7 @@ __global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows(Lay
             for (int e = 0; e < V::N; ++e)
                 if (sh.own(i, e)) s += f[i][e];
         }
-        const float mean = row_sum<WPR>(s, red, 0) * a.inv_c;
+        const float mean = row_sum<LPR>(s, red, 0) * a.inv_c;
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -172,7 +168,7 @@ __global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows(Lay
                 if (sh.own(i, e)) s += f[i][e] * f[i][e];
             }
         }
-        const float rstd = rsqrtf(row_sum<WPR>(s, red, 1) * a.inv_c + a.eps);
+        const float rstd = rsqrtf(row_sum<LPR>(s, red, 1) * a.inv_c + a.eps);
         if (!on) continue;
         E *const y = (E *)a.y + n * a.C;
 #pragma unroll
@@ -198,22 +194,21 @@ __global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows(Lay
 
 // Rows shorter than a piece (a wave a row) or longer than registers hold (16
 // waves): read once for each sum and once more, from cache where a row fits it.
-template <typename T, int WPR>
-__global__ __launch_bounds__(64 * WPR) void k_ln_rows_any(LayerNormArgs a) {
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void k_ln_rows_any(LayerNormArgs a) {
     using E = typename T::T;
-    constexpr int NT = 64 * WPR;
-    __shared__ float red[2 * WPR];
+        __shared__ float red[2 * (NT / 64)];
     for (int64_t n = blockIdx.x; n < a.B; n += gridDim.x) {
         const E *const x = (const E *)a.x + n * a.C;
         float s = 0.0f;
         for (int c = threadIdx.x; c < a.C; c += NT) s += T::ld(x, c);
-        const float mean = row_sum<WPR>(s, red, 0) * a.inv_c;
+        const float mean = row_sum<NT>(s, red, 0) * a.inv_c;
         s = 0.0f;
         for (int c = threadIdx.x; c < a.C; c += NT) {
             const float d = T::ld(x, c) - mean;
             s += d * d;
         }
-        const float rstd = rsqrtf(row_sum<WPR>(s, red, 1) * a.inv_c + a.eps);
+        const float rstd = rsqrtf(row_sum<NT>(s, red, 1) * a.inv_c + a.eps);
         E *const y = (E *)a.y + n * a.C;
         for (int c = threadIdx.x; c < a.C; c += NT) {
             float v = (T::ld(x, c) - mean) * rstd;
@@ -230,15 +225,15 @@ __global__ __launch_bounds__(64 * WPR) void k_ln_rows_any(LayerNormArgs a) {
 
 // Backward of rows.  Workgroups stride over the rows; a lane keeps its
 // channels' parameter gradients in registers until the end.
-template <typename T, int WPR, int NV, bool ODD>
-__global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows_bwd(LayerNormArgs a) {
+template <typename T, int LPR, int NV, bool ODD>
+__global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows_bwd(LayerNormArgs a) {
     using V = Vec<T>;
     using E = typename T::T;
-    using S = RowShape<T, WPR, NV, ODD>;
+    using S = RowShape<T, LPR, NV, ODD>;
     constexpr int RPB = S::RPB;
-    __shared__ float red[4 * WPR];
-    __shared__ float acc[RPB > 1 ? 64 * NV * V::N : 1];
-    const int lane = threadIdx.x % (64 * WPR), grp = threadIdx.x / (64 * WPR);
+    __shared__ float red[LPR > 64 ? 4 * (LPR / 64) : 1];
+    __shared__ float acc[RPB > 1 ? LPR * NV * V::N : 1];
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const bool params = a.gw || a.gb;
     const S sh(lane, a.C);
     float gw[NV][V::N] = {}, gb[NV][V::N] = {};
@@ -280,8 +275,8 @@ __global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows_bwd
             }
         }
         if (a.y) {
-            s1 = row_sum<WPR>(s1, red, slot) * a.inv_c;
-            s2 = row_sum<WPR>(s2, red, slot + 1) * a.inv_c;
+            s1 = row_sum<LPR>(s1, red, slot) * a.inv_c;
+            s2 = row_sum<LPR>(s2, red, slot + 1) * a.inv_c;
             slot ^= 2;
             if (n < a.B) {
                 E *const y = (E *)a.y + n * a.C;
@@ -296,28 +291,38 @@ __global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows_bwd
         }
     }
     if (!params) return;
-    // the workgroup's sums: its row groups in order
+    // the workgroup's sums: over the row groups of a wave, then the waves in order
+    constexpr int GROUPS = LPR < 64 ? 4 : RPB;
+    const int turn = LPR < 64 ? threadIdx.x / 64 : grp;
+    const bool first = LPR >= 64 || threadIdx.x % 64 < LPR;
     float *const pw = a.ws + (int64_t)blockIdx.x * 2 * a.C, *const pb = pw + a.C;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         float *const p = which ? pb : pw;
+        float v[NV][V::N];
 #pragma unroll
-        for (int k = 0; k < RPB; ++k) {
-            if constexpr (RPB > 1) __syncthreads();
-            if (grp == k) {
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
+            for (int e = 0; e < V::N; ++e) {
+                v[i][e] = which ? gb[i][e] : gw[i][e];
 #pragma unroll
-                    for (int e = 0; e < V::N; ++e) {
-                        float v = which ? gb[i][e] : gw[i][e];
-                        if constexpr (RPB > 1) {
-                            float &sum = acc[(i * 64 + lane) * V::N + e];
-                            if (k > 0) v += sum;
-                            if (k < RPB - 1) sum = v;
-                        }
-                        if (k == RPB - 1 && sh.own(i, e)) p[sh.at[i] + e] = v;
-                    }
+                for (int d = LPR; d < 64; d <<= 1) v[i][e] += __shfl_xor(v[i][e], d);
             }
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+            if constexpr (GROUPS > 1) __syncthreads();
+            if (turn != k || !first) continue;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < V::N; ++e) {
+                    if constexpr (GROUPS > 1) {
+                        float &sum = acc[(i * LPR + lane) * V::N + e];
+                        if (k > 0) v[i][e] += sum;
+                        if (k < GROUPS - 1) sum = v[i][e];
+                    }
+                    if (k == GROUPS - 1 && sh.own(i, e)) p[sh.at[i] + e] = v[i][e];
+                }
         }
     }
 }
@@ -325,11 +330,10 @@ __global__ __launch_bounds__((RowShape<T, WPR, NV, ODD>::NT)) void k_ln_rows_bwd
 // Backward of rows shorter than a piece or longer than registers hold: a
 // workgroup strides over the rows, its threads over the channels; the
 // parameter sums are kept in the workgroup's part of the workspace.
-template <typename T, int WPR>
-__global__ __launch_bounds__(64 * WPR) void k_ln_rows_bwd_any(LayerNormArgs a) {
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void k_ln_rows_bwd_any(LayerNormArgs a) {
     using E = typename T::T;
-    constexpr int NT = 64 * WPR;
-    __shared__ float red[4 * WPR];
+        __shared__ float red[4 * (NT / 64)];
     const bool params = a.gw || a.gb;
     float *const pw = params ? a.ws + (int64_t)blockIdx.x * 2 * a.C : nullptr, *const pb = pw + a.C;
     int slot = 0;
@@ -350,8 +354,8 @@ __global__ __launch_bounds__(64 * WPR) void k_ln_rows_bwd_any(LayerNormArgs a) {
         }
         fresh = false;
         if (!a.y) continue;
-        s1 = row_sum<WPR>(s1, red, slot) * a.inv_c;
-        s2 = row_sum<WPR>(s2, red, slot + 1) * a.inv_c;
+        s1 = row_sum<NT>(s1, red, slot) * a.inv_c;
+        s2 = row_sum<NT>(s2, red, slot + 1) * a.inv_c;
         slot ^= 2;
         E *const y = (E *)a.y + n * a.C;
         for (int c = threadIdx.x; c < a.C; c += NT) {
@@ -763,22 +767,26 @@ dim3 grid_of(int64_t blocks) { return dim3((uint32_t)(blocks < 1 << 20 ? blocks 
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// Which kernel serves the rows: pieces per lane and waves per row.  nv = 0:
+// Which kernel serves the rows: lanes per row and pieces per lane.  nv = 0:
 // from memory for each pass, as rows of less than a piece or of more than
-// eight waves hold are.
+// eight waves hold are.  Rows of few pieces share a wave: 131072 x 101 bf16
+// takes 50 us with a wave to a row and 15 with 16 lanes (gradients 69 and 25).
 struct RowChoice {
-    int wpr, nv;
+    int lpr, nv;
 };
 RowChoice choose_rows(int C, int per) {
-    if (C < per) return {1, 0};
-    const int lanes = ((C + per - 1) / per + 63) / 64;  // 16-byte pieces a lane of one wave
-    if (lanes <= 1) return {1, 1};
-    if (lanes <= 2) return {1, 2};
-    if (lanes <= 4) return {1, 4};
-    if (lanes <= 8) return {4, 2};
-    if (lanes <= 16) return {4, 4};
-    if (lanes <= 32) return {8, 4};
-    return {16, 0};
+    if (C < per) return {64, 0};
+    const int pieces = (C + per - 1) / per;
+    if (pieces <= 8) return {8, 1};
+    if (pieces <= 16) return {16, 1};
+    if (pieces <= 32) return {32, 1};
+    if (pieces <= 64) return {64, 1};
+    if (pieces <= 128) return {64, 2};
+    if (pieces <= 256) return {64, 4};
+    if (pieces <= 512) return {256, 2};
+    if (pieces <= 1024) return {256, 4};
+    if (pieces <= 2048) return {512, 4};
+    return {1024, 0};
 }
 
 // Which kernel serves channels first: threads across a row, channels held per
@@ -807,15 +815,18 @@ bool whole(const LayerNormArgs &a, bool backward) {
 }
 
 // Every combination that choose_rows and choose_cols give.
-#define DC1D_ROWS_SWITCH(ODD)                                \
-    if (c.nv == 0 && c.wpr == 1) DC1D_ANY(1);                \
-    else if (c.nv == 0) DC1D_ANY(16);                        \
-    else if (c.wpr == 1 && c.nv == 1) DC1D_ROWS(1, 1, ODD);  \
-    else if (c.wpr == 1 && c.nv == 2) DC1D_ROWS(1, 2, ODD);  \
-    else if (c.wpr == 1) DC1D_ROWS(1, 4, ODD);               \
-    else if (c.wpr == 4 && c.nv == 2) DC1D_ROWS(4, 2, ODD);  \
-    else if (c.wpr == 4) DC1D_ROWS(4, 4, ODD);               \
-    else DC1D_ROWS(8, 4, ODD);
+#define DC1D_ROWS_SWITCH(ODD)                                  \
+    if (c.nv == 0 && c.lpr == 64) DC1D_ANY(64);                \
+    else if (c.nv == 0) DC1D_ANY(1024);                        \
+    else if (c.lpr == 8) DC1D_ROWS(8, 1, ODD);                 \
+    else if (c.lpr == 16) DC1D_ROWS(16, 1, ODD);               \
+    else if (c.lpr == 32) DC1D_ROWS(32, 1, ODD);               \
+    else if (c.lpr == 64 && c.nv == 1) DC1D_ROWS(64, 1, ODD);  \
+    else if (c.lpr == 64 && c.nv == 2) DC1D_ROWS(64, 2, ODD);  \
+    else if (c.lpr == 64) DC1D_ROWS(64, 4, ODD);               \
+    else if (c.lpr == 256 && c.nv == 2) DC1D_ROWS(256, 2, ODD);\
+    else if (c.lpr == 256) DC1D_ROWS(256, 4, ODD);             \
+    else DC1D_ROWS(512, 4, ODD);
 #define DC1D_COLS_SWITCH(V, ODD)                             \
     if (c.np == 0) DC1D_COLS(V, 8, 0, 1024, ODD);            \
     else if (c.nt == 256) DC1D_COLS(V, 8, 8, 256, ODD);      \
@@ -828,10 +839,11 @@ hipError_t forward_typed(const LayerNormArgs &a, hipStream_t st) {
     const bool even = whole<T>(a, false);
     if (a.L == 1) {
         const RowChoice c = choose_rows(a.C, Vec<T>::N);
-#define DC1D_ROWS(W, N, O)                                                                                       \
-    hipLaunchKernelGGL((k_ln_rows<T, W, N, O>), grid_of(W < 4 ? (a.B + 3) / 4 : a.B), dim3(W > 4 ? 64 * W : 256), 0, \
-                       st, a)
-#define DC1D_ANY(W) hipLaunchKernelGGL((k_ln_rows_any<T, W>), grid_of(a.B), dim3(64 * W), 0, st, a)
+#define DC1D_ROWS(R, N, O)                                                                                       \
+    hipLaunchKernelGGL((k_ln_rows<T, R, N, O>),                                                                    \
+                       grid_of((a.B + RowShape<T, R, N, O>::RPB - 1) / RowShape<T, R, N, O>::RPB),                 \
+                       dim3((RowShape<T, R, N, O>::NT)), 0, st, a)
+#define DC1D_ANY(N) hipLaunchKernelGGL((k_ln_rows_any<T, N>), grid_of(a.B), dim3(N), 0, st, a)
         if (even) {
             DC1D_ROWS_SWITCH(false)
         } else {
@@ -878,11 +890,12 @@ hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
     if (a.L == 1) {
         const int64_t most = backward_blocks(a.B, a.L, num_cus);
         const RowChoice c = choose_rows(a.C, Vec<T>::N);
-        const int64_t need = c.wpr == 1 && c.nv > 0 ? (a.B + 3) / 4 : a.B, fit = c.wpr > 4 ? (most + 1) / 2 : most;
+        const int rpb = c.nv > 0 && c.lpr < 256 ? 256 / c.lpr : 1;
+        const int64_t need = (a.B + rpb - 1) / rpb, fit = c.lpr > 256 ? (most + 1) / 2 : most;
         blocks = (uint32_t)(need < fit ? need : fit);
-#define DC1D_ROWS(W, N, O) \
-    hipLaunchKernelGGL((k_ln_rows_bwd<T, W, N, O>), dim3(blocks), dim3(W > 4 ? 64 * W : 256), 0, st, a)
-#define DC1D_ANY(W) hipLaunchKernelGGL((k_ln_rows_bwd_any<T, W>), dim3(blocks), dim3(64 * W), 0, st, a)
+#define DC1D_ROWS(R, N, O) \
+    hipLaunchKernelGGL((k_ln_rows_bwd<T, R, N, O>), dim3(blocks), dim3((RowShape<T, R, N, O>::NT)), 0, st, a)
+#define DC1D_ANY(N) hipLaunchKernelGGL((k_ln_rows_bwd_any<T, N>), dim3(blocks), dim3(N), 0, st, a)
         if (even) {
             DC1D_ROWS_SWITCH(false)
         } else {

@@ -148,7 +148,7 @@ def test_layer_norm_in_place_and_unaligned():
 ODD_SHAPES = [
     (9, 1), (6, 5), (5, 9), (7, 15), (3, 65), (6, 513), (5, 1022), (3, 2047), (3, 4099), (2, 8191), (2, 12345), (2, 16383), (2, 16391),
     (3, 6, 2), (2, 9, 7), (2, 1030, 3), (2, 5, 9), (2, 64, 97), (1, 256, 131), (2, 300, 65), (1, 700, 71), (2, 1025, 19), (1, 2051, 37),
-    (1, 33, 4093), (3, 65, 641),
+    (1, 33, 4093), (3, 65, 641), (1, 33), (77, 40), (301, 101), (70, 200), (4099, 37),
 ]
 
 
