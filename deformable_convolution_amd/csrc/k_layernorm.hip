@@ -16,6 +16,7 @@
 // The parameter gradients are summed per workgroup over all the positions
 // that it visits, left in the workspace and added in workgroup order: no
 // atomics, the same bits every time.
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_tile.h"
@@ -107,6 +108,10 @@ __device__ __forceinline__ float row_sum(float v, float *red, int slot) {
 // row (C >= Vec::N), and the elements that it shares with the one before it
 // are left to that one: 16 bytes a load at any address take what aligned ones
 // take, element by element a row of 1022 bf16 took four times as long.
+template <typename T>
+constexpr int row_bwd_waves(int nv) {  // a SIMD: four floats of registers an element, and 16 bytes loaded for each tensor
+    return nv * Vec<T>::N > 16 ? 2 : nv > 2 ? 3 : 4;
+}
 template <typename T, int LPR, int NV, bool ODD>
 struct RowShape {
     static constexpr int NT = LPR > 256 ? LPR : 256, RPB = NT / LPR;
@@ -226,7 +231,7 @@ __global__ __launch_bounds__(NT) void k_ln_rows_any(LayerNormArgs a) {
 // Backward of rows.  Workgroups stride over the rows; a lane keeps its
 // channels' parameter gradients in registers until the end.
 template <typename T, int LPR, int NV, bool ODD>
-__global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows_bwd(LayerNormArgs a) {
+__global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT), row_bwd_waves<T>(NV)) void k_ln_rows_bwd(LayerNormArgs a) {
     using V = Vec<T>;
     using E = typename T::T;
     using S = RowShape<T, LPR, NV, ODD>;
@@ -237,7 +242,7 @@ __global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows_bwd
     const bool params = a.gw || a.gb;
     const S sh(lane, a.C);
     float gw[NV][V::N] = {}, gb[NV][V::N] = {};
-    u32x4 wr[NV];
+    u32x4 wr[NV] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (a.w) wr[i] = load16<ODD>((const E *)a.w + sh.at[i]);
@@ -258,6 +263,7 @@ __global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows_bwd
             V::widen(xr[i], xh[i]);
             V::widen(gr[i], u[i]);
             float w[V::N];
+            asm volatile("" : "+v"(wr[i]));  // stays packed between rows, in half the registers
             if (a.w) V::widen(wr[i], w);
 #pragma unroll
             for (int e = 0; e < V::N; ++e) {
@@ -888,10 +894,10 @@ hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
     const bool even = whole<T>(a, true);
     uint32_t blocks;
     if (a.L == 1) {
-        const int64_t most = backward_blocks(a.B, a.L, num_cus);
         const RowChoice c = choose_rows(a.C, Vec<T>::N);
-        const int rpb = c.nv > 0 && c.lpr < 256 ? 256 / c.lpr : 1;
-        const int64_t need = (a.B + rpb - 1) / rpb, fit = c.lpr > 256 ? (most + 1) / 2 : most;
+        const int rpb = c.nv > 0 && c.lpr < 256 ? 256 / c.lpr : 1, nt = c.nv > 0 && c.lpr < 256 ? 256 : c.lpr;
+        const int64_t fit = (int64_t)num_cus * std::min(4, (c.nv > 0 ? row_bwd_waves<T>(c.nv) : 8) * 256 / nt);
+        const int64_t need = (a.B + rpb - 1) / rpb;
         blocks = (uint32_t)(need < fit ? need : fit);
 #define DC1D_ROWS(R, N, O) \
     hipLaunchKernelGGL((k_ln_rows_bwd<T, R, N, O>), dim3(blocks), dim3((RowShape<T, R, N, O>::NT)), 0, st, a)
