@@ -145,7 +145,9 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, typename Tile<T>::Frag
 // ---- rows split among the waves ---------------------------------------------
 //
 // 128 rows a workgroup, 32 a wave; tiles of KT keys, double-buffered, the
-// next one on its way while this one is used.
+// next one on its way while this one is used.  8 x 4096 positions, 8 heads of
+// 64, bf16: 302 to 317 us (0.9 PFLOP/s), bound by the vector instructions of the
+// softmax (matrix unit 48% busy); 4 x 4096, 8 heads of 128: 263 us (1.05).
 template <typename T, int DP>
 struct RowsShape {
     static constexpr int KT = sizeof(typename T::T) == 2 ? 64 : 32;
@@ -240,7 +242,9 @@ __global__ __launch_bounds__(256, (RowsShape<T, DP>::blocks)) void k_attn_rows(A
 // of the workgroup's part of the keys, with no barrier between them, so the
 // keys and values stream.  The waves' results are joined through LDS; where
 // the keys are also split among workgroups (`splits`) each part leaves its
-// maximum, sum and unscaled o, and k_attn_join adds the parts in order.
+// maximum, sum and unscaled o, and k_attn_join adds the parts in order.  Single
+// positions are bound by HBM: 16 sequences of up to 16384 keys, 2 key heads of
+// 128, bf16: 39 us (4.5 TB/s).
 template <typename T, int DP>
 struct KeysShape {
     static constexpr int KT = 32;
@@ -383,7 +387,7 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
 
 // The parts of a row joined, a workgroup a row: every wave forms the parts'
 // weights (a lane a part), adds up every fourth part, and the waves' sums are
-// added in wave order.
+// added in wave order.  The same 16 sequences: 5 us, mostly latency.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     using E = typename T::T;

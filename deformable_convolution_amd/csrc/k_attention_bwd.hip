@@ -22,7 +22,8 @@ namespace dc1d {
 
 namespace {
 
-// delta[b][hk][row], eight threads a row.
+// delta[b][hk][row], eight threads a row.  Bound by HBM: 4 x 4096 positions, 8
+// heads of 128, bf16: 12.6 us (5.3 TB/s).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a) {
     using E = typename T::T;
@@ -294,7 +295,8 @@ __device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, uin
     if (a.gv) drain<DP>(ws, dv, 1.0f, lane, put(a.gv, a.gvs));
 }
 
-// The parts of dK and dV added in order: a thread four elements.
+// The parts of dK and dV added in order: a thread four elements.  Bound by HBM:
+// two parts of 4 x 4096 positions, 2 key heads of 128: 14.5 us (5.8 TB/s).
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(256) void k_attn_bwd_sum(AttnArgs a) {
     using E = typename T::T;
@@ -421,6 +423,9 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, u
 // GPU where each alone would leave part of it idle (16 x 128 positions, 8
 // heads of 64, fp32: 128 workgroups each on 256 CUs, 49 us one after the
 // other and 28 at once), and the shorter one fills the longer one's end.
+// Causal, 4 x 4096 positions, 8 heads over 2 of 128, bf16: 502 to 524 us with
+// the two kernels beside it, the matrix unit 50% busy: two waves a SIMD, each
+// waiting for its own chain from the scores to the gradients.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks < QShape<T, DP>::blocks ? KvShape<T, DP>::blocks : QShape<T, DP>::blocks))
 void k_attn_bwd(AttnArgs a, uint32_t kv_blocks, int keys_first) {

@@ -108,6 +108,8 @@ __device__ __forceinline__ float row_sum(float v, float *red, int slot) {
 // row (C >= Vec::N), and the elements that it shares with the one before it
 // are left to that one: 16 bytes a load at any address take what aligned ones
 // take, element by element a row of 1022 bf16 took four times as long.
+// 32768 x 1024 bf16: 22 us (6.0 TB/s); x 1022: 25 us; 131072 x 101 fp32: 18 us
+// (5.8 TB/s); 4096 x 16384 bf16: 68 us (3.9 TB/s).
 template <typename T>
 constexpr int row_bwd_waves(int nv) {  // a SIMD: four floats of registers an element, and 16 bytes loaded for each tensor
     return nv * Vec<T>::N > 16 ? 2 : nv > 2 ? 3 : 4;
@@ -199,6 +201,7 @@ __global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows(Lay
 
 // Rows shorter than a piece (a wave a row) or longer than registers hold (16
 // waves): read once for each sum and once more, from cache where a row fits it.
+// 4096 x 32768 fp32: 495 us (2.2 TB/s), gradients 998 us.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void k_ln_rows_any(LayerNormArgs a) {
     using E = typename T::T;
@@ -229,7 +232,8 @@ __global__ __launch_bounds__(NT) void k_ln_rows_any(LayerNormArgs a) {
 }
 
 // Backward of rows.  Workgroups stride over the rows; a lane keeps its
-// channels' parameter gradients in registers until the end.
+// channels' parameter gradients in registers until the end.  32768 x 1024 bf16:
+// 42 us with the parameters' sums (4.7 TB/s); x 1022: 47 us.
 template <typename T, int LPR, int NV, bool ODD>
 __global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT), row_bwd_waves<T>(NV)) void k_ln_rows_bwd(LayerNormArgs a) {
     using V = Vec<T>;
@@ -382,7 +386,9 @@ __global__ __launch_bounds__(NT) void k_ln_rows_bwd_any(LayerNormArgs a) {
 // thread then reads of positions before its own it neither adds nor stores.  TPR threads stand across a tile's row:
 // 8 (whole 128-byte lines), fewer where C channels would not fit otherwise.
 // Neighbouring tiles go to one XCD: where rows are not whole lines they share
-// the lines at their edges.
+// the lines at their edges.  8 x 256 x 16384 bf16: 31 us (4.4 TB/s), x 16383:
+// 32 us; 16 x 512 x 4092 fp32: 64 us (4.2 TB/s); with NP = 0, 4 x 4096 x 1024
+// fp32: 50 us (2.7 TB/s).
 template <int EPT, int TPR_, int NT>
 struct ColShape {
     static constexpr int TPR = TPR_, TL = TPR * EPT, RP = NT / TPR;
@@ -596,6 +602,8 @@ __global__ __launch_bounds__(NT, 1024 / NT) void k_ln_cols(LayerNormArgs a) {
 // the one before it is worked on.  With the channels in registers (NP > 0) so
 // are their parameter sums; otherwise they are kept in the workgroup's part
 // of the workspace, a thread row (TPR neighbouring lanes) owning its channels.
+// 16 x 512 x 4092 fp32: 95 us (4.2 TB/s), x 4091: 99 us; 8 x 256 x 16384 bf16:
+// 54 us (3.7 TB/s); with NP = 0, 4 x 4096 x 1024 fp32: 110 us.
 template <typename T, int EPT, int TPR, int NP, int NT, bool ODD>
 __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(LayerNormArgs a) {
     using E = typename T::T;
@@ -742,7 +750,7 @@ __global__ __launch_bounds__(NT, (NT < 512 ? 512 / NT : 1)) void k_ln_cols_bwd(L
 
 // gw, gb: the workgroups' parts [parts][2][C] in order.  16 channels by 64
 // runs of the parts a workgroup, so that few loads follow one another; the
-// runs are added in order.
+// runs are added in order.  1024 parts of 1024 channels: 4.9 us.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_ln_params(LayerNormArgs a, int parts) {
     using E = typename T::T;
