@@ -474,11 +474,16 @@ AttnBwdPlan plan_attention_backward(const AttnArgs &a, int num_cus) {
     // out (two to a CU; 4 x 4096 positions, 2 key heads: 1012 us unsplit, 498 in
     // two parts, 510 in four), none with fewer than 512 rows: the parts' sums cost
     // more than they save where the query workgroups already share the GPU (4 x
-    // 512 positions, 8 heads of 64, fp32: 86 us whole, 97 in four parts).  Only
-    // where hardly any CU has a workgroup are parts of 128 rows better (2 x 256
-    // positions, 2 key heads of 128: 37 and 26 us).
+    // 512 positions, 8 heads of 64, fp32: 86 us whole, 97 in four parts).  Parts
+    // of 256 or 128 rows only while every workgroup, those of the queries too,
+    // still has a CU to itself (8 heads over 2 of 128: 2 x 256 positions, bf16,
+    // 37 and 26 us; 13 x 136, 4 over 1, fp32, 99 and 57 us).
     int64_t splits = blocks > 0 ? (2 * (int64_t)num_cus + blocks - 1) / blocks : 1;
-    const int64_t least = 16 * blocks <= num_cus ? 128 : 512, most = (a.rows + least - 1) / least;
+    const int64_t q_blocks = heads * ((a.rows + 127) / 128);
+    int64_t least = 512;
+    for (int64_t rows = 256; rows >= 128; rows /= 2)
+        if (blocks * ((a.rows + rows - 1) / rows) + q_blocks <= num_cus) least = rows;
+    const int64_t most = (a.rows + least - 1) / least;
     splits = splits > most ? most : splits;
     pl.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
     pl.delta_bytes = ((size_t)heads * a.rows * sizeof(float) + 255) / 256 * 256;

@@ -422,6 +422,30 @@ def test_attention_backward(case, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,mask", [
+    ((3, 136, 136, 4, 1, 128), dict(causal=True, kv_lens=(34, 0, 136))),
+    ((2, 300, 90, 4, 1, 64), dict(window=70, kv_lens=(90, 17))),
+    ((1, 129, 200, 2, 1, 32), dict(causal=True)),
+    ((2, 513, 33, 1, 1, 80), dict()),
+    ((1, 97, 260, 8, 2, 64), dict(causal=True, window=40)),
+])
+def test_attention_gradients_in_short_parts(shape, mask, dtype):
+    """Few workgroups: the rows of a key tile in parts of 128 or 256, some of them with nothing to do."""
+    print("attention gradients in parts", shape, mask, dtype, flush=True)
+    mask = dict(mask)
+    if "kv_lens" in mask:
+        mask["kv_lens"] = torch.tensor(mask["kv_lens"], dtype=torch.int32, device=DEV)
+    q, k, v, g = att_inputs(29, *shape, dtype)
+    out, lse = sequence.attention(q, k, v, with_lse=True, **mask)
+    got = sequence.attention_backward(q, k, v, out, lse, g, **mask)
+    want, bound = ref.attention_backward(q, k, v, g, storage=dtype, **ref_mask(mask, shape[2]))
+    for key in "qkv":
+        within(got[key], want[key], bound[key] * 1.01 + 1e-30, "grad_" + key)
+    again = sequence.attention_backward(q, k, v, out, lse, g, **mask)
+    assert all(torch.equal(again[key], got[key]) for key in "qkv")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attention_larger(dtype):
     """Several tiles of keys and rows per workgroup, and split gradients."""
     for shape, mask in (((2, 700, 1500, 4, 1, 128), dict(causal=True)), ((1, 1024, 1024, 8, 2, 64), dict(causal=True, window=300))):
