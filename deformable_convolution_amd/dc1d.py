@@ -189,9 +189,15 @@ def _device_ctx(device):
 def _workspace(nbytes: int, device):
     """A cached workspace per (device, stream), grown as needed (the library
     needs no initialisation of it; calls on one stream are ordered, so they
-    can share it)."""
+    can share it).  A call that is being captured into a graph gets memory of
+    the graph's own instead: the graph writes there at every replay, on
+    whatever stream, and holds no reference that would keep a cached
+    workspace from being replaced."""
     if nbytes == 0:
         return None
+    with _device_ctx(device):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
     stream = torch.cuda.current_stream(device)
     key = (device.index, stream.cuda_stream)
     buf = _ws_cache.get(key)
