@@ -222,7 +222,8 @@ int attn_shape(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided 
     if (B >= kLim31 || Hq >= kLim31 || Lq > kLen || Lk > kLen) return DC1D_ERR_BAD_SHAPE;
     const int64_t G = Hq / Hkv;
     if (Lq * G >= kLim31) return DC1D_ERR_BAD_SHAPE;
-    // keeps every launch below 2^24 workgroups of 256 threads
+    // keeps every kind of workgroup's number far inside 32 bits; the forward's
+    // are fewer than 2^24 of 256 threads, which one launch holds
     const int64_t heads = B > 0 && Hkv > kMaxElems / B ? kMaxElems : B * Hkv;
     if (heads >= (1 << 24) || heads * (Lq * G) >= kLen || heads * Lk >= kLim31) return DC1D_ERR_BAD_SHAPE;
     memset(a, 0, sizeof(*a));

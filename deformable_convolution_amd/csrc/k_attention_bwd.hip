@@ -25,10 +25,10 @@ namespace {
 // delta[b][hk][row], eight threads a row.  Bound by HBM: 4 x 4096 positions, 8
 // heads of 128, bf16: 12.6 us (5.3 TB/s).
 template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a) {
+__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, uint32_t first) {
     using E = typename T::T;
     constexpr int CH = Tile<T>::CH;
-    const int64_t n = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    const int64_t n = (int64_t)(first + blockIdx.x) * 32 + (threadIdx.x >> 3);
     const int part = threadIdx.x & 7;
     const int64_t all = (int64_t)a.B * a.Hkv * a.rows, m = n < all ? n : all - 1;
     const uint32_t bh = (uint32_t)m / (uint32_t)a.rows, r = (uint32_t)m - bh * (uint32_t)a.rows;
@@ -428,16 +428,25 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, u
 // waiting for its own chain from the scores to the gradients.
 template <typename T, int DP, bool VEC>
 __global__ __launch_bounds__(256, (KvShape<T, DP>::blocks < QShape<T, DP>::blocks ? KvShape<T, DP>::blocks : QShape<T, DP>::blocks))
-void k_attn_bwd(AttnArgs a, uint32_t kv_blocks, int keys_first) {
+void k_attn_bwd(AttnArgs a, uint32_t kv_blocks, uint32_t q_blocks, uint32_t first, int keys_first) {
     extern __shared__ __align__(512) char smem[];
-    const uint32_t q_blocks = gridDim.x - kv_blocks, kv0 = keys_first ? 0 : q_blocks, q0 = keys_first ? kv_blocks : 0;
-    if (blockIdx.x - kv0 < kv_blocks)
-        key_gradients<T, DP, VEC>(a, smem, blockIdx.x - kv0, kv_blocks);
+    const uint32_t id = first + blockIdx.x, kv0 = keys_first ? 0 : q_blocks, q0 = keys_first ? kv_blocks : 0;
+    if (id - kv0 < kv_blocks)
+        key_gradients<T, DP, VEC>(a, smem, id - kv0, kv_blocks);
     else
-        query_gradients<T, DP, VEC>(a, smem, blockIdx.x - q0, q_blocks);
+        query_gradients<T, DP, VEC>(a, smem, id - q0, q_blocks);
 }
 
 int padded(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+
+// A launch holds fewer than 2^32 threads; within the documented sizes the
+// key and query workgroups are up to three times that.
+template <typename Launch>
+void in_parts(int64_t blocks, Launch launch) {
+    constexpr int64_t most = 1 << 23;  // a multiple of the XCDs, which xcd_order() counts on
+    for (int64_t first = 0; first < blocks; first += most)
+        launch((uint32_t)first, dim3((uint32_t)(blocks - first < most ? blocks - first : most)));
+}
 
 template <typename T, int DP, bool VEC>
 hipError_t launch(const AttnArgs &a, hipStream_t stream) {
@@ -446,11 +455,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t stream) {
     const int64_t kv_blocks = a.gk || a.gv ? heads * ((a.Lk + 127) / 128) * a.splits : 0;
     const int64_t q_blocks = a.gq ? heads * ((a.rows + 127) / 128) : 0;
     if (kv_blocks + q_blocks == 0) return hipSuccess;
-    if (a.rows > 0)
-        hipLaunchKernelGGL((k_attn_delta<T, VEC>), dim3((uint32_t)((heads * a.rows + 31) / 32)), dim3(256), 0, stream, a);
-    hipLaunchKernelGGL((k_attn_bwd<T, DP, VEC>), dim3((uint32_t)(kv_blocks + q_blocks)), dim3(256),
-                       q_lds > kv_lds ? q_lds : kv_lds, stream, a, (uint32_t)kv_blocks,
-                       (int)(4 * (a.rows / a.splits) >= 3 * (int64_t)a.Lk));  // the longer workgroups: 4 and 3 products a tile
+    in_parts((heads * a.rows + 31) / 32, [&](uint32_t first, dim3 grid) {
+        hipLaunchKernelGGL((k_attn_delta<T, VEC>), grid, dim3(256), 0, stream, a, first);
+    });
+    const int keys_first = 4 * (a.rows / a.splits) >= 3 * (int64_t)a.Lk;  // the longer workgroups: 4 and 3 products a tile
+    in_parts(kv_blocks + q_blocks, [&](uint32_t first, dim3 grid) {
+        hipLaunchKernelGGL((k_attn_bwd<T, DP, VEC>), grid, dim3(256), q_lds > kv_lds ? q_lds : kv_lds, stream, a, (uint32_t)kv_blocks,
+                           (uint32_t)q_blocks, first, keys_first);
+    });
     if (kv_blocks > 0 && a.splits > 1)
         hipLaunchKernelGGL((k_attn_bwd_sum<T, DP, VEC>), dim3((uint32_t)((2 * heads * a.Lk * (DP / 4) + 255) / 256)),
                            dim3(256), 0, stream, a);
