@@ -108,6 +108,8 @@ struct Workspace {
             if (!THPVariable_Check(given)) throw torch::TypeError("workspace must be a tensor");
             t = THPVariable_Unpack(given);
             if (!t.is_cuda() || t.get_device() != device) refuse("the workspace must be on the tensors' device");
+            // a view's elements need not be as many bytes of memory (expand), nor the view's alone (a step)
+            if (!t.is_contiguous()) refuse("the workspace must be contiguous");
         } else if (need > 0) {
             PyObject *o = PyObject_CallFunction(get, "ni", (Py_ssize_t)need, device);
             if (!o) return false;
