@@ -192,8 +192,9 @@ __device__ __forceinline__ RowAt row_at(const AttnArgs &a, int64_t n) {
 }
 
 // A tile of ROWS rows of DP elements brought into LDS by NT threads (whole
-// waves).  Rows at and past `limit` and elements at and past D become zero,
-// whatever memory holds there.
+// waves).  Rows ahead of `from`, rows at and past `limit` and elements at and
+// past D become zero, whatever memory holds there: what no row of the other
+// operand sees meets probability 0 in a product, where a NaN would not vanish.
 //
 // Aligned rows (VEC) go from memory to LDS without passing through registers:
 // a load of the wave writes 64 consecutive pieces of LDS, each lane's from an
@@ -246,9 +247,9 @@ struct Stage {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, off, 0, 0, 0);
     }
     // pieces whose rows are `step` elements apart from base on
-    __device__ __forceinline__ void fetch(E *lds, const E *base, int64_t step, int limit, int D, int t) const {
+    __device__ __forceinline__ void fetch(E *lds, const E *base, int64_t step, int from, int limit, int D, int t) const {
         E *const to = lds + __builtin_amdgcn_readfirstlane(t >> 6) * 64 * CH;
-        if (limit >= ROWS && D == DP) {
+        if (from <= 0 && limit >= ROWS && D == DP) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 to_lds(base + i * step, rows_at + (col ^ col_flip(i)) * (uint32_t)sizeof(E), to + i * NT * CH);
@@ -256,21 +257,22 @@ struct Stage {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = col ^ col_flip(i);
-                const bool in = (int)row + i * STEP < limit && c < D;
+                const int r = (int)row + i * STEP;
+                const bool in = r >= from && r < limit && c < D;
                 to_lds(base + i * step, in ? rows_at + c * (uint32_t)sizeof(E) : kOut, to + i * NT * CH);
             }
         }
     }
 
     // base: the tile's row 0, `limit` (at least 1) rows may be read
-    __device__ __forceinline__ void load(E *lds, const E *base, int64_t stride, int limit, int D, int t) const {
+    __device__ __forceinline__ void load(E *lds, const E *base, int64_t stride, int from, int limit, int D, int t) const {
         if (PART && t >= ROWS * PER) return;  // whole waves
-        if (VEC && near) return fetch(lds, base, STEP * stride, limit, D, t);
+        if (VEC && near) return fetch(lds, base, STEP * stride, from, limit, D, t);
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
             const int r = row + i * STEP, c = col ^ (mix<PER>(i * STEP) * CH);
             u32x4 v = load_piece<T, VEC>(base + (int64_t)min(r, limit - 1) * stride, c, D);
-            if (r >= limit || (VEC && c >= D)) v = u32x4{0, 0, 0, 0};
+            if (r < from || r >= limit || (VEC && c >= D)) v = u32x4{0, 0, 0, 0};
             *(u32x4 *)(lds + (t + i * NT) * CH) = v;
         }
     }
@@ -280,7 +282,7 @@ struct Stage {
                                               int limit, int t) const {
         if (PART && t >= ROWS * PER) return;
         if (VEC && near)
-            return fetch(lds, base + (int64_t)fdiv((uint32_t)row0, a.by_G) * st.l, (int64_t)fdiv(STEP, a.by_G) * st.l, limit,
+            return fetch(lds, base + (int64_t)fdiv((uint32_t)row0, a.by_G) * st.l, (int64_t)fdiv(STEP, a.by_G) * st.l, 0, limit,
                          a.D, t);
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {

@@ -194,8 +194,8 @@ __global__ __launch_bounds__(256, (RowsShape<T, DP>::blocks)) void k_attn_rows(A
     vs.init(a.vs.l, t);
     ks.near = vs.near = ks.near && vs.near;
     auto load = [&](int at, int k0) {
-        ks.load(kbuf + at * S::tile, kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
-        vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
+        ks.load(kbuf + at * S::tile, kp + k0 * a.ks.l, a.ks.l, lo - k0, hi - k0, a.D, t);
+        vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, lo - k0, hi - k0, a.D, t);
     };
     int k0 = lo / KT * KT;
     // one tile: the buffer it stands in is a constant, so that every read's
@@ -297,8 +297,12 @@ __global__ __launch_bounds__(256, (KeysShape<T, DP>::lds > 80 << 10 ? 1 : 2)) vo
     ks.init(a.ks.l, lane);
     vs.init(a.vs.l, lane);
     ks.near = vs.near = ks.near && vs.near;
-    auto load_k = [&](int n) { ks.load(kbuf, kp + (int64_t)n * KT * a.ks.l, a.ks.l, final.hi - n * KT, a.D, lane); };
-    auto load_v = [&](int n) { vs.load(vbuf, vp + (int64_t)n * KT * a.vs.l, a.vs.l, final.hi - n * KT, a.D, lane); };
+    auto load_k = [&](int n) {
+        ks.load(kbuf, kp + (int64_t)n * KT * a.ks.l, a.ks.l, first.lo - n * KT, final.hi - n * KT, a.D, lane);
+    };
+    auto load_v = [&](int n) {
+        vs.load(vbuf, vp + (int64_t)n * KT * a.vs.l, a.vs.l, first.lo - n * KT, final.hi - n * KT, a.D, lane);
+    };
     constexpr int LOADS = decltype(ks)::N;  // of one tile, in flight where the rows are near
     int n = s0 + wave;
     if (n < s1) {

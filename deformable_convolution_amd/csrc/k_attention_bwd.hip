@@ -370,8 +370,8 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, u
     vs.init(a.vs.l, t);
     ks.near = vs.near = ks.near && vs.near;
     auto load = [&](int at, int k0) {
-        ks.load(kbuf + at * S::tile, kp + k0 * a.ks.l, a.ks.l, hi - k0, a.D, t);
-        vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, hi - k0, a.D, t);
+        ks.load(kbuf + at * S::tile, kp + k0 * a.ks.l, a.ks.l, lo - k0, hi - k0, a.D, t);
+        vs.load(vbuf + at * S::tile, vp + k0 * a.vs.l, a.vs.l, lo - k0, hi - k0, a.D, t);
     };
     int k0 = lo / KT * KT;
     if (k0 < hi) load(0, k0);

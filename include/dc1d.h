@@ -541,9 +541,10 @@ int dc1d_rotary(const dc1d_strided *q, const dc1d_strided *k_or_null, const dc1d
  *   s_ij = scale * q[b,i,h] . k[b,j,h'],   lse = log sum_j exp s_ij,
  *
  * h' = h / (Hq / Hkv): neighbouring query heads share a key head.  A query
- * that sees no key gives out 0 and lse -infinity.  Keys and values at and
- * past kv_lens[b] are never used, whatever they hold; those before it should
- * be finite even where causal or window hide them.
+ * that sees no key gives out 0 and lse -infinity.  Keys and values that no
+ * query of the batch sees (at and past kv_lens[b], past the last query where
+ * causal, ahead of the first one's window) are never used, whatever they hold;
+ * those that one query sees should be finite for the sake of the others, too.
  *
  *   q, out    [B, Lq, Hq, D], k, v [B, Lk, Hkv, D], Hkv dividing Hq, D <= 128
  *   kv_lens   [B] int32, clamped to [0, Lk], or NULL (Lk)
