@@ -279,17 +279,17 @@ struct Stage {
     // The rows from row0 (a multiple of ROWS) on of a key head's queries; base: its
     // first query head, position 0
     __device__ __forceinline__ void load_rows(E *lds, const E *base, const AttnArgs &a, const Strides3 &st, int64_t row0,
-                                              int limit, int t) const {
+                                              int from, int limit, int t) const {
         if (PART && t >= ROWS * PER) return;
         if (VEC && near)
-            return fetch(lds, base + (int64_t)fdiv((uint32_t)row0, a.by_G) * st.l, (int64_t)fdiv(STEP, a.by_G) * st.l, 0, limit,
-                         a.D, t);
+            return fetch(lds, base + (int64_t)fdiv((uint32_t)row0, a.by_G) * st.l, (int64_t)fdiv(STEP, a.by_G) * st.l, from,
+                         limit, a.D, t);
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
             const int r = row + i * STEP, c = col ^ (mix<PER>(i * STEP) * CH);
             const RowAt at = row_at(a, row0 + min(r, limit - 1));
             u32x4 v = load_piece<T, VEC>(base + at.pos * st.l + at.head * st.h, c, a.D);
-            if (r >= limit || (VEC && c >= a.D)) v = u32x4{0, 0, 0, 0};
+            if (r < from || r >= limit || (VEC && c >= a.D)) v = u32x4{0, 0, 0, 0};
             *(u32x4 *)(lds + (t + i * NT) * CH) = v;
         }
     }

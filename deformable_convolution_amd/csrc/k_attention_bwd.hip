@@ -190,9 +190,10 @@ __device__ __forceinline__ void key_gradients(const AttnArgs &a, char *smem, uin
             lse = lp[(int64_t)row_at(a, n).head * a.Lq + row_at(a, n).pos];
             del = dp[n];
         }
-        const int limit = (int)min(r1 - r, (int64_t)RT);
-        qs.load_rows(qbuf + at * S::tile, qp, a, a.qs, r, limit, t);
-        gs.load_rows(gbuf + at * S::tile, gp, a, a.gs, r, limit, t);
+        // rows ahead of i0 see none of the keys (some see none at all, and hold anything)
+        const int skip = (int)((int64_t)i0 * a.G - r), limit = (int)min(r1 - r, (int64_t)RT);
+        qs.load_rows(qbuf + at * S::tile, qp, a, a.qs, r, skip, limit, t);
+        gs.load_rows(gbuf + at * S::tile, gp, a, a.gs, r, skip, limit, t);
     };
     auto store = [&](int64_t r, int at) {
         const int limit = (int)min(r1 - r, (int64_t)RT);

@@ -582,11 +582,12 @@ int dc1d_attention_plan(const dc1d_strided *q, const dc1d_strided *k, const dc1d
  *   grad_q = scale * dS k,  grad_k = scale * dS^T q,  grad_v = P^T grad_out,
  *
  * grad_k and grad_v summed over the query heads that share a key head.
- * Keys that no query sees get zeros.  NULL gradients are not computed.  The
- * other arguments are the forward's; gradients must not overlap the inputs or
- * each other unless as disjoint head slices of one buffer.  workspace: at
- * least dc1d_attention_backward_workspace_bytes() bytes, 256-byte aligned,
- * when that is not 0.
+ * Keys that no query sees get zeros, and so do queries that see no key; what
+ * those hold, and their grad_out, reaches no gradient.  NULL gradients are not
+ * computed.  The other arguments are the forward's; gradients must not overlap
+ * the inputs or each other unless as disjoint head slices of one buffer.
+ * workspace: at least dc1d_attention_backward_workspace_bytes() bytes, 256-byte
+ * aligned, when that is not 0.
  */
 int dc1d_attention_backward_workspace_bytes(const dc1d_strided *q, const dc1d_strided *k, const dc1d_strided *v,
                                             size_t *bytes_out);

@@ -67,3 +67,35 @@ def test_keys_that_no_query_sees(case, dtype, spread):
         assert torch.equal(o2, out) and torch.equal(l2, lse), junk
         assert all(torch.equal(g2[n], grads[n]) for n in "qkv"), junk
     assert not grads["k"][unseen].any() and not grads["v"][unseen].any()
+
+
+# B, Lq, Lk, Hq, Hkv, D, mask
+QUERIES = [
+    (2, 65, 63, 4, 2, 64, dict(causal=True)),
+    (2, 90, 40, 6, 2, 128, dict(causal=True)),
+    (1, 300, 170, 5, 1, 64, dict(causal=True)),
+    (3, 50, 70, 2, 1, 20, dict(kv_lens=(70, 0, 13), causal=True, q_start=(-20, 20, -37))),
+    (2, 45, 60, 4, 1, 80, dict(window=9, q_start=(-30, 45))),
+    (2, 45, 60, 4, 1, 33, dict(window=9, causal=True, q_start=(-30, 45))),
+    (32, 65, 40, 8, 8, 64, dict(causal=True)),
+    (4, 520, 500, 2, 2, 32, dict(causal=True)),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", QUERIES, ids=lambda c: "-".join(str(v) for v in c[:6]) + "-" + "-".join(c[6]))
+def test_queries_that_see_nothing(case, dtype):
+    """Padding: their results are 0, and what q and grad_out hold there reaches no gradient."""
+    print("queries that see nothing", case, dtype, flush=True)
+    mask = mask_of(case[6])
+    q, k, v, g = att_inputs(62, *case[:6], dtype)
+    blind = ~ref.visible(case[0], case[1], case[2], device=DEV, **mask).any(2)
+    assert blind.any() and not blind.all()
+    out, lse, grads = gradients(q, k, v, g, mask)
+    for junk in junk_of(dtype):
+        qj, gj = q.clone(), g.clone()
+        qj[blind], gj[blind] = junk, junk
+        o2, l2, g2 = gradients(qj, k, v, gj, mask)
+        assert torch.equal(o2, out) and torch.equal(l2, lse), junk
+        assert all(torch.equal(g2[n], grads[n]) for n in "qkv"), junk
+    assert not out[blind].any() and not grads["q"][blind].any()
