@@ -883,13 +883,24 @@ hipError_t forward_typed(const LayerNormArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// The most workgroups (parts of the parameter gradients) of a backward call:
-// those that fit the GPU at once.
-int64_t backward_blocks(int64_t B, int64_t L, int num_cus) {
-    // no more than the smallest unit that any of the kernels takes at a time: a row, or 8 positions
-    const int64_t units = L == 1 ? B : B * ((L + 7) / 8);
-    const int64_t most = (int64_t)num_cus * (L == 1 ? 4 : 2);
-    return units < most ? units : most;
+// Workgroups of a backward call, and so parts of the parameter gradients: no
+// more than fit the GPU at once.
+template <typename T>
+uint32_t backward_blocks(int64_t B, int C, int64_t L, int num_cus) {
+    int64_t need, fit;
+    if (L == 1) {
+        const RowChoice c = choose_rows(C, Vec<T>::N);
+        const int rpb = c.nv > 0 && c.lpr < 256 ? 256 / c.lpr : 1, nt = c.nv > 0 && c.lpr < 256 ? 256 : c.lpr;
+        need = (B + rpb - 1) / rpb;
+        fit = (int64_t)num_cus * std::min(4, (c.nv > 0 ? row_bwd_waves<T>(c.nv) : 8) * 256 / nt);
+    } else {
+        constexpr int V = Vec<T>::N;
+        const ColChoice c = choose_cols(C, L, V);
+        const int TL = c.tpr * (L < V ? 1 : V);
+        need = B * ((L + TL - 1) / TL);
+        fit = (int64_t)num_cus * (c.nt < 512 ? 512 / c.nt : 1);
+    }
+    return (uint32_t)(need < fit ? need : fit);
 }
 
 template <typename T>
@@ -900,13 +911,9 @@ hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
         return hipGetLastError();
     }
     const bool even = whole<T>(a, true);
-    uint32_t blocks;
+    const uint32_t blocks = backward_blocks<T>(a.B, a.C, a.L, num_cus);
     if (a.L == 1) {
         const RowChoice c = choose_rows(a.C, Vec<T>::N);
-        const int rpb = c.nv > 0 && c.lpr < 256 ? 256 / c.lpr : 1, nt = c.nv > 0 && c.lpr < 256 ? 256 : c.lpr;
-        const int64_t fit = (int64_t)num_cus * std::min(4, (c.nv > 0 ? row_bwd_waves<T>(c.nv) : 8) * 256 / nt);
-        const int64_t need = (a.B + rpb - 1) / rpb;
-        blocks = (uint32_t)(need < fit ? need : fit);
 #define DC1D_ROWS(R, N, O) \
     hipLaunchKernelGGL((k_ln_rows_bwd<T, R, N, O>), dim3(blocks), dim3((RowShape<T, R, N, O>::NT)), 0, st, a)
 #define DC1D_ANY(N) hipLaunchKernelGGL((k_ln_rows_bwd_any<T, N>), dim3(blocks), dim3(N), 0, st, a)
@@ -920,9 +927,6 @@ hipError_t backward_typed(const LayerNormArgs &a, int num_cus, hipStream_t st) {
     } else {
         constexpr int V = Vec<T>::N;
         const ColChoice c = choose_cols(a.C, a.L, V);
-        const int TL = c.tpr * (a.L < V ? 1 : V);
-        const int64_t need = a.B * ((a.L + TL - 1) / TL), fit = (int64_t)num_cus * (c.nt < 512 ? 512 / c.nt : 1);
-        blocks = (uint32_t)(need < fit ? need : fit);
 #define DC1D_COLS(E, R, P, N, O) hipLaunchKernelGGL((k_ln_cols_bwd<T, E, R, P, N, O>), dim3(blocks), dim3(N), 0, st, a)
         if (a.L < V) {
             if (c.np == 0) DC1D_COLS(1, 8, 0, 1024, false);
@@ -946,9 +950,10 @@ hipError_t launch_layer_norm(const LayerNormArgs &a, int, hipStream_t stream) {
     return a.dtype == kF32 ? forward_typed<F32>(a, stream) : forward_typed<BF16>(a, stream);
 }
 
-size_t layer_norm_backward_workspace(int64_t B, int C, int64_t L, int, bool want_params, int num_cus) {
+size_t layer_norm_backward_workspace(int64_t B, int C, int64_t L, int dtype, bool want_params, int num_cus) {
     if (!want_params || B == 0 || L == 0) return 0;
-    return (size_t)backward_blocks(B, L, num_cus) * 2 * C * sizeof(float);
+    const uint32_t parts = dtype == kF32 ? backward_blocks<F32>(B, C, L, num_cus) : backward_blocks<BF16>(B, C, L, num_cus);
+    return (size_t)parts * 2 * C * sizeof(float);
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormArgs &a, int num_cus, hipStream_t stream) {

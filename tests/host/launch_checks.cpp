@@ -77,6 +77,26 @@ int main() {
         seen.clear();
         check("attention", a, launch_attention(a, f, some, nullptr), f.blocks + (f.splits > 1 ? heads * a.rows : 0));
     }
+    // layer norm's gradients: the workspace holds the sums of the workgroups that there are
+    for (int dtype : {(int)kF32, (int)kBF16})
+        for (int C : {1, 7, 40, 101, 512, 1024, 2000, 4099, 8192, 8200, 16384, 32768, 1 << 20})
+            for (int64_t L : {1, 2, 5, 9, 128, 4092, 1 << 22})
+                for (int64_t B : {1, 3, 300, 4096, 131072}) {
+                    if (B * L * C > (int64_t)1 << 40) continue;
+                    LayerNormArgs a;
+                    memset((void *)&a, 0, sizeof(a));
+                    a.x = a.g = a.y = some, a.gw = a.gb = some, a.mean = a.rstd = a.ws = (float *)some;
+                    a.dtype = dtype, a.B = B, a.L = L, a.C = C;
+                    seen.clear();
+                    ++calls;
+                    const size_t bytes = layer_norm_backward_workspace(B, C, L, dtype, true, 256);
+                    if (launch_layer_norm_backward(a, 256, nullptr) != hipSuccess || seen.size() != 2 ||
+                        bytes != (size_t)seen[0].blocks * 2 * C * sizeof(float)) {
+                        printf("layer norm gradients, %lld x %d x %lld: %zu bytes for %lld workgroups\n", (long long)B, C, (long long)L,
+                               bytes, seen.empty() ? -1 : (long long)seen[0].blocks);
+                        ++failures;
+                    }
+                }
     printf("launch checks: %d calls, %d failure(s)\n", calls, failures);
     return failures != 0;
 }

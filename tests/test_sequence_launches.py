@@ -1,7 +1,8 @@
 """Every launch of attention and its gradients stays within the runtime's
-limit of threads up to the documented sizes (no GPU needed: the kernels'
-regular build linked with tests/host/launch_checks.cpp, whose own launch call
-only records the grid)."""
+limit of threads up to the documented sizes, and layer norm's gradients ask
+for the workspace of the workgroups that they launch (no GPU needed: the
+kernels' regular build linked with tests/host/launch_checks.cpp, whose own
+launch call only records the grid)."""
 import os
 import subprocess
 
@@ -20,7 +21,7 @@ def _run(cmd):
 def test_launches_within_the_documented_limits(tmp_path):
     if not os.path.exists(HIPCC):
         pytest.skip("hipcc not available")
-    kernels = [os.path.join(CSRC, "_build", f) for f in ("k_attention.o", "k_attention_bwd.o")]
+    kernels = [os.path.join(CSRC, "_build", f) for f in ("k_attention.o", "k_attention_bwd.o", "k_layernorm.o")]
     if not all(os.path.exists(o) for o in kernels):
         from deformable_convolution_amd.csrc import build
         build.build()
