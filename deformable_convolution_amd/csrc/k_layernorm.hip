@@ -9,10 +9,13 @@
 // backward to read x and g and write gx, and each is done in one pass with
 // the channels of a position held in registers between the sums (the
 // variance is that of the centred values, so a large mean costs no digits).
+// Rows of less than 16 bytes or of more than 2048 pieces of them, and more
+// than 2048 channels first, are read again for each sum instead.
 //
-// Rows (L = 1): a wave, or the four waves of a workgroup, hold a row.
-// Channels first (L > 1): a workgroup holds every channel of 128 bytes'
-// worth of neighbouring positions, so that HBM is read in whole lines.
+// Rows (L = 1): 8 to 512 lanes hold a row; several short ones share a wave.
+// Channels first (L > 1): a workgroup holds every channel of 128 bytes' worth
+// (fewer from 513 channels on) of neighbouring positions, so that HBM is read
+// in whole lines.
 // The parameter gradients are summed per workgroup over all the positions
 // that it visits, left in the workspace and added in workgroup order: no
 // atomics, the same bits every time.
@@ -199,7 +202,7 @@ __global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT)) void k_ln_rows(Lay
     }
 }
 
-// Rows shorter than a piece (a wave a row) or longer than registers hold (16
+// Rows shorter than a piece (a wave a row) or longer than k_ln_rows holds (16
 // waves): read once for each sum and once more, from cache where a row fits it.
 // 4096 x 32768 fp32: 495 us (2.2 TB/s), gradients 998 us.
 template <typename T, int NT>
@@ -337,7 +340,7 @@ __global__ __launch_bounds__((RowShape<T, LPR, NV, ODD>::NT), row_bwd_waves<T>(N
     }
 }
 
-// Backward of rows shorter than a piece or longer than registers hold: a
+// Backward of rows shorter than a piece or longer than k_ln_rows_bwd holds: a
 // workgroup strides over the rows, its threads over the channels; the
 // parameter sums are kept in the workgroup's part of the workspace.
 template <typename T, int NT>
@@ -386,9 +389,12 @@ __global__ __launch_bounds__(NT) void k_ln_rows_bwd_any(LayerNormArgs a) {
 // thread then reads of positions before its own it neither adds nor stores.  TPR threads stand across a tile's row:
 // 8 (whole 128-byte lines), fewer where C channels would not fit otherwise.
 // Neighbouring tiles go to one XCD: where rows are not whole lines they share
-// the lines at their edges.  8 x 256 x 16384 bf16: 31 us (4.4 TB/s), x 16383:
-// 32 us; 16 x 512 x 4092 fp32: 64 us (4.2 TB/s); with NP = 0, 4 x 4096 x 1024
-// fp32: 50 us (2.7 TB/s).
+// the lines at their edges.  8 x 256 x 16384 bf16: 36 us (3.7 TB/s) over
+// inputs of more than the last-level cache, 31 where two alternate in it, x
+// 16383: 32 us; 16 x 512 x 4092 fp32: 64 us (4.2 TB/s) either way; with NP = 0,
+// 4 x 4096 x 1024 fp32: 50 us (2.7 TB/s).  A piece past C is loaded all the same
+// (from the tile's first row): C = 300 issues the loads of 512, 1280 those of
+// 2048 (64 x 300 x 1001 bf16: 29 us, 2.7 TB/s; 1 x 1280 x 4383 fp32: 21, 2.2).
 template <int EPT, int TPR_, int NT>
 struct ColShape {
     static constexpr int TPR = TPR_, TL = TPR * EPT, RP = NT / TPR;

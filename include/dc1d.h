@@ -45,7 +45,8 @@
  * returns, and has no mutable global state other than a per-device
  * capability cache filled once.  Work is enqueued on the given HIP stream and
  * the call returns without synchronising; buffers must stay alive until that
- * stream's work is done.  Calls are re-entrant; calls that share a workspace
+ * stream's work is done (of a call captured into a graph: as long as the graph
+ * is replayed).  Calls are re-entrant; calls that share a workspace
  * must be ordered on one stream.
  *
  * Logging: with the environment variable DC1D_LOG set to a non-zero value
