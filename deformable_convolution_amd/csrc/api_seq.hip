@@ -149,9 +149,45 @@ bool head_slices(const dc1d_strided *a, const dc1d_strided *b) {
     return gap + inner(b) * es <= unit * es;
 }
 
+// Whether s[0] d[0] + ... = r has a solution with lo[i] <= d[i] <= hi[i], the
+// strides s falling and positive; true also where too many are left to try.
+bool reachable(const int64_t *s, const int64_t *lo, const int64_t *hi, int n, int64_t r) {
+    if (n == 0) return r == 0;
+    int64_t least = 0, most = 0;  // what the dimensions after this one can add up to
+    for (int i = 1; i < n; ++i) least += s[i] * lo[i], most += s[i] * hi[i];
+    auto down = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    int64_t from = -down(most - r, s[0]), to = down(r - least, s[0]);
+    from = from > lo[0] ? from : lo[0];
+    to = to < hi[0] ? to : hi[0];
+    if (to - from >= 8) return true;
+    for (int64_t d = from; d <= to; ++d)
+        if (reachable(s + 1, lo + 1, hi + 1, n - 1, r - s[0] * d)) return true;
+    return false;
+}
+
+// Whether two tensors of one dtype at the same strides (slices of one buffer
+// along any dimension) share no element: no two indices' difference times the
+// strides makes up the distance between their first elements.
+bool apart(const dc1d_strided *a, const dc1d_strided *b) {
+    const int64_t es = (int64_t)elem_size(a->dtype), gap = (int64_t)((uintptr_t)b->data - (uintptr_t)a->data);
+    if (gap % es) return false;
+    int64_t s[4], lo[4], hi[4];
+    int n = 0;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t na = a->shape[i], nb = b->shape[i];
+        const int64_t st = i == 3 ? 1 : na > 1 ? a->stride[i] : b->stride[i];
+        if (i < 3 && na > 1 && nb > 1 && b->stride[i] != st) return false;
+        if ((na <= 1 && nb <= 1) || st == 0) continue;
+        int at = n++;
+        for (; at > 0 && s[at - 1] < st; --at) s[at] = s[at - 1], lo[at] = lo[at - 1], hi[at] = hi[at - 1];
+        s[at] = st, lo[at] = -(nb - 1), hi[at] = na - 1;
+    }
+    return !reachable(s, lo, hi, n, gap / es);
+}
+
 // An output against another tensor.
 bool clash(const dc1d_strided *out, const dc1d_strided *t) {
-    return out && t && meet(range(out), range(t)) && !head_slices(out, t);
+    return out && t && meet(range(out), range(t)) && !head_slices(out, t) && !apart(out, t);
 }
 bool clash(const dc1d_strided *out, const dc1d_tensor *t) { return out && t && meet(range(out), range(t)); }
 bool clash(Range w, const dc1d_strided *t) { return t && meet(w, range(t)); }

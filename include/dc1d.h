@@ -456,7 +456,11 @@ int dc1d_plan(const dc1d_tensor *x, const dc1d_tensor *offsets, const dc1d_tenso
 /* A tensor in device memory with a stride (in elements) for each dimension.
  * Strides are not negative and the last dimension is contiguous (stride 1,
  * any where its size is 1); a stride of 0 repeats an input.  An output's
- * elements must not share memory. */
+ * elements must not share memory, and an output must not overlap another
+ * tensor of the call: tensors whose ranges of memory meet are taken as apart
+ * where they are slices of one buffer at the same strides, along any
+ * dimension, that share no element (q, k and v packed in [B, L, 3, H, D], say),
+ * or slices of its heads. */
 typedef struct dc1d_strided {
     void *data;
     int32_t dtype; /* a dc1d_dtype */
@@ -524,8 +528,7 @@ int dc1d_layer_norm_backward(const dc1d_tensor *x, const dc1d_tensor *weight_or_
  *
  * Positions outside [0, P) are taken as the nearest end of the tables.  An
  * output may be its own input (in place); otherwise it must not overlap any
- * input or the other output, except that two tensors may be disjoint head
- * slices of one buffer.  Limits: B * L < 2^31, (Hq + Hkv) * D < 2^30,
+ * input or the other output.  Limits: B * L < 2^31, (Hq + Hkv) * D < 2^30,
  * B * L * (Hq + Hkv) * D < 2^40.
  */
 int dc1d_rotary(const dc1d_strided *q, const dc1d_strided *k_or_null, const dc1d_tensor *cos, const dc1d_tensor *sin,
@@ -555,7 +558,7 @@ int dc1d_rotary(const dc1d_strided *q, const dc1d_strided *k_or_null, const dc1d
  *   scale     finite, > 0 (usually 1 / sqrt(D));  window >= 0, 0: none
  *
  * Strides are free, so q, k, v and out may be slices of larger buffers; out
- * must not overlap the inputs unless as a disjoint head slice of one buffer.
+ * must not overlap the inputs.
  * |q_start| and window are clamped to 2^29.  workspace: at least
  * dc1d_attention_workspace_bytes() bytes, 256-byte aligned, when that is not
  * 0 (few queries over many keys: the partial results of parts of the keys).
@@ -586,7 +589,7 @@ int dc1d_attention_plan(const dc1d_strided *q, const dc1d_strided *k, const dc1d
  * Keys that no query sees get zeros, and so do queries that see no key; what
  * those hold, and their grad_out, reaches no gradient.  NULL gradients are not
  * computed.  The other arguments are the forward's; gradients must not overlap
- * the inputs or each other unless as disjoint head slices of one buffer.
+ * the inputs or each other.
  * workspace: at least dc1d_attention_backward_workspace_bytes() bytes, 256-byte
  * aligned, when that is not 0.
  */
