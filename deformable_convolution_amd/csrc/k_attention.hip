@@ -152,7 +152,7 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, typename Tile<T>::Frag
 //
 // 128 rows a workgroup, 32 a wave; tiles of KT keys, double-buffered, the
 // next one on its way while this one is used.  8 x 4096 positions, 8 heads of
-// 64, bf16: 302 to 326 us (0.84 to 0.9 PFLOP/s, by the card), bound by the vector
+// 64, bf16: 300 to 326 us (0.84 to 0.9 PFLOP/s, by the card), bound by the vector
 // instructions of the softmax (matrix unit 48% busy); 4 x 4096, 8 heads of 128:
 // 263 us (1.05), causal over 2 key heads 144 us (0.96).
 template <typename T, int DP>

@@ -424,7 +424,7 @@ __device__ __forceinline__ void query_gradients(const AttnArgs &a, char *smem, u
 // GPU where each alone would leave part of it idle (16 x 128 positions, 8
 // heads of 64, fp32: 128 workgroups each on 256 CUs, 49 us one after the
 // other and 28 at once), and the shorter one fills the longer one's end.
-// Causal, 4 x 4096 positions, 8 heads over 2 of 128, bf16: 502 to 539 us with
+// Causal, 4 x 4096 positions, 8 heads over 2 of 128, bf16: 497 to 539 us with
 // the two kernels beside it, the matrix unit 50% busy: two waves a SIMD, each
 // waiting for its own chain from the scores to the gradients.
 template <typename T, int DP, bool VEC>
