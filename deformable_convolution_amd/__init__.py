@@ -1,8 +1,8 @@
 """MI355X-native 1D deformable convolution (DeformConv1d): forward, backward, and
 the packed layer whose offsets (and mask) are generated from its input, and
 2D modulated deformable convolution (DCNv2); and the sequence operators a
-model puts next to them: layer norm, rotary positions with several axes, and
-attention, with their gradients.
+model puts next to them: layer norm, rotary positions with several axes,
+attention, group norm and a gated linear recurrence, with their gradients.
 
 The compute lives in ``libdc1d.so`` (HIP kernels for gfx950 behind a C ABI
 declared in ``include/dc1d.h``); ``deformable_convolution_amd.dc1d`` is the
@@ -35,6 +35,10 @@ from .sequence import (  # noqa: F401
     attention,
     attention_backward,
     attention_plan,
+    gated_recurrence,
+    gated_recurrence_backward,
+    group_norm,
+    group_norm_backward,
     layer_norm,
     layer_norm_backward,
     rotary,

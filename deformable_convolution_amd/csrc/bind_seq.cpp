@@ -25,6 +25,14 @@ struct Entries {
     decltype(&dc1d_attention) attention;
     decltype(&dc1d_attention_backward_workspace_bytes) attention_backward_ws;
     decltype(&dc1d_attention_backward) attention_backward;
+    decltype(&dc1d_group_norm_workspace_bytes) group_norm_ws;
+    decltype(&dc1d_group_norm) group_norm;
+    decltype(&dc1d_group_norm_backward_workspace_bytes) group_norm_backward_ws;
+    decltype(&dc1d_group_norm_backward) group_norm_backward;
+    decltype(&dc1d_gated_recurrence_workspace_bytes) gated_recurrence_ws;
+    decltype(&dc1d_gated_recurrence) gated_recurrence;
+    decltype(&dc1d_gated_recurrence_backward_workspace_bytes) gated_recurrence_backward_ws;
+    decltype(&dc1d_gated_recurrence_backward) gated_recurrence_backward;
 } entry;
 
 int32_t dtype_of(const at::Tensor &t) {
@@ -83,12 +91,12 @@ struct Dense {
 struct Strided {
     dc1d_strided d;
     const dc1d_strided *p = nullptr;
-    void set(const at::Tensor &t, const char *name) {
-        if (t.dim() != 4) refuse(std::string(name) + " must have four dimensions");
+    void set(const at::Tensor &t, const char *name, int ndim = 4) {
+        if (t.dim() != ndim) refuse(std::string(name) + (ndim == 4 ? " must have four dimensions" : " must have three dimensions"));
         d.data = t.data_ptr();
         d.dtype = dtype_of(t);
-        d.ndim = 4;
-        for (int i = 0; i < 4; ++i) d.shape[i] = t.size(i), d.stride[i] = t.stride(i);
+        d.ndim = ndim;
+        for (int i = 0; i < 4; ++i) d.shape[i] = i < ndim ? t.size(i) : 0, d.stride[i] = i < ndim ? t.stride(i) : 0;
         p = &d;
     }
     void set(const Arg &a, const char *name) {
@@ -320,12 +328,146 @@ PyObject *attention_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// x, groups, weight, bias, lens, eps, activation, with_stats, out, workspace, get, stream -> status, y, mean, rstd
+PyObject *group_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 12);
+    Call c;
+    const at::Tensor x = c.tensor(a[0], "x");
+    const Arg w = c.maybe(a[2], "weight"), b = c.maybe(a[3], "bias"), lens = c.maybe(a[4], "lens"), out = c.maybe(a[8], "out");
+    const int64_t groups = integer(a[1]);
+    Dense dx, dw, db, dl, dy, dm, dr;
+    dx.set(x, "x");
+    dw.set(w, "weight");
+    db.set(b, "bias");
+    dl.set(lens, "lens");
+    size_t need = 0;
+    if (const int st = entry.group_norm_ws(dx.p, groups, &need)) return failed(st, 3);
+    const at::Tensor y = out.given ? out.t : fresh(x, x.sizes());
+    dy.set(y, "out");
+    at::Tensor mean, rstd;
+    if (truth(a[7])) {
+        mean = at::empty({x.size(0), groups}, x.options().dtype(at::kFloat));
+        rstd = at::empty({x.size(0), groups}, x.options().dtype(at::kFloat));
+        dm.set(mean, "mean");
+        dr.set(rstd, "rstd");
+    }
+    Workspace ws;
+    if (!ws.take(a[9], a[10], need, c.device)) return nullptr;
+    return result(entry.group_norm(dx.p, dw.p, db.p, dl.p, dy.p, dm.p, dr.p, groups, number(a[5]), (int)integer(a[6]), ws.p, ws.n,
+                                   stream_of(a[11])),
+                  {y, mean, rstd});
+    END_HANDLE_TH_ERRORS
+}
+
+// x, groups, grad_out, mean, rstd, weight, bias, lens, activation, need x, need weight, need bias, workspace, get, stream
+// -> status, grad x, grad weight, grad bias
+PyObject *group_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 15);
+    Call c;
+    const at::Tensor x = c.tensor(a[0], "x"), g = c.tensor(a[2], "grad_out"), m = c.tensor(a[3], "mean"), r = c.tensor(a[4], "rstd");
+    const Arg w = c.maybe(a[5], "weight"), b = c.maybe(a[6], "bias"), lens = c.maybe(a[7], "lens");
+    const int64_t groups = integer(a[1]);
+    Dense dx, dg, dm, dr, dw, db, dl, gx, gw, gb;
+    dx.set(x, "x");
+    dg.set(g, "grad_out");
+    dm.set(m, "mean");
+    dr.set(r, "rstd");
+    dw.set(w, "weight");
+    db.set(b, "bias");
+    dl.set(lens, "lens");
+    size_t need = 0;
+    const bool params = truth(a[10]) || truth(a[11]);
+    if (const int st = entry.group_norm_backward_ws(dx.p, groups, params, &need)) return failed(st, 3);
+    at::Tensor tx, tw, tb;
+    const int64_t C = x.size(x.dim() - 1);
+    if (truth(a[9])) tx = fresh(x, x.sizes()), gx.set(tx, "grad_x");
+    if (truth(a[10])) tw = fresh(x, {C}), gw.set(tw, "grad_weight");
+    if (truth(a[11])) tb = fresh(x, {C}), gb.set(tb, "grad_bias");
+    Workspace ws;
+    if (!ws.take(a[12], a[13], need, c.device)) return nullptr;
+    return result(entry.group_norm_backward(dx.p, dw.p, db.p, dl.p, dg.p, dm.p, dr.p, gx.p, gw.p, gb.p, groups, (int)integer(a[8]), ws.p,
+                                            ws.n, stream_of(a[14])),
+                  {tx, tw, tb});
+    END_HANDLE_TH_ERRORS
+}
+
+// x, gate, state, lens, blend, reverse, with_states, out, last, workspace, get, stream -> status, y, last, states
+PyObject *gated_recurrence(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 12);
+    Call c;
+    const at::Tensor x = c.tensor(a[0], "x"), gate = c.tensor(a[1], "gate");
+    const Arg state = c.maybe(a[2], "state"), lens = c.maybe(a[3], "lens"), out = c.maybe(a[7], "out"), given = c.maybe(a[8], "last");
+    Strided dx, dg, dy;
+    Dense ds, dl, dlast, dstates;
+    dx.set(x, "x", 3);
+    dg.set(gate, "gate", 3);
+    ds.set(state, "state");
+    dl.set(lens, "lens");
+    size_t need = 0;
+    if (const int st = entry.gated_recurrence_ws(dx.p, &need)) return failed(st, 3);
+    const at::Tensor y = out.given ? out.t : fresh(x, x.sizes());
+    dy.set(y, "out", 3);
+    const at::Tensor last = given.given ? given.t : at::empty({x.size(0), x.size(2)}, x.options().dtype(at::kFloat));
+    dlast.set(last, "last");
+    at::Tensor states;
+    if (truth(a[6])) {
+        states = at::empty({x.size(0), (x.size(1) + 63) / 64, x.size(2)}, x.options().dtype(at::kFloat));
+        dstates.set(states, "states");
+    }
+    Workspace ws;
+    if (!ws.take(a[9], a[10], need, c.device)) return nullptr;
+    return result(entry.gated_recurrence(dx.p, dg.p, ds.p, dl.p, dy.p, dlast.p, dstates.p, truth(a[4]), truth(a[5]), ws.p, ws.n,
+                                         stream_of(a[11])),
+                  {y, last, states});
+    END_HANDLE_TH_ERRORS
+}
+
+// x, gate, states, grad_out, grad_last, lens, blend, reverse, then for x, gate and state: a tensor to
+// write, True (allocate) or None (not wanted), workspace, get, stream -> status, grad x, grad gate, grad state
+PyObject *gated_recurrence_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 14);
+    Call c;
+    const at::Tensor x = c.tensor(a[0], "x"), gate = c.tensor(a[1], "gate"), states = c.tensor(a[2], "states");
+    const at::Tensor g = c.tensor(a[3], "grad_out");
+    const Arg g_last = c.maybe(a[4], "grad_last"), lens = c.maybe(a[5], "lens");
+    Strided dx, dgate, dg, grad[2];
+    Dense dstates, dlast, dl, gs;
+    dx.set(x, "x", 3);
+    dgate.set(gate, "gate", 3);
+    dstates.set(states, "states");
+    dg.set(g, "grad_out", 3);
+    dlast.set(g_last, "grad_last");
+    dl.set(lens, "lens");
+    size_t need = 0;
+    if (const int st = entry.gated_recurrence_backward_ws(dx.p, &need)) return failed(st, 3);
+    at::Tensor grads[2], ts;
+    for (int i = 0; i < 2; ++i) {
+        if (a[8 + i] == Py_None) continue;
+        grads[i] = a[8 + i] == Py_True ? fresh(x, x.sizes()) : c.tensor(a[8 + i], "grads");
+        grad[i].set(grads[i], "grads", 3);
+    }
+    if (a[10] != Py_None) {
+        ts = a[10] == Py_True ? at::empty({x.size(0), x.size(2)}, x.options().dtype(at::kFloat)) : c.tensor(a[10], "grads");
+        gs.set(ts, "grads");
+    }
+    Workspace ws;
+    if (!ws.take(a[11], a[12], need, c.device)) return nullptr;
+    return result(entry.gated_recurrence_backward(dx.p, dgate.p, dstates.p, dl.p, dg.p, dlast.p, grad[0].p, grad[1].p, gs.p, truth(a[6]),
+                                                  truth(a[7]), ws.p, ws.n, stream_of(a[13])),
+                  {grads[0], grads[1], ts});
+    END_HANDLE_TH_ERRORS
+}
+
 // The entries' addresses, in the order of Entries.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    void *p[8];
-    expect(n, 8);
-    for (int i = 0; i < 8; ++i) p[i] = stream_of(a[i]);
+    void *p[16];
+    expect(n, 16);
+    for (int i = 0; i < 16; ++i) p[i] = stream_of(a[i]);
     static_assert(sizeof(entry) == sizeof(p), "one address an entry");
     memcpy(&entry, p, sizeof(p));
     Py_RETURN_NONE;
@@ -334,6 +476,7 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define FN(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FN(bind), FN(layer_norm), FN(layer_norm_backward), FN(rotary), FN(attention), FN(attention_backward),
+                         FN(group_norm), FN(group_norm_backward), FN(gated_recurrence), FN(gated_recurrence_backward),
                          {nullptr, nullptr, 0, nullptr}};
 #undef FN
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_seq", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

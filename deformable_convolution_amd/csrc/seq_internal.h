@@ -1,5 +1,6 @@
 // seq_internal.h -- private declarations of the sequence operators (layer
-// norm, rotary positions, attention): parameter blocks and launchers.
+// norm, rotary positions, attention, group norm, gated recurrence): parameter
+// blocks and launchers.
 #pragma once
 
 #include "dc1d_internal.h"
@@ -88,5 +89,47 @@ struct AttnBwdPlan {
 };
 AttnBwdPlan plan_attention_backward(const AttnArgs &a, int num_cus);
 hipError_t launch_attention_backward(AttnArgs a, const AttnBwdPlan &pl, void *ws, hipStream_t stream);
+
+// ---- group norm, channels last --------------------------------------------------
+//
+// x [B][S][C]: S positions a sample, G groups of D channels.  w, b may be null.
+struct GroupNormArgs {
+    const void *x, *w, *b, *g;  // g: the output's gradient (backward)
+    void *y;                    // forward: y; backward: x's gradient (may be null)
+    float *mean, *rstd;         // [B][G]; forward: written unless null; backward: read
+    void *gw, *gb;              // backward: may be null
+    const int *lens;            // [B] or null
+    int dtype, act;             // a dc1d_activation
+    int64_t B, S;
+    int C, G, D;
+    float eps;
+    void *ws;
+};
+size_t group_norm_workspace(int64_t B, int64_t S, int C, int G, int dtype, int num_cus);
+hipError_t launch_group_norm(const GroupNormArgs &a, int num_cus, hipStream_t stream);
+size_t group_norm_backward_workspace(int64_t B, int64_t S, int C, int G, int dtype, bool want_params, int num_cus);
+hipError_t launch_group_norm_backward(const GroupNormArgs &a, int num_cus, hipStream_t stream);
+
+// ---- gated recurrence -------------------------------------------------------------
+
+constexpr int kStateEvery = 64;  // positions from one kept state to the next
+
+struct Strides2 {
+    int64_t b, l;  // elements; the channels are contiguous
+};
+struct RecurrenceArgs {
+    const void *x, *gate, *g;  // g: the output's gradient (backward)
+    void *y, *gx, *gg;         // backward: x's and gate's gradients (may be null)
+    Strides2 xs, gates, gs, ys, gxs, ggs;
+    const int *lens;           // [B] or null
+    const float *state, *g_last;  // [B][C] or null
+    float *last, *g_state;     // [B][C] or null
+    float *states;             // [B][ceil(L / 64)][C]; forward: written unless null, backward: read
+    int dtype, B, L, C, blend, reverse;
+    void *ws;
+};
+size_t recurrence_workspace(int B, int L, int C, int dtype, bool backward, int num_cus);
+hipError_t launch_recurrence(const RecurrenceArgs &a, int num_cus, hipStream_t stream);
+hipError_t launch_recurrence_backward(const RecurrenceArgs &a, int num_cus, hipStream_t stream);
 
 }  // namespace dc1d

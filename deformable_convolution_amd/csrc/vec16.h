@@ -1,5 +1,5 @@
-// vec16.h -- 16-byte pieces of a row of either storage type: loads, stores, and
-// the elements in 32 bits.
+// vec16.h -- pieces of a row of either storage type: loads, stores, and the
+// elements in 32 bits.
 #pragma once
 
 #include "attn_tile.h"
@@ -61,6 +61,74 @@ __device__ __forceinline__ void store16(typename T::T *p, const float *f, int sk
     } else {
         *(u32x4 *)p = Vec<T>::narrow(f);
     }
+}
+
+// Pieces of N neighbouring elements at any element's address, each one load and
+// one store.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_odd __attribute__((aligned(2)));
+
+template <typename T, int N>
+struct Piece;
+template <typename T>
+struct Piece<T, 1> {
+    using E = typename T::T;
+    using Raw = E;
+    static __device__ __forceinline__ Raw load(const E *p) { return *p; }
+    static __device__ __forceinline__ void widen(Raw r, float *f) { f[0] = T::ld(&r, 0); }
+    static __device__ __forceinline__ void store(E *p, const float *f) { T::st(p, 0, f[0]); }
+};
+template <>
+struct Piece<F32, 4> {
+    using E = float;
+    using Raw = u32x4;
+    static __device__ __forceinline__ Raw load(const E *p) { return load16<true>(p); }
+    static __device__ __forceinline__ void widen(Raw r, float *f) { Vec<F32>::widen(r, f); }
+    static __device__ __forceinline__ void store(E *p, const float *f) { *(u32x4_odd *)p = Vec<F32>::narrow(f); }
+};
+template <>
+struct Piece<BF16, 8> {
+    using E = uint16_t;
+    using Raw = u32x4;
+    static __device__ __forceinline__ Raw load(const E *p) { return load16<true>(p); }
+    static __device__ __forceinline__ void widen(Raw r, float *f) { Vec<BF16>::widen(r, f); }
+    static __device__ __forceinline__ void store(E *p, const float *f) { *(u32x4_odd *)p = Vec<BF16>::narrow(f); }
+};
+template <>
+struct Piece<BF16, 4> {
+    using E = uint16_t;
+    using Raw = u32x2;
+    static __device__ __forceinline__ Raw load(const E *p) { return *(const u32x2_odd *)p; }
+    static __device__ __forceinline__ void widen(Raw r, float *f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[2 * i] = __uint_as_float(r[i] << 16);
+            f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(E *p, const float *f) {
+        *(u32x2_odd *)p = __builtin_bit_cast(u32x2, __builtin_convertvector(f32x4{f[0], f[1], f[2], f[3]}, bf16x4));
+    }
+};
+// The elements from `skip` on of a piece: those before it are its neighbour's.
+template <typename T, int N>
+__device__ __forceinline__ void store_own(typename T::T *p, const float *f, int skip) {
+    if (skip == 0) {
+        Piece<T, N>::store(p, f);
+    } else {
+#pragma unroll
+        for (int e = 1; e < N; ++e)
+            if (e >= skip) T::st(p, e, f[e]);
+    }
+}
+
+// sigmoid(z) and 1 - sigmoid(z): the smaller one from exp(-|z|), the larger one as
+// 1 minus it, so that neither cancels.  v_exp_f32 and v_rcp_f32 are off by an
+// ulp, and the exponent's product with log2 e by 2^-24 |z|.
+__device__ __forceinline__ void sigmoid_pair(float z, float &p, float &q) {
+    const float e = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e), s = e * __builtin_amdgcn_rcpf(1.0f + e), b = 1.0f - s;
+    p = z < 0.0f ? s : b;
+    q = z < 0.0f ? b : s;
 }
 
 }  // namespace dc1d

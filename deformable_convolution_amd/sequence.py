@@ -1,6 +1,7 @@
 """Binding over libdc1d's sequence operators (include/dc1d.h): layer norm over
-axis 1, rotary positions with several axes, and attention, each with its
-gradient.
+axis 1, rotary positions with several axes, attention, group norm with an
+activation over channels-last positions, and a gated linear recurrence, each
+with its gradient.
 
 Argument marshalling only, like ``dc1d``: torch tensors become descriptors,
 the work is enqueued on torch's current stream, status codes become
@@ -19,7 +20,9 @@ from .dc1d import _check, _nullctx, _workspace
 
 _ENTRIES = ("dc1d_layer_norm", "dc1d_layer_norm_backward_workspace_bytes", "dc1d_layer_norm_backward", "dc1d_rotary",
             "dc1d_attention_workspace_bytes", "dc1d_attention", "dc1d_attention_backward_workspace_bytes",
-            "dc1d_attention_backward")
+            "dc1d_attention_backward", "dc1d_group_norm_workspace_bytes", "dc1d_group_norm",
+            "dc1d_group_norm_backward_workspace_bytes", "dc1d_group_norm_backward", "dc1d_gated_recurrence_workspace_bytes",
+            "dc1d_gated_recurrence", "dc1d_gated_recurrence_backward_workspace_bytes", "dc1d_gated_recurrence_backward")
 
 _bound = None
 
@@ -150,6 +153,94 @@ def attention_backward(q, k, v, out, lse, grad_out, causal=False, window=0, scal
     if status:
         _check(status, "dc1d_attention_backward")
     return {n: g for n, g in zip("qkv", got) if g is not None}
+
+
+_ACTIVATIONS = {None: 0, "relu": 1, "silu": 2}
+
+
+def _activation(name):
+    try:
+        return _ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError("activation must be None, 'relu' or 'silu', not %r" % (name,)) from None
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, activation=None, lens=None, with_stats=False, out=None, workspace=None):
+    """Group norm of x [N, C], [B, L, C] or [B, H, W, C] (float32 or bfloat16,
+    contiguous: channels last) over a sample's positions and each of ``groups``
+    runs of C / groups channels: (x - mean) / sqrt(var + eps) * weight + bias,
+    then ``activation`` (None, "relu" or "silu").  With lens (int32 [B], for
+    [B, L, C]) only the first lens[b] positions count, and the others give 0.
+    Returns y (allocated unless given as ``out``, which may be x), or with
+    with_stats (y, mean, rstd), float32 [B, groups]."""
+    seq = _bound or _binding()
+    index = x.get_device()
+    with _on(index):
+        status, y, mean, rstd = seq.group_norm(x, groups, weight, bias, lens, eps, _activation(activation), with_stats, out, workspace,
+                                               _get, _stream(index))
+    if status:
+        _check(status, "dc1d_group_norm")
+    return (y, mean, rstd) if with_stats else y
+
+
+def group_norm_backward(x, groups, grad_out, mean, rstd, weight=None, bias=None, activation=None, lens=None,
+                        need=("x", "weight", "bias"), workspace=None):
+    """Gradients of sum(grad_out * group_norm(x, groups, weight, bias, ...)) from
+    the forward's mean and rstd: a dict with the requested keys, each gradient
+    in x's dtype.  bias is that of the forward (the activation's derivative
+    depends on it)."""
+    seq = _bound or _binding()
+    index = x.get_device()
+    with _on(index):
+        status, *grads = seq.group_norm_backward(x, groups, grad_out, mean, rstd, weight, bias, lens, _activation(activation),
+                                                 "x" in need, "weight" in need, "bias" in need, workspace, _get, _stream(index))
+    if status:
+        _check(status, "dc1d_group_norm_backward")
+    return {n: g for n, g in zip(("x", "weight", "bias"), grads) if g is not None}
+
+
+def gated_recurrence(x, gate, state=None, lens=None, blend=False, reverse=False, with_states=False, out=None, last=None,
+                     workspace=None):
+    """The recurrence h_t = a_t h_{t-1} + u_t with a = sigmoid(gate) and u = x, or
+    (1 - a) x if blend, along the positions of x [B, L, C] (gate alike; any
+    strides over contiguous channels, also 0: ``gate.expand(...)``), from its
+    end if reverse.  ``state`` is the state ahead of the first position (float32
+    [B, C]; None: zeros); with lens (int32 [B]) a sequence ends after lens[b]
+    positions, and those past it give 0.  Returns (y, last): every position's
+    state in x's dtype (allocated unless given as ``out``, which may be x), and
+    the last one, float32 [B, C] (allocated unless given as ``last``, which may
+    be ``state``: a sequence taken up again, a position at a time or more).
+    with_states adds the states that the backward pass starts from, float32
+    [B, ceil(L / 64), C]."""
+    seq = _bound or _binding()
+    index = x.get_device()
+    with _on(index):
+        status, y, last, states = seq.gated_recurrence(x, gate, state, lens, blend, reverse, with_states, out, last, workspace, _get,
+                                                       _stream(index))
+    if status:
+        _check(status, "dc1d_gated_recurrence")
+    return (y, last, states) if with_states else (y, last)
+
+
+def gated_recurrence_backward(x, gate, states, grad_out, grad_last=None, lens=None, blend=False, reverse=False,
+                              need=("x", "gate", "state"), grads=None, workspace=None):
+    """Gradients of sum(grad_out * y) + sum(grad_last * last) for
+    y, last = gated_recurrence(x, gate, ...) from the forward's inputs and states
+    (grad_last None: zeros): a dict with the requested keys, x's and gate's of
+    x's shape and dtype, state's float32 [B, C] (allocated, or given in
+    ``grads`` under its key: for x and gate any strides, for instance slices of
+    one buffer).  A gate expanded along a dimension gets the gradient of its
+    expanded elements, to be summed along it."""
+    seq = _bound or _binding()
+    index = x.get_device()
+    given = grads or {}
+    want = [(given.get(n) if given.get(n) is not None else True) if n in need else None for n in ("x", "gate", "state")]
+    with _on(index):
+        status, *got = seq.gated_recurrence_backward(x, gate, states, grad_out, grad_last, lens, blend, reverse, *want, workspace, _get,
+                                                     _stream(index))
+    if status:
+        _check(status, "dc1d_gated_recurrence_backward")
+    return {n: g for n, g in zip(("x", "gate", "state"), got) if g is not None}
 
 
 def _scale(scale, q):

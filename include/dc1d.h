@@ -443,8 +443,9 @@ int dc1d_plan(const dc1d_tensor *x, const dc1d_tensor *offsets, const dc1d_tenso
 /* ---- sequence operators ------------------------------------------------------
  *
  * What a sequence or image model puts next to a deformable convolution:
- * layer norm over the channels, rotary positions with several axes, and
- * attention, each with its gradient.  fp32 or bf16 storage (one dtype per
+ * layer norm over the channels, rotary positions with several axes,
+ * attention, group norm, and a gated linear recurrence, each with its
+ * gradient.  fp32 or bf16 storage (one dtype per
  * call for the data tensors); sums, statistics and softmax are held in fp32
  * and each result is rounded once, to nearest even; probabilities and score
  * gradients of bf16 calls are rounded to bf16 as operands of the matrix
@@ -602,6 +603,125 @@ int dc1d_attention_backward(const dc1d_strided *q, const dc1d_strided *k, const 
                             const dc1d_strided *grad_q_or_null, const dc1d_strided *grad_k_or_null,
                             const dc1d_strided *grad_v_or_null, int causal, int64_t window, double scale,
                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Group norm over positions in channels-last order, with an activation:
+ *
+ *   mean, rstd  of the n[b] * D elements of group k of sample b: its first
+ *               n[b] positions and the D = C / groups channels k D ... k D + D - 1,
+ *               rstd = 1 / sqrt(mean of (x - mean)^2 + eps)
+ *   z = (x - mean) * rstd * weight + bias
+ *   y = z, max(z, 0) or z / (1 + exp(-z))
+ *
+ *   x, y       [N, C] (one position each), [B, L, C] or [B, H, W, C]
+ *   weight, bias  [C], x's dtype, or NULL (ones, zeros)
+ *   lens       [B] int32, clamped to [0, L], or NULL (L); with [B, L, C] only
+ *   mean, rstd  [B, groups] fp32, or NULL (not wanted)
+ *   activation  a dc1d_activation
+ *
+ * Positions past a sample's length give 0, whatever they hold; a sample of
+ * length 0 has mean 0 and rstd 0.  y may be x itself (in place); otherwise
+ * outputs must not overlap the inputs or each other.  eps is finite and not
+ * negative; groups divides C.  An empty x is a no-op (with L = 0, mean and rstd
+ * are 0).  workspace: at least dc1d_group_norm_workspace_bytes() bytes, 256-byte
+ * aligned, when that is not 0 (the partial statistics of samples that one
+ * workgroup does not hold).  Limits: C <= 2^24, fewer than 2^31 positions,
+ * B * groups < 2^31.
+ */
+typedef enum dc1d_activation { DC1D_ACT_NONE = 0, DC1D_ACT_RELU = 1, DC1D_ACT_SILU = 2 } dc1d_activation;
+
+int dc1d_group_norm_workspace_bytes(const dc1d_tensor *x, int64_t groups, size_t *bytes_out);
+
+int dc1d_group_norm(const dc1d_tensor *x, const dc1d_tensor *weight_or_null, const dc1d_tensor *bias_or_null,
+                    const dc1d_tensor *lens_or_null, const dc1d_tensor *y, const dc1d_tensor *mean_or_null,
+                    const dc1d_tensor *rstd_or_null, int64_t groups, double eps, int activation, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum(grad_out * y) with respect to x, weight and bias, from
+ * the forward's x, mean and rstd (NULL: not computed):
+ *
+ *   g = grad_out * (the activation's derivative at z),  u = g * weight,
+ *   xh = (x - mean) * rstd,
+ *   grad_x = rstd * (u - mean of u - xh * mean of (u * xh)),  the means over the group
+ *   grad_weight[c] = sum of g * xh,   grad_bias[c] = sum of g
+ *
+ * in their inputs' shapes and dtype.  The derivative of relu at 0 is 0.  bias
+ * is read where there is an activation.  Positions past a sample's length get
+ * zeros, and nothing that they or their grad_out hold reaches a gradient.
+ * grad_x may be grad_out itself.  An empty x gives zero grad_weight and
+ * grad_bias.  workspace: at least dc1d_group_norm_backward_workspace_bytes()
+ * bytes, 256-byte aligned, when that is not 0 (partial sums).
+ */
+int dc1d_group_norm_backward_workspace_bytes(const dc1d_tensor *x, int64_t groups, int want_params, size_t *bytes_out);
+
+int dc1d_group_norm_backward(const dc1d_tensor *x, const dc1d_tensor *weight_or_null, const dc1d_tensor *bias_or_null,
+                             const dc1d_tensor *lens_or_null, const dc1d_tensor *grad_out, const dc1d_tensor *mean,
+                             const dc1d_tensor *rstd, const dc1d_tensor *grad_x_or_null,
+                             const dc1d_tensor *grad_weight_or_null, const dc1d_tensor *grad_bias_or_null,
+                             int64_t groups, int activation, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A gated linear recurrence along the positions of x [B, L, C], every channel
+ * on its own:
+ *
+ *   a_t = sigmoid(gate_t),   h_t = a_t * h_{t-1} + u_t,   y_t = h_t,
+ *   u_t = x_t,  or (1 - a_t) * x_t where blend is not 0,
+ *
+ * over t = 0 ... n - 1, or n - 1 ... 0 where reverse is not 0, n = lens[b]; the
+ * state ahead of the first one is state[b].
+ *
+ *   x, gate, y  [B, L, C], any strides over contiguous channels (rank 3 of
+ *               dc1d_strided); a gate that is the same for all batches or
+ *               positions has stride 0 there
+ *   state, last [B, C] fp32: the states ahead of the first position (NULL:
+ *               zeros) and after the last one (NULL: not wanted); last may be
+ *               state itself, for one position at a time
+ *   lens        [B] int32, clamped to [0, L], or NULL (L)
+ *   states      [B, ceil(L / 64), C] fp32: the state ahead of every 64th position
+ *               in the recurrence's order, from the first on, which the backward
+ *               pass starts from (past the length: the last state), or NULL
+ *
+ * The state is held in fp32 throughout.  A gate of -infinity starts anew
+ * (a = 0), one of +infinity holds the state (a = 1).  Positions past a
+ * sequence's length give 0, whatever they hold; an empty one leaves its state.
+ * y may be x itself (in place); otherwise outputs must not overlap the inputs
+ * or each other.  workspace: at least dc1d_gated_recurrence_workspace_bytes()
+ * bytes, 256-byte aligned, when that is not 0 (long sequences of few channels:
+ * what its parts do to a state).  Limits: L <= 2^29, C <= 2^24, B * L < 2^31,
+ * B * C < 2^31.
+ */
+int dc1d_gated_recurrence_workspace_bytes(const dc1d_strided *x, size_t *bytes_out);
+
+int dc1d_gated_recurrence(const dc1d_strided *x, const dc1d_strided *gate, const dc1d_tensor *state_or_null,
+                          const dc1d_tensor *lens_or_null, const dc1d_strided *y, const dc1d_tensor *last_or_null,
+                          const dc1d_tensor *states_or_null, int blend, int reverse, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum(grad_out * y) + sum(grad_last * last) with respect to x,
+ * gate and state, from the forward's x, gate and states (NULL: not computed;
+ * grad_last NULL: zeros).  In the recurrence's order:
+ *
+ *   r_t = grad_out_t + a_{t+1} * r_{t+1},   r_n = grad_last (with a_n = 1),
+ *   grad_x = r,              grad_gate = r * h_{t-1} * a * (1 - a),
+ *   or r * (1 - a),          or r * (h_{t-1} - x) * a * (1 - a) where blend,
+ *   grad_state = a_0 * r_0
+ *
+ * The states between those given are formed again in fp32.  Positions past a
+ * sequence's length get zeros, and nothing that they hold reaches a gradient.
+ * grad_x and grad_gate may have any strides over contiguous channels; each is
+ * the gradient of one element of the full [B, L, C].  grad_x may be grad_out
+ * itself.  Gradients must not overlap the inputs or each other otherwise;
+ * grad_state may be grad_last itself.
+ */
+int dc1d_gated_recurrence_backward_workspace_bytes(const dc1d_strided *x, size_t *bytes_out);
+
+int dc1d_gated_recurrence_backward(const dc1d_strided *x, const dc1d_strided *gate, const dc1d_tensor *states,
+                                   const dc1d_tensor *lens_or_null, const dc1d_strided *grad_out,
+                                   const dc1d_tensor *grad_last_or_null, const dc1d_strided *grad_x_or_null,
+                                   const dc1d_strided *grad_gate_or_null, const dc1d_tensor *grad_state_or_null,
+                                   int blend, int reverse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* A static, NUL-terminated description of a status code. */
 const char *dc1d_status_string(int status);
