@@ -10,11 +10,12 @@
 // Bound by HBM: the forward has to read x and gate and write y, the backward to
 // read x, gate and g and write two gradients.
 //
-// A workgroup is kSlots slots of kPer positions by kLanes pieces of N channels,
-// so that rows are read in runs of kLanes pieces; a tile is kTile positions.  A
-// slot's positions stay in registers: their map is formed, the slots' maps are
-// joined over the wave's lanes and the waves, and the states follow.
+// A workgroup is 16 slots of a few positions by 16 pieces of N channels, so that
+// rows are read in runs of 16 pieces; a tile is the slots' positions.  A slot's
+// positions stay in registers: their map is formed, the slots' maps are joined
+// over the wave's lanes and the waves, and the states follow.
 #include <algorithm>
+#include <type_traits>
 
 #include "vec16.h"
 
@@ -22,10 +23,12 @@ namespace dc1d {
 
 namespace {
 
-constexpr int kLanes = 16, kSlots = 16, kPer = 4, kTile = kSlots * kPer, kThreads = kLanes * kSlots;
+constexpr int kLanes = 16, kSlots = 16, kThreads = kLanes * kSlots;
 constexpr int kWaveSlots = 64 / kLanes, kWaves = kThreads / 64;
-static_assert(kStateEvery % kTile == 0 || kTile % kStateEvery == 0, "a tile starts at a kept state or the other way round");
+constexpr int kPer = 8, kPerBack = 4;  // positions of a slot
+constexpr int kTile = kSlots * kPer, kTileBack = kSlots * kPerBack;
 static_assert(kStateEvery % kPer == 0, "a kept state stands ahead of a slot");
+static_assert(kTileBack % kStateEvery == 0, "a tile of the backward pass starts at a kept state");
 
 struct RecPlan {
     int slabs, segs, seg_tiles;
@@ -36,11 +39,11 @@ int rec_piece(int C) { return C >= 4 ? 4 : 1; }
 
 // The positions in segments of whole tiles, a workgroup each, until there are
 // four workgroups for every CU; with one segment a workgroup walks through all of them.
-RecPlan plan_recurrence(int B, int L, int C, int num_cus) {
+RecPlan plan_recurrence(int B, int L, int C, int tile, int num_cus) {
     RecPlan p;
     const int P = (C + rec_piece(C) - 1) / rec_piece(C);
     p.slabs = (P + kLanes - 1) / kLanes;
-    const int64_t rows = (int64_t)B * p.slabs, tiles = std::max(1, (L + kTile - 1) / kTile);
+    const int64_t rows = (int64_t)B * p.slabs, tiles = std::max(1, (L + tile - 1) / tile);
     const int64_t want = rows > 0 ? (4ll * num_cus + rows - 1) / rows : 1;
     p.segs = (int)std::max<int64_t>(1, std::min({want, tiles, (int64_t)64}));
     p.seg_tiles = (int)((tiles + p.segs - 1) / p.segs);
@@ -49,10 +52,10 @@ RecPlan plan_recurrence(int B, int L, int C, int num_cus) {
     return p;
 }
 
-// A thread's channels and the order of its sequence.
+// A thread's channels and its sequence.
 template <int N>
 struct Lane {
-    int b, n, slot, at, skip, seg;
+    int b, n, slot, at, skip, seg;  // n: positions within the length
     bool on;
     __device__ __forceinline__ Lane(const RecurrenceArgs &a, const RecPlan &p, int64_t job) {
         const int slab = (int)(job % p.slabs);
@@ -66,10 +69,19 @@ struct Lane {
         at = on ? min(c, a.C - N) : 0;
         skip = on ? c - at : N;
     }
-    __device__ __forceinline__ int64_t row(const RecurrenceArgs &a, int s) const {
-        return a.reverse && s < n ? n - 1 - s : s;
-    }
     __device__ __forceinline__ bool own(int e) const { return e >= skip; }
+};
+
+// A thread's channels of a tensor along the recurrence: position s at p + s * step.
+template <typename T>
+struct Walk {
+    typename T::T *p;
+    int64_t step;
+    template <int N>
+    __device__ __forceinline__ Walk(const void *t, Strides2 st, const RecurrenceArgs &a, const Lane<N> &l) {
+        p = (typename T::T *)t + l.b * st.b + l.at + (a.reverse ? (int64_t)(l.n - 1) * st.l : 0);
+        step = a.reverse ? -st.l : st.l;
+    }
 };
 
 template <int N>
@@ -102,108 +114,174 @@ __device__ __forceinline__ void join_slots(Map<N> own, Map<N> &ahead, Map<N> &ti
     const int place = BACK ? kWaveSlots - 1 - slot : slot;
 #pragma unroll
     for (int d = 1; d < kWaveSlots; d <<= 1) {
-        Map<N> o;
+        const int from = (lane + (BACK ? d : -d) * kLanes) & 63;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const int from = lane + (BACK ? d : -d) * kLanes;
-            o.A[e] = __shfl(own.A[e], from & 63);
-            o.H[e] = __shfl(own.H[e], from & 63);
+            const float A = __shfl(own.A[e], from), H = __shfl(own.H[e], from);
+            own.H[e] = fmaf(own.A[e], place >= d ? H : 0.0f, own.H[e]);
+            own.A[e] *= place >= d ? A : 1.0f;
         }
-        if (place >= d) own.after(o);
     }
+    if (place == kWaveSlots - 1) ends[w][p] = own;
+    const int from = (lane + (BACK ? 1 : -1) * kLanes) & 63;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const int from = lane + (BACK ? 1 : -1) * kLanes;
-        ahead.A[e] = __shfl(own.A[e], from & 63);
-        ahead.H[e] = __shfl(own.H[e], from & 63);
+        const float A = __shfl(own.A[e], from), H = __shfl(own.H[e], from);
+        ahead.A[e] = place > 0 ? A : 1.0f;
+        ahead.H[e] = place > 0 ? H : 0.0f;
     }
-    if (place == 0) ahead.clear();
-    if (place == kWaveSlots - 1) ends[w][p] = own;
     __syncthreads();
     tile.clear();
     Map<N> before = tile;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-        const int from = BACK ? kWaves - 1 - i : i;
-        if (from == w) before = tile;
-        Map<N> o = ends[from][p];
+        const int wave = BACK ? kWaves - 1 - i : i;
+        if (wave == w) before = tile;  // the same for all of a wave
+        Map<N> o = ends[wave][p];
         o.after(tile);
         tile = o;
     }
     ahead.after(before);
 }
 
-// The factors and terms of a slot's positions, (1, 0) past the length.
-template <typename T, int N>
-struct Slot {
-    using P = Piece<T, N>;
-    using E = typename T::T;
-    float a[kPer][N], q[kPer][N], x[kPer][N];  // sigmoid(gate), 1 - it
-    __device__ __forceinline__ void load(const RecurrenceArgs &r, const Lane<N> &t, int s0) {
-        const E *const xp = (const E *)r.x + t.b * r.xs.b + t.at, *const gp = (const E *)r.gate + t.b * r.gates.b + t.at;
-        typename P::Raw xr[kPer], gr[kPer];
+// The rows of a slot's positions, PER of them from s0 on; the last one within
+// the length in place of those past it where FULL is false.
+template <typename T, int N, int PER>
+struct Rows {
+    typename Piece<T, N>::Raw r[PER];
+    template <bool FULL>
+    __device__ __forceinline__ void load(const Walk<T> &w, int s0, int n) {
+        const typename T::T *const p = w.p + (int64_t)s0 * w.step;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int s = s0 + k;
-            if (!t.on || s >= t.n) continue;
-            const int64_t row = t.row(r, s);
-            xr[k] = P::load(xp + row * r.xs.l);
-            gr[k] = P::load(gp + row * r.gates.l);
-        }
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const bool in = t.on && s0 + k < t.n;
-            float f[N] = {}, z[N] = {};
-            if (in) {
-                P::widen(xr[k], f);
-                P::widen(gr[k], z);
-            }
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                sigmoid_pair(z[e], a[k][e], q[k][e]);
-                x[k][e] = f[e];
-                if (!in) a[k][e] = 1.0f, q[k][e] = 0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ float term(int k, int e, bool blend) const { return blend ? q[k][e] * x[k][e] : x[k][e]; }
-    __device__ __forceinline__ Map<N> map(bool blend) const {
-        Map<N> m;
-        m.clear();
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                m.H[e] = fmaf(a[k][e], m.H[e], term(k, e, blend));
-                m.A[e] *= a[k][e];
-            }
-        return m;
+        for (int k = 0; k < PER; ++k)
+            r[k] = Piece<T, N>::load(FULL ? p + k * w.step : w.p + (int64_t)min(s0 + k, n - 1) * w.step);
     }
 };
 
+// sigmoid(gate) and 1 - it, (1, 0) past the length.
+template <typename T, int N, int PER>
+struct Gates {
+    float a[PER][N], q[PER][N];
+    __device__ __forceinline__ Gates(const Rows<T, N, PER> &g) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            float z[N];
+            Piece<T, N>::widen(g.r[k], z);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sigmoid_pair(z[e], a[k][e], q[k][e]);
+        }
+    }
+    __device__ __forceinline__ void end(int s0, int n) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (s0 + k >= n)
+#pragma unroll
+                for (int e = 0; e < N; ++e) a[k][e] = 1.0f, q[k][e] = 0.0f;
+    }
+};
+
+// f in 32 bits, 0 past the length.
+template <typename T, int N, int PER>
+__device__ __forceinline__ void widen_rows(const Rows<T, N, PER> &r, float (*f)[N]) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) Piece<T, N>::widen(r.r[k], f[k]);
+}
+template <int N, int PER>
+__device__ __forceinline__ void end_rows(float (*f)[N], int s0, int n) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        if (s0 + k >= n)
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[k][e] = 0.0f;
+}
+
+template <int N, int PER>
+__device__ __forceinline__ Map<N> map_of(const float (*a)[N], const float (*u)[N]) {
+    Map<N> m;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m.A[e] = a[0][e], m.H[e] = u[0][e];
+#pragma unroll
+    for (int k = 1; k < PER; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            m.H[e] = fmaf(a[k][e], m.H[e], u[k][e]);
+            m.A[e] *= a[k][e];
+        }
+    return m;
+}
+
+// Rows past the length, in a segment's part of the positions, become 0.
+template <typename T, int N>
+__device__ __forceinline__ void clear_rows(void *t, Strides2 st, const Lane<N> &l, int from, int to) {
+    if (!t || !l.on) return;
+    const float zero[N] = {};
+    typename T::T *const p = (typename T::T *)t + l.b * st.b + l.at;
+    for (int s = from + l.slot; s < to; s += kSlots) store_own<T, N>(p + s * st.l, zero, l.skip);
+}
+
+// Walks the tiles of a segment within the length: next(i, FULL) starts the loads
+// of tile i, tile(i, FULL) uses what was loaded last.  A tile's loads are in
+// flight while the one before it is worked on.
+template <int TILE, bool BACK, typename Next, typename Work>
+__device__ __forceinline__ void walk(int first, int past, int n, Next next, Work work) {
+    past = min(past, (n + TILE - 1) / TILE);
+    const int tiles = past - first;
+    for (int j = 0; j < tiles; ++j) {
+        const int i = BACK ? past - 1 - j : first + j;
+        work(i, j, [&] {
+            if (j + 1 < tiles) next(BACK ? i - 1 : i + 1);
+        });
+    }
+}
+
 // The map of every segment but the last: [b][seg][C].  In the last one's place
 // stands the first state, which the next kernel may overwrite with the last.
-template <typename T, int N>
+template <typename T, int N, bool BLEND>
 __global__ __launch_bounds__(kThreads) void k_rec_segments(RecurrenceArgs a, RecPlan p, float2 *out, int64_t jobs) {
     __shared__ Map<N> ends[2][kWaves][kLanes];
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const Lane<N> t(a, p, job);
+        const Walk<T> xw(a.x, a.xs, a, t), gw(a.gate, a.gates, a, t);
         Map<N> all;
         all.clear();
-        const bool none = t.seg == p.segs - 1;
-        if (none && a.state) {
+        if (t.seg == p.segs - 1) {
+            if (a.state)
 #pragma unroll
-            for (int e = 0; e < N; ++e) all.H[e] = a.state[(int64_t)t.b * a.C + t.at + e];
-        }
-        for (int i = 0; i < p.seg_tiles && !none; ++i) {
-            const int s0 = (t.seg * p.seg_tiles + i) * kTile;
-            if (s0 >= t.n) break;
-            Slot<T, N> v;
-            v.load(a, t, s0 + t.slot * kPer);
-            Map<N> ahead, tile;
-            join_slots<N, false>(v.map(a.blend), ahead, tile, ends[i & 1]);
-            tile.after(all);
-            all = tile;
+                for (int e = 0; e < N; ++e) all.H[e] = a.state[(int64_t)t.b * a.C + t.at + e];
+        } else {
+            const int first = t.seg * p.seg_tiles, past = first + p.seg_tiles;
+            Rows<T, N, kPer> xr, gr;
+            auto next = [&](int i) {
+                const int s0 = i * kTile + t.slot * kPer;
+                if ((i + 1) * kTile <= t.n) {
+                    xr.template load<true>(xw, s0, t.n);
+                    gr.template load<true>(gw, s0, t.n);
+                } else {
+                    xr.template load<false>(xw, s0, t.n);
+                    gr.template load<false>(gw, s0, t.n);
+                }
+            };
+            if (first * kTile < t.n) next(first);
+            walk<kTile, false>(first, past, t.n, next, [&](int i, int j, auto then) {
+                const int s0 = i * kTile + t.slot * kPer;
+                Gates<T, N, kPer> v(gr);
+                float u[kPer][N];
+                widen_rows<T, N, kPer>(xr, u);
+                then();
+                if (BLEND)
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k)
+#pragma unroll
+                        for (int e = 0; e < N; ++e) u[k][e] *= v.q[k][e];
+                if ((i + 1) * kTile > t.n) {
+                    v.end(s0, t.n);
+                    end_rows<N, kPer>(u, s0, t.n);
+                }
+                Map<N> ahead, tile;
+                join_slots<N, false>(map_of<N, kPer>(v.a, u), ahead, tile, ends[j & 1]);
+                tile.after(all);
+                all = tile;
+            });
         }
         __syncthreads();
         if (t.slot == 0) {
@@ -220,7 +298,6 @@ __global__ __launch_bounds__(kThreads) void k_rec_segments(RecurrenceArgs a, Rec
 template <int N>
 __device__ __forceinline__ void carry_in(const RecurrenceArgs &a, const RecPlan &p, const Lane<N> &t, const float *start,
                                          const float2 *maps, int from, int to, int step, float *h) {
-    if (!t.on) return;
     if (p.segs > 1) {  // from the place of the map that nobody needs
         const float2 *const m = maps + ((int64_t)t.b * p.segs + (step > 0 ? p.segs - 1 : 0)) * a.C + t.at;
 #pragma unroll
@@ -239,47 +316,76 @@ __device__ __forceinline__ void carry_in(const RecurrenceArgs &a, const RecPlan 
     }
 }
 
-template <typename T, int N>
+template <typename T, int N, bool BLEND>
 __global__ __launch_bounds__(kThreads) void k_recurrence(RecurrenceArgs a, RecPlan p, const float2 *maps, int64_t jobs) {
     using E = typename T::T;
     __shared__ Map<N> ends[2][kWaves][kLanes];
-    const int kept = (a.L + kStateEvery - 1) / kStateEvery, tiles = (a.L + kTile - 1) / kTile;
+    const int kept = (a.L + kStateEvery - 1) / kStateEvery;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const Lane<N> t(a, p, job);
+        const Walk<T> xw(a.x, a.xs, a, t), gw(a.gate, a.gates, a, t), yw(a.y, a.ys, a, t);
         const int64_t bc = (int64_t)t.b * a.C + t.at;
+        const int first = t.seg * p.seg_tiles, past = first + p.seg_tiles;
+        Rows<T, N, kPer> xr, gr;
+        auto next = [&](int i) {
+            const int s0 = i * kTile + t.slot * kPer;
+            if ((i + 1) * kTile <= t.n) {
+                xr.template load<true>(xw, s0, t.n);
+                gr.template load<true>(gw, s0, t.n);
+            } else {
+                xr.template load<false>(xw, s0, t.n);
+                gr.template load<false>(gw, s0, t.n);
+            }
+        };
+        if (first * kTile < t.n) next(first);
         float h0[N] = {};
         carry_in<N>(a, p, t, a.state, maps, 0, t.seg, 1, h0);
-        const int first = t.seg * p.seg_tiles, past = min(first + p.seg_tiles, tiles);
-        for (int i = first; i < past; ++i) {
+        auto keep = [&](int s, const float *h) {
+            float *const o = a.states + ((int64_t)t.b * kept + s / kStateEvery) * a.C + t.at;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (t.own(e)) o[e] = h[e];
+        };
+        walk<kTile, false>(first, past, t.n, next, [&](int i, int j, auto then) {
             const int s0 = i * kTile + t.slot * kPer;
-            Slot<T, N> v;
-            v.load(a, t, s0);
+            const bool full = (i + 1) * kTile <= t.n;
+            Gates<T, N, kPer> v(gr);
+            float u[kPer][N];
+            widen_rows<T, N, kPer>(xr, u);
+            then();
+            if (BLEND)
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) u[k][e] *= v.q[k][e];
+            if (!full) {
+                v.end(s0, t.n);
+                end_rows<N, kPer>(u, s0, t.n);
+            }
             Map<N> ahead, tile;
-            join_slots<N, false>(v.map(a.blend), ahead, tile, ends[i & 1]);
+            join_slots<N, false>(map_of<N, kPer>(v.a, u), ahead, tile, ends[j & 1]);
             float h[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) h[e] = h0[e];
             ahead.apply(h);
             tile.apply(h0);
-            if (a.states && t.on && s0 % kStateEvery == 0 && s0 < a.L) {
-                float *const o = a.states + ((int64_t)t.b * kept + s0 / kStateEvery) * a.C + t.at;
+            if (!t.on) return;
+            if (a.states && s0 % kStateEvery == 0 && s0 < a.L) keep(s0, h);
 #pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (t.own(e)) o[e] = h[e];
-            }
-            E *const y = (E *)a.y + t.b * a.ys.b + t.at;
+            for (int k = 0; k < kPer; ++k)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int s = s0 + k;
-                float f[N];
+                for (int e = 0; e < N; ++e) u[k][e] = h[e] = fmaf(v.a[k][e], h[e], u[k][e]);
+            E *const y = yw.p + (int64_t)s0 * yw.step;
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    h[e] = fmaf(v.a[k][e], h[e], v.term(k, e, a.blend));
-                    f[e] = s < t.n ? h[e] : 0.0f;
-                }
-                if (t.on && s < a.L) store_own<T, N>(y + t.row(a, s) * a.ys.l, f, t.skip);
-            }
-        }
+            for (int k = 0; k < kPer; ++k)
+                if (full || s0 + k < t.n) store_own<T, N>(y + k * yw.step, u[k], t.skip);
+        });
+        // past the length: no outputs, and the last state from the next tile's start on
+        const int from = max(first * kTile, t.n), to = min(past * kTile, a.L);
+        clear_rows<T, N>(a.y, a.ys, t, from, to);
+        if (a.states && t.on)
+            for (int s = (max((t.n + kTile - 1) / kTile, first) * (kTile / kPer) + t.slot) * kPer; s < to; s += kTile)
+                if (s % kStateEvery == 0) keep(s, h0);
         __syncthreads();
         if (a.last && t.on && t.seg == p.segs - 1 && t.slot == 0) {
 #pragma unroll
@@ -294,29 +400,16 @@ __global__ __launch_bounds__(kThreads) void k_recurrence(RecurrenceArgs a, RecPl
 // m_s = a_s r_s = a_s (m_{s+1} + g_s): the gradient of the state ahead of s, a
 // scan from the end whose maps have the same factors.
 
-template <typename T, int N>
-__device__ __forceinline__ void load_grad(const RecurrenceArgs &r, const Lane<N> &t, int s0, float (*g)[N]) {
-    using P = Piece<T, N>;
-    const typename T::T *const p = (const typename T::T *)r.g + t.b * r.gs.b + t.at;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        float f[N] = {};
-        if (t.on && s0 + k < t.n) P::widen(P::load(p + t.row(r, s0 + k) * r.gs.l), f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) g[k][e] = f[e];
-    }
-}
-
-template <typename T, int N>
-__device__ __forceinline__ Map<N> back_map(const Slot<T, N> &v, float (*g)[N]) {
+template <int N, int PER>
+__device__ __forceinline__ Map<N> back_map(const float (*a)[N], const float (*g)[N]) {
     Map<N> m;
     m.clear();
 #pragma unroll
-    for (int k = kPer - 1; k >= 0; --k)
+    for (int k = PER - 1; k >= 0; --k)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            m.H[e] = v.a[k][e] * (m.H[e] + g[k][e]);
-            m.A[e] *= v.a[k][e];
+            m.H[e] = a[k][e] * (m.H[e] + g[k][e]);
+            m.A[e] *= a[k][e];
         }
     return m;
 }
@@ -326,28 +419,45 @@ __device__ __forceinline__ Map<N> back_map(const Slot<T, N> &v, float (*g)[N]) {
 template <typename T, int N>
 __global__ __launch_bounds__(kThreads) void k_rec_back_segments(RecurrenceArgs a, RecPlan p, float2 *out, int64_t jobs) {
     __shared__ Map<N> ends[2][kWaves][kLanes];
-    const int tiles = (a.L + kTile - 1) / kTile;
+    constexpr int TILE = kTileBack, PER = kPerBack;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const Lane<N> t(a, p, job);
+        const Walk<T> dw(a.g, a.gs, a, t), gw(a.gate, a.gates, a, t);
         Map<N> all;
         all.clear();
-        const bool none = t.seg == 0;
-        if (none && a.g_last) {
+        if (t.seg == 0) {
+            if (a.g_last)
 #pragma unroll
-            for (int e = 0; e < N; ++e) all.H[e] = a.g_last[(int64_t)t.b * a.C + t.at + e];
-        }
-        const int first = t.seg * p.seg_tiles, past = min(first + p.seg_tiles, tiles);
-        for (int i = past - 1; i >= first && !none; --i) {
-            if (i * kTile >= t.n) continue;
-            const int s0 = i * kTile + t.slot * kPer;
-            Slot<T, N> v;
-            v.load(a, t, s0);
-            float g[kPer][N];
-            load_grad<T, N>(a, t, s0, g);
-            Map<N> behind, tile;
-            join_slots<N, true>(back_map<T, N>(v, g), behind, tile, ends[i & 1]);
-            tile.after(all);
-            all = tile;
+                for (int e = 0; e < N; ++e) all.H[e] = a.g_last[(int64_t)t.b * a.C + t.at + e];
+        } else {
+            const int first = t.seg * p.seg_tiles, past = min(first + p.seg_tiles, (t.n + TILE - 1) / TILE);
+            Rows<T, N, PER> dr, gr;
+            auto next = [&](int i) {
+                const int s0 = i * TILE + t.slot * PER;
+                if ((i + 1) * TILE <= t.n) {
+                    dr.template load<true>(dw, s0, t.n);
+                    gr.template load<true>(gw, s0, t.n);
+                } else {
+                    dr.template load<false>(dw, s0, t.n);
+                    gr.template load<false>(gw, s0, t.n);
+                }
+            };
+            if (past > first) next(past - 1);
+            walk<TILE, true>(first, past, t.n, next, [&](int i, int j, auto then) {
+                const int s0 = i * TILE + t.slot * PER;
+                Gates<T, N, PER> v(gr);
+                float g[PER][N];
+                widen_rows<T, N, PER>(dr, g);
+                then();
+                if ((i + 1) * TILE > t.n) {
+                    v.end(s0, t.n);
+                    end_rows<N, PER>(g, s0, t.n);
+                }
+                Map<N> behind, tile;
+                join_slots<N, true>(back_map<N, PER>(v.a, g), behind, tile, ends[j & 1]);
+                tile.after(all);
+                all = tile;
+            });
         }
         __syncthreads();
         if (t.slot == 0) {
@@ -359,63 +469,98 @@ __global__ __launch_bounds__(kThreads) void k_rec_back_segments(RecurrenceArgs a
     }
 }
 
-template <typename T, int N>
+template <typename T, int N, bool BLEND>
 __global__ __launch_bounds__(kThreads) void k_recurrence_back(RecurrenceArgs a, RecPlan p, const float2 *maps, int64_t jobs) {
     using E = typename T::T;
     __shared__ Map<N> ends[2][2][kWaves][kLanes];
-    const int kept = (a.L + kStateEvery - 1) / kStateEvery, tiles = (a.L + kTile - 1) / kTile;
+    constexpr int TILE = kTileBack, PER = kPerBack;
+    const int kept = (a.L + kStateEvery - 1) / kStateEvery;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const Lane<N> t(a, p, job);
+        const Walk<T> xw(a.x, a.xs, a, t), gw(a.gate, a.gates, a, t), dw(a.g, a.gs, a, t), gxw(a.gx, a.gxs, a, t), ggw(a.gg, a.ggs, a, t);
         const int64_t bc = (int64_t)t.b * a.C + t.at;
+        const int first = t.seg * p.seg_tiles, whole = first + p.seg_tiles, past = min(whole, (t.n + TILE - 1) / TILE);
+        Rows<T, N, PER> xr, gr, dr;
+        float hn[N];  // the state that a tile starts from
+        auto next = [&](int i) {
+            const int s0 = i * TILE + t.slot * PER;
+            if ((i + 1) * TILE <= t.n) {
+                xr.template load<true>(xw, s0, t.n);
+                gr.template load<true>(gw, s0, t.n);
+                dr.template load<true>(dw, s0, t.n);
+            } else {
+                xr.template load<false>(xw, s0, t.n);
+                gr.template load<false>(gw, s0, t.n);
+                dr.template load<false>(dw, s0, t.n);
+            }
+            const float *const st = a.states + ((int64_t)t.b * kept + (int64_t)i * TILE / kStateEvery) * a.C + t.at;
+#pragma unroll
+            for (int e = 0; e < N; ++e) hn[e] = st[e];
+        };
+        if (past > first) next(past - 1);
         float m0[N] = {};
         carry_in<N>(a, p, t, a.g_last, maps, p.segs - 1, t.seg, -1, m0);
-        const int first = t.seg * p.seg_tiles, past = min(first + p.seg_tiles, tiles);
-        for (int i = past - 1; i >= first; --i) {
-            const int s0 = i * kTile + t.slot * kPer;
-            Slot<T, N> v;
-            v.load(a, t, s0);
-            float g[kPer][N], h[N] = {}, m[N];
-            load_grad<T, N>(a, t, s0, g);
-            if (t.on) {
-                const float *const st = a.states + ((int64_t)t.b * kept + (int64_t)i * kTile / kStateEvery) * a.C + t.at;
+        walk<TILE, true>(first, past, t.n, next, [&](int i, int j, auto then) {
+            const int s0 = i * TILE + t.slot * PER;
+            const bool full = (i + 1) * TILE <= t.n;
+            Gates<T, N, PER> v(gr);
+            float x[PER][N], g[PER][N], h[N], m[N], u[PER][N];
+            widen_rows<T, N, PER>(xr, x);
+            widen_rows<T, N, PER>(dr, g);
 #pragma unroll
-                for (int e = 0; e < N; ++e) h[e] = st[e];
+            for (int e = 0; e < N; ++e) h[e] = hn[e];
+            then();
+            if (!full) {
+                v.end(s0, t.n);
+                end_rows<N, PER>(x, s0, t.n);
+                end_rows<N, PER>(g, s0, t.n);
             }
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+#pragma unroll
+                for (int e = 0; e < N; ++e) u[k][e] = BLEND ? v.q[k][e] * x[k][e] : x[k][e];
             Map<N> ahead, behind, tile;
-            join_slots<N, false>(v.map(a.blend), ahead, tile, ends[i & 1][0]);
-            join_slots<N, true>(back_map<T, N>(v, g), behind, tile, ends[i & 1][1]);
+            join_slots<N, false>(map_of<N, PER>(v.a, u), ahead, tile, ends[j & 1][0]);
+            join_slots<N, true>(back_map<N, PER>(v.a, g), behind, tile, ends[j & 1][1]);
             ahead.apply(h);
 #pragma unroll
             for (int e = 0; e < N; ++e) m[e] = m0[e];
             behind.apply(m);
             tile.apply(m0);
+            if (!t.on) return;
             // the state ahead of each position (less x), then the gradients from the last one on
-            float d[kPer][N];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
+            for (int k = 0; k < PER; ++k)
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    d[k][e] = a.blend ? h[e] - v.x[k][e] : h[e];
-                    h[e] = fmaf(v.a[k][e], h[e], v.term(k, e, a.blend));
+                    x[k][e] = BLEND ? h[e] - x[k][e] : h[e];
+                    h[e] = fmaf(v.a[k][e], h[e], u[k][e]);
                 }
-            E *const gx = (E *)a.gx + t.b * a.gxs.b + t.at, *const gg = (E *)a.gg + t.b * a.ggs.b + t.at;
 #pragma unroll
-            for (int k = kPer - 1; k >= 0; --k) {
-                const int s = s0 + k;
-                float fx[N], fg[N];
+            for (int k = PER - 1; k >= 0; --k)
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     const float r = m[e] + g[k][e];
                     m[e] = v.a[k][e] * r;
-                    fx[e] = s < t.n ? (a.blend ? r * v.q[k][e] : r) : 0.0f;
-                    fg[e] = s < t.n ? m[e] * v.q[k][e] * d[k][e] : 0.0f;
+                    g[k][e] = BLEND ? r * v.q[k][e] : r;
+                    x[k][e] = m[e] * v.q[k][e] * x[k][e];
                 }
-                if (!t.on || s >= a.L) continue;
-                const int64_t row = t.row(a, s);
-                if (a.gx) store_own<T, N>(gx + row * a.gxs.l, fx, t.skip);
-                if (a.gg) store_own<T, N>(gg + row * a.ggs.l, fg, t.skip);
+            if (a.gx) {
+                E *const o = gxw.p + (int64_t)s0 * gxw.step;
+#pragma unroll
+                for (int k = 0; k < PER; ++k)
+                    if (full || s0 + k < t.n) store_own<T, N>(o + k * gxw.step, g[k], t.skip);
             }
-        }
+            if (a.gg) {
+                E *const o = ggw.p + (int64_t)s0 * ggw.step;
+#pragma unroll
+                for (int k = 0; k < PER; ++k)
+                    if (full || s0 + k < t.n) store_own<T, N>(o + k * ggw.step, x[k], t.skip);
+            }
+        });
+        const int from = max(first * TILE, t.n), to = min(whole * TILE, a.L);
+        clear_rows<T, N>(a.gx, a.gxs, t, from, to);
+        clear_rows<T, N>(a.gg, a.ggs, t, from, to);
         __syncthreads();
         if (a.g_state && t.on && t.seg == 0 && t.slot == 0) {
 #pragma unroll
@@ -428,37 +573,48 @@ __global__ __launch_bounds__(kThreads) void k_recurrence_back(RecurrenceArgs a, 
 constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch; more jobs are looped over
 unsigned grid_for(int64_t jobs) { return (unsigned)std::min(jobs, kMaxGrid); }
 
-template <typename T, int N>
+template <typename T, int N, bool BLEND>
 hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    const RecPlan p = plan_recurrence(a.B, a.L, a.C, num_cus);
+    const RecPlan p = plan_recurrence(a.B, a.L, a.C, kTile, num_cus);
     const int64_t jobs = (int64_t)a.B * p.segs * p.slabs;
-    if (p.segs > 1) hipLaunchKernelGGL((k_rec_segments<T, N>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (float2 *)a.ws, jobs);
-    hipLaunchKernelGGL((k_recurrence<T, N>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (const float2 *)a.ws, jobs);
+    if (p.segs > 1)
+        hipLaunchKernelGGL((k_rec_segments<T, N, BLEND>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (float2 *)a.ws, jobs);
+    hipLaunchKernelGGL((k_recurrence<T, N, BLEND>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (const float2 *)a.ws, jobs);
     return hipGetLastError();
 }
 
-template <typename T, int N>
+template <typename T, int N, bool BLEND>
 hipError_t run_back(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    const RecPlan p = plan_recurrence(a.B, a.L, a.C, num_cus);
+    const RecPlan p = plan_recurrence(a.B, a.L, a.C, kTileBack, num_cus);
     const int64_t jobs = (int64_t)a.B * p.segs * p.slabs;
     if (p.segs > 1)
         hipLaunchKernelGGL((k_rec_back_segments<T, N>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (float2 *)a.ws, jobs);
-    hipLaunchKernelGGL((k_recurrence_back<T, N>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (const float2 *)a.ws, jobs);
+    hipLaunchKernelGGL((k_recurrence_back<T, N, BLEND>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (const float2 *)a.ws, jobs);
     return hipGetLastError();
+}
+
+template <typename F>
+hipError_t by_type(const RecurrenceArgs &a, F f) {
+    auto blend = [&](auto t, auto n) { return a.blend ? f(t, n, std::true_type()) : f(t, n, std::false_type()); };
+    auto piece = [&](auto t) {
+        return rec_piece(a.C) == 4 ? blend(t, std::integral_constant<int, 4>()) : blend(t, std::integral_constant<int, 1>());
+    };
+    return a.dtype == kF32 ? piece(F32()) : piece(BF16());
 }
 
 }  // namespace
 
-size_t recurrence_workspace(int B, int L, int C, int, bool, int num_cus) { return plan_recurrence(B, L, C, num_cus).ws_bytes; }
+size_t recurrence_workspace(int B, int L, int C, int, bool backward, int num_cus) {
+    return plan_recurrence(B, L, C, backward ? kTileBack : kTile, num_cus).ws_bytes;
+}
 
 hipError_t launch_recurrence(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    if (a.dtype == kF32) return a.C >= 4 ? run<F32, 4>(a, num_cus, stream) : run<F32, 1>(a, num_cus, stream);
-    return a.C >= 4 ? run<BF16, 4>(a, num_cus, stream) : run<BF16, 1>(a, num_cus, stream);
+    return by_type(a, [&](auto t, auto n, auto blend) { return run<decltype(t), decltype(n)::value, decltype(blend)::value>(a, num_cus, stream); });
 }
 
 hipError_t launch_recurrence_backward(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    if (a.dtype == kF32) return a.C >= 4 ? run_back<F32, 4>(a, num_cus, stream) : run_back<F32, 1>(a, num_cus, stream);
-    return a.C >= 4 ? run_back<BF16, 4>(a, num_cus, stream) : run_back<BF16, 1>(a, num_cus, stream);
+    return by_type(a,
+                   [&](auto t, auto n, auto blend) { return run_back<decltype(t), decltype(n)::value, decltype(blend)::value>(a, num_cus, stream); });
 }
 
 }  // namespace dc1d
