@@ -6,14 +6,15 @@
 //   ggate = r (h_{s-1} or h_{s-1} - x) a (1 - a),  gstate = a_0 r_0
 //
 // s counts the positions in the recurrence's order.  Both are scans of affine
-// maps h -> A h + H, which are joined as (A, H) then (A', H') = (A A', A' H + H').
-// Bound by HBM: the forward has to read x and gate and write y, the backward to
-// read x, gate and g and write two gradients.
+// maps h -> A h + H, joined as (A, H) then (A', H') = (A A', A' H + H').  Bound
+// by HBM: the forward has to read x and gate and write y, the backward to read x,
+// gate and g and write two gradients; at some 30 and 45 instructions an element
+// the arithmetic takes more than half of that time and has to run beside it.
 //
 // A workgroup is 16 slots of a few positions by 16 pieces of N channels, so that
 // rows are read in runs of 16 pieces; a tile is the slots' positions.  A slot's
 // positions stay in registers: their map is formed, the slots' maps are joined
-// over the wave's lanes and the waves, and the states follow.
+// over the wave's rows of lanes and the waves, and the states follow.
 #include <algorithm>
 #include <type_traits>
 
@@ -23,45 +24,24 @@ namespace dc1d {
 
 namespace {
 
-constexpr int kLanes = 16, kSlots = 16, kThreads = kLanes * kSlots;
-constexpr int kWaveSlots = 64 / kLanes, kWaves = kThreads / 64;
-constexpr int kPer = 8, kPerBack = 4;  // positions of a slot
-constexpr int kTile = kSlots * kPer, kTileBack = kSlots * kPerBack;
+constexpr int kLanes = 16, kSlots = 16, kThreads = kLanes * kSlots, kWaves = kThreads / 64;
+constexpr int kPer = 4, kPerBack = 4;  // positions of a slot
 static_assert(kStateEvery % kPer == 0, "a kept state stands ahead of a slot");
-static_assert(kTileBack % kStateEvery == 0, "a tile of the backward pass starts at a kept state");
+static_assert(kSlots * kPerBack % kStateEvery == 0, "a tile of the backward pass starts at a kept state");
 
-struct RecPlan {
-    int slabs, segs, seg_tiles;
-    size_t ws_bytes;
-};
-
-int rec_piece(int C) { return C >= 4 ? 4 : 1; }
-
-// The positions in segments of whole tiles, a workgroup each, until there are
-// four workgroups for every CU; with one segment a workgroup walks through all of them.
-RecPlan plan_recurrence(int B, int L, int C, int tile, int num_cus) {
-    RecPlan p;
-    const int P = (C + rec_piece(C) - 1) / rec_piece(C);
-    p.slabs = (P + kLanes - 1) / kLanes;
-    const int64_t rows = (int64_t)B * p.slabs, tiles = std::max(1, (L + tile - 1) / tile);
-    const int64_t want = rows > 0 ? (4ll * num_cus + rows - 1) / rows : 1;
-    p.segs = (int)std::max<int64_t>(1, std::min({want, tiles, (int64_t)64}));
-    p.seg_tiles = (int)((tiles + p.segs - 1) / p.segs);
-    p.segs = (int)((tiles + p.seg_tiles - 1) / p.seg_tiles);
-    p.ws_bytes = p.segs > 1 ? (size_t)B * p.segs * C * sizeof(float2) : 0;
-    return p;
-}
+// Offsets inside a tile: 32 bits for pieces of four channels, 64 for single ones,
+// which also serve rows too far apart for that.
+template <int N>
+using Offset = std::conditional_t<N == 1, int64_t, uint32_t>;
 
 // A thread's channels and its sequence.
 template <int N>
 struct Lane {
-    int b, n, slot, at, skip, seg;  // n: positions within the length
+    int b, n, slot, at, skip;  // n: positions within the length
     bool on;
-    __device__ __forceinline__ Lane(const RecurrenceArgs &a, const RecPlan &p, int64_t job) {
-        const int slab = (int)(job % p.slabs);
-        const int64_t q = job / p.slabs;
-        seg = (int)(q % p.segs);
-        b = (int)(q / p.segs);
+    __device__ __forceinline__ Lane(const RecurrenceArgs &a, uint32_t chain, const FastDiv &by_slabs) {
+        b = (int)fdiv(chain, by_slabs);
+        const int slab = (int)(chain - (uint32_t)b * by_slabs.d);
         n = a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
         slot = threadIdx.x / kLanes;
         const int c = (slab * kLanes + threadIdx.x % kLanes) * N;
@@ -70,19 +50,71 @@ struct Lane {
         skip = on ? c - at : N;
     }
     __device__ __forceinline__ bool own(int e) const { return e >= skip; }
-};
-
-// A thread's channels of a tensor along the recurrence: position s at p + s * step.
-template <typename T>
-struct Walk {
-    typename T::T *p;
-    int64_t step;
-    template <int N>
-    __device__ __forceinline__ Walk(const void *t, Strides2 st, const RecurrenceArgs &a, const Lane<N> &l) {
-        p = (typename T::T *)t + l.b * st.b + l.at + (a.reverse ? (int64_t)(l.n - 1) * st.l : 0);
-        step = a.reverse ? -st.l : st.l;
+    __device__ __forceinline__ int64_t state(const RecurrenceArgs &a) const { return (int64_t)b * a.C + at; }
+    // the kept state ahead of position s
+    __device__ __forceinline__ int64_t kept(const RecurrenceArgs &a, int s) const {
+        return ((int64_t)b * ((a.L + kStateEvery - 1) / kStateEvery) + s / kStateEvery) * a.C + at;
     }
 };
+
+// A piece's store; only where C is no multiple of a piece (ODD) may elements of it
+// be its neighbour's.
+template <typename T, int N, bool ODD>
+__device__ __forceinline__ void put(typename T::T *p, const float *f, int skip) {
+    if constexpr (ODD)
+        store_own<T, N>(p, f, skip);
+    else
+        Piece<T, N>::store(p, f);
+}
+
+// A slot's rows of a tensor in one tile: a base that all threads share, and
+// offsets.  Reversed, the tile's last position is the base.
+template <typename T, int N, int PER>
+struct Walk {
+    static constexpr int TILE = kSlots * PER;
+    using E = typename T::T;
+    char *base;
+    Offset<N> off, step;
+    __device__ __forceinline__ Walk(const void *t, Strides2 st, const RecurrenceArgs &a, const Lane<N> &l, int tile) {
+        const int64_t row = a.reverse ? (int64_t)max(l.n, 1) - (int64_t)(tile + 1) * TILE : (int64_t)tile * TILE;
+        base = (char *)t + (l.b * st.b + row * st.l) * (int64_t)sizeof(E);
+        step = (Offset<N>)(st.l * (int64_t)sizeof(E));
+        off = (Offset<N>)(l.at * sizeof(E)) + (Offset<N>)(a.reverse ? TILE - 1 - l.slot * PER : l.slot * PER) * step;
+        if (a.reverse) step = 0 - step;
+    }
+    __device__ __forceinline__ E *at(int k) const { return (E *)(base + (off + (Offset<N>)k * step)); }
+};
+
+// A tile past the length reads the last one within it (and uses none of it): the
+// rows that are read lie in the tile that they are read from, so that no offset
+// is negative.
+template <int TILE>
+__device__ __forceinline__ int last_tile(int n, int i) {
+    return min(i, (max(n, 1) - 1) / TILE);
+}
+
+template <typename T, int N, int PER>
+struct Rows {
+    typename Piece<T, N>::Raw r[PER];
+    // `last`: the sequence's last position within the length (the first, for none),
+    // counted from the slot's first, in place of those past it
+    template <bool FULL>
+    __device__ __forceinline__ void load(const Walk<T, N, PER> &w, int last) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) r[k] = Piece<T, N>::load(w.at(FULL ? k : min(k, last)));
+    }
+    __device__ __forceinline__ void widen(float (*f)[N]) const {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) Piece<T, N>::widen(r[k], f[k]);
+    }
+};
+
+// Keeps what uses `v` behind what came before: the compiler would start all of a
+// slot's exponentials at once and hold some 100 registers more for them.
+template <typename V>
+__device__ __forceinline__ void hold(V &v) {
+    asm volatile("" : "+v"(v));
+}
 
 template <int N>
 struct Map {  // h -> A h + H
@@ -103,114 +135,94 @@ struct Map {  // h -> A h + H
 #pragma unroll
         for (int e = 0; e < N; ++e) h[e] = fmaf(A[e], h[e], H[e]);
     }
-};
-
-// The maps of the slots ahead of a thread's in its tile (of those behind it
-// where BACK), and the whole tile's.  `ends` holds a map for every wave and lane;
-// the caller's barriers keep one tile's from the next.
-template <int N, bool BACK>
-__device__ __forceinline__ void join_slots(Map<N> own, Map<N> &ahead, Map<N> &tile, Map<N> (*ends)[kLanes]) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, slot = lane / kLanes, p = lane % kLanes;
-    const int place = BACK ? kWaveSlots - 1 - slot : slot;
-#pragma unroll
-    for (int d = 1; d < kWaveSlots; d <<= 1) {
-        const int from = (lane + (BACK ? d : -d) * kLanes) & 63;
+    // this one, then h -> a h + u
+    __device__ __forceinline__ void then(const float *a, const float *u) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const float A = __shfl(own.A[e], from), H = __shfl(own.H[e], from);
-            own.H[e] = fmaf(own.A[e], place >= d ? H : 0.0f, own.H[e]);
-            own.A[e] *= place >= d ? A : 1.0f;
+            H[e] = fmaf(a[e], H[e], u[e]);
+            A[e] *= a[e];
         }
     }
-    if (place == kWaveSlots - 1) ends[w][p] = own;
-    const int from = (lane + (BACK ? 1 : -1) * kLanes) & 63;
+    __device__ __forceinline__ void hold_all() {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            hold(A[e]);
+            hold(H[e]);
+        }
+    }
+    // this one, then h -> a (h + g)
+    __device__ __forceinline__ void then_back(const float *a, const float *g) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            H[e] = a[e] * (H[e] + g[e]);
+            A[e] *= a[e];
+        }
+    }
+};
+
+// A wave's four slots: the map of those ahead of a thread's (of those behind it
+// where BACK) to `ahead`, the wave's to `ends`.  The slots are rows of 16 lanes:
+// v_permlane16_swap gives both rows of a pair their even and odd row's values,
+// v_permlane32_swap both halves' to both.  The caller's barriers keep `ends` from
+// the next use; two of them in turn need one barrier each.
+template <int N>
+using Ends = Map<N>[kWaves][kLanes];
+
+template <int N, bool BACK>
+__device__ __forceinline__ void join_slots(const Map<N> &own, Map<N> &ahead, Ends<N> &ends) {
+    const int lane = threadIdx.x & 63;
+    const bool second = ((lane >> 4) & 1) != BACK, later = (lane >> 5) != BACK;
+    Map<N> all;
+    auto both = [](float v, bool wide, float &first, float &next) {
+        const auto r = wide ? __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false)
+                            : __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        first = __uint_as_float(r[BACK ? 1 : 0]);
+        next = __uint_as_float(r[BACK ? 0 : 1]);
+    };
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const float A = __shfl(own.A[e], from), H = __shfl(own.H[e], from);
-        ahead.A[e] = place > 0 ? A : 1.0f;
-        ahead.H[e] = place > 0 ? H : 0.0f;
+        float A1, A2, H1, H2;
+        both(own.A[e], false, A1, A2);
+        both(own.H[e], false, H1, H2);
+        const float A = second ? A1 : 1.0f, H = second ? H1 : 0.0f;
+        H2 = fmaf(A2, H1, H2);
+        A2 *= A1;
+        both(A2, true, A1, A2);
+        both(H2, true, H1, H2);
+        ahead.A[e] = A * (later ? A1 : 1.0f);
+        ahead.H[e] = fmaf(A, later ? H1 : 0.0f, H);
+        all.A[e] = A2 * A1;
+        all.H[e] = fmaf(A2, H1, H2);
     }
-    __syncthreads();
-    tile.clear();
-    Map<N> before = tile;
+    if (lane < kLanes) ends[threadIdx.x >> 6][lane] = all;
+}
+
+// After a barrier: h goes from the tile's start to its end, and `here` is the state ahead of the thread's wave.
+template <int N, bool BACK>
+__device__ __forceinline__ void pass_waves(const Ends<N> &ends, float *h, float *here) {
+    const int w = threadIdx.x >> 6, p = threadIdx.x % kLanes;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
         const int wave = BACK ? kWaves - 1 - i : i;
-        if (wave == w) before = tile;  // the same for all of a wave
-        Map<N> o = ends[wave][p];
-        o.after(tile);
-        tile = o;
+        if (wave == w)  // the same for all of a wave
+#pragma unroll
+            for (int e = 0; e < N; ++e) here[e] = h[e];
+        ends[wave][p].apply(h);
     }
-    ahead.after(before);
 }
 
-// The rows of a slot's positions, PER of them from s0 on; the last one within
-// the length in place of those past it where FULL is false.
-template <typename T, int N, int PER>
-struct Rows {
-    typename Piece<T, N>::Raw r[PER];
-    template <bool FULL>
-    __device__ __forceinline__ void load(const Walk<T> &w, int s0, int n) {
-        const typename T::T *const p = w.p + (int64_t)s0 * w.step;
+// After a barrier: the map of all of the waves' slots, behind `m`.
+template <int N, bool BACK>
+__device__ __forceinline__ void join_waves(const Ends<N> &ends, Map<N> &m) {
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
-            r[k] = Piece<T, N>::load(FULL ? p + k * w.step : w.p + (int64_t)min(s0 + k, n - 1) * w.step);
+    for (int i = 0; i < kWaves; ++i) {
+        Map<N> o = ends[BACK ? kWaves - 1 - i : i][threadIdx.x % kLanes];
+        o.after(m);
+        m = o;
     }
-};
-
-// sigmoid(gate) and 1 - it, (1, 0) past the length.
-template <typename T, int N, int PER>
-struct Gates {
-    float a[PER][N], q[PER][N];
-    __device__ __forceinline__ Gates(const Rows<T, N, PER> &g) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            float z[N];
-            Piece<T, N>::widen(g.r[k], z);
-#pragma unroll
-            for (int e = 0; e < N; ++e) sigmoid_pair(z[e], a[k][e], q[k][e]);
-        }
-    }
-    __device__ __forceinline__ void end(int s0, int n) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-            if (s0 + k >= n)
-#pragma unroll
-                for (int e = 0; e < N; ++e) a[k][e] = 1.0f, q[k][e] = 0.0f;
-    }
-};
-
-// f in 32 bits, 0 past the length.
-template <typename T, int N, int PER>
-__device__ __forceinline__ void widen_rows(const Rows<T, N, PER> &r, float (*f)[N]) {
-#pragma unroll
-    for (int k = 0; k < PER; ++k) Piece<T, N>::widen(r.r[k], f[k]);
-}
-template <int N, int PER>
-__device__ __forceinline__ void end_rows(float (*f)[N], int s0, int n) {
-#pragma unroll
-    for (int k = 0; k < PER; ++k)
-        if (s0 + k >= n)
-#pragma unroll
-            for (int e = 0; e < N; ++e) f[k][e] = 0.0f;
 }
 
-template <int N, int PER>
-__device__ __forceinline__ Map<N> map_of(const float (*a)[N], const float (*u)[N]) {
-    Map<N> m;
-#pragma unroll
-    for (int e = 0; e < N; ++e) m.A[e] = a[0][e], m.H[e] = u[0][e];
-#pragma unroll
-    for (int k = 1; k < PER; ++k)
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            m.H[e] = fmaf(a[k][e], m.H[e], u[k][e]);
-            m.A[e] *= a[k][e];
-        }
-    return m;
-}
-
-// Rows past the length, in a segment's part of the positions, become 0.
+// Rows past the length become 0: positions from ... to - 1, slot by slot.
 template <typename T, int N>
 __device__ __forceinline__ void clear_rows(void *t, Strides2 st, const Lane<N> &l, int from, int to) {
     if (!t || !l.on) return;
@@ -219,180 +231,195 @@ __device__ __forceinline__ void clear_rows(void *t, Strides2 st, const Lane<N> &
     for (int s = from + l.slot; s < to; s += kSlots) store_own<T, N>(p + s * st.l, zero, l.skip);
 }
 
-// Walks the tiles of a segment within the length: next(i, FULL) starts the loads
-// of tile i, tile(i, FULL) uses what was loaded last.  A tile's loads are in
-// flight while the one before it is worked on.
-template <int TILE, bool BACK, typename Next, typename Work>
-__device__ __forceinline__ void walk(int first, int past, int n, Next next, Work work) {
-    past = min(past, (n + TILE - 1) / TILE);
-    const int tiles = past - first;
-    for (int j = 0; j < tiles; ++j) {
-        const int i = BACK ? past - 1 - j : first + j;
-        work(i, j, [&] {
-            if (j + 1 < tiles) next(BACK ? i - 1 : i + 1);
-        });
-    }
-}
-
-// The map of every segment but the last: [b][seg][C].  In the last one's place
-// stands the first state, which the next kernel may overwrite with the last.
-template <typename T, int N, bool BLEND>
-__global__ __launch_bounds__(kThreads) void k_rec_segments(RecurrenceArgs a, RecPlan p, float2 *out, int64_t jobs) {
-    __shared__ Map<N> ends[2][kWaves][kLanes];
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Lane<N> t(a, p, job);
-        const Walk<T> xw(a.x, a.xs, a, t), gw(a.gate, a.gates, a, t);
-        Map<N> all;
-        all.clear();
-        if (t.seg == p.segs - 1) {
-            if (a.state)
-#pragma unroll
-                for (int e = 0; e < N; ++e) all.H[e] = a.state[(int64_t)t.b * a.C + t.at + e];
-        } else {
-            const int first = t.seg * p.seg_tiles, past = first + p.seg_tiles;
-            Rows<T, N, kPer> xr, gr;
-            auto next = [&](int i) {
-                const int s0 = i * kTile + t.slot * kPer;
-                if ((i + 1) * kTile <= t.n) {
-                    xr.template load<true>(xw, s0, t.n);
-                    gr.template load<true>(gw, s0, t.n);
-                } else {
-                    xr.template load<false>(xw, s0, t.n);
-                    gr.template load<false>(gw, s0, t.n);
-                }
-            };
-            if (first * kTile < t.n) next(first);
-            walk<kTile, false>(first, past, t.n, next, [&](int i, int j, auto then) {
-                const int s0 = i * kTile + t.slot * kPer;
-                Gates<T, N, kPer> v(gr);
-                float u[kPer][N];
-                widen_rows<T, N, kPer>(xr, u);
-                then();
-                if (BLEND)
-#pragma unroll
-                    for (int k = 0; k < kPer; ++k)
-#pragma unroll
-                        for (int e = 0; e < N; ++e) u[k][e] *= v.q[k][e];
-                if ((i + 1) * kTile > t.n) {
-                    v.end(s0, t.n);
-                    end_rows<N, kPer>(u, s0, t.n);
-                }
-                Map<N> ahead, tile;
-                join_slots<N, false>(map_of<N, kPer>(v.a, u), ahead, tile, ends[j & 1]);
-                tile.after(all);
-                all = tile;
-            });
-        }
-        __syncthreads();
-        if (t.slot == 0) {
-            float2 *const o = out + ((int64_t)t.b * p.segs + t.seg) * a.C + t.at;
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t.own(e)) o[e] = make_float2(all.A[e], all.H[e]);
-        }
-    }
-}
-
-// The state ahead of a segment: the one that a call starts from, and the maps of
-// the segments before it.
 template <int N>
-__device__ __forceinline__ void carry_in(const RecurrenceArgs &a, const RecPlan &p, const Lane<N> &t, const float *start,
-                                         const float2 *maps, int from, int to, int step, float *h) {
-    if (p.segs > 1) {  // from the place of the map that nobody needs
-        const float2 *const m = maps + ((int64_t)t.b * p.segs + (step > 0 ? p.segs - 1 : 0)) * a.C + t.at;
+__device__ __forceinline__ void store_state(float *o, const Lane<N> &t, const float *h) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) h[e] = m[e].y;
-    } else if (start) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) h[e] = start[(int64_t)t.b * a.C + t.at + e];
-    }
-    for (int i = from; i != to; i += step) {
-        const float2 *const m = maps + ((int64_t)t.b * p.segs + i) * a.C + t.at;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float2 v = m[e];
-            h[e] = fmaf(v.x, h[e], v.y);
+    for (int e = 0; e < N; ++e)
+        if (t.own(e)) o[e] = h[e];
+}
+
+// ---- the forward's tile -------------------------------------------------------------
+
+template <typename T, int N, int PER, bool ODD, bool BLEND>
+struct Tile {
+    static constexpr int TILE = kSlots * PER;
+    Rows<T, N, PER> xr, gr;
+    float a[PER][N], u[PER][N];
+    __device__ __forceinline__ void load(const RecurrenceArgs &r, const Lane<N> &t, int i) {
+        const int from = last_tile<TILE>(t.n, i), last = max(t.n, 1) - 1 - from * TILE - t.slot * PER;
+        const Walk<T, N, PER> gw(r.gate, r.gates, r, t, from), xw(r.x, r.xs, r, t, from);
+        if ((i + 1) * TILE <= t.n) {
+            gr.template load<true>(gw, last);
+            xr.template load<true>(xw, last);
+        } else {
+            gr.template load<false>(gw, last);
+            xr.template load<false>(xw, last);
         }
     }
+    // The slot's map, from its last position on where BACK; nothing past `left`.
+    template <bool FULL, bool BACK>
+    __device__ __forceinline__ Map<N> form(int left) {
+        Map<N> m;
+        m.clear();
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int k = BACK ? PER - 1 - j : j;
+            float z[N], q[N];
+            hold(gr.r[k]);
+            hold(xr.r[k]);
+            Piece<T, N>::widen(gr.r[k], z);
+            Piece<T, N>::widen(xr.r[k], u[k]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                sigmoid_pair(z[e], a[k][e], q[e]);
+                if (BLEND) u[k][e] *= q[e];
+                if (!FULL && k >= left) a[k][e] = 1.0f, u[k][e] = 0.0f;
+            }
+            if (BACK)
+                m.then_back(a[k], u[k]);
+            else
+                m.then(a[k], u[k]);
+            m.hold_all();
+        }
+        return m;
+    }
+    template <bool BACK = false>
+    __device__ __forceinline__ Map<N> form(const Lane<N> &t, int i) {
+        return (i + 1) * TILE <= t.n ? form<true, BACK>(0) : form<false, BACK>(t.n - i * TILE - t.slot * PER);
+    }
+    // the states from h on, to y
+    __device__ __forceinline__ void store(const RecurrenceArgs &r, const Lane<N> &t, int i, float *h) {
+        if (!t.on) return;
+        const int s0 = i * TILE + t.slot * PER, left = t.n - s0;
+        if (r.states && s0 % kStateEvery == 0 && s0 < r.L) store_state<N>(r.states + t.kept(r, s0), t, h);
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) u[k][e] = h[e] = fmaf(a[k][e], h[e], u[k][e]);
+        const Walk<T, N, PER> yw(r.y, r.ys, r, t, i);
+        if ((i + 1) * TILE <= t.n) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip);
+        } else {
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                if (k < left) put<T, N, ODD>(yw.at(k), u[k], t.skip);
+            clear_rows<T, N>(r.y, r.ys, t, max(i * TILE, t.n), min((i + 1) * TILE, r.L));
+        }
+    }
+};
+
+// ---- segments -----------------------------------------------------------------------
+//
+// A chain (a sequence's 16 pieces of channels) is cut into segments of whole
+// tiles, a workgroup each.  Where there is more than one, a kernel ahead forms
+// every segment's map; a workgroup joins those of the segments ahead of its own,
+// 16 slots of them side by side, and walks through its tiles.
+struct Segments {
+    int segs, tiles;          // segments of a chain, tiles of a segment (the last one may have fewer)
+    FastDiv by_segs, by_slabs;
+    uint32_t jobs, first;     // workgroups in all, and where a launch begins
+    float2 *maps;             // [chain][seg][kLanes * N]: the maps; in place of the one that nobody needs, the first state
+    template <int N>
+    __device__ __forceinline__ float2 *at(uint32_t chain, int seg, int lane) const {
+        return maps + (((int64_t)chain * segs + seg) * kLanes + lane) * N;
+    }
+};
+
+// The state ahead of segment `to` in the order of the scan (BACK: from the last segment on).
+template <int N, bool BACK>
+__device__ __forceinline__ void carry_in(const Segments &g, uint32_t chain, int seg, const float *start, float *h, Ends<N> &ends) {
+    const int slot = threadIdx.x / kLanes, p = threadIdx.x % kLanes;
+    if (g.segs == 1) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[e] = start ? start[e] : 0.0f;
+        return;
+    }
+    const int before = BACK ? g.segs - 1 - seg : seg, each = (before + kSlots - 1) / kSlots;  // of every slot
+    const float2 *const s = g.at<N>(chain, BACK ? 0 : g.segs - 1, p);
+    Map<N> m, rest;
+    m.clear();
+    const int from = (BACK ? kSlots - 1 - slot : slot) * each;
+    for (int i = from; i < min(from + each, before); ++i) {
+        const float2 *const o = g.at<N>(chain, BACK ? g.segs - 1 - i : i, p);
+        Map<N> n;
+#pragma unroll
+        for (int e = 0; e < N; ++e) n.A[e] = o[e].x, n.H[e] = o[e].y;
+        n.after(m);
+        m = n;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) h[e] = s[e].y;
+    join_slots<N, BACK>(m, rest, ends);
+    __syncthreads();
+    float here[N];
+    pass_waves<N, BACK>(ends, h, here);
+}
+
+template <int N>
+__device__ __forceinline__ void store_map(float2 *o, const Map<N> &m) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = make_float2(m.A[e], m.H[e]);
 }
 
 template <typename T, int N, bool BLEND>
-__global__ __launch_bounds__(kThreads) void k_recurrence(RecurrenceArgs a, RecPlan p, const float2 *maps, int64_t jobs) {
-    using E = typename T::T;
-    __shared__ Map<N> ends[2][kWaves][kLanes];
-    const int kept = (a.L + kStateEvery - 1) / kStateEvery;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Lane<N> t(a, p, job);
-        const Walk<T> xw(a.x, a.xs, a, t), gw(a.gate, a.gates, a, t), yw(a.y, a.ys, a, t);
-        const int64_t bc = (int64_t)t.b * a.C + t.at;
-        const int first = t.seg * p.seg_tiles, past = first + p.seg_tiles;
-        Rows<T, N, kPer> xr, gr;
-        auto next = [&](int i) {
-            const int s0 = i * kTile + t.slot * kPer;
-            if ((i + 1) * kTile <= t.n) {
-                xr.template load<true>(xw, s0, t.n);
-                gr.template load<true>(gw, s0, t.n);
-            } else {
-                xr.template load<false>(xw, s0, t.n);
-                gr.template load<false>(gw, s0, t.n);
-            }
-        };
-        if (first * kTile < t.n) next(first);
-        float h0[N] = {};
-        carry_in<N>(a, p, t, a.state, maps, 0, t.seg, 1, h0);
-        auto keep = [&](int s, const float *h) {
-            float *const o = a.states + ((int64_t)t.b * kept + s / kStateEvery) * a.C + t.at;
+__global__ __launch_bounds__(kThreads) void k_rec_maps(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N> ends[2];
+    using W = Tile<T, N, kPer, false, BLEND>;
+    const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
+    const int seg = (int)(job - chain * g.by_segs.d);
+    const Lane<N> t(a, chain, g.by_slabs);
+    Map<N> all;
+    all.clear();
+    const int first = seg * g.tiles, past = min(first + g.tiles, (t.n + W::TILE - 1) / W::TILE);
+    if (seg == g.segs - 1) {
+        if (a.state)
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t.own(e)) o[e] = h[e];
-        };
-        walk<kTile, false>(first, past, t.n, next, [&](int i, int j, auto then) {
-            const int s0 = i * kTile + t.slot * kPer;
-            const bool full = (i + 1) * kTile <= t.n;
-            Gates<T, N, kPer> v(gr);
-            float u[kPer][N];
-            widen_rows<T, N, kPer>(xr, u);
-            then();
-            if (BLEND)
-#pragma unroll
-                for (int k = 0; k < kPer; ++k)
-#pragma unroll
-                    for (int e = 0; e < N; ++e) u[k][e] *= v.q[k][e];
-            if (!full) {
-                v.end(s0, t.n);
-                end_rows<N, kPer>(u, s0, t.n);
-            }
-            Map<N> ahead, tile;
-            join_slots<N, false>(map_of<N, kPer>(v.a, u), ahead, tile, ends[j & 1]);
-            float h[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) h[e] = h0[e];
-            ahead.apply(h);
-            tile.apply(h0);
-            if (!t.on) return;
-            if (a.states && s0 % kStateEvery == 0 && s0 < a.L) keep(s0, h);
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-#pragma unroll
-                for (int e = 0; e < N; ++e) u[k][e] = h[e] = fmaf(v.a[k][e], h[e], u[k][e]);
-            E *const y = yw.p + (int64_t)s0 * yw.step;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (full || s0 + k < t.n) store_own<T, N>(y + k * yw.step, u[k], t.skip);
-        });
-        // past the length: no outputs, and the last state from the next tile's start on
-        const int from = max(first * kTile, t.n), to = min(past * kTile, a.L);
-        clear_rows<T, N>(a.y, a.ys, t, from, to);
-        if (a.states && t.on)
-            for (int s = (max((t.n + kTile - 1) / kTile, first) * (kTile / kPer) + t.slot) * kPer; s < to; s += kTile)
-                if (s % kStateEvery == 0) keep(s, h0);
-        __syncthreads();
-        if (a.last && t.on && t.seg == p.segs - 1 && t.slot == 0) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t.own(e)) a.last[bc + e] = h0[e];
+            for (int e = 0; e < N; ++e) all.H[e] = a.state[t.state(a) + e];
+    } else if (first < past) {
+        W v;
+        v.load(a, t, first);
+        for (int i = first;;) {
+            const Map<N> own = v.form(t, i);
+            if (i + 1 < past) v.load(a, t, i + 1);
+            Map<N> ahead;
+            join_slots<N, false>(own, ahead, ends[i & 1]);
+            __syncthreads();
+            join_waves<N, false>(ends[i & 1], all);
+            if (++i == past) break;
         }
     }
+    if (t.slot == 0) store_map<N>(g.at<N>(chain, seg, threadIdx.x), all);
+}
+
+// A tile's loads are in flight while the one before it is worked on.
+template <typename T, int N, bool ODD, bool BLEND>
+__global__ __launch_bounds__(kThreads) void k_rec_walk(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N> ends[2];
+    using W = Tile<T, N, kPer, ODD, BLEND>;
+    const int tiles = (a.L + W::TILE - 1) / W::TILE;
+    const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
+    const int seg = (int)(job - chain * g.by_segs.d);
+    const Lane<N> t(a, chain, g.by_slabs);
+    const int first = seg * g.tiles, past = min(first + g.tiles, tiles);
+    W v;
+    v.load(a, t, first);
+    float h0[N];
+    carry_in<N, false>(g, chain, seg, a.state ? a.state + t.state(a) : nullptr, h0, ends[(first & 1) ^ 1]);
+    for (int i = first;;) {
+        const Map<N> own = v.form(t, i);
+        if (i + 1 < past) v.load(a, t, i + 1);
+        Map<N> ahead;
+        join_slots<N, false>(own, ahead, ends[i & 1]);
+        __syncthreads();
+        float h[N];
+        pass_waves<N, false>(ends[i & 1], h0, h);
+        ahead.apply(h);
+        v.store(a, t, i, h);
+        if (++i == past) break;
+    }
+    __syncthreads();  // every thread has read the state, which `last` may be
+    if (a.last && t.on && seg == g.segs - 1 && t.slot == 0) store_state<N>(a.last + t.state(a), t, h0);
 }
 
 // ---- gradients -------------------------------------------------------------------
@@ -400,221 +427,284 @@ __global__ __launch_bounds__(kThreads) void k_recurrence(RecurrenceArgs a, RecPl
 // m_s = a_s r_s = a_s (m_{s+1} + g_s): the gradient of the state ahead of s, a
 // scan from the end whose maps have the same factors.
 
-template <int N, int PER>
-__device__ __forceinline__ Map<N> back_map(const float (*a)[N], const float (*g)[N]) {
-    Map<N> m;
-    m.clear();
-#pragma unroll
-    for (int k = PER - 1; k >= 0; --k)
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            m.H[e] = a[k][e] * (m.H[e] + g[k][e]);
-            m.A[e] *= a[k][e];
-        }
-    return m;
-}
-
-// The map from the end of every segment but the first, in whose place stands
-// the last state's gradient.
-template <typename T, int N>
-__global__ __launch_bounds__(kThreads) void k_rec_back_segments(RecurrenceArgs a, RecPlan p, float2 *out, int64_t jobs) {
-    __shared__ Map<N> ends[2][kWaves][kLanes];
-    constexpr int TILE = kTileBack, PER = kPerBack;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Lane<N> t(a, p, job);
-        const Walk<T> dw(a.g, a.gs, a, t), gw(a.gate, a.gates, a, t);
-        Map<N> all;
-        all.clear();
-        if (t.seg == 0) {
-            if (a.g_last)
-#pragma unroll
-                for (int e = 0; e < N; ++e) all.H[e] = a.g_last[(int64_t)t.b * a.C + t.at + e];
+template <typename T, int N, int PER, bool ODD, bool BLEND>
+struct TileBack {
+    static constexpr int TILE = kSlots * PER;
+    Rows<T, N, PER> xr, gr, dr;
+    float kept[N];  // the state that the tile starts from
+    float a[PER][N], q[PER][N], x[PER][N], g[PER][N];
+    __device__ __forceinline__ void load(const RecurrenceArgs &r, const Lane<N> &t, int i) {
+        const int from = last_tile<TILE>(t.n, i), last = max(t.n, 1) - 1 - from * TILE - t.slot * PER;
+        const Walk<T, N, PER> gw(r.gate, r.gates, r, t, from), xw(r.x, r.xs, r, t, from), dw(r.g, r.gs, r, t, from);
+        if ((i + 1) * TILE <= t.n) {
+            gr.template load<true>(gw, last);
+            xr.template load<true>(xw, last);
+            dr.template load<true>(dw, last);
         } else {
-            const int first = t.seg * p.seg_tiles, past = min(first + p.seg_tiles, (t.n + TILE - 1) / TILE);
-            Rows<T, N, PER> dr, gr;
-            auto next = [&](int i) {
-                const int s0 = i * TILE + t.slot * PER;
-                if ((i + 1) * TILE <= t.n) {
-                    dr.template load<true>(dw, s0, t.n);
-                    gr.template load<true>(gw, s0, t.n);
-                } else {
-                    dr.template load<false>(dw, s0, t.n);
-                    gr.template load<false>(gw, s0, t.n);
-                }
-            };
-            if (past > first) next(past - 1);
-            walk<TILE, true>(first, past, t.n, next, [&](int i, int j, auto then) {
-                const int s0 = i * TILE + t.slot * PER;
-                Gates<T, N, PER> v(gr);
-                float g[PER][N];
-                widen_rows<T, N, PER>(dr, g);
-                then();
-                if ((i + 1) * TILE > t.n) {
-                    v.end(s0, t.n);
-                    end_rows<N, PER>(g, s0, t.n);
-                }
-                Map<N> behind, tile;
-                join_slots<N, true>(back_map<N, PER>(v.a, g), behind, tile, ends[j & 1]);
-                tile.after(all);
-                all = tile;
-            });
+            gr.template load<false>(gw, last);
+            xr.template load<false>(xw, last);
+            dr.template load<false>(dw, last);
         }
-        __syncthreads();
-        if (t.slot == 0) {
-            float2 *const o = out + ((int64_t)t.b * p.segs + t.seg) * a.C + t.at;
+        const float *const st = r.states + t.kept(r, i * TILE);
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t.own(e)) o[e] = make_float2(all.A[e], all.H[e]);
-        }
+        for (int e = 0; e < N; ++e) kept[e] = st[e];
     }
-}
-
-template <typename T, int N, bool BLEND>
-__global__ __launch_bounds__(kThreads) void k_recurrence_back(RecurrenceArgs a, RecPlan p, const float2 *maps, int64_t jobs) {
-    using E = typename T::T;
-    __shared__ Map<N> ends[2][2][kWaves][kLanes];
-    constexpr int TILE = kTileBack, PER = kPerBack;
-    const int kept = (a.L + kStateEvery - 1) / kStateEvery;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Lane<N> t(a, p, job);
-        const Walk<T> xw(a.x, a.xs, a, t), gw(a.gate, a.gates, a, t), dw(a.g, a.gs, a, t), gxw(a.gx, a.gxs, a, t), ggw(a.gg, a.ggs, a, t);
-        const int64_t bc = (int64_t)t.b * a.C + t.at;
-        const int first = t.seg * p.seg_tiles, whole = first + p.seg_tiles, past = min(whole, (t.n + TILE - 1) / TILE);
-        Rows<T, N, PER> xr, gr, dr;
-        float hn[N];  // the state that a tile starts from
-        auto next = [&](int i) {
-            const int s0 = i * TILE + t.slot * PER;
-            if ((i + 1) * TILE <= t.n) {
-                xr.template load<true>(xw, s0, t.n);
-                gr.template load<true>(gw, s0, t.n);
-                dr.template load<true>(dw, s0, t.n);
+    __device__ __forceinline__ float term(int k, int e) const { return BLEND ? q[k][e] * x[k][e] : x[k][e]; }
+    template <bool FULL>
+    __device__ __forceinline__ Map<N> form(int left) {
+        Map<N> m;
+        m.clear();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            float z[N], u[N];
+            hold(gr.r[k]);
+            hold(xr.r[k]);
+            hold(dr.r[k]);
+            Piece<T, N>::widen(gr.r[k], z);
+            Piece<T, N>::widen(xr.r[k], x[k]);
+            Piece<T, N>::widen(dr.r[k], g[k]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                sigmoid_pair(z[e], a[k][e], q[k][e]);
+                if (!FULL && k >= left) a[k][e] = 1.0f, q[k][e] = x[k][e] = g[k][e] = 0.0f;
+                u[e] = term(k, e);
+            }
+            m.then(a[k], u);
+            m.hold_all();
+        }
+        return m;
+    }
+    // the slot's map of the states, and h = the state that the tile starts from
+    __device__ __forceinline__ Map<N> form(const Lane<N> &t, int i, float *h) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[e] = kept[e];
+        return (i + 1) * TILE <= t.n ? form<true>(0) : form<false>(t.n - i * TILE - t.slot * PER);
+    }
+    __device__ __forceinline__ Map<N> map_back() const {
+        Map<N> m;
+        m.clear();
+#pragma unroll
+        for (int k = PER - 1; k >= 0; --k) m.then_back(a[k], g[k]);
+        return m;
+    }
+    // the gradients from the state h ahead of the slot and m behind it
+    __device__ __forceinline__ void store(const RecurrenceArgs &r, const Lane<N> &t, int i, float *h, float *m) {
+        if (!t.on) return;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float u = term(k, e);
+                x[k][e] = BLEND ? h[e] - x[k][e] : h[e];
+                h[e] = fmaf(a[k][e], h[e], u);
+            }
+#pragma unroll
+        for (int k = PER - 1; k >= 0; --k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = m[e] + g[k][e];
+                m[e] = a[k][e] * d;
+                g[k][e] = BLEND ? d * q[k][e] : d;
+                x[k][e] = m[e] * q[k][e] * x[k][e];
+            }
+        const bool full = (i + 1) * TILE <= t.n;
+        const int left = t.n - i * TILE - t.slot * PER;
+        if (r.gx) {
+            const Walk<T, N, PER> w(r.gx, r.gxs, r, t, i);
+            if (full) {
+#pragma unroll
+                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip);
             } else {
-                xr.template load<false>(xw, s0, t.n);
-                gr.template load<false>(gw, s0, t.n);
-                dr.template load<false>(dw, s0, t.n);
-            }
-            const float *const st = a.states + ((int64_t)t.b * kept + (int64_t)i * TILE / kStateEvery) * a.C + t.at;
-#pragma unroll
-            for (int e = 0; e < N; ++e) hn[e] = st[e];
-        };
-        if (past > first) next(past - 1);
-        float m0[N] = {};
-        carry_in<N>(a, p, t, a.g_last, maps, p.segs - 1, t.seg, -1, m0);
-        walk<TILE, true>(first, past, t.n, next, [&](int i, int j, auto then) {
-            const int s0 = i * TILE + t.slot * PER;
-            const bool full = (i + 1) * TILE <= t.n;
-            Gates<T, N, PER> v(gr);
-            float x[PER][N], g[PER][N], h[N], m[N], u[PER][N];
-            widen_rows<T, N, PER>(xr, x);
-            widen_rows<T, N, PER>(dr, g);
-#pragma unroll
-            for (int e = 0; e < N; ++e) h[e] = hn[e];
-            then();
-            if (!full) {
-                v.end(s0, t.n);
-                end_rows<N, PER>(x, s0, t.n);
-                end_rows<N, PER>(g, s0, t.n);
-            }
-#pragma unroll
-            for (int k = 0; k < PER; ++k)
-#pragma unroll
-                for (int e = 0; e < N; ++e) u[k][e] = BLEND ? v.q[k][e] * x[k][e] : x[k][e];
-            Map<N> ahead, behind, tile;
-            join_slots<N, false>(map_of<N, PER>(v.a, u), ahead, tile, ends[j & 1][0]);
-            join_slots<N, true>(back_map<N, PER>(v.a, g), behind, tile, ends[j & 1][1]);
-            ahead.apply(h);
-#pragma unroll
-            for (int e = 0; e < N; ++e) m[e] = m0[e];
-            behind.apply(m);
-            tile.apply(m0);
-            if (!t.on) return;
-            // the state ahead of each position (less x), then the gradients from the last one on
-#pragma unroll
-            for (int k = 0; k < PER; ++k)
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    x[k][e] = BLEND ? h[e] - x[k][e] : h[e];
-                    h[e] = fmaf(v.a[k][e], h[e], u[k][e]);
-                }
-#pragma unroll
-            for (int k = PER - 1; k >= 0; --k)
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float r = m[e] + g[k][e];
-                    m[e] = v.a[k][e] * r;
-                    g[k][e] = BLEND ? r * v.q[k][e] : r;
-                    x[k][e] = m[e] * v.q[k][e] * x[k][e];
-                }
-            if (a.gx) {
-                E *const o = gxw.p + (int64_t)s0 * gxw.step;
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if (full || s0 + k < t.n) store_own<T, N>(o + k * gxw.step, g[k], t.skip);
+                    if (k < left) put<T, N, ODD>(w.at(k), g[k], t.skip);
             }
-            if (a.gg) {
-                E *const o = ggw.p + (int64_t)s0 * ggw.step;
+        }
+        if (r.gg) {
+            const Walk<T, N, PER> w(r.gg, r.ggs, r, t, i);
+            if (full) {
+#pragma unroll
+                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip);
+            } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if (full || s0 + k < t.n) store_own<T, N>(o + k * ggw.step, x[k], t.skip);
+                    if (k < left) put<T, N, ODD>(w.at(k), x[k], t.skip);
             }
-        });
-        const int from = max(first * TILE, t.n), to = min(whole * TILE, a.L);
-        clear_rows<T, N>(a.gx, a.gxs, t, from, to);
-        clear_rows<T, N>(a.gg, a.ggs, t, from, to);
-        __syncthreads();
-        if (a.g_state && t.on && t.seg == 0 && t.slot == 0) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (t.own(e)) a.g_state[bc + e] = m0[e];
+        }
+        if (!full) {
+            const int from = max(i * TILE, t.n), to = min((i + 1) * TILE, r.L);
+            clear_rows<T, N>(r.gx, r.gxs, t, from, to);
+            clear_rows<T, N>(r.gg, r.ggs, t, from, to);
         }
     }
+};
+
+// Of every segment, from its end: its own kernel reads gate and g only.
+template <typename T, int N>
+__global__ __launch_bounds__(kThreads) void k_rec_maps_back(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N> ends[2];
+    a.x = a.g, a.xs = a.gs;
+    using W = Tile<T, N, kPerBack, false, false>;
+    const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
+    const int seg = (int)(job - chain * g.by_segs.d);
+    const Lane<N> t(a, chain, g.by_slabs);
+    Map<N> all;
+    all.clear();
+    const int first = seg * g.tiles, past = min(first + g.tiles, (t.n + W::TILE - 1) / W::TILE);
+    if (seg == 0) {
+        if (a.g_last)
+#pragma unroll
+            for (int e = 0; e < N; ++e) all.H[e] = a.g_last[t.state(a) + e];
+    } else if (first < past) {
+        W v;
+        v.load(a, t, past - 1);
+        for (int i = past - 1;;) {
+            const Map<N> own = v.template form<true>(t, i);
+            if (i > first) v.load(a, t, i - 1);
+            Map<N> behind;
+            join_slots<N, true>(own, behind, ends[i & 1]);
+            __syncthreads();
+            join_waves<N, true>(ends[i & 1], all);
+            if (i-- == first) break;
+        }
+    }
+    if (t.slot == 0) store_map<N>(g.at<N>(chain, seg, threadIdx.x), all);
 }
 
-constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch; more jobs are looped over
-unsigned grid_for(int64_t jobs) { return (unsigned)std::min(jobs, kMaxGrid); }
+template <typename T, int N, bool ODD, bool BLEND>
+__global__ __launch_bounds__(kThreads) void k_rec_walk_back(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N> ends[2][2];
+    using W = TileBack<T, N, kPerBack, ODD, BLEND>;
+    const int tiles = (a.L + W::TILE - 1) / W::TILE;
+    const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
+    const int seg = (int)(job - chain * g.by_segs.d);
+    const Lane<N> t(a, chain, g.by_slabs);
+    const int first = seg * g.tiles, past = min(first + g.tiles, tiles);
+    W v;
+    v.load(a, t, past - 1);
+    float m0[N];
+    carry_in<N, true>(g, chain, seg, a.g_last ? a.g_last + t.state(a) : nullptr, m0, ends[past & 1][0]);
+    for (int i = past - 1;;) {
+        float start[N], h[N], m[N];
+        const Map<N> own = v.form(t, i, start);
+        if (i > first) v.load(a, t, i - 1);
+        Map<N> ahead, behind;
+        join_slots<N, false>(own, ahead, ends[i & 1][0]);
+        join_slots<N, true>(v.map_back(), behind, ends[i & 1][1]);
+        __syncthreads();
+        pass_waves<N, false>(ends[i & 1][0], start, h);
+        ahead.apply(h);
+        pass_waves<N, true>(ends[i & 1][1], m0, m);
+        behind.apply(m);
+        v.store(a, t, i, h, m);
+        if (i-- == first) break;
+    }
+    __syncthreads();
+    if (a.g_state && t.on && seg == 0 && t.slot == 0) store_state<N>(a.g_state + t.state(a), t, m0);
+}
 
-template <typename T, int N, bool BLEND>
-hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    const RecPlan p = plan_recurrence(a.B, a.L, a.C, kTile, num_cus);
-    const int64_t jobs = (int64_t)a.B * p.segs * p.slabs;
-    if (p.segs > 1)
-        hipLaunchKernelGGL((k_rec_segments<T, N, BLEND>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (float2 *)a.ws, jobs);
-    hipLaunchKernelGGL((k_recurrence<T, N, BLEND>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (const float2 *)a.ws, jobs);
+// ---- launches ------------------------------------------------------------------------
+
+struct RecPlan {
+    Segments g;
+    size_t ws_bytes;
+};
+
+RecPlan plan_recurrence(int B, int L, int C, int N, int tile, int num_cus) {
+    RecPlan p = {};
+    const int slabs = (C + N * kLanes - 1) / (N * kLanes);
+    const int64_t chains = (int64_t)B * slabs, tiles = std::max<int64_t>(1, (L + (int64_t)tile - 1) / tile);
+    const int64_t want = chains > 0 ? (8ll * num_cus + chains - 1) / chains : 1;
+    p.g.segs = (int)(chains >= 2 * num_cus || tiles <= 2 ? 1 : std::min({want, tiles, (int64_t)256}));
+    p.g.tiles = (int)((tiles + p.g.segs - 1) / p.g.segs);
+    p.g.segs = (int)((tiles + p.g.tiles - 1) / p.g.tiles);
+    p.g.by_segs = make_fastdiv((uint32_t)p.g.segs);
+    p.g.by_slabs = make_fastdiv((uint32_t)slabs);
+    p.g.jobs = (uint32_t)(chains * p.g.segs);
+    p.ws_bytes = p.g.segs > 1 ? (size_t)chains * p.g.segs * kLanes * N * sizeof(float2) : 0;
+    return p;
+}
+
+// Pieces of four channels, where a tile's rows lie within 2^31 bytes of each other.
+int rec_piece(const RecurrenceArgs &a, int tile) {
+    if (a.C < 4) return 1;
+    const int64_t far = ((int64_t)1 << 31) / 4 - a.C;
+    for (const Strides2 &s : {a.xs, a.gates, a.gs, a.ys, a.gxs, a.ggs})
+        if (s.l > far / tile) return 1;
+    return 4;
+}
+
+// No positions: the state stays.
+__global__ __launch_bounds__(256) void k_rec_empty(const float *from, float *to, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) to[i] = from ? from[i] : 0.0f;
+}
+hipError_t run_empty(const RecurrenceArgs &a, const float *from, float *to, hipStream_t stream) {
+    const int64_t n = (int64_t)a.B * a.C;
+    if (to && to != from)
+        hipLaunchKernelGGL(k_rec_empty, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16)), dim3(256), 0, stream, from, to, n);
     return hipGetLastError();
 }
 
-template <typename T, int N, bool BLEND>
-hipError_t run_back(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    const RecPlan p = plan_recurrence(a.B, a.L, a.C, kTileBack, num_cus);
-    const int64_t jobs = (int64_t)a.B * p.segs * p.slabs;
-    if (p.segs > 1)
-        hipLaunchKernelGGL((k_rec_back_segments<T, N>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (float2 *)a.ws, jobs);
-    hipLaunchKernelGGL((k_recurrence_back<T, N, BLEND>), dim3(grid_for(jobs)), dim3(kThreads), 0, stream, a, p, (const float2 *)a.ws, jobs);
-    return hipGetLastError();
-}
+constexpr uint32_t kMaxGrid = 1 << 23;  // workgroups of a launch
 
+// f(workgroups), for all of the jobs
 template <typename F>
-hipError_t by_type(const RecurrenceArgs &a, F f) {
-    auto blend = [&](auto t, auto n) { return a.blend ? f(t, n, std::true_type()) : f(t, n, std::false_type()); };
+hipError_t in_launches(Segments &g, F f) {
+    for (g.first = 0; g.first < g.jobs; g.first += std::min(g.jobs - g.first, kMaxGrid)) f(dim3(std::min(g.jobs - g.first, kMaxGrid)));
+    return hipGetLastError();
+}
+
+template <typename T, int N, bool ODD, bool BLEND>
+hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
+    Segments g = plan_recurrence(a.B, a.L, a.C, N, kSlots * kPer, num_cus).g;
+    g.maps = (float2 *)a.ws;
+    const dim3 block(kThreads);
+    if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps<T, N, BLEND>), grid, block, 0, stream, a, g); });
+    return in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_walk<T, N, ODD, BLEND>), grid, block, 0, stream, a, g); });
+}
+
+template <typename T, int N, bool ODD, bool BLEND>
+hipError_t run_back(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
+    Segments g = plan_recurrence(a.B, a.L, a.C, N, kSlots * kPerBack, num_cus).g;
+    g.maps = (float2 *)a.ws;
+    const dim3 block(kThreads);
+    if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps_back<T, N>), grid, block, 0, stream, a, g); });
+    return in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_walk_back<T, N, ODD, BLEND>), grid, block, 0, stream, a, g); });
+}
+
+// f(storage type, elements of a piece, whether C is no multiple of it, blend)
+template <typename F>
+hipError_t by_type(const RecurrenceArgs &a, int tile, F f) {
+    auto blend = [&](auto t, auto n, auto odd) { return a.blend ? f(t, n, odd, std::true_type()) : f(t, n, odd, std::false_type()); };
     auto piece = [&](auto t) {
-        return rec_piece(a.C) == 4 ? blend(t, std::integral_constant<int, 4>()) : blend(t, std::integral_constant<int, 1>());
+        if (rec_piece(a, tile) == 1) return blend(t, std::integral_constant<int, 1>(), std::false_type());
+        return a.C % 4 ? blend(t, std::integral_constant<int, 4>(), std::true_type())
+                       : blend(t, std::integral_constant<int, 4>(), std::false_type());
     };
     return a.dtype == kF32 ? piece(F32()) : piece(BF16());
 }
 
 }  // namespace
 
+// The strides decide between pieces of four channels and single ones: room for either.
 size_t recurrence_workspace(int B, int L, int C, int, bool backward, int num_cus) {
-    return plan_recurrence(B, L, C, backward ? kTileBack : kTile, num_cus).ws_bytes;
+    const int tile = kSlots * (backward ? kPerBack : kPer);
+    const size_t one = plan_recurrence(B, L, C, 1, tile, num_cus).ws_bytes;
+    return C < 4 ? one : std::max(one, plan_recurrence(B, L, C, 4, tile, num_cus).ws_bytes);
 }
 
 hipError_t launch_recurrence(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    return by_type(a, [&](auto t, auto n, auto blend) { return run<decltype(t), decltype(n)::value, decltype(blend)::value>(a, num_cus, stream); });
+    if (a.L == 0) return run_empty(a, a.state, a.last, stream);
+    return by_type(a, kSlots * kPer, [&](auto t, auto n, auto odd, auto blend) {
+        return run<decltype(t), decltype(n)::value, decltype(odd)::value, decltype(blend)::value>(a, num_cus, stream);
+    });
 }
 
 hipError_t launch_recurrence_backward(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    return by_type(a,
-                   [&](auto t, auto n, auto blend) { return run_back<decltype(t), decltype(n)::value, decltype(blend)::value>(a, num_cus, stream); });
+    if (a.L == 0) return run_empty(a, a.g_last, a.g_state, stream);
+    return by_type(a, kSlots * kPerBack, [&](auto t, auto n, auto odd, auto blend) {
+        return run_back<decltype(t), decltype(n)::value, decltype(odd)::value, decltype(blend)::value>(a, num_cus, stream);
+    });
 }
 
 }  // namespace dc1d

@@ -73,9 +73,14 @@ struct Piece;
 template <typename T>
 struct Piece<T, 1> {
     using E = typename T::T;
-    using Raw = E;
-    static __device__ __forceinline__ Raw load(const E *p) { return *p; }
-    static __device__ __forceinline__ void widen(Raw r, float *f) { f[0] = T::ld(&r, 0); }
+    using Raw = uint32_t;  // the element's bits
+    static __device__ __forceinline__ Raw load(const E *p) {
+        if constexpr (sizeof(E) == 4)
+            return __float_as_uint(*p);
+        else
+            return *p;
+    }
+    static __device__ __forceinline__ void widen(Raw r, float *f) { f[0] = __uint_as_float(sizeof(E) == 4 ? r : r << 16); }
     static __device__ __forceinline__ void store(E *p, const float *f) { T::st(p, 0, f[0]); }
 };
 template <>
