@@ -1,0 +1,355 @@
+// groupnorm.h -- what group norm's kernels and those of its gradients share: the
+// activations, samples held by a workgroup, samples in parts.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "vec16.h"
+
+namespace dc1d {
+
+enum Act { kNone = 0, kRelu = 1, kSilu = 2 };
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays
+    if constexpr (ACT == kSilu) {
+        float p, q;
+        sigmoid_pair(z, p, q);
+        return z * p;
+    }
+    return z;
+}
+// The gradient g of act(z) taken to z.
+template <int ACT>
+__device__ __forceinline__ float activate_back(float z, float g) {
+    if constexpr (ACT == kRelu) return z > 0.0f ? g : 0.0f;
+    if constexpr (ACT == kSilu) {
+        float p, q;
+        sigmoid_pair(z, p, q);
+        return g * (p + z * p * q);
+    }
+    return g;
+}
+
+// A sample's positions that count.
+__device__ __forceinline__ int64_t positions(const GroupNormArgs &a, int64_t b) {
+    if (!a.lens) return a.S;
+    const int n = a.lens[b];
+    return n < 0 ? 0 : n < a.S ? n : a.S;
+}
+
+// ---- held samples ------------------------------------------------------------------
+//
+// A workgroup holds the positions of nb samples times a slab of gs groups in
+// registers: x (and g) are read once.  Its threads are nb samples x rt rows x P
+// pieces of the slab's channels, R rows each (row t, t + rt, ...).  The mean is
+// taken first and the squares about it next, both from registers.
+struct HeldPlan {
+    int P, gs, slabs, rt, nb, nt, R;
+    int64_t batches;       // of nb samples
+    int grid_rows;         // backward: workgroups of a slab
+    int per, team;         // a group's partial sums in LDS a row of threads; lanes that add them
+    int mode;
+    FastDiv by_P, by_rt, by_per, by_gs, by_D;
+    size_t lds;
+};
+enum Mode { kShuffle, kWhole, kMixed };  // a group's lanes share a wave; a piece lies in one group; it may not
+
+// The sums of v over every group of a workgroup: [K] values for each of a
+// thread's NV groups.
+template <int N, int MODE, int K>
+struct GroupSums {
+    static constexpr int NV = MODE == kMixed ? N : 1;
+    float *red, *sums;
+    int np;
+    __device__ __forceinline__ GroupSums(const HeldPlan &p, float *lds) : red(lds), sums(lds + (size_t)p.nt * NV * K), np(p.nb * p.gs) {}
+    // channels: of the slab; slot: where the first of a thread's groups is among np (its sample's, for kMixed)
+    __device__ __forceinline__ void operator()(const HeldPlan &p, float (*v)[NV], int channels, int D, int slot, const int *of) {
+        if constexpr (MODE == kShuffle) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                for (int d = 1; d < p.per; d <<= 1) v[k][0] += __shfl_xor(v[k][0], d);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < NV; ++e) red[((size_t)k * p.nt + threadIdx.x) * NV + e] = v[k][e];
+            __syncthreads();
+            const int lane = threadIdx.x & (p.team - 1), all = p.rt * p.per, last = (channels + N - 1) / N - 1;
+            for (int g = threadIdx.x / p.team; g < np; g += p.nt / p.team) {
+                const int sm = (int)fdiv(g, p.by_gs), first = (g - sm * p.gs) * p.per;
+                float s[K] = {};
+                for (int i = lane; i < all; i += p.team) {
+                    const int r = (int)fdiv(i, p.by_per), j = first + i - r * p.per;
+                    int at;
+                    if constexpr (MODE == kWhole) {
+                        at = j;
+                    } else {
+                        if (j >= channels) break;  // the last slab's groups are fewer
+                        at = j >= last * N ? last * N + j - (channels - N) : j;
+                    }
+                    at += (sm * p.rt + r) * p.P * NV;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) s[k] += red[(size_t)k * p.nt * NV + at];
+                }
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    for (int d = 1; d < p.team; d <<= 1) s[k] += __shfl_xor(s[k], d);
+                    if (lane == 0) sums[k * np + g] = s[k];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < NV; ++e) v[k][e] = sums[k * np + slot + (MODE == kMixed ? of[e] : 0)];
+        }
+    }
+};
+
+// Workgroup i runs on XCD i % 8, which has an L2 of its own: neighbouring numbers
+// (slabs whose rows share lines) to one XCD.
+__device__ __forceinline__ uint32_t by_xcd(uint32_t i, uint32_t n) {
+    const uint32_t x = i & 7, q = n >> 3, r = n & 7;
+    return x * q + min(x, r) + (i >> 3);
+}
+
+// A thread's place among the samples and channels of a workgroup.
+template <int N, int MODE>
+struct HeldPlace {
+    static constexpr int NV = MODE == kMixed ? N : 1;
+    int rt, sm, at, skip, channels, group, slot, of[NV];  // group: of the piece's first element, or the slab's; of: its elements', from there
+    bool in;                                               // a piece of the slab
+    __device__ __forceinline__ HeldPlace(const GroupNormArgs &a, const HeldPlan &p, int slab) {
+        const int q = (int)fdiv(threadIdx.x, p.by_P), j = threadIdx.x - q * p.P;
+        sm = (int)fdiv(q, p.by_rt);
+        rt = q - sm * p.rt;
+        const int g0 = slab * p.gs, c0 = g0 * a.D, end = min(c0 + p.gs * a.D, a.C), c = c0 + j * N;
+        channels = end - c0;
+        in = c < end && sm < p.nb;
+        at = in ? min(c, end - N) : c0 + N <= a.C ? c0 : a.C - N;
+        skip = in ? c - at : N;
+        sm = min(sm, p.nb - 1);
+        if constexpr (MODE == kMixed) {
+            group = g0;
+            slot = sm * p.gs;
+#pragma unroll
+            for (int e = 0; e < N; ++e) of[e] = max((int)fdiv(at + e, p.by_D) - g0, 0);
+        } else {
+            group = (int)fdiv(at, p.by_D);
+            slot = sm * p.gs + group - g0;
+            of[0] = 0;
+        }
+    }
+    __device__ __forceinline__ int v(int e) const { return MODE == kMixed ? e : 0; }
+    // Bytes from the batch's first element to row i of the thread's in sample `s` of
+    // the batch; the sample's first row in place of those that are not read.
+    __device__ __forceinline__ uint32_t offset(const GroupNormArgs &a, const HeldPlan &p, int es, int s, int i, bool there) const {
+        const uint32_t row = (uint32_t)(s * (int)a.S) + (there ? (uint32_t)(rt + i * p.rt) : 0u);
+        return (row * (uint32_t)a.C + (uint32_t)at) * (uint32_t)es;
+    }
+};
+template <typename T, int N, int MODE>
+__device__ __forceinline__ void put(char *p, const float *f, int skip) {
+    if constexpr (MODE == kMixed)
+        store_own<T, N>((typename T::T *)p, f, skip);
+    else
+        Piece<T, N>::store((typename T::T *)p, f);
+}
+
+// How a workgroup can hold samples, if it can: R == 0 if not.  `tensors` that are
+// held: 16 pieces a thread in all.
+inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, int tensors, int num_cus) {
+    HeldPlan p = {};
+    const int D = C / G, most = tensors == 1 ? 16 : 8, threads = tensors == 1 ? 1024 : 512;
+    const bool inside = D % N == 0;
+    const int64_t whole = S * D * esize;  // bytes of a sample's group
+    const int least = (N + D - 1) / D;    // groups of a piece
+    if (N == 1 || S < 1 || S > threads * most || S * ((least * (int64_t)D + N - 1) / N) > threads * most) return p;
+    int64_t gs = std::max<int64_t>(1, (32768 / tensors) / whole);
+    while (gs < G && gs * D * esize < 64 && S * ((gs + 1) * D + N - 1) / N <= 512 * most) ++gs;
+    gs = std::min<int64_t>(std::max<int64_t>(gs, least), G);
+    while (gs > least && (gs * D + N - 1) / N > 256) --gs;  // at most 256 pieces a row
+    // few samples: workgroups for all CUs, of 64 bytes a row at least
+    const int64_t line = std::max<int64_t>(least, (64 + D * esize - 1) / (D * esize));
+    while (gs > line && B * ((G + gs - 1) / gs) < 2 * num_cus) gs = std::max(gs / 2, line);
+    p.slabs = (int)((G + gs - 1) / gs);
+    p.gs = (int)std::max<int64_t>((G + p.slabs - 1) / p.slabs, least);
+    p.slabs = (G + p.gs - 1) / p.gs;
+    p.P = (int)(((int64_t)p.gs * D + N - 1) / N);
+    for (p.nt = 256; p.nt <= threads; p.nt *= 2) {
+        p.rt = (int)std::min<int64_t>(p.nt / p.P, S);
+        if (p.rt < 1) continue;
+        const int64_t rows = (S + p.rt - 1) / p.rt;
+        if (rows <= (p.nt == 256 ? most / 2 : most)) {
+            for (p.R = 1; p.R < rows;) p.R *= 2;
+            break;
+        }
+    }
+    if (p.R > 8 && !inside) p.R = 0;  // registers
+    if (!p.R) return p;
+    p.rt = (int)((S + p.R - 1) / p.R);
+    p.nb = (int)std::max<int64_t>(1, std::min<int64_t>(p.nt / (p.P * p.rt), B));
+    // offsets inside a batch have 32 bits
+    const int64_t bytes = S * C * esize;
+    if (bytes >= (int64_t)1 << 31) p.R = 0;
+    if (!p.R) return p;
+    p.nb = (int)std::min<int64_t>(p.nb, ((int64_t)1 << 31) / bytes);
+    // few samples: as many workgroups as there are CUs
+    while (p.nb > 1 && (B + p.nb - 1) / p.nb * p.slabs < num_cus) --p.nb;
+    p.batches = (B + p.nb - 1) / p.nb;
+    p.nt = (p.nb * p.rt * p.P + 63) / 64 * 64;
+    const int dn = inside ? D / N : D;
+    p.mode = !inside ? kMixed : p.rt == 1 && dn <= 64 && !(dn & (dn - 1)) ? kShuffle : kWhole;
+    p.per = dn;
+    p.team = 64;
+    while (p.team > 1 && (p.team > p.nt / (p.nb * p.gs) || p.team / 2 >= p.rt * p.per)) p.team /= 2;
+    p.by_P = make_fastdiv(p.P), p.by_rt = make_fastdiv(p.rt), p.by_per = make_fastdiv(p.per), p.by_gs = make_fastdiv(p.gs);
+    p.by_D = make_fastdiv(D);
+    const size_t sums = (size_t)tensors * (p.nt * (p.mode == kMixed ? N : 1) + p.nb * p.gs) * sizeof(float);
+    p.lds = tensors == 1 ? sums : std::max(sums, (size_t)p.nt * N * sizeof(float2));
+    const int64_t rows = std::max<int64_t>(1, (8ll * num_cus + p.slabs - 1) / p.slabs);
+    p.grid_rows = (int)std::min<int64_t>(p.batches, rows);
+    if (p.lds > 64 * 1024) p.R = 0;
+    return p;
+}
+
+// ---- in parts --------------------------------------------------------------------
+//
+// A sample's positions are cut into parts, the channels into tiles of at most 256
+// pieces: a workgroup's threads are rt rows of tp pieces, and a thread keeps its
+// channels over the part's positions.  The parts' statistics (of each group where
+// a tile holds all of them, else of each channel) go to the workspace and are
+// joined in order, by a kernel of its own or, where they are few, by every
+// workgroup that needs them; x is read again, the last part first.
+struct GnParts {
+    int P, tp, tiles, rt, nt, parts;
+    int64_t rows;     // positions of a part
+    bool by_group;    // a part's statistics are kept for groups
+    bool joined;      // the workgroups that need a sample's statistics join them themselves
+    int entries;      // of a part: G or C
+    int team;         // lanes that add a group's values
+    size_t part_bytes, stat_bytes;
+};
+
+inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, int num_cus) {
+    GnParts p;
+    p.P = (C + N - 1) / N;
+    p.tiles = (p.P + 255) / 256;
+    p.tp = (p.P + p.tiles - 1) / p.tiles;
+    // threads in whole waves, 256 to 512 of them, with as few idle as possible
+    double best = 0.0;
+    for (int rt = 1; rt * p.tp <= 512; ++rt) {
+        const int nt = (rt * p.tp + 63) / 64 * 64;
+        const double used = (double)(rt * p.tp) / nt;
+        if ((nt >= 256 || (rt + 1) * p.tp > 512) && used > best + 0.02) best = used, p.rt = rt, p.nt = nt;
+    }
+    // four workgroups for every CU, of 8 rows a thread at least; offsets in a part have 32 bits
+    const int64_t jobs = std::max<int64_t>(1, B * p.tiles);
+    const int64_t want = (4ll * num_cus + jobs - 1) / jobs;
+    const int64_t most = (S + 8ll * p.rt - 1) / (8ll * p.rt);
+    const int64_t parts = std::max<int64_t>(1, std::min({want, most, (int64_t)1024}));
+    p.rows = std::max<int64_t>(1, std::min((S + parts - 1) / parts, ((int64_t)1 << 31) / ((int64_t)C * esize)));
+    p.parts = (int)std::max<int64_t>(1, (S + p.rows - 1) / p.rows);
+    p.by_group = p.tiles == 1;
+    p.entries = p.by_group ? G : C;
+    p.joined = p.by_group && G <= 1024 && (int64_t)p.parts * G <= 16384;
+    p.team = 64;
+    while (p.team > 1 && p.team > p.nt / G) p.team /= 2;
+    p.part_bytes = ((size_t)B * p.parts * p.entries * sizeof(float2) + 255) & ~(size_t)255;
+    p.stat_bytes = ((size_t)B * G * sizeof(float2) + 255) & ~(size_t)255;
+    return p;
+}
+
+// A thread's place in a job of a part and a tile.
+template <typename T, int N>
+struct Place {
+    int64_t b, base;  // sample; bytes to the part's first row
+    int n, rows;      // positions of the part within the length, and all of them
+    int part, tile, rt, j, at, skip;
+    uint32_t off, step;  // bytes from there to the thread's first row, and from one to the next
+    bool on;
+    __device__ __forceinline__ Place(const GroupNormArgs &a, const GnParts &p, int64_t job) {
+        tile = (int)(job % p.tiles);
+        const int64_t q = job / p.tiles;
+        b = q / p.parts;
+        part = (int)(q % p.parts);
+        const int64_t start = (int64_t)part * p.rows, past = min(start + p.rows, a.S);
+        rows = (int)(past - start);
+        n = (int)max(min(past, positions(a, b)) - start, (int64_t)0);
+        rt = threadIdx.x / p.tp;
+        j = threadIdx.x % p.tp;
+        const int piece = tile * p.tp + j, c = piece * N;
+        on = rt < p.rt && piece < p.P;
+        at = on ? min(c, a.C - N) : 0;
+        skip = on ? c - at : N;
+        constexpr int es = sizeof(typename T::T);
+        base = (b * a.S + start) * a.C * es;
+        off = ((uint32_t)(on ? rt : 0) * (uint32_t)a.C + (uint32_t)at) * es;
+        step = (uint32_t)p.rt * (uint32_t)a.C * es;
+    }
+    // how many of the first `of` rows of the part are row-thread i's
+    __device__ __forceinline__ static int rows_of(const GnParts &p, int i, int of) { return of > i ? (of - i + p.rt - 1) / p.rt : 0; }
+};
+
+constexpr int kBatch = 8;  // rows whose loads are in flight together
+
+// The sum over a workgroup of NT threads, the same value in every one.
+template <int NT>
+__device__ __forceinline__ float all_sum(float v, float *red) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    if constexpr (NT > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) v += red[i];
+    }
+    return v;
+}
+
+// f(part, entry, rows of the part) for every entry of group g, thread by thread.
+template <int NT, typename F>
+__device__ __forceinline__ void each_entry(const GnParts &p, int per, int64_t n, F f) {
+    const int cols = per < NT ? per : NT, rp = NT / cols;
+    const int c0 = threadIdx.x % cols, p0 = threadIdx.x / cols;
+    if (p0 >= rp) return;
+    for (int i = p0; i < p.parts; i += rp) {
+        const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
+        if (rows <= 0) return;
+        for (int c = c0; c < per; c += cols) f(i, c, (float)rows);
+    }
+}
+
+constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads); more jobs are looped over
+
+inline unsigned grid_for(int64_t jobs) { return (unsigned)std::min(jobs, kMaxGrid); }
+
+inline int piece_size(int C, int dtype) {
+    const int v = dtype == kF32 ? 4 : 8;
+    return C >= v ? v : 1;
+}
+
+// f(group, lane of its team) for every group of a sample; a team's lanes share a wave.
+template <typename F>
+__device__ __forceinline__ void each_group(const GroupNormArgs &a, const GnParts &p, F f) {
+    for (int g = threadIdx.x / p.team; g < a.G; g += blockDim.x / p.team) f(g, (int)threadIdx.x & (p.team - 1));
+}
+__device__ __forceinline__ float team_sum(const GnParts &p, float v) {
+    for (int d = 1; d < p.team; d <<= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// f(the activation as a type)
+template <typename F>
+hipError_t by_activation(int act, F f) {
+    if (act == kSilu) return f(std::integral_constant<int, kSilu>());
+    if (act == kRelu) return f(std::integral_constant<int, kRelu>());
+    return f(std::integral_constant<int, kNone>());
+}
+
+}  // namespace dc1d

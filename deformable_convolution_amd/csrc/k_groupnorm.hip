@@ -8,113 +8,98 @@
 //
 // Bound by HBM: the forward has to read x and write y, the backward to read x
 // and g and write gx.
-#include <algorithm>
-
-#include "vec16.h"
+#include "groupnorm.h"
 
 namespace dc1d {
 
 namespace {
 
-enum Act { kNone = 0, kRelu = 1, kSilu = 2 };
-
-__device__ __forceinline__ float activate(float z, int act) {
-    if (act == kRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays
-    if (act == kSilu) {
-        float p, q;
-        sigmoid_pair(z, p, q);
-        return z * p;
+template <typename T, int N, int R, int MODE, int ACT>
+__global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, int64_t first) {
+    using P = Piece<T, N>;
+    using E = typename T::T;
+    extern __shared__ float lds[];
+    const int64_t job = first + (p.slabs > 1 ? by_xcd(blockIdx.x, gridDim.x) : blockIdx.x), batch = job / p.slabs;
+    const int slab = (int)(job - batch * p.slabs);
+    const HeldPlace<N, MODE> t(a, p, slab);
+    constexpr int NV = HeldPlace<N, MODE>::NV;
+    GroupSums<N, MODE, 1> sum(p, lds);
+    const int64_t b = min(batch * p.nb + t.sm, a.B - 1);
+    const bool on = t.in && batch * p.nb + t.sm < a.B;
+    const int n = (int)positions(a, b), s = (int)(b - batch * p.nb);
+    const int64_t base = batch * p.nb * a.S * a.C * (int64_t)sizeof(E);
+    const char *const x = (const char *)a.x + base;
+    typename P::Raw raw[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) raw[i] = P::load((const E *)(x + t.offset(a, p, sizeof(E), s, i, on && t.rt + i * p.rt < n)));
+    typename P::Raw wr, br;
+    if (a.w) wr = P::load((const E *)a.w + t.at);
+    if (a.b) br = P::load((const E *)a.b + t.at);
+    float v[1][NV] = {};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float f[N];
+        hold(raw[i]);
+        P::widen(raw[i], f);
+        const bool see = on && t.rt + i * p.rt < n;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[0][t.v(e)] += see && e >= t.skip ? f[e] : 0.0f;
+        hold(v[0][0]);
     }
-    return z;
+    sum(p, v, t.channels, a.D, t.slot, t.of);
+    const float all = (float)n * (float)a.D;
+    float mean[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) mean[e] = n > 0 ? v[0][e] / all : 0.0f, v[0][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float f[N];
+        hold(raw[i]);
+        P::widen(raw[i], f);
+        const bool see = on && t.rt + i * p.rt < n;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float d = f[e] - mean[t.v(e)];
+            v[0][t.v(e)] += see && e >= t.skip ? d * d : 0.0f;
+        }
+        hold(v[0][0]);
+    }
+    sum(p, v, t.channels, a.D, t.slot, t.of);
+    float r[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) r[e] = n > 0 ? rsqrtf(v[0][e] / all + a.eps) : 0.0f;
+    if (!on) return;
+    float w[N], c[N];
+    if (a.w) P::widen(wr, w);
+    if (a.b) P::widen(br, c);
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = a.w ? r[t.v(e)] * w[e] : r[t.v(e)], c[e] = a.b ? c[e] : 0.0f;
+    char *const y = (char *)a.y + base;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = t.rt + i * p.rt;
+            if (row >= a.S) continue;
+            float f[N];
+            hold(raw[i]);
+            P::widen(raw[i], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                f[e] = row < n ? activate<ACT>((f[e] - mean[t.v(e)]) * w[e] + c[e]) : 0.0f;
+                hold(f[e]);
+            }
+            put<T, N, MODE>(y + t.offset(a, p, sizeof(E), s, i, true), f, t.skip);
+        }
+    if (t.rt == 0) {
+        // the thread that holds a group's first element
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int ch = t.at + e, g = t.group + t.of[t.v(e)];
+            if (e < t.skip || ch != g * a.D) continue;
+            if (a.mean) a.mean[b * a.G + g] = mean[t.v(e)];
+            if (a.rstd) a.rstd[b * a.G + g] = r[t.v(e)];
+        }
+    }
 }
-// The gradient g of act(z) taken to z.
-__device__ __forceinline__ float activate_back(float z, float g, int act) {
-    if (act == kRelu) return z > 0.0f ? g : 0.0f;
-    if (act == kSilu) {
-        float p, q;
-        sigmoid_pair(z, p, q);
-        return g * (p + z * p * q);
-    }
-    return g;
-}
-
-__device__ __forceinline__ int64_t positions(const GroupNormArgs &a, int64_t b) {
-    if (!a.lens) return a.S;
-    const int n = a.lens[b];
-    return n < 0 ? 0 : n < a.S ? n : a.S;
-}
-
-// ---- in parts --------------------------------------------------------------------
-//
-// A sample's positions are cut into parts, the channels into tiles of at most NT
-// pieces: a workgroup's threads are rt rows of tp pieces, and a thread keeps its
-// channels over the part's positions.  The parts' statistics (of each channel,
-// or of each group where a tile holds all of them) go to the workspace, are
-// joined in order, and x is read again, the last part first, for y.
-struct GnParts {
-    int P, tp, tiles, rt, nt, parts;
-    int64_t rows;     // positions of a part
-    bool by_group;    // a part's statistics are kept for groups
-    int entries;      // of a part: G or C
-    size_t part_bytes, stat_bytes;
-};
-
-GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int num_cus) {
-    GnParts p;
-    p.P = (C + N - 1) / N;
-    p.tiles = (p.P + 255) / 256;
-    p.tp = (p.P + p.tiles - 1) / p.tiles;
-    // threads in whole waves, 256 to 512 of them, with as few idle as possible
-    double best = 0.0;
-    for (int rt = 1; rt * p.tp <= 512; ++rt) {
-        const int nt = (rt * p.tp + 63) / 64 * 64;
-        const double used = (double)(rt * p.tp) / nt;
-        if ((nt >= 256 || (rt + 1) * p.tp > 512) && used > best + 0.02) best = used, p.rt = rt, p.nt = nt;
-    }
-    // eight workgroups for every CU, of 16 rows a thread at least
-    const int64_t want = (8ll * num_cus + B * p.tiles - 1) / (B * p.tiles > 0 ? B * p.tiles : 1);
-    const int64_t most = (S + 16ll * p.rt - 1) / (16ll * p.rt);
-    int64_t parts = std::max<int64_t>(1, std::min({want, most, (int64_t)1024}));
-    p.rows = std::max<int64_t>(1, (S + parts - 1) / parts);
-    p.parts = (int)std::max<int64_t>(1, (S + p.rows - 1) / p.rows);
-    p.by_group = p.tiles == 1;
-    p.entries = p.by_group ? G : C;
-    p.part_bytes = ((size_t)B * p.parts * p.entries * sizeof(float2) + 255) & ~(size_t)255;
-    p.stat_bytes = ((size_t)B * G * sizeof(float2) + 255) & ~(size_t)255;
-    return p;
-}
-
-// A thread's place in a job of a part and a tile.
-template <int N>
-struct Place {
-    int64_t b, start, end;  // sample; its part's positions within the length
-    int64_t last;           // past the part's last position
-    int part, rt, at, skip, j;
-    bool on;
-    __device__ __forceinline__ Place(const GroupNormArgs &a, const GnParts &p, int64_t job) {
-        const int tile = (int)(job % p.tiles);
-        const int64_t q = job / p.tiles;
-        b = q / p.parts;
-        part = (int)(q % p.parts);
-        const int64_t n = positions(a, b);
-        start = (int64_t)part * p.rows;
-        last = min(start + p.rows, a.S);
-        end = min(last, n);
-        rt = threadIdx.x / p.tp;
-        j = threadIdx.x % p.tp;
-        const int piece = tile * p.tp + j, c = piece * N;
-        on = rt < p.rt && piece < p.P;
-        at = on ? min(c, a.C - N) : 0;
-        skip = on ? c - at : N;
-    }
-    // rows of the part that row-thread i visits
-    __device__ __forceinline__ float rows(const GnParts &p, int i) const {
-        const int64_t n = end - start - i;
-        return n > 0 ? (float)((n + p.rt - 1) / p.rt) : 0.0f;
-    }
-};
-
-constexpr int kBatch = 8;  // rows whose loads are in flight together
 
 template <typename T, int N>
 __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts p, float2 *out, int64_t jobs) {
@@ -122,128 +107,92 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
     using E = typename T::T;
     extern __shared__ float2 red[];  // [rt][tp][N], then of the channels
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Place<N> t(a, p, job);
-        const E *const x = (const E *)a.x + t.b * a.S * a.C + t.at;
+        const Place<T, N> t(a, p, job);
+        const char *const x = (const char *)a.x + t.base;
+        const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
         float n = 0.0f, mean[N] = {}, m2[N] = {};
-        if (t.on) {
-            for (int64_t r = t.start + t.rt; r < t.end; r += (int64_t)kBatch * p.rt) {
-                typename P::Raw raw[kBatch];
-                int have = 0;
+        for (int i0 = 0; i0 < mine; i0 += kBatch) {
+            typename P::Raw raw[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int64_t row = r + (int64_t)i * p.rt;
-                    have += row < t.end;
-                    raw[i] = P::load(x + (row < t.end ? row : r) * a.C);
-                }
-                // the batch's mean and squares about it, joined with those so far
-                const float m = (float)have, all = n + m, share = m / all;
-                float s[N] = {}, d[N] = {};
+            for (int i = 0; i < kBatch; ++i) raw[i] = P::load((const E *)(x + (t.off + (uint32_t)min(i0 + i, mine - 1) * t.step)));
+            // the batch's mean and squares about it, joined with those so far
+            const int have = min(mine - i0, kBatch);
+            const float m = (float)have, all = n + m, share = m / all;
+            float s[N] = {}, d[N] = {};
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    float f[N];
-                    P::widen(raw[i], f);
+            for (int i = 0; i < kBatch; ++i) {
+                float f[N];
+                hold(raw[i]);
+                P::widen(raw[i], f);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) s[e] += i < have ? f[e] : 0.0f;
-                }
+                for (int e = 0; e < N; ++e) s[e] += i < have ? f[e] : 0.0f;
+            }
 #pragma unroll
-                for (int e = 0; e < N; ++e) s[e] = have == kBatch ? s[e] * (1.0f / kBatch) : s[e] / m;  // equal values have their own as mean
+            for (int e = 0; e < N; ++e) s[e] = have == kBatch ? s[e] * (1.0f / kBatch) : s[e] / m;  // equal values have their own as mean
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    float f[N];
-                    P::widen(raw[i], f);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const float v = i < have ? f[e] - s[e] : 0.0f;
-                        d[e] += v * v;
-                    }
-                }
+            for (int i = 0; i < kBatch; ++i) {
+                float f[N];
+                hold(raw[i]);
+                P::widen(raw[i], f);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float v = s[e] - mean[e];
-                    mean[e] += v * share;
-                    m2[e] += d[e] + v * v * n * share;
+                    const float v = i < have ? f[e] - s[e] : 0.0f;
+                    d[e] += v * v;
                 }
-                n = all;
             }
-            for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(mean[e], m2[e]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float v = s[e] - mean[e];
+                mean[e] += v * share;
+                m2[e] += d[e] + v * v * n * share;
+            }
+            n = all;
         }
+        if (t.on)
+#pragma unroll
+            for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(mean[e], m2[e]);
         __syncthreads();
         // the row-threads' statistics of a channel
         const int channels = p.tp * N;
-        const float rows = (float)max(t.end - t.start, (int64_t)1);
+        const float rows = (float)max(t.n, 1);
         float2 *const own = red + p.rt * channels;
         for (int k = threadIdx.x; k < channels; k += blockDim.x) {
             float mu = 0.0f, q = 0.0f;
-            for (int i = 0; i < p.rt; ++i) mu += red[i * channels + k].x * t.rows(p, i);
+            for (int i = 0; i < p.rt; ++i) mu += red[i * channels + k].x * (float)t.rows_of(p, i, t.n);
             mu /= rows;
             for (int i = 0; i < p.rt; ++i) {
                 const float2 v = red[i * channels + k];
                 const float d = v.x - mu;
-                q += v.y + d * d * t.rows(p, i);
+                q += v.y + d * d * (float)t.rows_of(p, i, t.n);
             }
             own[k] = make_float2(mu, q);
         }
         __syncthreads();
-        const int tile = (int)(job % p.tiles);
         float2 *const o = out + (t.b * p.parts + t.part) * p.entries;
         if (!p.by_group) {
             for (int k = threadIdx.x; k < channels; k += blockDim.x) {
-                const int c = (tile * p.tp) * N + k, piece = c / N;
+                const int piece = t.tile * p.tp + k / N, c = piece * N;
                 if (piece >= p.P) continue;
-                const int at = min(piece * N, a.C - N);
-                if (k % N >= piece * N - at) o[at + k % N] = own[k];
+                const int at = min(c, a.C - N);
+                if (k % N >= c - at) o[at + k % N] = own[k];
             }
         } else {
-            // lanes in teams of 8 to a group
-            const int lane = threadIdx.x & 7;
-            for (int g = threadIdx.x >> 3; g < a.G; g += blockDim.x >> 3) {
+            // the last piece is moved back to end with the row
+            auto of = [&](int c) { return own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c]; };
+            each_group(a, p, [&](int g, int lane) {
                 float mu = 0.0f, q = 0.0f;
-                for (int i = lane; i < a.D; i += 8) {
-                    const int c = g * a.D + i, last = a.C - N;
-                    mu += own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - last : c].x;
-                }
-                for (int d = 1; d < 8; d <<= 1) mu += __shfl_xor(mu, d);
-                mu /= (float)a.D;
-                for (int i = lane; i < a.D; i += 8) {
-                    const int c = g * a.D + i, last = a.C - N;
-                    const float2 v = own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - last : c];
+                for (int i = lane; i < a.D; i += p.team) mu += of(g * a.D + i).x;
+                mu = team_sum(p, mu) / (float)a.D;
+                for (int i = lane; i < a.D; i += p.team) {
+                    const float2 v = of(g * a.D + i);
                     const float d = v.x - mu;
                     q += v.y + d * d * rows;
                 }
-                for (int d = 1; d < 8; d <<= 1) q += __shfl_xor(q, d);
+                q = team_sum(p, q);
                 if (lane == 0) o[g] = make_float2(mu, q);
-            }
+            });
         }
         __syncthreads();
-    }
-}
-
-// The sum over a workgroup of NT threads, the same value in every one.
-template <int NT>
-__device__ __forceinline__ float all_sum(float v, float *red) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    if constexpr (NT > 64) {
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NT / 64; ++i) v += red[i];
-    }
-    return v;
-}
-
-// f(part, entry, rows of the part) for every entry of group g, thread by thread.
-template <int NT, typename F>
-__device__ __forceinline__ void each_entry(const GnParts &p, int per, int64_t n, F f) {
-    const int cols = per < NT ? per : NT, rp = NT / cols;
-    const int c0 = threadIdx.x % cols, p0 = threadIdx.x / cols;
-    if (p0 >= rp) return;
-    for (int i = p0; i < p.parts; i += rp) {
-        const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
-        if (rows <= 0) return;
-        for (int c = c0; c < per; c += cols) f(i, c, (float)rows);
     }
 }
 
@@ -276,282 +225,149 @@ __global__ __launch_bounds__(NT) void k_gn_join(GroupNormArgs a, GnParts p, cons
     }
 }
 
-template <typename T, int N>
-__global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts p, const float2 *stat, int64_t jobs) {
+template <typename T, int N, int ACT>
+__global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts p, const float2 *part, float2 *stat, int64_t jobs) {
     using P = Piece<T, N>;
     using E = typename T::T;
-    for (int64_t at = blockIdx.x; at < jobs; at += gridDim.x) {
-        const Place<N> t(a, p, jobs - 1 - at);  // what was read last is still in cache
-        if (!t.on) continue;
-        const E *const x = (const E *)a.x + t.b * a.S * a.C + t.at;
-        E *const y = (E *)a.y + t.b * a.S * a.C + t.at;
-        float mean[N], r[N], w[N], b[N];
+    extern __shared__ float2 joined[];
+    for (int64_t k = blockIdx.x; k < jobs; k += gridDim.x) {
+        const Place<T, N> t(a, p, jobs - 1 - k);  // what was read last is still in cache
+        const char *const x = (const char *)a.x + t.base;
+        char *const y = (char *)a.y + t.base;
+        const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
+        typename P::Raw raw[kBatch];
+        auto load = [&](int i0) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float2 s = stat[t.b * a.G + (t.at + e) / a.D];
-            mean[e] = s.x, r[e] = s.y;
-            w[e] = a.w ? T::ld((const E *)a.w, t.at + e) : 1.0f;
-            b[e] = a.b ? T::ld((const E *)a.b, t.at + e) : 0.0f;
-        }
-        for (int64_t row0 = t.start + t.rt; row0 < t.last; row0 += (int64_t)kBatch * p.rt) {
-            typename P::Raw raw[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int64_t row = row0 + (int64_t)i * p.rt;
-                raw[i] = P::load(x + (row < t.end ? row : row0) * a.C);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int64_t row = row0 + (int64_t)i * p.rt;
-                if (row >= t.last) break;
-                float f[N];
-                P::widen(raw[i], f);
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    f[e] = row < t.end ? activate((f[e] - mean[e]) * r[e] * w[e] + b[e], a.act) : 0.0f;
-                store_own<T, N>(y + row * a.C, f, t.skip);
-            }
-        }
-    }
-}
-
-// ---- gradients in parts ------------------------------------------------------------
-
-// What a thread keeps of its channels.
-template <typename T, int N>
-struct Channels {
-    float mean[N], r[N], w[N], b[N];
-    __device__ __forceinline__ Channels(const GroupNormArgs &a, int64_t sample, int at) {
-        using E = typename T::T;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int64_t k = sample * a.G + (at + e) / a.D;
-            mean[e] = a.mean[k], r[e] = a.rstd[k];
-            w[e] = a.w ? T::ld((const E *)a.w, at + e) : 1.0f;
-            b[e] = a.b ? T::ld((const E *)a.b, at + e) : 0.0f;
-        }
-    }
-    // x becomes xh and g becomes g'
-    __device__ __forceinline__ void back(float *x, float *g, int act) const {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            x[e] = (x[e] - mean[e]) * r[e];
-            g[e] = activate_back(x[e] * w[e] + b[e], g[e], act);
-        }
-    }
-};
-
-// sum g' and sum g' xh of every channel over a part: [b][part][C].
-template <typename T, int N>
-__global__ __launch_bounds__(512) void k_gn_part_sums(GroupNormArgs a, GnParts p, float2 *out, int64_t jobs) {
-    using P = Piece<T, N>;
-    using E = typename T::T;
-    extern __shared__ float2 red[];
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Place<N> t(a, p, job);
-        const int64_t base = t.b * a.S * a.C + t.at;
-        const E *const x = (const E *)a.x + base, *const g = (const E *)a.g + base;
-        if (t.on) {
-            const Channels<T, N> ch(a, t.b, t.at);
-            float s1[N] = {}, s2[N] = {};
-            constexpr int U = kBatch / 2;
-            for (int64_t r = t.start + t.rt; r < t.end; r += (int64_t)U * p.rt) {
-                typename P::Raw xr[U], gr[U];
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int64_t row = r + (int64_t)i * p.rt;
-                    xr[i] = P::load(x + (row < t.end ? row : r) * a.C);
-                    gr[i] = P::load(g + (row < t.end ? row : r) * a.C);
+            for (int i = 0; i < kBatch; ++i) raw[i] = P::load((const E *)(x + (t.off + (uint32_t)max(min(i0 + i, mine - 1), 0) * t.step)));
+        };
+        if (every) load(0);
+        if (p.joined) {
+            const int64_t n = positions(a, t.b);
+            const float2 *const v = part + t.b * p.parts * p.entries;
+            each_group(a, p, [&](int g, int lane) {
+                float s = 0.0f, q = 0.0f;
+                for (int i = lane; i < p.parts; i += p.team) {
+                    const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
+                    if (rows > 0) s += v[(int64_t)i * a.G + g].x * (float)rows;
                 }
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    if (r + (int64_t)i * p.rt >= t.end) break;
-                    float xh[N], u[N];
-                    P::widen(xr[i], xh);
-                    P::widen(gr[i], u);
-                    ch.back(xh, u, a.act);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        s1[e] += u[e];
-                        s2[e] += u[e] * xh[e];
+                const float mean = n > 0 ? team_sum(p, s) / (float)n : 0.0f;
+                for (int i = lane; i < p.parts; i += p.team) {
+                    const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
+                    const float2 e = v[(int64_t)i * a.G + g];
+                    const float d = e.x - mean;
+                    if (rows > 0) q += e.y + d * d * (float)rows * (float)a.D;
+                }
+                const float rstd = n > 0 ? rsqrtf(team_sum(p, q) / ((float)n * (float)a.D) + a.eps) : 0.0f;
+                if (lane == 0) {
+                    joined[g] = make_float2(mean, rstd);
+                    if (t.part == 0) {
+                        if (a.mean) a.mean[t.b * a.G + g] = mean;
+                        if (a.rstd) a.rstd[t.b * a.G + g] = rstd;
                     }
                 }
-            }
-            for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(s1[e], s2[e]);
+            });
+            __syncthreads();
         }
-        __syncthreads();
-        const int channels = p.tp * N, tile = (int)(job % p.tiles);
-        float2 *const o = out + (t.b * p.parts + t.part) * a.C;
-        for (int k = threadIdx.x; k < channels; k += blockDim.x) {
-            const int c = tile * channels + k, piece = c / N;
-            if (piece >= p.P) continue;
-            const int at = min(piece * N, a.C - N);
-            if (k % N < piece * N - at) continue;
-            float2 s = make_float2(0.0f, 0.0f);
-            for (int i = 0; i < p.rt; ++i) {
-                s.x += red[i * channels + k].x;
-                s.y += red[i * channels + k].y;
+        if (every) {
+            float mean[N], r[N], b[N];
+            if (a.b) {
+                P::widen(P::load((const E *)a.b + t.at), b);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) b[e] = 0.0f;
             }
-            o[at + k % N] = s;
+            if (a.w) {
+                P::widen(P::load((const E *)a.w + t.at), r);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) r[e] = 1.0f;
+            }
+            int g = t.at / a.D, c = t.at - g * a.D;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float2 s = p.joined ? joined[g] : stat[t.b * a.G + g];
+                mean[e] = s.x, r[e] *= s.y;
+                if (++c == a.D) c = 0, g = min(g + 1, a.G - 1);
+            }
+            for (int i0 = 0; i0 < every; i0 += kBatch) {
+                if (i0) load(i0);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (i0 + i >= every) break;
+                    float f[N];
+                    hold(raw[i]);
+                    P::widen(raw[i], f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        f[e] = i0 + i < mine ? activate<ACT>((f[e] - mean[e]) * r[e] + b[e]) : 0.0f;
+                        hold(f[e]);
+                    }
+                    store_own<T, N>((E *)(y + (t.off + (uint32_t)(i0 + i) * t.step)), f, t.skip);
+                }
+            }
         }
-        __syncthreads();
+        if (p.joined) __syncthreads();
     }
 }
 
-// mean u and mean(u xh) of a group.
-template <typename T, int NT>
-__global__ __launch_bounds__(NT) void k_gn_join_back(GroupNormArgs a, GnParts p, const float2 *part, float2 *stat) {
-    using E = typename T::T;
-    __shared__ float red[NT / 64];
-    const int64_t jobs = a.B * a.G;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int64_t b = job / a.G, n = positions(a, b);
-        const int g = (int)(job % a.G);
-        const float2 *const v = part + b * p.parts * a.C + (int64_t)g * a.D;
-        float s = 0.0f, q = 0.0f;
-        each_entry<NT>(p, a.D, n, [&](int i, int c, float) {
-            const float2 e = v[(int64_t)i * a.C + c];
-            const float w = a.w ? T::ld((const E *)a.w, (int64_t)g * a.D + c) : 1.0f;
-            s += e.x * w;
-            q += e.y * w;
-        });
-        s = all_sum<NT>(s, red);
-        q = all_sum<NT>(q, red);
-        const float inv = n > 0 ? 1.0f / ((float)n * (float)a.D) : 0.0f;
-        if (threadIdx.x == 0) stat[job] = make_float2(s * inv, q * inv);
+template <typename T, int N, int R, int ACT>
+hipError_t run_held(const GroupNormArgs &a, const HeldPlan &p, hipStream_t stream) {
+    const int64_t jobs = p.batches * p.slabs;
+    for (int64_t first = 0; first < jobs; first += kMaxGrid) {
+        const dim3 grid((unsigned)std::min(jobs - first, kMaxGrid)), block(p.nt);
+        if (p.mode == kShuffle)
+            hipLaunchKernelGGL((k_gn_held<T, N, R, kShuffle, ACT>), grid, block, p.lds, stream, a, p, first);
+        else if (p.mode == kWhole)
+            hipLaunchKernelGGL((k_gn_held<T, N, R, kWhole, ACT>), grid, block, p.lds, stream, a, p, first);
+        else if constexpr (R <= 8)
+            hipLaunchKernelGGL((k_gn_held<T, N, R, kMixed, ACT>), grid, block, p.lds, stream, a, p, first);
     }
+    return hipGetLastError();
 }
 
-template <typename T, int N>
-__global__ __launch_bounds__(512) void k_gn_part_back(GroupNormArgs a, GnParts p, const float2 *stat, int64_t jobs) {
-    using P = Piece<T, N>;
-    using E = typename T::T;
-    for (int64_t k = blockIdx.x; k < jobs; k += gridDim.x) {
-        const Place<N> t(a, p, jobs - 1 - k);
-        if (!t.on) continue;
-        const int64_t base = t.b * a.S * a.C + t.at;
-        const E *const x = (const E *)a.x + base, *const g = (const E *)a.g + base;
-        E *const y = (E *)a.y + base;
-        const Channels<T, N> ch(a, t.b, t.at);
-        float c1[N], c2[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float2 s = stat[t.b * a.G + (t.at + e) / a.D];
-            c1[e] = s.x, c2[e] = s.y;
-        }
-        constexpr int U = kBatch / 2;
-        for (int64_t row0 = t.start + t.rt; row0 < t.last; row0 += (int64_t)U * p.rt) {
-            typename P::Raw xr[U], gr[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int64_t row = row0 + (int64_t)i * p.rt;
-                xr[i] = P::load(x + (row < t.end ? row : row0) * a.C);
-                gr[i] = P::load(g + (row < t.end ? row : row0) * a.C);
-            }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int64_t row = row0 + (int64_t)i * p.rt;
-                if (row >= t.last) break;
-                float xh[N], u[N];
-                P::widen(xr[i], xh);
-                P::widen(gr[i], u);
-                ch.back(xh, u, a.act);
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    u[e] = row < t.end ? ch.r[e] * (u[e] * ch.w[e] - c1[e] - xh[e] * c2[e]) : 0.0f;
-                store_own<T, N>(y + row * a.C, u, t.skip);
-            }
+template <typename T, int N, int ACT>
+hipError_t run(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
+    const HeldPlan h = plan_held(a.B, a.S, a.C, a.G, N, sizeof(typename T::T), 1, num_cus);
+    if constexpr (N > 1) {
+        switch (h.R) {
+        case 1: return run_held<T, N, 1, ACT>(a, h, stream);
+        case 2: return run_held<T, N, 2, ACT>(a, h, stream);
+        case 4: return run_held<T, N, 4, ACT>(a, h, stream);
+        case 8: return run_held<T, N, 8, ACT>(a, h, stream);
+        case 16: return run_held<T, N, 16, ACT>(a, h, stream);
         }
     }
-}
-
-// The parameters' gradients: sum over `rows` rows of [C] pairs (sum g', sum g' xh).
-// 16 channels of 16 row-threads; the rows of a thread, then the threads in order.
-template <typename T>
-__global__ __launch_bounds__(256) void k_gn_params(const float2 *sums, int64_t rows, int C, void *gw, void *gb) {
-    using E = typename T::T;
-    __shared__ float2 red[16][17];
-    const int64_t c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
-    const int r0 = threadIdx.x >> 4;
-    float2 s = make_float2(0.0f, 0.0f);
-    if (c < C)
-        for (int64_t r = r0; r < rows; r += 16) {
-            const float2 v = sums[r * C + c];
-            s.x += v.x, s.y += v.y;
-        }
-    red[r0][threadIdx.x & 15] = s;
-    __syncthreads();
-    if (r0 == 0 && c < C) {
-        for (int i = 1; i < 16; ++i) s.x += red[i][threadIdx.x].x, s.y += red[i][threadIdx.x].y;
-        if (gw) T::st((E *)gw, c, s.y);
-        if (gb) T::st((E *)gb, c, s.x);
-    }
-}
-
-constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads); more jobs are looped over
-
-unsigned grid_for(int64_t jobs) { return (unsigned)std::min(jobs, kMaxGrid); }
-
-int piece_size(int C, int dtype) {
-    const int v = dtype == kF32 ? 4 : 8;
-    return C >= v ? v : 1;
-}
-
-template <typename T, int N>
-hipError_t run_parts(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
-    const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, num_cus);
+    const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, sizeof(typename T::T), num_cus);
     float2 *const part = (float2 *)a.ws, *const stat = (float2 *)((char *)a.ws + p.part_bytes);
     const int64_t jobs = a.B * p.parts * p.tiles;
     const size_t lds = (size_t)(p.rt + 1) * p.tp * N * sizeof(float2);
     hipLaunchKernelGGL((k_gn_part_stats<T, N>), dim3(grid_for(jobs)), dim3(p.nt), lds, stream, a, p, part, jobs);
-    if ((int64_t)p.parts * (p.by_group ? 1 : a.D) <= 256)
-        hipLaunchKernelGGL((k_gn_join<64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, stat);
-    else
-        hipLaunchKernelGGL((k_gn_join<1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, stat);
-    hipLaunchKernelGGL((k_gn_part_apply<T, N>), dim3(grid_for(jobs)), dim3(p.nt), 0, stream, a, p, stat, jobs);
-    return hipGetLastError();
-}
-
-template <typename T, int N>
-hipError_t run_parts_back(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
-    const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, num_cus);
-    const size_t part_bytes = ((size_t)a.B * p.parts * a.C * sizeof(float2) + 255) & ~(size_t)255;
-    float2 *const part = (float2 *)a.ws, *const stat = (float2 *)((char *)a.ws + part_bytes);
-    const int64_t jobs = a.B * p.parts * p.tiles;
-    const size_t lds = (size_t)p.rt * p.tp * N * sizeof(float2);
-    if (jobs > 0) hipLaunchKernelGGL((k_gn_part_sums<T, N>), dim3(grid_for(jobs)), dim3(p.nt), lds, stream, a, p, part, jobs);
-    if (a.y && jobs > 0 && a.S > 0) {
-        if ((int64_t)p.parts * a.D <= 256)
-            hipLaunchKernelGGL((k_gn_join_back<T, 64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, stat);
+    if (!p.joined) {
+        if ((int64_t)p.parts * (p.by_group ? 1 : a.D) <= 256)
+            hipLaunchKernelGGL((k_gn_join<64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, stat);
         else
-            hipLaunchKernelGGL((k_gn_join_back<T, 1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, stat);
-        hipLaunchKernelGGL((k_gn_part_back<T, N>), dim3(grid_for(jobs)), dim3(p.nt), 0, stream, a, p, stat, jobs);
+            hipLaunchKernelGGL((k_gn_join<1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, stat);
     }
-    if (a.gw || a.gb)
-        hipLaunchKernelGGL((k_gn_params<T>), dim3((a.C + 15) / 16), dim3(256), 0, stream, part, a.B * p.parts, a.C, a.gw, a.gb);
+    hipLaunchKernelGGL((k_gn_part_apply<T, N, ACT>), dim3(grid_for(jobs)), dim3(p.nt), p.joined ? a.G * sizeof(float2) : 0, stream, a, p,
+                       part, stat, jobs);
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t group_norm_workspace(int64_t B, int64_t S, int C, int G, int dtype, int num_cus) {
-    const GnParts p = plan_parts(B, S, C, G, piece_size(C, dtype), num_cus);
+    const int N = piece_size(C, dtype);
+    if (plan_held(B, S, C, G, N, dtype == kF32 ? 4 : 2, 1, num_cus).R) return 0;
+    const GnParts p = plan_parts(B, S, C, G, N, dtype == kF32 ? 4 : 2, num_cus);
     return p.part_bytes + p.stat_bytes;
 }
 
 hipError_t launch_group_norm(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
-    if (a.dtype == kF32) return a.C >= 4 ? run_parts<F32, 4>(a, num_cus, stream) : run_parts<F32, 1>(a, num_cus, stream);
-    return a.C >= 8 ? run_parts<BF16, 8>(a, num_cus, stream) : run_parts<BF16, 1>(a, num_cus, stream);
-}
-
-size_t group_norm_backward_workspace(int64_t B, int64_t S, int C, int G, int dtype, bool, int num_cus) {
-    const GnParts p = plan_parts(B, S, C, G, piece_size(C, dtype), num_cus);
-    return (((size_t)B * p.parts * C * sizeof(float2) + 255) & ~(size_t)255) + p.stat_bytes;
-}
-
-hipError_t launch_group_norm_backward(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
-    if (a.dtype == kF32) return a.C >= 4 ? run_parts_back<F32, 4>(a, num_cus, stream) : run_parts_back<F32, 1>(a, num_cus, stream);
-    return a.C >= 8 ? run_parts_back<BF16, 8>(a, num_cus, stream) : run_parts_back<BF16, 1>(a, num_cus, stream);
+    return by_activation(a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (a.dtype == kF32) return a.C >= 4 ? run<F32, 4, ACT>(a, num_cus, stream) : run<F32, 1, ACT>(a, num_cus, stream);
+        return a.C >= 8 ? run<BF16, 8, ACT>(a, num_cus, stream) : run<BF16, 1, ACT>(a, num_cus, stream);
+    });
 }
 
 }  // namespace dc1d

@@ -109,13 +109,6 @@ struct Rows {
     }
 };
 
-// Keeps what uses `v` behind what came before: the compiler would start all of a
-// slot's exponentials at once and hold some 100 registers more for them.
-template <typename V>
-__device__ __forceinline__ void hold(V &v) {
-    asm volatile("" : "+v"(v));
-}
-
 template <int N>
 struct Map {  // h -> A h + H
     float A[N], H[N];

@@ -127,6 +127,15 @@ __device__ __forceinline__ void store_own(typename T::T *p, const float *f, int 
     }
 }
 
+// Keeps what uses `v` behind what came before (and its packed form in registers
+// till then): left to itself the compiler starts the exponentials of all of a
+// thread's elements at once, or widens them once for several passes, and holds
+// up to 100 registers more for them.
+template <typename V>
+__device__ __forceinline__ void hold(V &v) {
+    asm volatile("" : "+v"(v));
+}
+
 // sigmoid(z) and 1 - sigmoid(z): the smaller one from exp(-|z|), the larger one as
 // 1 minus it, so that neither cancels.  v_exp_f32 and v_rcp_f32 are off by an
 // ulp, and the exponent's product with log2 e by 2^-24 |z|.
