@@ -14,21 +14,17 @@ enum Act { kNone = 0, kRelu = 1, kSilu = 2 };
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays
-    if constexpr (ACT == kSilu) {
-        float p, q;
-        sigmoid_pair(z, p, q);
-        return z * p;
-    }
+    if constexpr (ACT == kSilu) return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
     return z;
 }
-// The gradient g of act(z) taken to z.
+// The gradient g of act(z) taken to z.  silu: p (1 + z q), p = 1 / (1 + t) and q =
+// t p = 1 - p for t = exp(-z), held below 2^126 (z > -87) so that t p stays finite.
 template <int ACT>
 __device__ __forceinline__ float activate_back(float z, float g) {
     if constexpr (ACT == kRelu) return z > 0.0f ? g : 0.0f;
     if constexpr (ACT == kSilu) {
-        float p, q;
-        sigmoid_pair(z, p, q);
-        return g * (p + z * p * q);
+        const float t = __builtin_amdgcn_exp2f(fminf(-z * kLog2e, 126.0f)), p = __builtin_amdgcn_rcpf(1.0f + t);
+        return g * (p * fmaf(z, t * p, 1.0f));
     }
     return g;
 }
@@ -152,9 +148,9 @@ struct HeldPlace {
     }
 };
 template <typename T, int N, int MODE>
-__device__ __forceinline__ void put(char *p, const float *f, int skip) {
+__device__ __forceinline__ void put(char *p, const float *f, int skip, bool in_place) {
     if constexpr (MODE == kMixed)
-        store_own<T, N>((typename T::T *)p, f, skip);
+        store_own<T, N>((typename T::T *)p, f, skip, in_place);
     else
         Piece<T, N>::store((typename T::T *)p, f);
 }
@@ -231,8 +227,11 @@ struct GnParts {
     bool joined;      // the workgroups that need a sample's statistics join them themselves
     int entries;      // of a part: G or C
     int team;         // lanes that add a group's values
+    FastDiv by_tiles, by_parts, by_tp, by_rt, by_D;
     size_t part_bytes, stat_bytes;
 };
+
+constexpr int kJoinHere = 4096;  // statistics of a sample (32 KB) that every workgroup joins itself
 
 inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, int num_cus) {
     GnParts p;
@@ -255,9 +254,11 @@ inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, 
     p.parts = (int)std::max<int64_t>(1, (S + p.rows - 1) / p.rows);
     p.by_group = p.tiles == 1;
     p.entries = p.by_group ? G : C;
-    p.joined = p.by_group && G <= 1024 && (int64_t)p.parts * G <= 16384;
+    p.joined = p.by_group && (int64_t)p.parts * G <= kJoinHere;
     p.team = 64;
     while (p.team > 1 && p.team > p.nt / G) p.team /= 2;
+    p.by_tiles = make_fastdiv(p.tiles), p.by_parts = make_fastdiv(p.parts), p.by_tp = make_fastdiv(p.tp);
+    p.by_rt = make_fastdiv(p.rt), p.by_D = make_fastdiv(C / G);
     p.part_bytes = ((size_t)B * p.parts * p.entries * sizeof(float2) + 255) & ~(size_t)255;
     p.stat_bytes = ((size_t)B * G * sizeof(float2) + 255) & ~(size_t)255;
     return p;
@@ -271,16 +272,16 @@ struct Place {
     int part, tile, rt, j, at, skip;
     uint32_t off, step;  // bytes from there to the thread's first row, and from one to the next
     bool on;
-    __device__ __forceinline__ Place(const GroupNormArgs &a, const GnParts &p, int64_t job) {
-        tile = (int)(job % p.tiles);
-        const int64_t q = job / p.tiles;
-        b = q / p.parts;
-        part = (int)(q % p.parts);
+    __device__ __forceinline__ Place(const GroupNormArgs &a, const GnParts &p, int64_t first, uint32_t job) {
+        const uint32_t q = fdiv(job, p.by_tiles), s = fdiv(q, p.by_parts);
+        tile = (int)(job - q * p.tiles);
+        b = first + s;
+        part = (int)(q - s * p.parts);
         const int64_t start = (int64_t)part * p.rows, past = min(start + p.rows, a.S);
         rows = (int)(past - start);
         n = (int)max(min(past, positions(a, b)) - start, (int64_t)0);
-        rt = threadIdx.x / p.tp;
-        j = threadIdx.x % p.tp;
+        rt = (int)fdiv(threadIdx.x, p.by_tp);
+        j = threadIdx.x - rt * p.tp;
         const int piece = tile * p.tp + j, c = piece * N;
         on = rt < p.rt && piece < p.P;
         at = on ? min(c, a.C - N) : 0;
@@ -291,7 +292,7 @@ struct Place {
         step = (uint32_t)p.rt * (uint32_t)a.C * es;
     }
     // how many of the first `of` rows of the part are row-thread i's
-    __device__ __forceinline__ static int rows_of(const GnParts &p, int i, int of) { return of > i ? (of - i + p.rt - 1) / p.rt : 0; }
+    __device__ __forceinline__ static int rows_of(const GnParts &p, int i, int of) { return of > i ? (int)fdiv(of - i + p.rt - 1, p.by_rt) : 0; }
 };
 
 constexpr int kBatch = 8;  // rows whose loads are in flight together
@@ -325,13 +326,32 @@ __device__ __forceinline__ void each_entry(const GnParts &p, int per, int64_t n,
     }
 }
 
-constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads); more jobs are looped over
+constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads)
+
+// f(first sample, workgroups) for launches of whole samples, the last samples first where `back`.
+template <typename F>
+void by_samples(int64_t B, const GnParts &p, bool back, F f) {
+    const int64_t per = (int64_t)p.parts * p.tiles, some = std::max<int64_t>(1, kMaxGrid / per), n = (B + some - 1) / some;
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t b = (back ? n - 1 - i : i) * some;
+        f(b, dim3((unsigned)(std::min(some, B - b) * per)));
+    }
+}
 
 inline unsigned grid_for(int64_t jobs) { return (unsigned)std::min(jobs, kMaxGrid); }
 
 inline int piece_size(int C, int dtype) {
     const int v = dtype == kF32 ? 4 : 8;
     return C >= v ? v : 1;
+}
+
+// A sample's statistics of all parts, [part][G], to LDS.
+__device__ __forceinline__ void fetch_parts(const GroupNormArgs &a, const GnParts &p, const float2 *from, int64_t b, float2 *to) {
+    const int n = p.parts * a.G;
+    const float2 *const v = from + b * n;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = v[i];
+    __syncthreads();
 }
 
 // f(group, lane of its team) for every group of a sample; a team's lanes share a wave.

@@ -87,7 +87,7 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
                 f[e] = row < n ? activate<ACT>((f[e] - mean[t.v(e)]) * w[e] + c[e]) : 0.0f;
                 hold(f[e]);
             }
-            put<T, N, MODE>(y + t.offset(a, p, sizeof(E), s, i, true), f, t.skip);
+            put<T, N, MODE>(y + t.offset(a, p, sizeof(E), s, i, true), f, t.skip, a.y == a.x || t.channels < N);  // fewer: the others' groups are not here
         }
     if (t.rt == 0) {
         // the thread that holds a group's first element
@@ -102,97 +102,100 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
 }
 
 template <typename T, int N>
-__global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts p, float2 *out, int64_t jobs) {
+__global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts p, float2 *out, int64_t first) {
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 red[];  // [rt][tp][N], then of the channels
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Place<T, N> t(a, p, job);
-        const char *const x = (const char *)a.x + t.base;
-        const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
-        float n = 0.0f, mean[N] = {}, m2[N] = {};
-        for (int i0 = 0; i0 < mine; i0 += kBatch) {
-            typename P::Raw raw[kBatch];
+    const Place<T, N> t(a, p, first, blockIdx.x);
+    const char *const x = (const char *)a.x + t.base;
+    const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
+    float n = 0.0f, mean[N] = {}, m2[N] = {};
+    typename P::Raw raw[kBatch], next[kBatch];
+    auto load = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) raw[i] = P::load((const E *)(x + (t.off + (uint32_t)min(i0 + i, mine - 1) * t.step)));
-            // the batch's mean and squares about it, joined with those so far
-            const int have = min(mine - i0, kBatch);
-            const float m = (float)have, all = n + m, share = m / all;
-            float s[N] = {}, d[N] = {};
+        for (int i = 0; i < kBatch; ++i) next[i] = P::load((const E *)(x + (t.off + (uint32_t)min(i0 + i, mine - 1) * t.step)));
+    };
+    if (mine) load(0);
+    for (int i0 = 0; i0 < mine; i0 += kBatch) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                float f[N];
-                hold(raw[i]);
-                P::widen(raw[i], f);
+        for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+        if (i0 + kBatch < mine) load(i0 + kBatch);
+        // the batch's mean and squares about it, joined with those so far
+        const int have = min(mine - i0, kBatch);
+        const float m = (float)have, all = n + m, share = m / all;
+        float s[N] = {}, d[N] = {};
 #pragma unroll
-                for (int e = 0; e < N; ++e) s[e] += i < have ? f[e] : 0.0f;
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            float f[N];
+            hold(raw[i]);
+            P::widen(raw[i], f);
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e] = have == kBatch ? s[e] * (1.0f / kBatch) : s[e] / m;  // equal values have their own as mean
+            for (int e = 0; e < N; ++e) s[e] += i < have ? f[e] : 0.0f;
+        }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                float f[N];
-                hold(raw[i]);
-                P::widen(raw[i], f);
+        for (int e = 0; e < N; ++e) s[e] = have == kBatch ? s[e] * (1.0f / kBatch) : s[e] / m;  // equal values have their own as mean
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float v = i < have ? f[e] - s[e] : 0.0f;
-                    d[e] += v * v;
-                }
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            float f[N];
+            hold(raw[i]);
+            P::widen(raw[i], f);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float v = s[e] - mean[e];
-                mean[e] += v * share;
-                m2[e] += d[e] + v * v * n * share;
+                const float v = i < have ? f[e] - s[e] : 0.0f;
+                d[e] += v * v;
             }
-            n = all;
         }
-        if (t.on)
 #pragma unroll
-            for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(mean[e], m2[e]);
-        __syncthreads();
-        // the row-threads' statistics of a channel
-        const int channels = p.tp * N;
-        const float rows = (float)max(t.n, 1);
-        float2 *const own = red + p.rt * channels;
+        for (int e = 0; e < N; ++e) {
+            const float v = s[e] - mean[e];
+            mean[e] += v * share;
+            m2[e] += d[e] + v * v * n * share;
+        }
+        n = all;
+    }
+    if (t.on)
+#pragma unroll
+        for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(mean[e], m2[e]);
+    __syncthreads();
+    // the row-threads' statistics of a channel
+    const int channels = p.tp * N;
+    const float rows = (float)max(t.n, 1);
+    float2 *const own = red + p.rt * channels;
+    for (int k = threadIdx.x; k < channels; k += blockDim.x) {
+        float mu = 0.0f, q = 0.0f;
+        for (int i = 0; i < p.rt; ++i) mu += red[i * channels + k].x * (float)t.rows_of(p, i, t.n);
+        mu /= rows;
+        for (int i = 0; i < p.rt; ++i) {
+            const float2 v = red[i * channels + k];
+            const float d = v.x - mu;
+            q += v.y + d * d * (float)t.rows_of(p, i, t.n);
+        }
+        own[k] = make_float2(mu, q);
+    }
+    __syncthreads();
+    float2 *const o = out + (t.b * p.parts + t.part) * p.entries;
+    if (!p.by_group) {
         for (int k = threadIdx.x; k < channels; k += blockDim.x) {
+            const int piece = t.tile * p.tp + k / N, c = piece * N;
+            if (piece >= p.P) continue;
+            const int at = min(c, a.C - N);
+            if (k % N >= c - at) o[at + k % N] = own[k];
+        }
+    } else {
+        // the last piece is moved back to end with the row
+        auto of = [&](int c) { return own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c]; };
+        each_group(a, p, [&](int g, int lane) {
             float mu = 0.0f, q = 0.0f;
-            for (int i = 0; i < p.rt; ++i) mu += red[i * channels + k].x * (float)t.rows_of(p, i, t.n);
-            mu /= rows;
-            for (int i = 0; i < p.rt; ++i) {
-                const float2 v = red[i * channels + k];
+            for (int i = lane; i < a.D; i += p.team) mu += of(g * a.D + i).x;
+            mu = team_sum(p, mu) / (float)a.D;
+            for (int i = lane; i < a.D; i += p.team) {
+                const float2 v = of(g * a.D + i);
                 const float d = v.x - mu;
-                q += v.y + d * d * (float)t.rows_of(p, i, t.n);
+                q += v.y + d * d * rows;
             }
-            own[k] = make_float2(mu, q);
-        }
-        __syncthreads();
-        float2 *const o = out + (t.b * p.parts + t.part) * p.entries;
-        if (!p.by_group) {
-            for (int k = threadIdx.x; k < channels; k += blockDim.x) {
-                const int piece = t.tile * p.tp + k / N, c = piece * N;
-                if (piece >= p.P) continue;
-                const int at = min(c, a.C - N);
-                if (k % N >= c - at) o[at + k % N] = own[k];
-            }
-        } else {
-            // the last piece is moved back to end with the row
-            auto of = [&](int c) { return own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c]; };
-            each_group(a, p, [&](int g, int lane) {
-                float mu = 0.0f, q = 0.0f;
-                for (int i = lane; i < a.D; i += p.team) mu += of(g * a.D + i).x;
-                mu = team_sum(p, mu) / (float)a.D;
-                for (int i = lane; i < a.D; i += p.team) {
-                    const float2 v = of(g * a.D + i);
-                    const float d = v.x - mu;
-                    q += v.y + d * d * rows;
-                }
-                q = team_sum(p, q);
-                if (lane == 0) o[g] = make_float2(mu, q);
-            });
-        }
-        __syncthreads();
+            q = team_sum(p, q);
+            if (lane == 0) o[g] = make_float2(mu, q);
+        });
     }
 }
 
@@ -226,87 +229,87 @@ __global__ __launch_bounds__(NT) void k_gn_join(GroupNormArgs a, GnParts p, cons
 }
 
 template <typename T, int N, int ACT>
-__global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts p, const float2 *part, float2 *stat, int64_t jobs) {
+__global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts p, const float2 *part, float2 *stat, int64_t first) {
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 joined[];
-    for (int64_t k = blockIdx.x; k < jobs; k += gridDim.x) {
-        const Place<T, N> t(a, p, jobs - 1 - k);  // what was read last is still in cache
-        const char *const x = (const char *)a.x + t.base;
-        char *const y = (char *)a.y + t.base;
-        const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
-        typename P::Raw raw[kBatch];
-        auto load = [&](int i0) {
+    const Place<T, N> t(a, p, first, gridDim.x - 1 - blockIdx.x);  // what was read last is still in cache
+    const char *const x = (const char *)a.x + t.base;
+    char *const y = (char *)a.y + t.base;
+    const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
+    typename P::Raw raw[kBatch], next[kBatch];
+    auto load = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) raw[i] = P::load((const E *)(x + (t.off + (uint32_t)max(min(i0 + i, mine - 1), 0) * t.step)));
-        };
-        if (every) load(0);
-        if (p.joined) {
-            const int64_t n = positions(a, t.b);
-            const float2 *const v = part + t.b * p.parts * p.entries;
-            each_group(a, p, [&](int g, int lane) {
-                float s = 0.0f, q = 0.0f;
-                for (int i = lane; i < p.parts; i += p.team) {
-                    const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
-                    if (rows > 0) s += v[(int64_t)i * a.G + g].x * (float)rows;
+        for (int i = 0; i < kBatch; ++i) next[i] = P::load((const E *)(x + (t.off + (uint32_t)max(min(i0 + i, mine - 1), 0) * t.step)));
+    };
+    if (every) load(0);
+    if (p.joined) {
+        const int64_t n = positions(a, t.b);
+        float2 *const v = joined + a.G;
+        fetch_parts(a, p, part, t.b, v);
+        each_group(a, p, [&](int g, int lane) {
+            float s = 0.0f, q = 0.0f;
+            for (int i = lane; i < p.parts; i += p.team) {
+                const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
+                if (rows > 0) s += v[i * a.G + g].x * (float)rows;
+            }
+            const float mean = n > 0 ? team_sum(p, s) / (float)n : 0.0f;
+            for (int i = lane; i < p.parts; i += p.team) {
+                const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
+                const float2 e = v[i * a.G + g];
+                const float d = e.x - mean;
+                if (rows > 0) q += e.y + d * d * (float)rows * (float)a.D;
+            }
+            const float rstd = n > 0 ? rsqrtf(team_sum(p, q) / ((float)n * (float)a.D) + a.eps) : 0.0f;
+            if (lane == 0) {
+                joined[g] = make_float2(mean, rstd);
+                if (t.part == 0) {
+                    if (a.mean) a.mean[t.b * a.G + g] = mean;
+                    if (a.rstd) a.rstd[t.b * a.G + g] = rstd;
                 }
-                const float mean = n > 0 ? team_sum(p, s) / (float)n : 0.0f;
-                for (int i = lane; i < p.parts; i += p.team) {
-                    const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
-                    const float2 e = v[(int64_t)i * a.G + g];
-                    const float d = e.x - mean;
-                    if (rows > 0) q += e.y + d * d * (float)rows * (float)a.D;
-                }
-                const float rstd = n > 0 ? rsqrtf(team_sum(p, q) / ((float)n * (float)a.D) + a.eps) : 0.0f;
-                if (lane == 0) {
-                    joined[g] = make_float2(mean, rstd);
-                    if (t.part == 0) {
-                        if (a.mean) a.mean[t.b * a.G + g] = mean;
-                        if (a.rstd) a.rstd[t.b * a.G + g] = rstd;
-                    }
-                }
-            });
-            __syncthreads();
+            }
+        });
+        __syncthreads();
+    }
+    if (every) {
+        float mean[N], r[N], b[N];
+        if (a.b) {
+            P::widen(P::load((const E *)a.b + t.at), b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) b[e] = 0.0f;
         }
-        if (every) {
-            float mean[N], r[N], b[N];
-            if (a.b) {
-                P::widen(P::load((const E *)a.b + t.at), b);
-            } else {
+        if (a.w) {
+            P::widen(P::load((const E *)a.w + t.at), r);
+        } else {
 #pragma unroll
-                for (int e = 0; e < N; ++e) b[e] = 0.0f;
-            }
-            if (a.w) {
-                P::widen(P::load((const E *)a.w + t.at), r);
-            } else {
+            for (int e = 0; e < N; ++e) r[e] = 1.0f;
+        }
+        int g = (int)fdiv(t.at, p.by_D), c = t.at - g * a.D;
 #pragma unroll
-                for (int e = 0; e < N; ++e) r[e] = 1.0f;
-            }
-            int g = t.at / a.D, c = t.at - g * a.D;
+        for (int e = 0; e < N; ++e) {
+            const float2 s = p.joined ? joined[g] : stat[t.b * a.G + g];
+            mean[e] = s.x, r[e] *= s.y;
+            if (++c == a.D) c = 0, g = min(g + 1, a.G - 1);
+        }
+        for (int i0 = 0; i0 < every; i0 += kBatch) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float2 s = p.joined ? joined[g] : stat[t.b * a.G + g];
-                mean[e] = s.x, r[e] *= s.y;
-                if (++c == a.D) c = 0, g = min(g + 1, a.G - 1);
-            }
-            for (int i0 = 0; i0 < every; i0 += kBatch) {
-                if (i0) load(i0);
+            for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+            if (i0 + kBatch < every) load(i0 + kBatch);
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    if (i0 + i >= every) break;
-                    float f[N];
-                    hold(raw[i]);
-                    P::widen(raw[i], f);
+            for (int i = 0; i < kBatch; ++i) {
+                if (i0 + i >= every) break;
+                float f[N];
+                hold(raw[i]);
+                P::widen(raw[i], f);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        f[e] = i0 + i < mine ? activate<ACT>((f[e] - mean[e]) * r[e] + b[e]) : 0.0f;
-                        hold(f[e]);
-                    }
-                    store_own<T, N>((E *)(y + (t.off + (uint32_t)(i0 + i) * t.step)), f, t.skip);
+                for (int e = 0; e < N; ++e) {
+                    f[e] = i0 + i < mine ? activate<ACT>((f[e] - mean[e]) * r[e] + b[e]) : 0.0f;
+                    hold(f[e]);
                 }
+                store_own<T, N>((E *)(y + (t.off + (uint32_t)(i0 + i) * t.step)), f, t.skip, a.y == a.x);
             }
         }
-        if (p.joined) __syncthreads();
     }
 }
 
@@ -339,17 +342,20 @@ hipError_t run(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
     }
     const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, sizeof(typename T::T), num_cus);
     float2 *const part = (float2 *)a.ws, *const stat = (float2 *)((char *)a.ws + p.part_bytes);
-    const int64_t jobs = a.B * p.parts * p.tiles;
     const size_t lds = (size_t)(p.rt + 1) * p.tp * N * sizeof(float2);
-    hipLaunchKernelGGL((k_gn_part_stats<T, N>), dim3(grid_for(jobs)), dim3(p.nt), lds, stream, a, p, part, jobs);
+    by_samples(a.B, p, false, [&](int64_t b, dim3 grid) {
+        hipLaunchKernelGGL((k_gn_part_stats<T, N>), grid, dim3(p.nt), lds, stream, a, p, part, b);
+    });
     if (!p.joined) {
         if ((int64_t)p.parts * (p.by_group ? 1 : a.D) <= 256)
             hipLaunchKernelGGL((k_gn_join<64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, stat);
         else
             hipLaunchKernelGGL((k_gn_join<1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, stat);
     }
-    hipLaunchKernelGGL((k_gn_part_apply<T, N, ACT>), dim3(grid_for(jobs)), dim3(p.nt), p.joined ? a.G * sizeof(float2) : 0, stream, a, p,
-                       part, stat, jobs);
+    const size_t here = p.joined ? (size_t)a.G * (1 + p.parts) * sizeof(float2) : 0;
+    by_samples(a.B, p, true, [&](int64_t b, dim3 grid) {
+        hipLaunchKernelGGL((k_gn_part_apply<T, N, ACT>), grid, dim3(p.nt), here, stream, a, p, part, stat, b);
+    });
     return hipGetLastError();
 }
 

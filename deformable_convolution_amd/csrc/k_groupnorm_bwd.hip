@@ -88,7 +88,7 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
                     u[e] = row < n ? r[t.v(e)] * (u[e] * w[e] - v[0][t.v(e)] * inv - xh[e] * (v[1][t.v(e)] * inv)) : 0.0f;
 #pragma unroll
                 for (int e = 0; e < N; ++e) hold(u[e]);
-                put<T, N, MODE>(y + t.offset(a, p, sizeof(E), s, i, true), u, t.skip);
+                put<T, N, MODE>(y + t.offset(a, p, sizeof(E), s, i, true), u, t.skip, a.y == a.g || t.channels < N);
             }
         }
     }
@@ -116,14 +116,14 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
 template <typename T, int N>
 struct Channels {
     float mean[N], r[N], w[N], b[N];
-    __device__ __forceinline__ Channels(const GroupNormArgs &a, int64_t sample, int at) {
+    __device__ __forceinline__ Channels(const GroupNormArgs &a, const GnParts &p, int64_t sample, int at) {
         using P = Piece<T, N>;
         using E = typename T::T;
 #pragma unroll
         for (int e = 0; e < N; ++e) w[e] = 1.0f, b[e] = 0.0f;
         if (a.w) P::widen(P::load((const E *)a.w + at), w);
         if (a.b) P::widen(P::load((const E *)a.b + at), b);
-        int g = at / a.D, c = at - g * a.D;
+        int g = (int)fdiv(at, p.by_D), c = at - g * a.D;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const int64_t k = sample * a.G + g;
@@ -145,84 +145,83 @@ struct Channels {
 // sum g' and sum g' xh of every channel over a part, [b][part][C], and where a
 // tile holds every group sum u and sum u xh of each, [b][part][G].
 template <typename T, int N, int ACT>
-__global__ __launch_bounds__(512) void k_gn_part_sums(GroupNormArgs a, GnParts p, float2 *out, float2 *groups, int64_t jobs) {
+__global__ __launch_bounds__(512) void k_gn_part_sums(GroupNormArgs a, GnParts p, float2 *out, float2 *groups, int64_t first) {
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 red[];
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const Place<T, N> t(a, p, job);
-        const char *const x = (const char *)a.x + t.base, *const g = (const char *)a.g + t.base;
-        const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
-        float s1[N] = {}, s2[N] = {};
-        constexpr int U = kBatch / 2;
-        typename P::Raw xr[U], gr[U];
-        auto load = [&](int i0) {
+    const Place<T, N> t(a, p, first, blockIdx.x);
+    const char *const x = (const char *)a.x + t.base, *const g = (const char *)a.g + t.base;
+    const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
+    float s1[N] = {}, s2[N] = {};
+    constexpr int U = kBatch / 2;
+    typename P::Raw xr[U], gr[U], xn[U], gn[U];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const uint32_t at = t.off + (uint32_t)min(i0 + i, mine - 1) * t.step;
+            xn[i] = P::load((const E *)(x + at));
+            gn[i] = P::load((const E *)(g + at));
+        }
+    };
+    if (mine) {
+        load(0);
+        const Channels<T, N> ch(a, p, t.b, t.at);
+        for (int i0 = 0; i0 < mine; i0 += U) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) xr[i] = xn[i], gr[i] = gn[i];
+            if (i0 + U < mine) load(i0 + U);
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const uint32_t at = t.off + (uint32_t)min(i0 + i, mine - 1) * t.step;
-                xr[i] = P::load((const E *)(x + at));
-                gr[i] = P::load((const E *)(g + at));
-            }
-        };
-        if (mine) {
-            load(0);
-            const Channels<T, N> ch(a, t.b, t.at);
-            for (int i0 = 0; i0 < mine; i0 += U) {
-                if (i0) load(i0);
+                float xh[N], u[N];
+                hold(xr[i]);
+                hold(gr[i]);
+                P::widen(xr[i], xh);
+                P::widen(gr[i], u);
+                ch.template back<ACT>(xh, u);
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    float xh[N], u[N];
-                    hold(xr[i]);
-                    hold(gr[i]);
-                    P::widen(xr[i], xh);
-                    P::widen(gr[i], u);
-                    ch.template back<ACT>(xh, u);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        s1[e] += i0 + i < mine ? u[e] : 0.0f;
-                        s2[e] += i0 + i < mine ? u[e] * xh[e] : 0.0f;
-                        hold(s1[e]);
-                        hold(s2[e]);
-                    }
+                for (int e = 0; e < N; ++e) {
+                    s1[e] += i0 + i < mine ? u[e] : 0.0f;
+                    s2[e] += i0 + i < mine ? u[e] * xh[e] : 0.0f;
+                    hold(s1[e]);
+                    hold(s2[e]);
                 }
             }
         }
-        if (t.on)
-#pragma unroll
-            for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(s1[e], s2[e]);
-        __syncthreads();
-        const int channels = p.tp * N;
-        float2 *const o = out + (t.b * p.parts + t.part) * a.C;
-        for (int k = threadIdx.x; k < channels; k += blockDim.x) {
-            const int piece = t.tile * p.tp + k / N, c = piece * N;
-            if (piece >= p.P) continue;
-            const int at = min(c, a.C - N);
-            if (k % N < c - at) continue;
-            float2 s = make_float2(0.0f, 0.0f);
-            for (int i = 0; i < p.rt; ++i) {
-                s.x += red[i * channels + k].x;
-                s.y += red[i * channels + k].y;
-            }
-            o[at + k % N] = s;
-            red[k] = s;  // row 0 is read by this thread alone
-        }
-        __syncthreads();
-        if (p.by_group)
-            each_group(a, p, [&](int k, int lane) {
-                float u = 0.0f, ux = 0.0f;
-                for (int i = lane; i < a.D; i += p.team) {
-                    const int c = k * a.D + i;
-                    const float2 s = red[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c];
-                    const float w = a.w ? T::ld((const E *)a.w, c) : 1.0f;
-                    u += s.x * w;
-                    ux += s.y * w;
-                }
-                u = team_sum(p, u);
-                ux = team_sum(p, ux);
-                if (lane == 0) groups[(t.b * p.parts + t.part) * a.G + k] = make_float2(u, ux);
-            });
-        __syncthreads();
     }
+    if (t.on)
+#pragma unroll
+        for (int e = 0; e < N; ++e) red[(t.rt * p.tp + t.j) * N + e] = make_float2(s1[e], s2[e]);
+    __syncthreads();
+    const int channels = p.tp * N;
+    float2 *const o = out + (t.b * p.parts + t.part) * a.C;
+    for (int k = threadIdx.x; k < channels; k += blockDim.x) {
+        const int piece = t.tile * p.tp + k / N, c = piece * N;
+        if (piece >= p.P) continue;
+        const int at = min(c, a.C - N);
+        if (k % N < c - at) continue;
+        float2 s = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < p.rt; ++i) {
+            s.x += red[i * channels + k].x;
+            s.y += red[i * channels + k].y;
+        }
+        o[at + k % N] = s;
+        red[k] = s;  // row 0 is read by this thread alone
+    }
+    __syncthreads();
+    if (p.by_group)
+        each_group(a, p, [&](int k, int lane) {
+            float u = 0.0f, ux = 0.0f;
+            for (int i = lane; i < a.D; i += p.team) {
+                const int c = k * a.D + i;
+                const float2 s = red[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c];
+                const float w = a.w ? T::ld((const E *)a.w, c) : 1.0f;
+                u += s.x * w;
+                ux += s.y * w;
+            }
+            u = team_sum(p, u);
+            ux = team_sum(p, ux);
+            if (lane == 0) groups[(t.b * p.parts + t.part) * a.G + k] = make_float2(u, ux);
+        });
 }
 
 // mean u and mean(u xh) of a group.
@@ -250,70 +249,70 @@ __global__ __launch_bounds__(NT) void k_gn_join_back(GroupNormArgs a, GnParts p,
 }
 
 template <typename T, int N, int ACT>
-__global__ __launch_bounds__(512) void k_gn_part_back(GroupNormArgs a, GnParts p, const float2 *groups, const float2 *stat, int64_t jobs) {
+__global__ __launch_bounds__(512) void k_gn_part_back(GroupNormArgs a, GnParts p, const float2 *groups, const float2 *stat, int64_t first) {
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 joined[];
-    for (int64_t k = blockIdx.x; k < jobs; k += gridDim.x) {
-        const Place<T, N> t(a, p, jobs - 1 - k);
-        const char *const x = (const char *)a.x + t.base, *const g = (const char *)a.g + t.base;
-        char *const y = (char *)a.y + t.base;
-        const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
-        constexpr int U = kBatch / 2;
-        typename P::Raw xr[U], gr[U];
-        auto load = [&](int i0) {
+    const Place<T, N> t(a, p, first, gridDim.x - 1 - blockIdx.x);
+    const char *const x = (const char *)a.x + t.base, *const g = (const char *)a.g + t.base;
+    char *const y = (char *)a.y + t.base;
+    const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
+    constexpr int U = kBatch / 2;
+    typename P::Raw xr[U], gr[U], xn[U], gn[U];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const uint32_t at = t.off + (uint32_t)max(min(i0 + i, mine - 1), 0) * t.step;
+            xn[i] = P::load((const E *)(x + at));
+            gn[i] = P::load((const E *)(g + at));
+        }
+    };
+    if (every) load(0);
+    if (p.joined) {
+        const int64_t n = positions(a, t.b);
+        const float inv = n > 0 ? 1.0f / ((float)n * (float)a.D) : 0.0f;
+        float2 *const v = joined + a.G;
+        fetch_parts(a, p, groups, t.b, v);
+        each_group(a, p, [&](int i, int lane) {
+            float s = 0.0f, q = 0.0f;
+            for (int j = lane; j < p.parts; j += p.team) s += v[j * a.G + i].x, q += v[j * a.G + i].y;
+            s = team_sum(p, s);
+            q = team_sum(p, q);
+            if (lane == 0) joined[i] = make_float2(s * inv, q * inv);
+        });
+        __syncthreads();
+    }
+    if (every) {
+        const Channels<T, N> ch(a, p, t.b, t.at);
+        float c1[N], c2[N];
+        int i = (int)fdiv(t.at, p.by_D), c = t.at - i * a.D;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float2 s = p.joined ? joined[i] : stat[t.b * a.G + i];
+            c1[e] = s.x, c2[e] = s.y;
+            if (++c == a.D) c = 0, i = min(i + 1, a.G - 1);
+        }
+        for (int i0 = 0; i0 < every; i0 += U) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) xr[i] = xn[i], gr[i] = gn[i];
+            if (i0 + U < every) load(i0 + U);
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const uint32_t at = t.off + (uint32_t)max(min(i0 + i, mine - 1), 0) * t.step;
-                xr[i] = P::load((const E *)(x + at));
-                gr[i] = P::load((const E *)(g + at));
-            }
-        };
-        if (every) load(0);
-        if (p.joined) {
-            const int64_t n = positions(a, t.b);
-            const float inv = n > 0 ? 1.0f / ((float)n * (float)a.D) : 0.0f;
-            each_group(a, p, [&](int i, int lane) {
-                const float2 *const v = groups + t.b * p.parts * a.G + i;
-                float s = 0.0f, q = 0.0f;
-                for (int j = lane; j < p.parts; j += p.team) s += v[(int64_t)j * a.G].x, q += v[(int64_t)j * a.G].y;
-                s = team_sum(p, s);
-                q = team_sum(p, q);
-                if (lane == 0) joined[i] = make_float2(s * inv, q * inv);
-            });
-            __syncthreads();
-        }
-        if (every) {
-            const Channels<T, N> ch(a, t.b, t.at);
-            float c1[N], c2[N];
-            int i = t.at / a.D, c = t.at - i * a.D;
+                if (i0 + i >= every) break;
+                float xh[N], u[N];
+                hold(xr[i]);
+                hold(gr[i]);
+                P::widen(xr[i], xh);
+                P::widen(gr[i], u);
+                ch.template back<ACT>(xh, u);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float2 s = p.joined ? joined[i] : stat[t.b * a.G + i];
-                c1[e] = s.x, c2[e] = s.y;
-                if (++c == a.D) c = 0, i = min(i + 1, a.G - 1);
-            }
-            for (int i0 = 0; i0 < every; i0 += U) {
-                if (i0) load(i0);
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    if (i0 + i >= every) break;
-                    float xh[N], u[N];
-                    hold(xr[i]);
-                    hold(gr[i]);
-                    P::widen(xr[i], xh);
-                    P::widen(gr[i], u);
-                    ch.template back<ACT>(xh, u);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        u[e] = i0 + i < mine ? ch.r[e] * (u[e] * ch.w[e] - c1[e] - xh[e] * c2[e]) : 0.0f;
-                        hold(u[e]);
-                    }
-                    store_own<T, N>((E *)(y + (t.off + (uint32_t)(i0 + i) * t.step)), u, t.skip);
+                for (int e = 0; e < N; ++e) {
+                    u[e] = i0 + i < mine ? ch.r[e] * (u[e] * ch.w[e] - c1[e] - xh[e] * c2[e]) : 0.0f;
+                    hold(u[e]);
                 }
+                store_own<T, N>((E *)(y + (t.off + (uint32_t)(i0 + i) * t.step)), u, t.skip, a.y == a.g);
             }
         }
-        if (p.joined) __syncthreads();
     }
 }
 
@@ -388,19 +387,21 @@ hipError_t run_back(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
     const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, sizeof(typename T::T), num_cus);
     const BackBytes by = back_bytes(a.B, a.C, a.G, p);
     float2 *const part = (float2 *)a.ws, *const groups = (float2 *)((char *)a.ws + by.part), *const stat = (float2 *)((char *)groups + by.groups);
-    const int64_t jobs = a.B * p.parts * p.tiles;
     const size_t lds = (size_t)p.rt * p.tp * N * sizeof(float2);
-    if (jobs > 0)
-        hipLaunchKernelGGL((k_gn_part_sums<T, N, ACT>), dim3(grid_for(jobs)), dim3(p.nt), lds, stream, a, p, part, groups, jobs);
-    if (a.y && jobs > 0 && a.S > 0) {
+    by_samples(a.B, p, false, [&](int64_t b, dim3 grid) {
+        hipLaunchKernelGGL((k_gn_part_sums<T, N, ACT>), grid, dim3(p.nt), lds, stream, a, p, part, groups, b);
+    });
+    if (a.y && a.B > 0 && a.S > 0) {
         if (!p.joined) {
             if ((int64_t)p.parts * (p.by_group ? 1 : a.D) <= 256)
                 hipLaunchKernelGGL((k_gn_join_back<T, 64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, groups, stat);
             else
                 hipLaunchKernelGGL((k_gn_join_back<T, 1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, groups, stat);
         }
-        hipLaunchKernelGGL((k_gn_part_back<T, N, ACT>), dim3(grid_for(jobs)), dim3(p.nt), p.joined ? a.G * sizeof(float2) : 0, stream, a, p,
-                           groups, stat, jobs);
+        const size_t here = p.joined ? (size_t)a.G * (1 + p.parts) * sizeof(float2) : 0;
+        by_samples(a.B, p, true, [&](int64_t b, dim3 grid) {
+            hipLaunchKernelGGL((k_gn_part_back<T, N, ACT>), grid, dim3(p.nt), here, stream, a, p, groups, stat, b);
+        });
     }
     if (a.gw || a.gb)
         hipLaunchKernelGGL((k_gn_params<T>), dim3((a.C + 15) / 16), dim3(1024), 0, stream, part, a.B * p.parts, a.C, a.gw, a.gb);

@@ -60,9 +60,9 @@ struct Lane {
 // A piece's store; only where C is no multiple of a piece (ODD) may elements of it
 // be its neighbour's.
 template <typename T, int N, bool ODD>
-__device__ __forceinline__ void put(typename T::T *p, const float *f, int skip) {
+__device__ __forceinline__ void put(typename T::T *p, const float *f, int skip, bool in_place) {
     if constexpr (ODD)
-        store_own<T, N>(p, f, skip);
+        store_own<T, N>(p, f, skip, in_place);
     else
         Piece<T, N>::store(p, f);
 }
@@ -292,11 +292,11 @@ struct Tile {
         const Walk<T, N, PER> yw(r.y, r.ys, r, t, i);
         if ((i + 1) * TILE <= t.n) {
 #pragma unroll
-            for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip);
+            for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.y == r.x);
         } else {
 #pragma unroll
             for (int k = 0; k < PER; ++k)
-                if (k < left) put<T, N, ODD>(yw.at(k), u[k], t.skip);
+                if (k < left) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.y == r.x);
             clear_rows<T, N>(r.y, r.ys, t, max(i * TILE, t.n), min((i + 1) * TILE, r.L));
         }
     }
@@ -506,22 +506,22 @@ struct TileBack {
             const Walk<T, N, PER> w(r.gx, r.gxs, r, t, i);
             if (full) {
 #pragma unroll
-                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip);
+                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip, r.gx == r.g);
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if (k < left) put<T, N, ODD>(w.at(k), g[k], t.skip);
+                    if (k < left) put<T, N, ODD>(w.at(k), g[k], t.skip, r.gx == r.g);
             }
         }
         if (r.gg) {
             const Walk<T, N, PER> w(r.gg, r.ggs, r, t, i);
             if (full) {
 #pragma unroll
-                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip);
+                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip, r.gx == r.g);
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if (k < left) put<T, N, ODD>(w.at(k), x[k], t.skip);
+                    if (k < left) put<T, N, ODD>(w.at(k), x[k], t.skip, r.gx == r.g);
             }
         }
         if (!full) {

@@ -115,10 +115,13 @@ struct Piece<BF16, 4> {
         *(u32x2_odd *)p = __builtin_bit_cast(u32x2, __builtin_convertvector(f32x4{f[0], f[1], f[2], f[3]}, bf16x4));
     }
 };
-// The elements from `skip` on of a piece: those before it are its neighbour's.
+// The elements from `skip` on of a piece: those before it are its neighbour's,
+// which computes the same values from the same inputs, so that all of them may be
+// stored unless the neighbour may have overwritten those inputs (in place).  One
+// store of 16 bytes in place of up to seven: a row of 255 bf16 took twice as long.
 template <typename T, int N>
-__device__ __forceinline__ void store_own(typename T::T *p, const float *f, int skip) {
-    if (skip == 0) {
+__device__ __forceinline__ void store_own(typename T::T *p, const float *f, int skip, bool in_place = true) {
+    if (skip == 0 || (!in_place && skip < N)) {
         Piece<T, N>::store(p, f);
     } else {
 #pragma unroll
