@@ -223,11 +223,12 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
 struct GnParts {
     int P, tp, tiles, rt, nt, parts;
     int64_t rows;     // positions of a part
+    int split;        // workgroups of the second pass to a part
     bool by_group;    // a part's statistics are kept for groups
     bool joined;      // the workgroups that need a sample's statistics join them themselves
     int entries;      // of a part: G or C
     int team;         // lanes that add a group's values
-    FastDiv by_tiles, by_parts, by_tp, by_rt, by_D;
+    FastDiv by_tiles, by_parts, by_split, by_tp, by_rt, by_D;
     size_t part_bytes, stat_bytes;
 };
 
@@ -245,9 +246,9 @@ inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, 
         const double used = (double)(rt * p.tp) / nt;
         if ((nt >= 256 || (rt + 1) * p.tp > 512) && used > best + 0.02) best = used, p.rt = rt, p.nt = nt;
     }
-    // four workgroups for every CU, of 8 rows a thread at least; offsets in a part have 32 bits
+    // two workgroups for every CU, of 8 rows a thread at least; offsets in a part have 32 bits
     const int64_t jobs = std::max<int64_t>(1, B * p.tiles);
-    const int64_t want = (4ll * num_cus + jobs - 1) / jobs;
+    const int64_t want = (2ll * num_cus + jobs - 1) / jobs;
     const int64_t most = (S + 8ll * p.rt - 1) / (8ll * p.rt);
     const int64_t parts = std::max<int64_t>(1, std::min({want, most, (int64_t)1024}));
     p.rows = std::max<int64_t>(1, std::min((S + parts - 1) / parts, ((int64_t)1 << 31) / ((int64_t)C * esize)));
@@ -257,6 +258,8 @@ inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, 
     p.joined = p.by_group && (int64_t)p.parts * G <= kJoinHere;
     p.team = 64;
     while (p.team > 1 && p.team > p.nt / G) p.team /= 2;
+    p.split = (int)std::max<int64_t>(1, std::min<int64_t>(4, p.rows / (8 * p.rt)));
+    p.by_split = make_fastdiv(p.split);
     p.by_tiles = make_fastdiv(p.tiles), p.by_parts = make_fastdiv(p.parts), p.by_tp = make_fastdiv(p.tp);
     p.by_rt = make_fastdiv(p.rt), p.by_D = make_fastdiv(C / G);
     p.part_bytes = ((size_t)B * p.parts * p.entries * sizeof(float2) + 255) & ~(size_t)255;
@@ -271,13 +274,22 @@ struct Place {
     int n, rows;      // positions of the part within the length, and all of them
     int part, tile, rt, j, at, skip;
     uint32_t off, step;  // bytes from there to the thread's first row, and from one to the next
-    bool on;
-    __device__ __forceinline__ Place(const GroupNormArgs &a, const GnParts &p, int64_t first, uint32_t job) {
-        const uint32_t q = fdiv(job, p.by_tiles), s = fdiv(q, p.by_parts);
-        tile = (int)(job - q * p.tiles);
+    bool on, lead;       // lead: the sample's first workgroup
+    // SPLIT: of one of the `split` pieces of the part
+    template <bool SPLIT>
+    static __device__ __forceinline__ Place of(const GroupNormArgs &a, const GnParts &p, int64_t first, uint32_t job) {
+        const uint32_t r = fdiv(job, p.by_tiles), q = SPLIT ? fdiv(r, p.by_split) : r;
+        return Place(a, p, first, q, (int)(job - r * p.tiles), SPLIT ? (int)(r - q * p.split) : 0, SPLIT ? p.split : 1);
+    }
+    __device__ __forceinline__ Place(const GroupNormArgs &a, const GnParts &p, int64_t first, uint32_t q, int of_tile, int sub, int split) {
+        const uint32_t s = fdiv(q, p.by_parts);
+        tile = of_tile;
         b = first + s;
         part = (int)(q - s * p.parts);
-        const int64_t start = (int64_t)part * p.rows, past = min(start + p.rows, a.S);
+        lead = part == 0 && sub == 0;
+        const int each = ((int)p.rows + split - 1) / split;
+        const int64_t begin = (int64_t)part * p.rows, until = min(begin + p.rows, a.S);
+        const int64_t start = min(begin + (int64_t)sub * each, until), past = min(start + each, until);
         rows = (int)(past - start);
         n = (int)max(min(past, positions(a, b)) - start, (int64_t)0);
         rt = (int)fdiv(threadIdx.x, p.by_tp);
@@ -330,8 +342,8 @@ constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 102
 
 // f(first sample, workgroups) for launches of whole samples, the last samples first where `back`.
 template <typename F>
-void by_samples(int64_t B, const GnParts &p, bool back, F f) {
-    const int64_t per = (int64_t)p.parts * p.tiles, some = std::max<int64_t>(1, kMaxGrid / per), n = (B + some - 1) / some;
+void by_samples(int64_t B, const GnParts &p, int split, bool back, F f) {
+    const int64_t per = (int64_t)p.parts * p.tiles * split, some = std::max<int64_t>(1, kMaxGrid / per), n = (B + some - 1) / some;
     for (int64_t i = 0; i < n; ++i) {
         const int64_t b = (back ? n - 1 - i : i) * some;
         f(b, dim3((unsigned)(std::min(some, B - b) * per)));

@@ -44,7 +44,8 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
         const bool see = on && t.rt + i * p.rt < n;
 #pragma unroll
         for (int e = 0; e < N; ++e) v[0][t.v(e)] += see && e >= t.skip ? f[e] : 0.0f;
-        hold(v[0][0]);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) hold(v[0][e]);
     }
     sum(p, v, t.channels, a.D, t.slot, t.of);
     const float all = (float)n * (float)a.D;
@@ -62,7 +63,8 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
             const float d = f[e] - mean[t.v(e)];
             v[0][t.v(e)] += see && e >= t.skip ? d * d : 0.0f;
         }
-        hold(v[0][0]);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) hold(v[0][e]);
     }
     sum(p, v, t.channels, a.D, t.slot, t.of);
     float r[NV];
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 red[];  // [rt][tp][N], then of the channels
-    const Place<T, N> t(a, p, first, blockIdx.x);
+    const Place<T, N> t = Place<T, N>::template of<false>(a, p, first, blockIdx.x);
     const char *const x = (const char *)a.x + t.base;
     const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
     float n = 0.0f, mean[N] = {}, m2[N] = {};
@@ -233,7 +235,7 @@ __global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts 
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 joined[];
-    const Place<T, N> t(a, p, first, gridDim.x - 1 - blockIdx.x);  // what was read last is still in cache
+    const Place<T, N> t = Place<T, N>::template of<true>(a, p, first, gridDim.x - 1 - blockIdx.x);  // what was read last is still in cache
     const char *const x = (const char *)a.x + t.base;
     char *const y = (char *)a.y + t.base;
     const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts 
             const float rstd = n > 0 ? rsqrtf(team_sum(p, q) / ((float)n * (float)a.D) + a.eps) : 0.0f;
             if (lane == 0) {
                 joined[g] = make_float2(mean, rstd);
-                if (t.part == 0) {
+                if (t.lead) {
                     if (a.mean) a.mean[t.b * a.G + g] = mean;
                     if (a.rstd) a.rstd[t.b * a.G + g] = rstd;
                 }
@@ -343,7 +345,7 @@ hipError_t run(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
     const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, sizeof(typename T::T), num_cus);
     float2 *const part = (float2 *)a.ws, *const stat = (float2 *)((char *)a.ws + p.part_bytes);
     const size_t lds = (size_t)(p.rt + 1) * p.tp * N * sizeof(float2);
-    by_samples(a.B, p, false, [&](int64_t b, dim3 grid) {
+    by_samples(a.B, p, 1, false, [&](int64_t b, dim3 grid) {
         hipLaunchKernelGGL((k_gn_part_stats<T, N>), grid, dim3(p.nt), lds, stream, a, p, part, b);
     });
     if (!p.joined) {
@@ -353,7 +355,7 @@ hipError_t run(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
             hipLaunchKernelGGL((k_gn_join<1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, stat);
     }
     const size_t here = p.joined ? (size_t)a.G * (1 + p.parts) * sizeof(float2) : 0;
-    by_samples(a.B, p, true, [&](int64_t b, dim3 grid) {
+    by_samples(a.B, p, p.split, true, [&](int64_t b, dim3 grid) {
         hipLaunchKernelGGL((k_gn_part_apply<T, N, ACT>), grid, dim3(p.nt), here, stream, a, p, part, stat, b);
     });
     return hipGetLastError();

@@ -71,6 +71,11 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
                 hold(pb[e]);
                 hold(pw[e]);
             }
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                hold(v[0][e]);
+                hold(v[1][e]);
+            }
         }
         if (!a.y) continue;
         sum(p, v, t.channels, a.D, t.slot, t.of);
@@ -149,7 +154,7 @@ __global__ __launch_bounds__(512) void k_gn_part_sums(GroupNormArgs a, GnParts p
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 red[];
-    const Place<T, N> t(a, p, first, blockIdx.x);
+    const Place<T, N> t = Place<T, N>::template of<false>(a, p, first, blockIdx.x);
     const char *const x = (const char *)a.x + t.base, *const g = (const char *)a.g + t.base;
     const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0;
     float s1[N] = {}, s2[N] = {};
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(512) void k_gn_part_back(GroupNormArgs a, GnParts p
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 joined[];
-    const Place<T, N> t(a, p, first, gridDim.x - 1 - blockIdx.x);
+    const Place<T, N> t = Place<T, N>::template of<true>(a, p, first, gridDim.x - 1 - blockIdx.x);
     const char *const x = (const char *)a.x + t.base, *const g = (const char *)a.g + t.base;
     char *const y = (char *)a.y + t.base;
     const int mine = t.on ? t.rows_of(p, t.rt, t.n) : 0, every = t.on ? t.rows_of(p, t.rt, t.rows) : 0;
@@ -388,7 +393,7 @@ hipError_t run_back(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
     const BackBytes by = back_bytes(a.B, a.C, a.G, p);
     float2 *const part = (float2 *)a.ws, *const groups = (float2 *)((char *)a.ws + by.part), *const stat = (float2 *)((char *)groups + by.groups);
     const size_t lds = (size_t)p.rt * p.tp * N * sizeof(float2);
-    by_samples(a.B, p, false, [&](int64_t b, dim3 grid) {
+    by_samples(a.B, p, 1, false, [&](int64_t b, dim3 grid) {
         hipLaunchKernelGGL((k_gn_part_sums<T, N, ACT>), grid, dim3(p.nt), lds, stream, a, p, part, groups, b);
     });
     if (a.y && a.B > 0 && a.S > 0) {
@@ -399,7 +404,7 @@ hipError_t run_back(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
                 hipLaunchKernelGGL((k_gn_join_back<T, 1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, groups, stat);
         }
         const size_t here = p.joined ? (size_t)a.G * (1 + p.parts) * sizeof(float2) : 0;
-        by_samples(a.B, p, true, [&](int64_t b, dim3 grid) {
+        by_samples(a.B, p, p.split, true, [&](int64_t b, dim3 grid) {
             hipLaunchKernelGGL((k_gn_part_back<T, N, ACT>), grid, dim3(p.nt), here, stream, a, p, groups, stat, b);
         });
     }
