@@ -67,23 +67,34 @@ __device__ __forceinline__ void put(typename T::T *p, const float *f, int skip, 
         Piece<T, N>::store(p, f);
 }
 
-// A slot's rows of a tensor in one tile: a base that all threads share, and
-// offsets.  Reversed, the tile's last position is the base.
+// A slot's rows of a tensor in one tile: a base that all threads share (of each
+// row, on scalar registers), and the slot's offset from it.  Reversed, the base is
+// the tile's last position.
 template <typename T, int N, int PER>
 struct Walk {
     static constexpr int TILE = kSlots * PER;
     using E = typename T::T;
     char *base;
-    Offset<N> off, step;
+    int64_t step;
+    Offset<N> off;
+    bool reverse;
     __device__ __forceinline__ Walk(const void *t, Strides2 st, const RecurrenceArgs &a, const Lane<N> &l, int tile) {
-        const int64_t row = a.reverse ? (int64_t)max(l.n, 1) - (int64_t)(tile + 1) * TILE : (int64_t)tile * TILE;
+        reverse = a.reverse;
+        const int64_t row = reverse ? (int64_t)max(l.n, 1) - (int64_t)(tile + 1) * TILE : (int64_t)tile * TILE;
         base = (char *)t + (l.b * st.b + row * st.l) * (int64_t)sizeof(E);
-        step = (Offset<N>)(st.l * (int64_t)sizeof(E));
-        off = (Offset<N>)(l.at * sizeof(E)) + (Offset<N>)(a.reverse ? TILE - 1 - l.slot * PER : l.slot * PER) * step;
-        if (a.reverse) step = 0 - step;
+        step = st.l * (int64_t)sizeof(E);
+        off = (Offset<N>)(l.at * sizeof(E)) + (Offset<N>)((reverse ? kSlots - 1 - l.slot : l.slot) * PER) * (Offset<N>)step;
     }
-    __device__ __forceinline__ E *at(int k) const { return (E *)(base + (off + (Offset<N>)k * step)); }
+    // Row k of the slot, the same k for all threads; or any of the tile's rows, counted from the slot's first.
+    __device__ __forceinline__ E *at(int k) const { return (E *)((base + (reverse ? PER - 1 - k : k) * step) + off); }
+    __device__ __forceinline__ E *any(int k) const {
+        return (E *)(base + (Offset<N>)(off + (Offset<N>)(reverse ? PER - 1 - k : k) * (Offset<N>)step));
+    }
 };
+
+// Ends a branch whose loads or stores the compiler would join with the other
+// branch's, at addresses of 64 bits a lane.
+__device__ __forceinline__ void apart() { asm volatile("; whole tile" ::: "memory"); }
 
 // A tile past the length reads the last one within it (and uses none of it): the
 // rows that are read lie in the tile that they are read from, so that no offset
@@ -93,19 +104,33 @@ __device__ __forceinline__ int last_tile(int n, int i) {
     return min(i, (max(n, 1) - 1) / TILE);
 }
 
+// A piece of a value's bits.
+template <typename T, int N>
+__device__ __forceinline__ typename Piece<T, N>::Raw every(uint32_t f32) {
+    const uint32_t w = std::is_same<T, F32>::value ? f32 : N == 1 ? f32 >> 16 : (f32 >> 16) * 0x10001u;
+    typename Piece<T, N>::Raw r;
+    if constexpr (N == 1)
+        r = w;
+    else
+        for (int i = 0; i < (int)(sizeof(r) / 4); ++i) r[i] = w;
+    return r;
+}
+
 template <typename T, int N, int PER>
 struct Rows {
     typename Piece<T, N>::Raw r[PER];
+    // From the slot's position `left` on, a value: a gate of infinity holds the state (a = 1, 1 - a = 0) and zeros add nothing.
+    __device__ __forceinline__ void end(int left, uint32_t f32) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (k >= left) r[k] = every<T, N>(f32);
+    }
     // `last`: the sequence's last position within the length (the first, for none),
     // counted from the slot's first, in place of those past it
     template <bool FULL>
     __device__ __forceinline__ void load(const Walk<T, N, PER> &w, int last) {
 #pragma unroll
-        for (int k = 0; k < PER; ++k) r[k] = Piece<T, N>::load(w.at(FULL ? k : min(k, last)));
-    }
-    __device__ __forceinline__ void widen(float (*f)[N]) const {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) Piece<T, N>::widen(r[k], f[k]);
+        for (int k = 0; k < PER; ++k) r[k] = Piece<T, N>::load(FULL ? w.at(k) : w.any(min(k, last)));
     }
 };
 
@@ -244,14 +269,20 @@ struct Tile {
         if ((i + 1) * TILE <= t.n) {
             gr.template load<true>(gw, last);
             xr.template load<true>(xw, last);
+            apart();
         } else {
             gr.template load<false>(gw, last);
             xr.template load<false>(xw, last);
         }
     }
-    // The slot's map, from its last position on where BACK; nothing past `left`.
-    template <bool FULL, bool BACK>
-    __device__ __forceinline__ Map<N> form(int left) {
+    // The slot's map, from its last position on where BACK.
+    template <bool BACK = false>
+    __device__ __forceinline__ Map<N> form(const Lane<N> &t, int i) {
+        if ((i + 1) * TILE > t.n) {
+            const int left = t.n - i * TILE - t.slot * PER;
+            gr.end(left, 0x7f800000u);
+            xr.end(left, 0u);
+        }
         Map<N> m;
         m.clear();
 #pragma unroll
@@ -266,7 +297,6 @@ struct Tile {
             for (int e = 0; e < N; ++e) {
                 sigmoid_pair(z[e], a[k][e], q[e]);
                 if (BLEND) u[k][e] *= q[e];
-                if (!FULL && k >= left) a[k][e] = 1.0f, u[k][e] = 0.0f;
             }
             if (BACK)
                 m.then_back(a[k], u[k]);
@@ -275,10 +305,6 @@ struct Tile {
             m.hold_all();
         }
         return m;
-    }
-    template <bool BACK = false>
-    __device__ __forceinline__ Map<N> form(const Lane<N> &t, int i) {
-        return (i + 1) * TILE <= t.n ? form<true, BACK>(0) : form<false, BACK>(t.n - i * TILE - t.slot * PER);
     }
     // the states from h on, to y
     __device__ __forceinline__ void store(const RecurrenceArgs &r, const Lane<N> &t, int i, float *h) {
@@ -293,11 +319,11 @@ struct Tile {
         if ((i + 1) * TILE <= t.n) {
 #pragma unroll
             for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.y == r.x);
+            apart();
         } else {
 #pragma unroll
             for (int k = 0; k < PER; ++k)
                 if (k < left) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.y == r.x);
-            clear_rows<T, N>(r.y, r.ys, t, max(i * TILE, t.n), min((i + 1) * TILE, r.L));
         }
     }
 };
@@ -411,6 +437,7 @@ __global__ __launch_bounds__(kThreads) void k_rec_walk(RecurrenceArgs a, Segment
         v.store(a, t, i, h);
         if (++i == past) break;
     }
+    clear_rows<T, N>(a.y, a.ys, t, max(first * W::TILE, t.n), min(past * W::TILE, a.L));
     __syncthreads();  // every thread has read the state, which `last` may be
     if (a.last && t.on && seg == g.segs - 1 && t.slot == 0) store_state<N>(a.last + t.state(a), t, h0);
 }
@@ -433,6 +460,7 @@ struct TileBack {
             gr.template load<true>(gw, last);
             xr.template load<true>(xw, last);
             dr.template load<true>(dw, last);
+            apart();
         } else {
             gr.template load<false>(gw, last);
             xr.template load<false>(xw, last);
@@ -443,8 +471,16 @@ struct TileBack {
         for (int e = 0; e < N; ++e) kept[e] = st[e];
     }
     __device__ __forceinline__ float term(int k, int e) const { return BLEND ? q[k][e] * x[k][e] : x[k][e]; }
-    template <bool FULL>
-    __device__ __forceinline__ Map<N> form(int left) {
+    // the slot's map of the states, and h = the state that the tile starts from
+    __device__ __forceinline__ Map<N> form(const Lane<N> &t, int i, float *h) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[e] = kept[e];
+        if ((i + 1) * TILE > t.n) {
+            const int left = t.n - i * TILE - t.slot * PER;
+            gr.end(left, 0x7f800000u);
+            xr.end(left, 0u);
+            dr.end(left, 0u);
+        }
         Map<N> m;
         m.clear();
 #pragma unroll
@@ -459,19 +495,13 @@ struct TileBack {
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 sigmoid_pair(z[e], a[k][e], q[k][e]);
-                if (!FULL && k >= left) a[k][e] = 1.0f, q[k][e] = x[k][e] = g[k][e] = 0.0f;
                 u[e] = term(k, e);
+                hold(q[k][e]);
             }
             m.then(a[k], u);
             m.hold_all();
         }
         return m;
-    }
-    // the slot's map of the states, and h = the state that the tile starts from
-    __device__ __forceinline__ Map<N> form(const Lane<N> &t, int i, float *h) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) h[e] = kept[e];
-        return (i + 1) * TILE <= t.n ? form<true>(0) : form<false>(t.n - i * TILE - t.slot * PER);
     }
     __device__ __forceinline__ Map<N> map_back() const {
         Map<N> m;
@@ -507,6 +537,7 @@ struct TileBack {
             if (full) {
 #pragma unroll
                 for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip, r.gx == r.g);
+                apart();
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
@@ -518,16 +549,12 @@ struct TileBack {
             if (full) {
 #pragma unroll
                 for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip, r.gx == r.g);
+                apart();
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
                     if (k < left) put<T, N, ODD>(w.at(k), x[k], t.skip, r.gx == r.g);
             }
-        }
-        if (!full) {
-            const int from = max(i * TILE, t.n), to = min((i + 1) * TILE, r.L);
-            clear_rows<T, N>(r.gx, r.gxs, t, from, to);
-            clear_rows<T, N>(r.gg, r.ggs, t, from, to);
         }
     }
 };
@@ -592,6 +619,9 @@ __global__ __launch_bounds__(kThreads) void k_rec_walk_back(RecurrenceArgs a, Se
         v.store(a, t, i, h, m);
         if (i-- == first) break;
     }
+    const int from = max(first * W::TILE, t.n), to = min(past * W::TILE, a.L);
+    clear_rows<T, N>(a.gx, a.gxs, t, from, to);
+    clear_rows<T, N>(a.gg, a.ggs, t, from, to);
     __syncthreads();
     if (a.g_state && t.on && seg == 0 && t.slot == 0) store_state<N>(a.g_state + t.state(a), t, m0);
 }
