@@ -1,7 +1,9 @@
 """The gated linear recurrence and its gradients on the GPU against a plain form
 in float64, which also gives the bounds (oracle/block.py: errors of 32-bit
 arithmetic carried along the sequence); a result in bf16 is rounded once more,
-by 2^-8 relative."""
+by 2^-8 relative.  The relative bounds hold for normal numbers: what lies below
+the least of them, 2^-126, or is a product of one that does and of factors below
+1, is off by less than 2^-126 if it becomes 0."""
 import pytest
 import torch
 
@@ -31,7 +33,7 @@ def within(got, want, name, dtype, what):
     w, bound = want[name], want[name + "_bound"]
     assert got.shape == w.shape and got.dtype == dtype, (what, got.shape, got.dtype)
     got = got.cpu().double()
-    bound = bound + w.abs() * ((2.0 ** -8 if dtype == BF16 else 2.0 ** -24) * 1.01)
+    bound = bound + w.abs() * ((2.0 ** -8 if dtype == BF16 else 2.0 ** -24) * 1.01) + 2.0 ** -126
     bad = ~((got - w).abs() <= bound) & (got != w)
     if bad.any():
         i = tuple(int(v) for v in bad.nonzero()[0])
@@ -65,6 +67,65 @@ def test_gated_recurrence(shape, dtype):
         for n in got:
             alone = sequence.gated_recurrence_backward(x, gate, states, go, g_last, blend=blend, reverse=reverse, need=(n,))
             assert list(alone) == [n] and torch.equal(alone[n], got[n])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(520, 140, 5), (1, 140, 33001), (1, 40000, 4), (2, 9000, 70)])
+def test_many_chains_and_many_segments(shape, dtype):
+    """Sequences and channels enough for one pass over several tiles; long ones cut into many segments."""
+    print("gated recurrence", shape, dtype, flush=True)
+    x, gate, state, go, g_last = inputs(*shape, dtype, 11)
+    lens = torch.full((shape[0],), shape[1], dtype=torch.int32, device=DEV)
+    lens[-1] = shape[1] - 67
+    check(x, gate, state, go, g_last, None, False, True)
+    check(x, gate, state, go, g_last, lens, True, False)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_rows_far_apart(reverse):
+    """Rows 33 MB apart, which a tile's 32-bit offsets do not span, and beside them rows that are."""
+    B, L, C = 1, 4, 8
+    x, gate, state, go, g_last = inputs(B, L, C, F32, 12)
+    step = (1 << 23) + 5
+    far = []
+    for t in (x, gate, go):
+        v = torch.zeros(step * L, device=DEV).as_strided((B, L, C), (step * L, step, 1))
+        v.copy_(t)
+        far.append(v)
+    check(far[0], far[1], state, far[2], g_last, None, True, reverse)
+    check(far[0], gate, state, go, g_last, None, False, reverse)
+    check(x, gate, state, far[2], g_last, None, False, reverse)
+    y = torch.zeros(step * L, device=DEV).as_strided((B, L, C), (step * L, step, 1))
+    sequence.gated_recurrence(x, gate, state, blend=True, reverse=reverse, out=y)
+    want = block.gated_recurrence(x, gate, state, None, True, reverse)
+    within(y, want, "y", F32, "far output")
+
+
+def test_past_32_bits():
+    """4.4 GB a tensor; a gate of -infinity 150 positions ahead of the end, from which the plain form starts."""
+    L, C, tail = (1 << 20) + 77, 2100, 150
+    x = torch.empty((1, L, C), dtype=BF16, device=DEV)
+    gate = torch.empty((1, L, C), dtype=BF16, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(14)
+    for i in range(0, L, 1 << 17):
+        for t, up in ((x, 0.0), (gate, 2.0)):
+            part = t[0, i:i + (1 << 17)]
+            part.copy_(torch.randn(part.shape, generator=gen, device=DEV, dtype=F32) + up)
+    gate[:, L - tail] = -float("inf")
+    ends = [t[:, L - tail:].clone() for t in (x, gate)]
+    go = ends[0].flip(1).contiguous()
+    want = block.gated_recurrence(ends[0], ends[1], None, None, False, False, go, None)
+    wide = torch.zeros_like(x)
+    wide[:, L - tail:] = go
+    y, last, states = sequence.gated_recurrence(x, gate, with_states=True)
+    within(y[:, L - tail:], want, "y", BF16, "tail")
+    within(last, want, "last", F32, "tail")
+    del y
+    got = sequence.gated_recurrence_backward(x, gate, states, wide, grads={"x": wide})
+    within(got["x"][:, L - tail:], want, "gx", BF16, "tail")
+    # the state ahead of the tail is another one than the plain form's, and its gate lets none of it through
+    within(got["gate"][:, L - tail:], want, "ggate", BF16, "tail")
+    assert not got["x"][:, :L - tail].any() and not got["gate"][:, :L - tail].any()
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -183,6 +244,30 @@ def test_nan_reaches_later_positions_of_its_channel_only():
     assert y[1, 77:, 5].isnan().all() and last[1, 5].isnan()
     y[1, 77:, 5] = want[1, 77:, 5]
     assert torch.equal(y, want)
+
+
+def test_nan_in_gates_and_gradients():
+    """A NaN gate reaches its channel's later states and the gradients of it and of the earlier positions, and a
+    NaN gradient those of its position and the earlier ones; nothing else, over several segments."""
+    x, gate, state, go, g_last = inputs(2, 1500, 12, F32, 13)
+    y0, last0, states = sequence.gated_recurrence(x, gate, state, blend=True, with_states=True)
+    want = sequence.gated_recurrence_backward(x, gate, states, go, g_last, blend=True)
+    bad = gate.clone()
+    bad[1, 777, 5] = float("nan")
+    y, last, states2 = sequence.gated_recurrence(x, bad, state, blend=True, with_states=True)
+    assert y[1, 777:, 5].isnan().all() and last[1, 5].isnan()
+    y[1, 777:, 5] = y0[1, 777:, 5]
+    assert torch.equal(y, y0)
+    bad = go.clone()
+    bad[0, 900, 3] = float("nan")
+    got = sequence.gated_recurrence_backward(x, gate, states, bad, g_last, blend=True)
+    for n in ("x", "gate"):
+        assert got[n][0, :901, 3].isnan().all()
+        got[n][0, :901, 3] = want[n][0, :901, 3]
+        assert torch.equal(got[n], want[n])
+    assert got["state"][0, 3].isnan()
+    got["state"][0, 3] = want["state"][0, 3]
+    assert torch.equal(got["state"], want["state"])
 
 
 def test_empty():

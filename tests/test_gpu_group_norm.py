@@ -2,21 +2,24 @@
 against plain forms in float64.
 
 Tolerances are bounds of rounding, u = 2^-24.  No value here passes through
-more than K = 80 roundings on its way into a group's mean or mean square (rows
-of a thread, row-threads, parts, channels of a group: each is a tree or a short
-chain at these sizes), so the mean is off by K u of the largest |x| of the
-sample, and
+more than K = 100 roundings on its way into a group's mean or mean square (a
+thread's rows, the row-threads, of which 500 x 3 has 85, and trees over channels
+and parts; the cases of test_in_parts say their own), so the mean is off by K u
+of the largest |x| of the sample, and
 
     xh = (x - mean) rstd  by  xe = K u (top rstd + |xh|),
     z = xh w + b          by  ze = |w| xe + 4 u (|z| + |b|),
     silu and its derivative have slopes of at most 1.1 and 0.5, and 12 + |z| roundings.
+
+A parameter's gradient adds up to 256 row-threads and then 64 others in order, W
+= 320 in all.
 
 A result in bf16 is rounded once more, by 2^-8 relative.
 """
 import pytest
 import torch
 
-from deformable_convolution_amd import sequence
+from deformable_convolution_amd import dc1d, sequence
 from oracle import block
 
 pytestmark = pytest.mark.gpu
@@ -24,7 +27,7 @@ pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 F32, BF16, F8 = torch.float32, torch.bfloat16, torch.float64
 U = 2.0 ** -24
-K = 80
+K, W = 100, 320
 ACTS = [None, "relu", "silu"]
 
 SHAPES = [
@@ -62,7 +65,7 @@ def once(want, dtype):
     return want.abs() * ((2.0 ** -8 if dtype == BF16 else 4 * U) * 1.01)
 
 
-def widths(x, w, b, full, lens=None):
+def widths(x, w, b, full, lens=None, K=K):
     """xe and ze of every element."""
     v = x.detach().cpu().double()
     if lens is not None:
@@ -75,10 +78,10 @@ def widths(x, w, b, full, lens=None):
     return top, xe, wa * xe + 4 * U * (full["z"].abs() + ba)
 
 
-def check(x, groups, w, b, go, activation, lens=None, eps=1e-5):
+def check(x, groups, w, b, go, activation, lens=None, eps=1e-5, K=K, W=W):
     dtype = x.dtype
     wy, wm, wr, grads, full = block.group_norm(x, groups, w, b, eps, activation, lens, go)
-    top, xe, ze = widths(x, w, b, full, lens)
+    top, xe, ze = widths(x, w, b, full, lens, K)
     y, mean, rstd = sequence.group_norm(x, groups, w, b, eps, activation, lens, with_stats=True)
     t = top.reshape(-1, 1)
     within(mean, wm, K * U * t, "mean")
@@ -101,9 +104,9 @@ def check(x, groups, w, b, go, activation, lens=None, eps=1e-5):
     e = ue + n(ue) + xh * n(ue * xh + u * xe) + xe * full["aux"] + K * U * (u + full["au"] + xh * full["aux"])
     within(got["x"], grads["x"], r * e * 1.05 + once(grads["x"], dtype), "grad x")
     rest = tuple(range(x.dim() - 1))
-    within(got["weight"], grads["weight"], (ge * xh + full["gz"].abs() * xe + K * U * full["gz"].abs() * xh).sum(rest) * 1.05 +
+    within(got["weight"], grads["weight"], (ge * xh + full["gz"].abs() * xe + W * U * full["gz"].abs() * xh).sum(rest) * 1.05 +
            once(grads["weight"], dtype), "grad weight")
-    within(got["bias"], grads["bias"], (ge + K * U * full["gz"].abs()).sum(rest) * 1.05 + once(grads["bias"], dtype), "grad bias")
+    within(got["bias"], grads["bias"], (ge + W * U * full["gz"].abs()).sum(rest) * 1.05 + once(grads["bias"], dtype), "grad bias")
     return y, mean, rstd, got
 
 
@@ -188,6 +191,103 @@ def test_in_place_and_off_alignment(shape, groups, dtype):
         assert (obuf[:by + 1] == 7).all() and (obuf[by + 1 + x.numel():] == 7).all()  # nothing around it is written
         again = sequence.group_norm_backward(xs, groups, gs, mean, rstd, ws, bs, "silu")
         assert all(torch.equal(again[n], grads[n]) for n in grads)
+
+
+# Samples too large to hold: with fewer parts' statistics than every workgroup joins itself and with more, channels in
+# several tiles, parts whose second pass is split, one and few channels.  K: 8 rows of a thread, the row-threads (253 of
+# 8 channels), then a part's channels and the parts over 64 lanes, or over 1024 threads (5 channels of each in 38
+# parts, 3 in 125).
+PARTS = [((2, 5000, 64), 1, 100), ((2, 3000, 264), 3, 100), ((3, 1300, 512), 512, 192), ((2, 6000, 96), 96, 100),
+         ((1, 4100, 1030), 2, 300), ((1, 300, 5000), 1, 256), ((1, 2000, 2056), 1, 440), ((1, 30000, 8), 1, 320)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,groups,k", PARTS)
+def test_in_parts(shape, groups, k, dtype):
+    print("group norm in parts", shape, groups, dtype, flush=True)
+    x, w, b, go = inputs(shape, dtype, 10)
+    y, mean, rstd, got = check(x, groups, w, b, go, "silu", K=k, W=max(k, W))
+    assert torch.equal(y, sequence.group_norm(x, groups, w, b, activation="silu"))
+    same = x.clone()
+    sequence.group_norm(same, groups, w, b, activation="silu", out=same)
+    assert torch.equal(same, y)
+    over = go.clone()
+    again = sequence.group_norm_backward(x, groups, over, mean, rstd, w, b, "silu")
+    assert all(torch.equal(got[n], again[n]) for n in got)
+    # lengths that end inside a part, at its first position and ahead of it
+    L = shape[1]
+    lens = torch.tensor([L - 7, 9, 1][:shape[0]], dtype=torch.int32, device=DEV)
+    check(x, groups, w, b, go, None, lens, K=k, W=max(k, W))
+    # a NaN stays in its group
+    plain = sequence.group_norm(x, groups)
+    x[0, L // 2, 3] = float("nan")
+    y, D, g = sequence.group_norm(x, groups), shape[2] // groups, 3 * groups // shape[2]
+    assert y[0, :, g * D:(g + 1) * D].isnan().all()
+    y[0, :, g * D:(g + 1) * D] = plain[0, :, g * D:(g + 1) * D]
+    assert torch.equal(y, plain)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_samples_in_parts(dtype):
+    """Workgroups enough without parts: a second pass of several workgroups to a sample."""
+    x, w, b, go = inputs((520, 601, 36), dtype, 11)
+    lens = torch.full((520,), 601, dtype=torch.int32, device=DEV)
+    lens[::3], lens[1::5], lens[7] = 300, 2, 0
+    check(x, 1, w, b, go, "relu")
+    check(x, 1, w, b, go, "silu", lens)
+
+
+def test_workspace():
+    """A caller's workspace: too small, unaligned and overlapping ones are refused, and what it holds does not matter."""
+    x, w, b, go = inputs((2, 5000, 64), F32, 12)
+    want = sequence.group_norm(x, 4, w, b, with_stats=True)
+    ws = torch.full((1 << 22,), 255, dtype=torch.uint8, device=DEV)
+    got = sequence.group_norm(x, 4, w, b, with_stats=True, workspace=ws)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    grads = sequence.group_norm_backward(x, 4, go, want[1], want[2], w, b)
+    again = sequence.group_norm_backward(x, 4, go, want[1], want[2], w, b, workspace=ws.fill_(127))
+    assert all(torch.equal(grads[n], again[n]) for n in grads)
+    for bad in (ws[:128], ws[8:]):
+        with pytest.raises(dc1d.Dc1dValueError):
+            sequence.group_norm(x, 4, w, b, workspace=bad)
+        with pytest.raises(dc1d.Dc1dValueError):
+            sequence.group_norm_backward(x, 4, go, want[1], want[2], w, b, workspace=bad)
+    inside = x.view(-1).view(torch.uint8)[:1 << 20]
+    with pytest.raises(dc1d.Dc1dValueError):
+        sequence.group_norm(x, 4, w, b, workspace=inside)
+
+
+@pytest.mark.parametrize("shape", [((1 << 20) + 3, 2100), (1, (1 << 20) + 3, 2100)])
+def test_past_32_bits(shape):
+    """4.4 GB: many samples of one position, and one of many.  The last rows and the statistics; K = 1400: 1366 rows of
+    a thread, 8 to a batch that is joined in 3 roundings, then 256 parts."""
+    C, rows = shape[-1], (1 << 20) + 3
+    x = torch.empty(shape, dtype=BF16, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(13)
+    flat = x.view(rows, C)
+    for i in range(0, rows, 1 << 17):
+        part = flat[i:i + (1 << 17)]
+        part.copy_(torch.randn(part.shape, generator=gen, device=DEV, dtype=F32) + 1)
+    tail = flat[-5:].cpu().double()
+    k, groups = 1400, 3
+    if len(shape) == 2:
+        m = tail.view(5, groups, -1).mean(2)
+        var = ((tail.view(5, groups, -1) - m[..., None]) ** 2).mean(2)
+    else:
+        v = [flat[i:i + (1 << 17)].double().view(-1, groups, C // groups) for i in range(0, rows, 1 << 17)]
+        n = rows * (C // groups)
+        m = sum(t.sum((0, 2)) for t in v) / n
+        var = (sum(((t - m[None, :, None]) ** 2).sum((0, 2)) for t in v) / n).cpu().expand(5, groups)
+        m = m.cpu().expand(5, groups)
+        del v
+    r = (var + 1e-5) ** -0.5
+    y, mean, rstd = sequence.group_norm(x, groups, out=x, with_stats=True)
+    last = 5 if len(shape) == 2 else 1
+    top = 8.0  # |x| below, of 2^31 normal numbers about 1
+    within(mean[-last:], m[-last:], k * U * top, "mean")
+    within(rstd[-last:], r[-last:], k * U * (1 + top) ** 2, "rstd")
+    want = ((tail.view(5, groups, -1) - m[..., None]) * r[..., None]).view(5, C)
+    within(y.view(rows, C)[-5:], want, k * U * 2 * top + once(want, BF16), "y")
 
 
 def test_large_mean():
