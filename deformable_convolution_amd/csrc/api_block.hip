@@ -291,6 +291,7 @@ int dc1d_gated_recurrence(const dc1d_strided *x_, const dc1d_strided *gate_, con
     a.last = last_or_null ? (float *)last_or_null->data : nullptr;
     a.states = states_or_null ? (float *)states_or_null->data : nullptr;
     a.blend = blend != 0, a.reverse = reverse != 0;
+    a.in_place = a.y == a.x || (a.last && a.last == a.state);
     a.ws = workspace;
     return launched(launch_recurrence(a, cus, (hipStream_t)stream));
 }
@@ -365,6 +366,7 @@ int dc1d_gated_recurrence_backward(const dc1d_strided *x_, const dc1d_strided *g
     a.g_last = grad_last_or_null ? (const float *)grad_last_or_null->data : nullptr;
     a.g_state = grad_state_or_null ? (float *)grad_state_or_null->data : nullptr;
     a.blend = blend != 0, a.reverse = reverse != 0;
+    a.in_place = a.gx == a.g || (a.g_state && a.g_state == a.g_last);
     a.ws = workspace;
     if (a.B == 0 || (!a.gx && !a.gg && !a.g_state)) return DC1D_OK;
     return launched(launch_recurrence_backward(a, cus, (hipStream_t)stream));

@@ -232,6 +232,7 @@ struct GnParts {
     size_t part_bytes, stat_bytes;
 };
 
+constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads)
 constexpr int kJoinHere = 4096;  // statistics of a sample (32 KB) that every workgroup joins itself
 
 inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, int num_cus) {
@@ -258,7 +259,7 @@ inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, 
     p.joined = p.by_group && (int64_t)p.parts * G <= kJoinHere;
     p.team = 64;
     while (p.team > 1 && p.team > p.nt / G) p.team /= 2;
-    p.split = (int)std::max<int64_t>(1, std::min<int64_t>(4, p.rows / (8 * p.rt)));
+    p.split = (int)std::max<int64_t>(1, std::min({(int64_t)4, p.rows / (8 * p.rt), kMaxGrid / ((int64_t)p.parts * p.tiles)}));
     p.by_split = make_fastdiv(p.split);
     p.by_tiles = make_fastdiv(p.tiles), p.by_parts = make_fastdiv(p.parts), p.by_tp = make_fastdiv(p.tp);
     p.by_rt = make_fastdiv(p.rt), p.by_D = make_fastdiv(C / G);
@@ -337,8 +338,6 @@ __device__ __forceinline__ void each_entry(const GnParts &p, int per, int64_t n,
         for (int c = c0; c < per; c += cols) f(i, c, (float)rows);
     }
 }
-
-constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads)
 
 // f(first sample, workgroups) for launches of whole samples, the last samples first where `back`.
 template <typename F>

@@ -58,7 +58,9 @@ struct Lane {
 };
 
 // A piece's store; only where C is no multiple of a piece (ODD) may elements of it
-// be its neighbour's.
+// be its neighbour's.  Both threads then store the same values, unless the call
+// writes over what they are formed from (`in_place`): the neighbour's workgroup
+// may have done so already.
 template <typename T, int N, bool ODD>
 __device__ __forceinline__ void put(typename T::T *p, const float *f, int skip, bool in_place) {
     if constexpr (ODD)
@@ -318,12 +320,12 @@ struct Tile {
         const Walk<T, N, PER> yw(r.y, r.ys, r, t, i);
         if ((i + 1) * TILE <= t.n) {
 #pragma unroll
-            for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.y == r.x);
+            for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.in_place);
             apart();
         } else {
 #pragma unroll
             for (int k = 0; k < PER; ++k)
-                if (k < left) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.y == r.x);
+                if (k < left) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.in_place);
         }
     }
 };
@@ -536,24 +538,24 @@ struct TileBack {
             const Walk<T, N, PER> w(r.gx, r.gxs, r, t, i);
             if (full) {
 #pragma unroll
-                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip, r.gx == r.g);
+                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip, r.in_place);
                 apart();
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if (k < left) put<T, N, ODD>(w.at(k), g[k], t.skip, r.gx == r.g);
+                    if (k < left) put<T, N, ODD>(w.at(k), g[k], t.skip, r.in_place);
             }
         }
         if (r.gg) {
             const Walk<T, N, PER> w(r.gg, r.ggs, r, t, i);
             if (full) {
 #pragma unroll
-                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip, r.gx == r.g);
+                for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip, r.in_place);
                 apart();
             } else {
 #pragma unroll
                 for (int k = 0; k < PER; ++k)
-                    if (k < left) put<T, N, ODD>(w.at(k), x[k], t.skip, r.gx == r.g);
+                    if (k < left) put<T, N, ODD>(w.at(k), x[k], t.skip, r.in_place);
             }
         }
     }

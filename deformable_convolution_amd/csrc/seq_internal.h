@@ -126,6 +126,7 @@ struct RecurrenceArgs {
     float *last, *g_state;     // [B][C] or null
     float *states;             // [B][ceil(L / 64)][C]; forward: written unless null, backward: read
     int dtype, B, L, C, blend, reverse;
+    int in_place;              // outputs over what they are formed from: y over x or last over state; gx over g or g_state over g_last
     void *ws;
 };
 size_t recurrence_workspace(int B, int L, int C, int dtype, bool backward, int num_cus);

@@ -199,6 +199,24 @@ def test_layouts(B, L, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("C", [65, 67, 130, 515])
+def test_states_in_place_beside_another_workgroup(C, dtype):
+    """A row's last channels are read by the workgroup of its last piece and by the one before it, which may have
+    replaced their state by then: y and the gradients are those of states of their own."""
+    for L in (1, 3):
+        x, gate, state, go, g_last = inputs(3000, L, C, dtype, 15)
+        want, last, states = sequence.gated_recurrence(x, gate, state, blend=True, with_states=True)
+        grads = sequence.gated_recurrence_backward(x, gate, states, go, g_last, blend=True)
+        for _ in range(5):
+            s = state.clone()
+            y, _ = sequence.gated_recurrence(x, gate, s, blend=True, last=s)
+            assert torch.equal(y, want) and torch.equal(s, last)
+            gl = g_last.clone()
+            got = sequence.gated_recurrence_backward(x, gate, states, go, gl, blend=True, grads={"state": gl})
+            assert all(torch.equal(got[n], grads[n]) for n in grads)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_position_by_position(dtype):
     """A sequence taken up again at every position, or in pieces, gives what it gives at once, up to rounding."""
     x, gate, state, go, g_last = inputs(3, 75, 20, dtype, 5)
