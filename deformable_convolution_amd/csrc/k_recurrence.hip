@@ -635,12 +635,24 @@ struct RecPlan {
     size_t ws_bytes;
 };
 
-RecPlan plan_recurrence(int B, int L, int C, int N, int tile, int num_cus) {
+// One pass (a segment a chain) where the chains alone keep the memory busy: from
+// one for every CU on, three quarters of that in 32 bits, whose rows are twice as
+// long (16 x 4092 x 1024 fp32, 256 chains: 171 us in one pass, 261 in two,
+// gradients 272, 363; bf16 113, 145 and 180, 210; 12 x 4096 x 1024, 192 chains:
+// fp32 147, 209 and 223, 294, bf16 104, 106 and 180, 161; 8 x 4096 x 1024, 128
+// chains: fp32 137, 134 and 193, 188, bf16 102, 81 and 172, 121).  One too where
+// another launch costs more than the tiles one after another (16 x 384 x 512
+// fp32, 6 tiles: 13.2, 15.0; 8 x 512 x 512, 8 tiles: 15.1, 14.1; gradients 16 x 256 x
+// 256, 4 tiles: 13.8, 14.9; 4 x 384 x 256, 6 tiles: 17.9, 14.8).  Otherwise eight
+// workgroups a CU (16: 8 x 16384 x 256 bf16 77.4 -> 77.5, gradients 111 -> 120; 4:
+// 76.2, 111), in at most 256 segments.
+RecPlan plan_recurrence(int B, int L, int C, int N, int dtype, bool backward, int num_cus) {
     RecPlan p = {};
-    const int slabs = (C + N * kLanes - 1) / (N * kLanes);
+    const int slabs = (C + N * kLanes - 1) / (N * kLanes), tile = kSlots * (backward ? kPerBack : kPer);
     const int64_t chains = (int64_t)B * slabs, tiles = std::max<int64_t>(1, (L + (int64_t)tile - 1) / tile);
+    const bool one = 4 * chains >= (dtype == kF32 ? 3 : 4) * num_cus || tiles <= (backward ? 4 : 6);
     const int64_t want = chains > 0 ? (8ll * num_cus + chains - 1) / chains : 1;
-    p.g.segs = (int)(chains >= 2 * num_cus || tiles <= 2 ? 1 : std::min({want, tiles, (int64_t)256}));
+    p.g.segs = (int)(one ? 1 : std::min({want, tiles, (int64_t)256}));
     p.g.tiles = (int)((tiles + p.g.segs - 1) / p.g.segs);
     p.g.segs = (int)((tiles + p.g.tiles - 1) / p.g.tiles);
     p.g.by_segs = make_fastdiv((uint32_t)p.g.segs);
@@ -681,7 +693,7 @@ hipError_t in_launches(Segments &g, F f) {
 
 template <typename T, int N, bool ODD, bool BLEND>
 hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    Segments g = plan_recurrence(a.B, a.L, a.C, N, kSlots * kPer, num_cus).g;
+    Segments g = plan_recurrence(a.B, a.L, a.C, N, a.dtype, false, num_cus).g;
     g.maps = (float2 *)a.ws;
     const dim3 block(kThreads);
     if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps<T, N, BLEND>), grid, block, 0, stream, a, g); });
@@ -690,7 +702,7 @@ hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
 
 template <typename T, int N, bool ODD, bool BLEND>
 hipError_t run_back(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    Segments g = plan_recurrence(a.B, a.L, a.C, N, kSlots * kPerBack, num_cus).g;
+    Segments g = plan_recurrence(a.B, a.L, a.C, N, a.dtype, true, num_cus).g;
     g.maps = (float2 *)a.ws;
     const dim3 block(kThreads);
     if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps_back<T, N>), grid, block, 0, stream, a, g); });
@@ -712,10 +724,9 @@ hipError_t by_type(const RecurrenceArgs &a, int tile, F f) {
 }  // namespace
 
 // The strides decide between pieces of four channels and single ones: room for either.
-size_t recurrence_workspace(int B, int L, int C, int, bool backward, int num_cus) {
-    const int tile = kSlots * (backward ? kPerBack : kPer);
-    const size_t one = plan_recurrence(B, L, C, 1, tile, num_cus).ws_bytes;
-    return C < 4 ? one : std::max(one, plan_recurrence(B, L, C, 4, tile, num_cus).ws_bytes);
+size_t recurrence_workspace(int B, int L, int C, int dtype, bool backward, int num_cus) {
+    const size_t one = plan_recurrence(B, L, C, 1, dtype, backward, num_cus).ws_bytes;
+    return C < 4 ? one : std::max(one, plan_recurrence(B, L, C, 4, dtype, backward, num_cus).ws_bytes);
 }
 
 hipError_t launch_recurrence(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
