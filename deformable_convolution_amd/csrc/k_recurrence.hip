@@ -11,7 +11,7 @@
 // gate and g and write two gradients; at some 30 and 45 instructions an element
 // the arithmetic takes more than half of that time and has to run beside it.
 //
-// A workgroup is 16 slots of a few positions by 16 pieces of N channels, so that
+// A workgroup is 16 or 32 slots of a few positions by 16 pieces of N channels, so that
 // rows are read in runs of 16 pieces; a tile is the slots' positions.  A slot's
 // positions stay in registers: their map is formed, the slots' maps are joined
 // over the wave's rows of lanes and the waves, and the states follow.  Four
@@ -26,7 +26,7 @@ namespace dc1d {
 
 namespace {
 
-constexpr int kLanes = 16, kSlots = 16, kThreads = kLanes * kSlots, kWaves = kThreads / 64;
+constexpr int kLanes = 16, kSlots = 16;  // a workgroup has SL slots: kSlots or twice that
 constexpr int kPer = 4, kPerBack = 4;  // positions of a slot
 static_assert(kStateEvery % kPer == 0, "a kept state stands ahead of a slot");
 static_assert(kSlots * kPerBack % kStateEvery == 0, "a tile of the backward pass starts at a kept state");
@@ -74,9 +74,9 @@ __device__ __forceinline__ void put(typename T::T *p, const float *f, int skip, 
 // A slot's rows of a tensor in one tile: a base that all threads share (of each
 // row, on scalar registers), and the slot's offset from it.  Reversed, the base is
 // the tile's last position.
-template <typename T, int N, int PER>
+template <typename T, int N, int PER, int SL>
 struct Walk {
-    static constexpr int TILE = kSlots * PER;
+    static constexpr int TILE = SL * PER;
     using E = typename T::T;
     char *base;
     int64_t step;
@@ -87,7 +87,7 @@ struct Walk {
         const int64_t row = reverse ? (int64_t)max(l.n, 1) - (int64_t)(tile + 1) * TILE : (int64_t)tile * TILE;
         base = (char *)t + (l.b * st.b + row * st.l) * (int64_t)sizeof(E);
         step = st.l * (int64_t)sizeof(E);
-        off = (Offset<N>)(l.at * sizeof(E)) + (Offset<N>)((reverse ? kSlots - 1 - l.slot : l.slot) * PER) * (Offset<N>)step;
+        off = (Offset<N>)(l.at * sizeof(E)) + (Offset<N>)((reverse ? SL - 1 - l.slot : l.slot) * PER) * (Offset<N>)step;
     }
     // Row k of the slot, the same k for all threads; or any of the tile's rows, counted from the slot's first.
     __device__ __forceinline__ E *at(int k) const { return (E *)((base + (reverse ? PER - 1 - k : k) * step) + off); }
@@ -131,8 +131,8 @@ struct Rows {
     }
     // `last`: the sequence's last position within the length (the first, for none),
     // counted from the slot's first, in place of those past it
-    template <bool FULL>
-    __device__ __forceinline__ void load(const Walk<T, N, PER> &w, int last) {
+    template <bool FULL, int SL>
+    __device__ __forceinline__ void load(const Walk<T, N, PER, SL> &w, int last) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) r[k] = Piece<T, N>::load(FULL ? w.at(k) : w.any(min(k, last)));
     }
@@ -182,16 +182,16 @@ struct Map {  // h -> A h + H
     }
 };
 
-// A wave's four slots: the map of those ahead of a thread's (of those behind it
-// where BACK) to `ahead`, the wave's to `ends`.  The slots are rows of 16 lanes:
+// A wave has four slots.  The map of those ahead of a thread's goes to `ahead` (of
+// those behind it where BACK), the wave's to `ends`.  The slots are rows of 16 lanes:
 // v_permlane16_swap gives both rows of a pair their even and odd row's values,
 // v_permlane32_swap both halves' to both.  The caller's barriers keep `ends` from
 // the next use; two of them in turn need one barrier each.
-template <int N>
-using Ends = Map<N>[kWaves][kLanes];
+template <int N, int SL>
+using Ends = Map<N>[SL / 4][kLanes];
 
-template <int N, bool BACK>
-__device__ __forceinline__ void join_slots(const Map<N> &own, Map<N> &ahead, Ends<N> &ends) {
+template <int N, bool BACK, int SL>
+__device__ __forceinline__ void join_slots(const Map<N> &own, Map<N> &ahead, Ends<N, SL> &ends) {
     const int lane = threadIdx.x & 63;
     const bool second = ((lane >> 4) & 1) != BACK, later = (lane >> 5) != BACK;
     Map<N> all;
@@ -220,12 +220,12 @@ __device__ __forceinline__ void join_slots(const Map<N> &own, Map<N> &ahead, End
 }
 
 // After a barrier: h goes from the tile's start to its end, and `here` is the state ahead of the thread's wave.
-template <int N, bool BACK>
-__device__ __forceinline__ void pass_waves(const Ends<N> &ends, float *h, float *here) {
+template <int N, bool BACK, int SL>
+__device__ __forceinline__ void pass_waves(const Ends<N, SL> &ends, float *h, float *here) {
     const int w = threadIdx.x >> 6, p = threadIdx.x % kLanes;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        const int wave = BACK ? kWaves - 1 - i : i;
+    for (int i = 0; i < SL / 4; ++i) {
+        const int wave = BACK ? SL / 4 - 1 - i : i;
         if (wave == w)  // the same for all of a wave
 #pragma unroll
             for (int e = 0; e < N; ++e) here[e] = h[e];
@@ -234,23 +234,23 @@ __device__ __forceinline__ void pass_waves(const Ends<N> &ends, float *h, float 
 }
 
 // After a barrier: the map of all of the waves' slots, behind `m`.
-template <int N, bool BACK>
-__device__ __forceinline__ void join_waves(const Ends<N> &ends, Map<N> &m) {
+template <int N, bool BACK, int SL>
+__device__ __forceinline__ void join_waves(const Ends<N, SL> &ends, Map<N> &m) {
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        Map<N> o = ends[BACK ? kWaves - 1 - i : i][threadIdx.x % kLanes];
+    for (int i = 0; i < SL / 4; ++i) {
+        Map<N> o = ends[BACK ? SL / 4 - 1 - i : i][threadIdx.x % kLanes];
         o.after(m);
         m = o;
     }
 }
 
 // Rows past the length become 0: positions from ... to - 1, slot by slot.
-template <typename T, int N>
+template <typename T, int N, int SL>
 __device__ __forceinline__ void clear_rows(void *t, Strides2 st, const Lane<N> &l, int from, int to) {
     if (!t || !l.on) return;
     const float zero[N] = {};
     typename T::T *const p = (typename T::T *)t + l.b * st.b + l.at;
-    for (int s = from + l.slot; s < to; s += kSlots) store_own<T, N>(p + s * st.l, zero, l.skip);
+    for (int s = from + l.slot; s < to; s += SL) store_own<T, N>(p + s * st.l, zero, l.skip);
 }
 
 template <int N>
@@ -262,14 +262,14 @@ __device__ __forceinline__ void store_state(float *o, const Lane<N> &t, const fl
 
 // ---- the forward's tile -------------------------------------------------------------
 
-template <typename T, int N, int PER, bool ODD, bool BLEND>
+template <typename T, int N, int PER, int SL, bool ODD, bool BLEND>
 struct Tile {
-    static constexpr int TILE = kSlots * PER;
+    static constexpr int TILE = SL * PER;
     Rows<T, N, PER> xr, gr;
     float a[PER][N], u[PER][N];
     __device__ __forceinline__ void load(const RecurrenceArgs &r, const Lane<N> &t, int i) {
         const int from = last_tile<TILE>(t.n, i), last = max(t.n, 1) - 1 - from * TILE - t.slot * PER;
-        const Walk<T, N, PER> gw(r.gate, r.gates, r, t, from), xw(r.x, r.xs, r, t, from);
+        const Walk<T, N, PER, SL> gw(r.gate, r.gates, r, t, from), xw(r.x, r.xs, r, t, from);
         if ((i + 1) * TILE <= t.n) {
             gr.template load<true>(gw, last);
             xr.template load<true>(xw, last);
@@ -319,7 +319,7 @@ struct Tile {
         for (int k = 0; k < PER; ++k)
 #pragma unroll
             for (int e = 0; e < N; ++e) u[k][e] = h[e] = fmaf(a[k][e], h[e], u[k][e]);
-        const Walk<T, N, PER> yw(r.y, r.ys, r, t, i);
+        const Walk<T, N, PER, SL> yw(r.y, r.ys, r, t, i);
         if ((i + 1) * TILE <= t.n) {
 #pragma unroll
             for (int k = 0; k < PER; ++k) put<T, N, ODD>(yw.at(k), u[k], t.skip, r.in_place);
@@ -337,7 +337,7 @@ struct Tile {
 // A chain (a sequence's 16 pieces of channels) is cut into segments of whole
 // tiles, a workgroup each.  Where there is more than one, a kernel ahead forms
 // every segment's map; a workgroup joins those of the segments ahead of its own,
-// 16 slots of them side by side, and walks through its tiles.  So gate and x are
+// a slot some of them, and walks through its tiles.  So gate and x are
 // read twice: 8 x 16384 x 256 bf16 moves 335 MB in 32 + 43 us, gradients 470 in 35 +
 // 76.  (Joined as they come from workgroup to workgroup in one pass, the result
 // depends on the order of arrival; in a fixed order it waited longer: 95 us and
@@ -355,19 +355,19 @@ struct Segments {
 };
 
 // The state ahead of segment `to` in the order of the scan (BACK: from the last segment on).
-template <int N, bool BACK>
-__device__ __forceinline__ void carry_in(const Segments &g, uint32_t chain, int seg, const float *start, float *h, Ends<N> &ends) {
+template <int N, bool BACK, int SL>
+__device__ __forceinline__ void carry_in(const Segments &g, uint32_t chain, int seg, const float *start, float *h, Ends<N, SL> &ends) {
     const int slot = threadIdx.x / kLanes, p = threadIdx.x % kLanes;
     if (g.segs == 1) {
 #pragma unroll
         for (int e = 0; e < N; ++e) h[e] = start ? start[e] : 0.0f;
         return;
     }
-    const int before = BACK ? g.segs - 1 - seg : seg, each = (before + kSlots - 1) / kSlots;  // of every slot
+    const int before = BACK ? g.segs - 1 - seg : seg, each = (before + SL - 1) / SL;  // of every slot
     const float2 *const s = g.at<N>(chain, BACK ? 0 : g.segs - 1, p);
     Map<N> m, rest;
     m.clear();
-    const int from = (BACK ? kSlots - 1 - slot : slot) * each;
+    const int from = (BACK ? SL - 1 - slot : slot) * each;
     for (int i = from; i < min(from + each, before); ++i) {
         const float2 *const o = g.at<N>(chain, BACK ? g.segs - 1 - i : i, p);
         Map<N> n;
@@ -378,10 +378,10 @@ __device__ __forceinline__ void carry_in(const Segments &g, uint32_t chain, int 
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) h[e] = s[e].y;
-    join_slots<N, BACK>(m, rest, ends);
+    join_slots<N, BACK, SL>(m, rest, ends);
     __syncthreads();
     float here[N];
-    pass_waves<N, BACK>(ends, h, here);
+    pass_waves<N, BACK, SL>(ends, h, here);
 }
 
 template <int N>
@@ -391,9 +391,9 @@ __device__ __forceinline__ void store_map(float2 *o, const Map<N> &m) {
 }
 
 template <typename T, int N, bool BLEND>
-__global__ __launch_bounds__(kThreads) void k_rec_maps(RecurrenceArgs a, Segments g) {
-    __shared__ Ends<N> ends[2];
-    using W = Tile<T, N, kPer, false, BLEND>;
+__global__ __launch_bounds__(kLanes * kSlots) void k_rec_maps(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N, kSlots> ends[2];
+    using W = Tile<T, N, kPer, kSlots, false, BLEND>;
     const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
     const int seg = (int)(job - chain * g.by_segs.d);
     const Lane<N> t(a, chain, g.by_slabs);
@@ -411,9 +411,9 @@ __global__ __launch_bounds__(kThreads) void k_rec_maps(RecurrenceArgs a, Segment
             const Map<N> own = v.form(t, i);
             if (i + 1 < past) v.load(a, t, i + 1);
             Map<N> ahead;
-            join_slots<N, false>(own, ahead, ends[i & 1]);
+            join_slots<N, false, kSlots>(own, ahead, ends[i & 1]);
             __syncthreads();
-            join_waves<N, false>(ends[i & 1], all);
+            join_waves<N, false, kSlots>(ends[i & 1], all);
             if (++i == past) break;
         }
     }
@@ -423,10 +423,10 @@ __global__ __launch_bounds__(kThreads) void k_rec_maps(RecurrenceArgs a, Segment
 // A tile's loads are in flight while the one before it is worked on.  32 x 1024 x
 // 1024 fp32 in one pass: 82 us, 4.9 TB/s, at the rate of a copy; one position of 16
 // x 512: 4 us.
-template <typename T, int N, bool ODD, bool BLEND>
-__global__ __launch_bounds__(kThreads) void k_rec_walk(RecurrenceArgs a, Segments g) {
-    __shared__ Ends<N> ends[2];
-    using W = Tile<T, N, kPer, ODD, BLEND>;
+template <typename T, int N, int SL, bool ODD, bool BLEND>
+__global__ __launch_bounds__(kLanes * SL) void k_rec_walk(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N, SL> ends[2];
+    using W = Tile<T, N, kPer, SL, ODD, BLEND>;
     const int tiles = (a.L + W::TILE - 1) / W::TILE;
     const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
     const int seg = (int)(job - chain * g.by_segs.d);
@@ -435,20 +435,20 @@ __global__ __launch_bounds__(kThreads) void k_rec_walk(RecurrenceArgs a, Segment
     W v;
     v.load(a, t, first);
     float h0[N];
-    carry_in<N, false>(g, chain, seg, a.state ? a.state + t.state(a) : nullptr, h0, ends[(first & 1) ^ 1]);
+    carry_in<N, false, SL>(g, chain, seg, a.state ? a.state + t.state(a) : nullptr, h0, ends[(first & 1) ^ 1]);
     for (int i = first;;) {
         const Map<N> own = v.form(t, i);
         if (i + 1 < past) v.load(a, t, i + 1);
         Map<N> ahead;
-        join_slots<N, false>(own, ahead, ends[i & 1]);
+        join_slots<N, false, SL>(own, ahead, ends[i & 1]);
         __syncthreads();
         float h[N];
-        pass_waves<N, false>(ends[i & 1], h0, h);
+        pass_waves<N, false, SL>(ends[i & 1], h0, h);
         ahead.apply(h);
         v.store(a, t, i, h);
         if (++i == past) break;
     }
-    clear_rows<T, N>(a.y, a.ys, t, max(first * W::TILE, t.n), min(past * W::TILE, a.L));
+    clear_rows<T, N, SL>(a.y, a.ys, t, max(first * W::TILE, t.n), min(past * W::TILE, a.L));
     __syncthreads();  // every thread has read the state, which `last` may be
     if (a.last && t.on && seg == g.segs - 1 && t.slot == 0) store_state<N>(a.last + t.state(a), t, h0);
 }
@@ -458,15 +458,15 @@ __global__ __launch_bounds__(kThreads) void k_rec_walk(RecurrenceArgs a, Segment
 // m_s = a_s r_s = a_s (m_{s+1} + g_s): the gradient of the state ahead of s, a
 // scan from the end whose maps have the same factors.
 
-template <typename T, int N, int PER, bool ODD, bool BLEND>
+template <typename T, int N, int PER, int SL, bool ODD, bool BLEND>
 struct TileBack {
-    static constexpr int TILE = kSlots * PER;
+    static constexpr int TILE = SL * PER;
     Rows<T, N, PER> xr, gr, dr;
     float kept[N];  // the state that the tile starts from
     float a[PER][N], q[PER][N], x[PER][N], g[PER][N];
     __device__ __forceinline__ void load(const RecurrenceArgs &r, const Lane<N> &t, int i) {
         const int from = last_tile<TILE>(t.n, i), last = max(t.n, 1) - 1 - from * TILE - t.slot * PER;
-        const Walk<T, N, PER> gw(r.gate, r.gates, r, t, from), xw(r.x, r.xs, r, t, from), dw(r.g, r.gs, r, t, from);
+        const Walk<T, N, PER, SL> gw(r.gate, r.gates, r, t, from), xw(r.x, r.xs, r, t, from), dw(r.g, r.gs, r, t, from);
         if ((i + 1) * TILE <= t.n) {
             gr.template load<true>(gw, last);
             xr.template load<true>(xw, last);
@@ -544,7 +544,7 @@ struct TileBack {
         const bool full = (i + 1) * TILE <= t.n;
         const int left = t.n - i * TILE - t.slot * PER;
         if (r.gx) {
-            const Walk<T, N, PER> w(r.gx, r.gxs, r, t, i);
+            const Walk<T, N, PER, SL> w(r.gx, r.gxs, r, t, i);
             if (full) {
 #pragma unroll
                 for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), g[k], t.skip, r.in_place);
@@ -556,7 +556,7 @@ struct TileBack {
             }
         }
         if (r.gg) {
-            const Walk<T, N, PER> w(r.gg, r.ggs, r, t, i);
+            const Walk<T, N, PER, SL> w(r.gg, r.ggs, r, t, i);
             if (full) {
 #pragma unroll
                 for (int k = 0; k < PER; ++k) put<T, N, ODD>(w.at(k), x[k], t.skip, r.in_place);
@@ -572,10 +572,10 @@ struct TileBack {
 
 // Of every segment, from its end: its own kernel reads gate and g only.
 template <typename T, int N>
-__global__ __launch_bounds__(kThreads) void k_rec_maps_back(RecurrenceArgs a, Segments g) {
-    __shared__ Ends<N> ends[2];
+__global__ __launch_bounds__(kLanes * kSlots) void k_rec_maps_back(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N, kSlots> ends[2];
     a.x = a.g, a.xs = a.gs;
-    using W = Tile<T, N, kPerBack, false, false>;
+    using W = Tile<T, N, kPerBack, kSlots, false, false>;
     const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
     const int seg = (int)(job - chain * g.by_segs.d);
     const Lane<N> t(a, chain, g.by_slabs);
@@ -593,9 +593,9 @@ __global__ __launch_bounds__(kThreads) void k_rec_maps_back(RecurrenceArgs a, Se
             const Map<N> own = v.template form<true>(t, i);
             if (i > first) v.load(a, t, i - 1);
             Map<N> behind;
-            join_slots<N, true>(own, behind, ends[i & 1]);
+            join_slots<N, true, kSlots>(own, behind, ends[i & 1]);
             __syncthreads();
-            join_waves<N, true>(ends[i & 1], all);
+            join_waves<N, true, kSlots>(ends[i & 1], all);
             if (i-- == first) break;
         }
     }
@@ -606,10 +606,10 @@ __global__ __launch_bounds__(kThreads) void k_rec_maps_back(RecurrenceArgs a, Se
 // tile, the gradients from its end.  Two waves a SIMD of 200 registers (fp32 228):
 // 8 x 16384 x 256 bf16 76 us, 4.4 TB/s, the vector unit busy for 60 % of it; 13 x
 // 4092 x 511 fp32, ragged, 109 us.
-template <typename T, int N, bool ODD, bool BLEND>
-__global__ __launch_bounds__(kThreads) void k_rec_walk_back(RecurrenceArgs a, Segments g) {
-    __shared__ Ends<N> ends[2][2];
-    using W = TileBack<T, N, kPerBack, ODD, BLEND>;
+template <typename T, int N, int SL, bool ODD, bool BLEND>
+__global__ __launch_bounds__(kLanes * SL) void k_rec_walk_back(RecurrenceArgs a, Segments g) {
+    __shared__ Ends<N, SL> ends[2][2];
+    using W = TileBack<T, N, kPerBack, SL, ODD, BLEND>;
     const int tiles = (a.L + W::TILE - 1) / W::TILE;
     const uint32_t job = g.first + blockIdx.x, chain = fdiv(job, g.by_segs);
     const int seg = (int)(job - chain * g.by_segs.d);
@@ -618,25 +618,25 @@ __global__ __launch_bounds__(kThreads) void k_rec_walk_back(RecurrenceArgs a, Se
     W v;
     v.load(a, t, past - 1);
     float m0[N];
-    carry_in<N, true>(g, chain, seg, a.g_last ? a.g_last + t.state(a) : nullptr, m0, ends[past & 1][0]);
+    carry_in<N, true, SL>(g, chain, seg, a.g_last ? a.g_last + t.state(a) : nullptr, m0, ends[past & 1][0]);
     for (int i = past - 1;;) {
         float start[N], h[N], m[N];
         const Map<N> own = v.form(t, i, start);
         if (i > first) v.load(a, t, i - 1);
         Map<N> ahead, behind;
-        join_slots<N, false>(own, ahead, ends[i & 1][0]);
-        join_slots<N, true>(v.map_back(), behind, ends[i & 1][1]);
+        join_slots<N, false, SL>(own, ahead, ends[i & 1][0]);
+        join_slots<N, true, SL>(v.map_back(), behind, ends[i & 1][1]);
         __syncthreads();
-        pass_waves<N, false>(ends[i & 1][0], start, h);
+        pass_waves<N, false, SL>(ends[i & 1][0], start, h);
         ahead.apply(h);
-        pass_waves<N, true>(ends[i & 1][1], m0, m);
+        pass_waves<N, true, SL>(ends[i & 1][1], m0, m);
         behind.apply(m);
         v.store(a, t, i, h, m);
         if (i-- == first) break;
     }
     const int from = max(first * W::TILE, t.n), to = min(past * W::TILE, a.L);
-    clear_rows<T, N>(a.gx, a.gxs, t, from, to);
-    clear_rows<T, N>(a.gg, a.ggs, t, from, to);
+    clear_rows<T, N, SL>(a.gx, a.gxs, t, from, to);
+    clear_rows<T, N, SL>(a.gg, a.ggs, t, from, to);
     __syncthreads();
     if (a.g_state && t.on && seg == 0 && t.slot == 0) store_state<N>(a.g_state + t.state(a), t, m0);
 }
@@ -645,25 +645,31 @@ __global__ __launch_bounds__(kThreads) void k_rec_walk_back(RecurrenceArgs a, Se
 
 struct RecPlan {
     Segments g;
+    int slots;
     size_t ws_bytes;
 };
 
-// One pass (a segment a chain) where the chains alone keep the memory busy: from
-// one for every CU on, three quarters of that in 32 bits, whose rows are twice as
-// long (16 x 4092 x 1024 fp32, 256 chains: 171 us in one pass, 261 in two,
-// gradients 272, 363; bf16 113, 145 and 180, 210; 12 x 4096 x 1024, 192 chains:
-// fp32 147, 209 and 223, 294, bf16 104, 106 and 180, 161; 8 x 4096 x 1024, 128
-// chains: fp32 137, 134 and 193, 188, bf16 102, 81 and 172, 121).  One too where
-// another launch costs more than the tiles one after another (16 x 384 x 512
-// fp32, 6 tiles: 13.2, 15.0; 8 x 512 x 512, 8 tiles: 15.1, 14.1; gradients 16 x 256 x
-// 256, 4 tiles: 13.8, 14.9; 4 x 384 x 256, 6 tiles: 17.9, 14.8).  Otherwise eight
-// workgroups a CU (16: 8 x 16384 x 256 bf16 77.4 -> 77.5, gradients 111 -> 120; 4:
-// 76.2, 111), in at most 256 segments.
+// One pass (a segment a chain) where the chains alone keep the memory busy, with
+// twice the slots where a CU has no more than one or two of them.  8 x 4096 x 1024,
+// 128 chains: fp32 105 us, in two passes 134, gradients 184, 191; bf16 78, 80 and
+// (three quarters of a chain a CU are needed) 145, 121; 12 x 4096 x 1024 bf16,
+// 192 chains: 80, 106 and 155, 161; 6 x 4096 x 1024, 96 chains: fp32 96, 100 and
+// 176, 141, bf16 75, 54 and 135, 87.  Twice the slots: 16 x 4092 x 1024 bf16, 256
+// chains: 108 -> 88 us, gradients 185 -> 166; 28 x 1024 x 1024 bf16, 448 chains:
+// 42.2 -> 40.8, gradients 75.7 -> 81.9; four times: 104 and 52.7.  One too where another launch
+// costs more than the tiles one after another: 2 x 512 x 256, 8 tiles of 64: 11.4,
+// 15.4; 2 x 900 x 512, 15 of them: 20.4, 14.2; gradients 4 x 384 x 256, 6 tiles: 13.7,
+// 16.7; 2 x 512 x 256, 8 tiles: 16.7, 16.4.  Otherwise eight workgroups a CU (16: 8 x
+// 16384 x 256 bf16 77.4 -> 77.5, gradients 111 -> 120; 4: 76.2, 111), in at most 256
+// segments.
 RecPlan plan_recurrence(int B, int L, int C, int N, int dtype, bool backward, int num_cus) {
     RecPlan p = {};
-    const int slabs = (C + N * kLanes - 1) / (N * kLanes), tile = kSlots * (backward ? kPerBack : kPer);
-    const int64_t chains = (int64_t)B * slabs, tiles = std::max<int64_t>(1, (L + (int64_t)tile - 1) / tile);
-    const bool one = 4 * chains >= (dtype == kF32 ? 3 : 4) * num_cus || tiles <= (backward ? 4 : 6);
+    const int slabs = (C + N * kLanes - 1) / (N * kLanes), per = backward ? kPerBack : kPer;
+    const int64_t chains = (int64_t)B * slabs;
+    const auto of = [&](int slots) { return std::max<int64_t>(1, (L + (int64_t)slots * per - 1) / (slots * per)); };
+    const bool one = 4 * chains >= (backward && dtype != kF32 ? 3 : 2) * num_cus || of(kSlots) <= (backward ? 6 : 10);
+    p.slots = one && (backward ? chains <= num_cus : chains < 2 * num_cus) ? 2 * kSlots : kSlots;
+    const int64_t tiles = of(p.slots);
     const int64_t want = chains > 0 ? (8ll * num_cus + chains - 1) / chains : 1;
     p.g.segs = (int)(one ? 1 : std::min({want, tiles, (int64_t)256}));
     p.g.tiles = (int)((tiles + p.g.segs - 1) / p.g.segs);
@@ -706,20 +712,32 @@ hipError_t in_launches(Segments &g, F f) {
 
 template <typename T, int N, bool ODD, bool BLEND>
 hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    Segments g = plan_recurrence(a.B, a.L, a.C, N, a.dtype, false, num_cus).g;
+    const RecPlan p = plan_recurrence(a.B, a.L, a.C, N, a.dtype, false, num_cus);
+    Segments g = p.g;
     g.maps = (float2 *)a.ws;
-    const dim3 block(kThreads);
+    const dim3 block(kLanes * p.slots);
     if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps<T, N, BLEND>), grid, block, 0, stream, a, g); });
-    return in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_walk<T, N, ODD, BLEND>), grid, block, 0, stream, a, g); });
+    return in_launches(g, [&](dim3 grid) {
+        if (p.slots == kSlots)
+            hipLaunchKernelGGL((k_rec_walk<T, N, kSlots, ODD, BLEND>), grid, block, 0, stream, a, g);
+        else
+            hipLaunchKernelGGL((k_rec_walk<T, N, 2 * kSlots, ODD, BLEND>), grid, block, 0, stream, a, g);
+    });
 }
 
 template <typename T, int N, bool ODD, bool BLEND>
 hipError_t run_back(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
-    Segments g = plan_recurrence(a.B, a.L, a.C, N, a.dtype, true, num_cus).g;
+    const RecPlan p = plan_recurrence(a.B, a.L, a.C, N, a.dtype, true, num_cus);
+    Segments g = p.g;
     g.maps = (float2 *)a.ws;
-    const dim3 block(kThreads);
+    const dim3 block(kLanes * p.slots);
     if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps_back<T, N>), grid, block, 0, stream, a, g); });
-    return in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_walk_back<T, N, ODD, BLEND>), grid, block, 0, stream, a, g); });
+    return in_launches(g, [&](dim3 grid) {
+        if (p.slots == kSlots)
+            hipLaunchKernelGGL((k_rec_walk_back<T, N, kSlots, ODD, BLEND>), grid, block, 0, stream, a, g);
+        else
+            hipLaunchKernelGGL((k_rec_walk_back<T, N, 2 * kSlots, ODD, BLEND>), grid, block, 0, stream, a, g);
+    });
 }
 
 // f(storage type, elements of a piece, whether C is no multiple of it, blend)
@@ -744,14 +762,14 @@ size_t recurrence_workspace(int B, int L, int C, int dtype, bool backward, int n
 
 hipError_t launch_recurrence(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
     if (a.L == 0) return run_empty(a, a.state, a.last, stream);
-    return by_type(a, kSlots * kPer, [&](auto t, auto n, auto odd, auto blend) {
+    return by_type(a, 2 * kSlots * kPer, [&](auto t, auto n, auto odd, auto blend) {
         return run<decltype(t), decltype(n)::value, decltype(odd)::value, decltype(blend)::value>(a, num_cus, stream);
     });
 }
 
 hipError_t launch_recurrence_backward(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
     if (a.L == 0) return run_empty(a, a.g_last, a.g_state, stream);
-    return by_type(a, kSlots * kPerBack, [&](auto t, auto n, auto odd, auto blend) {
+    return by_type(a, 2 * kSlots * kPerBack, [&](auto t, auto n, auto odd, auto blend) {
         return run_back<decltype(t), decltype(n)::value, decltype(odd)::value, decltype(blend)::value>(a, num_cus, stream);
     });
 }

@@ -70,7 +70,7 @@ def test_gated_recurrence(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("shape", [(520, 140, 5), (1, 140, 33001), (1, 40000, 4), (2, 9000, 70)])
+@pytest.mark.parametrize("shape", [(520, 140, 5), (1, 140, 33001), (1, 40000, 4), (2, 9000, 70), (2, 1400, 3), (5, 700, 2049)])
 def test_many_chains_and_many_segments(shape, dtype):
     """Sequences and channels enough for one pass over several tiles; long ones cut into many segments."""
     print("gated recurrence", shape, dtype, flush=True)
@@ -203,8 +203,8 @@ def test_layouts(B, L, C, dtype):
 def test_states_in_place_beside_another_workgroup(C, dtype):
     """A row's last channels are read by the workgroup of its last piece and by the one before it, which may have
     replaced their state by then: y and the gradients are those of states of their own."""
-    for L in (1, 3):
-        x, gate, state, go, g_last = inputs(3000, L, C, dtype, 15)
+    for B, L in ((40, 1), (3000, 1), (3000, 3), (30, 70)):
+        x, gate, state, go, g_last = inputs(B, L, C, dtype, 15)
         want, last, states = sequence.gated_recurrence(x, gate, state, blend=True, with_states=True)
         grads = sequence.gated_recurrence_backward(x, gate, states, go, g_last, blend=True)
         for _ in range(5):
