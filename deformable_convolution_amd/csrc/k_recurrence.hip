@@ -716,7 +716,10 @@ hipError_t run(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
     Segments g = p.g;
     g.maps = (float2 *)a.ws;
     const dim3 block(kLanes * p.slots);
-    if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps<T, N, BLEND>), grid, block, 0, stream, a, g); });
+    if (g.segs > 1) {
+        const hipError_t e = in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps<T, N, BLEND>), grid, block, 0, stream, a, g); });
+        if (e != hipSuccess) return e;
+    }
     return in_launches(g, [&](dim3 grid) {
         if (p.slots == kSlots)
             hipLaunchKernelGGL((k_rec_walk<T, N, kSlots, ODD, BLEND>), grid, block, 0, stream, a, g);
@@ -731,7 +734,10 @@ hipError_t run_back(const RecurrenceArgs &a, int num_cus, hipStream_t stream) {
     Segments g = p.g;
     g.maps = (float2 *)a.ws;
     const dim3 block(kLanes * p.slots);
-    if (g.segs > 1) (void)in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps_back<T, N>), grid, block, 0, stream, a, g); });
+    if (g.segs > 1) {
+        const hipError_t e = in_launches(g, [&](dim3 grid) { hipLaunchKernelGGL((k_rec_maps_back<T, N>), grid, block, 0, stream, a, g); });
+        if (e != hipSuccess) return e;
+    }
     return in_launches(g, [&](dim3 grid) {
         if (p.slots == kSlots)
             hipLaunchKernelGGL((k_rec_walk_back<T, N, kSlots, ODD, BLEND>), grid, block, 0, stream, a, g);

@@ -684,8 +684,8 @@ int dc1d_group_norm_backward(const dc1d_tensor *x, const dc1d_tensor *weight_or_
  *
  * The state is held in fp32 throughout.  A gate of -infinity starts anew
  * (a = 0), one of +infinity holds the state (a = 1).  A NaN, or an infinite x
- * or state, reaches its channel's later states only, until a gate of -infinity;
- * those are then infinite or NaN.  Positions past a
+ * or state, reaches its channel's later states only, which are then infinite or
+ * NaN, also behind a gate of -infinity (0 times either is NaN).  Positions past a
  * sequence's length give 0, whatever they hold; an empty one leaves its state.
  * y may be x itself (in place); otherwise outputs must not overlap the inputs
  * or each other.  workspace: at least dc1d_gated_recurrence_workspace_bytes()

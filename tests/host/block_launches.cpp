@@ -1,7 +1,7 @@
 // The launches of group norm and the gated recurrence over sizes up to the ends
 // of their documented limits, with the runtime's launch calls replaced by ones
 // that only look (tests/test_block_launches.py builds and runs this; no GPU is
-// used): a launch holds fewer than 2^32 threads, a workgroup at most 1024 and
+// used): whichever launch fails is reported, a launch holds fewer than 2^32 threads, a workgroup at most 1024 and
 // 64 KB of LDS.  Group norm's plans besides: every element of a sample has one
 // thread's row and piece, 32-bit offsets span what they address, and the
 // workspace holds what is kept in it.
@@ -19,6 +19,8 @@ static dim3 next_grid, next_block;
 static size_t next_lds;
 static int failures = 0, calls = 0, launches = 0;
 static bool bad = false;
+static int fails_at = 0;  // the launch that fails, counted from 1
+static hipError_t last_error = hipSuccess;
 extern "C" hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds, hipStream_t) {
     next_grid = grid, next_block = block, next_lds = lds;
     return hipSuccess;
@@ -31,9 +33,32 @@ extern "C" hipError_t hipLaunchKernel(const void *, dim3 grid, dim3 block, void 
     ++launches;
     bad = bad || grid.x < 1 || grid.y != 1 || grid.z != 1 || block.y != 1 || block.z != 1 || block.x < 64 || block.x > 1024 ||
           (int64_t)grid.x * block.x >= (int64_t)1 << 32 || lds > 64 * 1024;
-    return hipSuccess;
+    if (launches == fails_at) last_error = hipErrorLaunchFailure;
+    return launches == fails_at ? hipErrorLaunchFailure : hipSuccess;
 }
-extern "C" hipError_t hipGetLastError() { return hipSuccess; }
+extern "C" hipError_t hipGetLastError() {
+    const hipError_t e = last_error;
+    last_error = hipSuccess;
+    return e;
+}
+
+// Whichever launch of a call fails, the call says so.
+template <typename F>
+static void every_failure(const char *what, F call) {
+    fails_at = launches = 0;
+    if (call() != hipSuccess) ++failures;
+    const int n = launches;
+    for (int i = 1; i <= n; ++i) {
+        fails_at = i, launches = 0;
+        ++calls;
+        if (call() == hipSuccess) {
+            printf("%s: launch %d of %d failed unseen\n", what, i, n);
+            ++failures;
+        }
+        last_error = hipSuccess;
+    }
+    fails_at = 0;
+}
 
 static void held_plan(const HeldPlan &p, int64_t B, int64_t S, int C, int G, int N, int es, int tensors) {
     const int D = C / G;
@@ -113,6 +138,24 @@ int main() {
                             ++failures;
                         }
                     }
+    for (int64_t S : {(int64_t)1, (int64_t)784, (int64_t)65536})
+        for (int64_t G : {(int64_t)1, (int64_t)512}) {
+            GroupNormArgs a;
+            memset((void *)&a, 0, sizeof(a));
+            a.x = a.g = a.y = some, a.mean = a.rstd = (float *)some, a.gw = a.gb = some, a.ws = some;
+            a.dtype = kF32, a.B = 4, a.S = S, a.C = 512, a.G = (int)G, a.D = (int)(512 / G);
+            every_failure("group norm", [&] { return launch_group_norm(a, 256, nullptr); });
+            every_failure("group norm gradients", [&] { return launch_group_norm_backward(a, 256, nullptr); });
+        }
+    for (int L : {0, 1, 90, 16384}) {
+        RecurrenceArgs a;
+        memset((void *)&a, 0, sizeof(a));
+        a.x = a.gate = a.g = some, a.y = a.gx = a.gg = some, a.states = a.last = a.g_state = (float *)some, a.ws = some;
+        a.dtype = kF32, a.B = 2, a.L = L, a.C = 64;
+        for (Strides2 *s : {&a.xs, &a.gates, &a.gs, &a.ys, &a.gxs, &a.ggs}) *s = {64 * L, 64};
+        every_failure("recurrence", [&] { return launch_recurrence(a, 256, nullptr); });
+        every_failure("recurrence gradients", [&] { return launch_recurrence_backward(a, 256, nullptr); });
+    }
     printf("block launches: %d calls, %d failure(s)\n", calls, failures);
     return failures != 0;
 }
