@@ -8,9 +8,10 @@ namespace {
 // Gradients: a workgroup strides over the batches of its slab; a thread keeps its
 // channels' parameter gradients, which it leaves in the workspace at the end
 // ([workgroup of the slab][C]), at most eight workgroups a CU of them.  The rows are
-// taken from registers twice, each widened and its z formed anew.  32768 rows of
-// 1024 bf16: 53 us with the parameters' 4 us, 3.9 TB/s; 32 x 784 x 512 fp32: 45 us,
-// 3.4 TB/s, which eight rows a thread of both tensors leave four waves a SIMD.
+// taken from registers twice: in 32 bits the first time leaves xh and g' there (45.5
+// -> 42.8 us below), in bf16 z is formed anew.  32768 rows of
+// 1024 bf16: 53 us with the parameters' 4 us, 3.9 TB/s; 32 x 784 x 512 fp32: 43 us,
+// 3.6 TB/s, which eight rows a thread of both tensors leave four waves a SIMD.
 template <typename T, int N, int R, int MODE, int ACT>
 __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan p, float2 *out) {
     using P = Piece<T, N>;
@@ -55,6 +56,20 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
                 xh[e] = (xh[e] - mean[t.v(e)]) * r[t.v(e)];
                 u[e] = activate_back<ACT>(xh[e] * w[e] + c[e], u[e]);
             }
+            if constexpr (sizeof(E) == 4) {
+                xr[i] = Vec<T>::narrow(xh);
+                gr[i] = Vec<T>::narrow(u);
+            }
+        };
+        auto again = [&](int i, float *xh, float *u) {
+            if constexpr (sizeof(E) == 4) {
+                hold(xr[i]);
+                hold(gr[i]);
+                P::widen(xr[i], xh);
+                P::widen(gr[i], u);
+            } else {
+                back(i, xh, u);
+            }
         };
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -90,7 +105,7 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
                 const int row = t.rt + i * p.rt;
                 if (row >= a.S) continue;
                 float xh[N], u[N];
-                back(i, xh, u);
+                again(i, xh, u);
 #pragma unroll
                 for (int e = 0; e < N; ++e)
                     u[e] = row < n ? r[t.v(e)] * (u[e] * w[e] - v[0][t.v(e)] * inv - xh[e] * (v[1][t.v(e)] * inv)) : 0.0f;
