@@ -17,14 +17,14 @@ __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == kSilu) return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
     return z;
 }
-// The gradient g of act(z) taken to z.  silu: p (1 + z q), p = 1 / (1 + t) and q =
-// t p = 1 - p for t = exp(-z), held below 2^126 (z > -87) so that t p stays finite.
+// The gradient g of act(z) taken to z.  silu: p (1 + z (1 - p)), p = 1 / (1 + exp(-z));
+// 1 - p is off by 2^-24, which counts z times beside 1.
 template <int ACT>
 __device__ __forceinline__ float activate_back(float z, float g) {
     if constexpr (ACT == kRelu) return z > 0.0f ? g : 0.0f;
     if constexpr (ACT == kSilu) {
-        const float t = __builtin_amdgcn_exp2f(fminf(-z * kLog2e, 126.0f)), p = __builtin_amdgcn_rcpf(1.0f + t);
-        return g * (p * fmaf(z, t * p, 1.0f));
+        const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
+        return g * (p * fmaf(z, 1.0f - p, 1.0f));
     }
     return g;
 }

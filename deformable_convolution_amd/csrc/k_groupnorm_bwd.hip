@@ -73,12 +73,17 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
         };
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            const bool see = on && t.rt + i * p.rt < n;
+            if (!__all(see)) {  // zeros add nothing, whatever stands there
+                const typename P::Raw zero = {};
+                if (!see) xr[i] = zero, gr[i] = zero;
+            }
             float xh[N], u[N];
             back(i, xh, u);
-            const bool see = on && t.rt + i * p.rt < n;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float d = see && e >= t.skip ? u[e] : 0.0f, dx = see && e >= t.skip ? u[e] * xh[e] : 0.0f;
+                const bool own = MODE != kMixed || e >= t.skip;
+                const float d = own ? u[e] : 0.0f, dx = own ? u[e] * xh[e] : 0.0f;
                 pb[e] += d;
                 pw[e] += dx;
                 v[0][t.v(e)] += d * w[e];
@@ -107,10 +112,13 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
                 float xh[N], u[N];
                 again(i, xh, u);
 #pragma unroll
-                for (int e = 0; e < N; ++e)
-                    u[e] = row < n ? r[t.v(e)] * (u[e] * w[e] - v[0][t.v(e)] * inv - xh[e] * (v[1][t.v(e)] * inv)) : 0.0f;
+                for (int e = 0; e < N; ++e) {
+                    u[e] = r[t.v(e)] * (u[e] * w[e] - v[0][t.v(e)] * inv - xh[e] * (v[1][t.v(e)] * inv));
+                    hold(u[e]);
+                }
+                if (row >= n)
 #pragma unroll
-                for (int e = 0; e < N; ++e) hold(u[e]);
+                    for (int e = 0; e < N; ++e) u[e] = 0.0f;
                 put<T, N, MODE>(y + t.offset(a, p, sizeof(E), s, i, true), u, t.skip, a.y == a.g || t.channels < N);
             }
         }
