@@ -45,7 +45,7 @@ __device__ __forceinline__ int64_t positions(const GroupNormArgs &a, int64_t b) 
 //
 // Samples that fit are held: against parts, which read twice, 32 x 784 x 512 fp32
 // takes 23 us (34), 4 x 4096 x 512 bf16 23 (29), 32768 rows of 1024 bf16 33
-// (325), gradients 46 (55) and 52 (456).
+// (325), gradients 43 (55) and 52 (456).
 struct HeldPlan {
     int P, gs, slabs, rt, nb, nt, R;
     int64_t batches;       // of nb samples

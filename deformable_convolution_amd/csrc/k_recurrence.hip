@@ -656,8 +656,8 @@ struct RecPlan {
 // 192 chains: 80, 106 and 155, 161; 6 x 4096 x 1024, 96 chains: fp32 96, 100 and
 // 176, 141, bf16 75, 54 and 135, 87.  Twice the slots: 16 x 4092 x 1024 bf16, 256
 // chains: 108 -> 88 us, gradients 185 -> 166; 28 x 1024 x 1024 bf16, 448 chains:
-// 42.2 -> 40.8, gradients 75.7 -> 81.9; four times: 104 and 52.7.  One too where another launch
-// costs more than the tiles one after another: 2 x 512 x 256, 8 tiles of 64: 11.4,
+// 42.2 -> 40.8, gradients 75.7 -> 81.9; four times: 104 and 52.7; 16 x 1 x 512: 4.4 ->
+// 5.3.  One pass too where another launch costs more than the tiles one after another: 2 x 512 x 256, 8 tiles of 64: 11.4,
 // 15.4; 2 x 900 x 512, 15 of them: 20.4, 14.2; gradients 4 x 384 x 256, 6 tiles: 13.7,
 // 16.7; 2 x 512 x 256, 8 tiles: 16.7, 16.4.  Otherwise eight workgroups a CU (16: 8 x
 // 16384 x 256 bf16 77.4 -> 77.5, gradients 111 -> 120; 4: 76.2, 111), in at most 256
@@ -668,7 +668,7 @@ RecPlan plan_recurrence(int B, int L, int C, int N, int dtype, bool backward, in
     const int64_t chains = (int64_t)B * slabs;
     const auto of = [&](int slots) { return std::max<int64_t>(1, (L + (int64_t)slots * per - 1) / (slots * per)); };
     const bool one = 4 * chains >= (backward && dtype != kF32 ? 3 : 2) * num_cus || of(kSlots) <= (backward ? 6 : 10);
-    p.slots = one && (backward ? chains <= num_cus : chains < 2 * num_cus) ? 2 * kSlots : kSlots;
+    p.slots = one && of(kSlots) > 1 && (backward ? chains <= num_cus : chains < 2 * num_cus) ? 2 * kSlots : kSlots;
     const int64_t tiles = of(p.slots);
     const int64_t want = chains > 0 ? (8ll * num_cus + chains - 1) / chains : 1;
     p.g.segs = (int)(one ? 1 : std::min({want, tiles, (int64_t)256}));
