@@ -203,6 +203,14 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
     // few samples: as many workgroups as there are CUs
     while (p.nb > 1 && (B + p.nb - 1) / p.nb * p.slabs < num_cus) --p.nb;
     p.batches = (B + p.nb - 1) / p.nb;
+    // Gradients, eight rows a thread of pieces of eight elements or of several groups: 150 to 220 registers, one
+    // workgroup a CU at a time.  With more of them than CUs parts are faster (32 x 784 x 768 bf16 in 32 groups 68 ->
+    // 59 us; 64 x 1500 x 90 bf16 in 9: 72 -> 34; 16 x 600 x 510 fp32 in 34: 36 -> 30; 256 x 400 x 60 fp32 in 4: 29 ->
+    // 31), with fewer not (16 x 600 x 510 bf16, 192 of them: 23, 26).
+    if (tensors == 2 && p.R == 8 && (!inside || N == 8) && p.batches * p.slabs > num_cus) {
+        p.R = 0;
+        return p;
+    }
     p.nt = (p.nb * p.rt * p.P + 63) / 64 * 64;
     const int dn = inside ? D / N : D;
     p.mode = !inside ? kMixed : p.rt == 1 && dn <= 64 && !(dn & (dn - 1)) ? kShuffle : kWhole;
