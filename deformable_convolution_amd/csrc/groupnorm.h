@@ -55,7 +55,10 @@ struct HeldPlan {
     FastDiv by_P, by_rt, by_per, by_gs, by_D;
     size_t lds;
 };
-enum Mode { kShuffle, kWhole, kMixed };  // a group's lanes share a wave; a piece lies in one group; it may not
+// A group's lanes share a wave; a piece lies in one group; the slab is one group,
+// whose last piece repeats some of it (as if it were several, 11031 rows of 890
+// bf16 took 42 us, not 19; gradients 60, not 35); a piece may lie in several.
+enum Mode { kShuffle, kWhole, kOne, kMixed };
 
 // The sums of v over every group of a workgroup: [K] values for each of a
 // thread's NV groups.
@@ -84,7 +87,7 @@ struct GroupSums {
                 for (int i = lane; i < all; i += p.team) {
                     const int r = (int)fdiv(i, p.by_per), j = first + i - r * p.per;
                     int at;
-                    if constexpr (MODE == kWhole) {
+                    if constexpr (MODE != kMixed) {
                         at = j;
                     } else {
                         if (j >= channels) break;  // the last slab's groups are fewer
@@ -191,7 +194,8 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
             break;
         }
     }
-    if (p.R > 8 && !inside) p.R = 0;  // registers
+    const bool mixed = !inside && p.gs > 1;
+    if (p.R > 8 && mixed) p.R = 0;  // registers
     if (!p.R) return p;
     p.rt = (int)((S + p.R - 1) / p.R);
     p.nb = (int)std::max<int64_t>(1, std::min<int64_t>(p.nt / (p.P * p.rt), B));
@@ -207,14 +211,14 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
     // workgroup a CU at a time.  With more of them than CUs parts are faster (32 x 784 x 768 bf16 in 32 groups 68 ->
     // 59 us; 64 x 1500 x 90 bf16 in 9: 72 -> 34; 16 x 600 x 510 fp32 in 34: 36 -> 30; 256 x 400 x 60 fp32 in 4: 29 ->
     // 31), with fewer not (16 x 600 x 510 bf16, 192 of them: 23, 26).
-    if (tensors == 2 && p.R == 8 && (!inside || N == 8) && p.batches * p.slabs > num_cus) {
+    if (tensors == 2 && p.R == 8 && (mixed || N == 8) && p.batches * p.slabs > num_cus) {
         p.R = 0;
         return p;
     }
     p.nt = (p.nb * p.rt * p.P + 63) / 64 * 64;
     const int dn = inside ? D / N : D;
-    p.mode = !inside ? kMixed : p.rt == 1 && dn <= 64 && !(dn & (dn - 1)) ? kShuffle : kWhole;
-    p.per = dn;
+    p.mode = mixed ? kMixed : !inside ? kOne : p.rt == 1 && dn <= 64 && !(dn & (dn - 1)) ? kShuffle : kWhole;
+    p.per = p.mode == kOne ? p.P : dn;
     p.team = 64;
     while (p.team > 1 && (p.team > p.nt / (p.nb * p.gs) || p.team / 2 >= p.rt * p.per)) p.team /= 2;
     p.by_P = make_fastdiv(p.P), p.by_rt = make_fastdiv(p.rt), p.by_per = make_fastdiv(p.per), p.by_gs = make_fastdiv(p.gs);
@@ -343,17 +347,25 @@ __device__ __forceinline__ float all_sum(float v, float *red) {
     return v;
 }
 
-// f(part, entry, rows of the part) for every entry of group g, thread by thread.
+// f(statistics, entry, rows of the part) for every entry of a group's [parts][per]
+// at v, thread by thread, some loads at a time (3236 x 1808 fp32 in 16 groups, some
+// 200 parts of 113 channels each: 42 -> 35 us, gradients 44 -> 40).
 template <int NT, typename F>
-__device__ __forceinline__ void each_entry(const GnParts &p, int per, int64_t n, F f) {
+__device__ __forceinline__ void each_entry(const GnParts &p, const float2 *v, int per, int64_t n, F f) {
     const int cols = per < NT ? per : NT, rp = NT / cols;
     const int c0 = threadIdx.x % cols, p0 = threadIdx.x / cols;
+    const int parts = (int)min((int64_t)p.parts, (n + p.rows - 1) / p.rows);  // that have rows
     if (p0 >= rp) return;
-    for (int i = p0; i < p.parts; i += rp) {
-        const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
-        if (rows <= 0) return;
-        for (int c = c0; c < per; c += cols) f(i, c, (float)rows);
-    }
+    constexpr int U = 4;
+    for (int c = c0; c < per; c += cols)
+        for (int i = p0; i < parts; i += U * rp) {
+            float2 e[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) e[k] = v[(int64_t)min(i + k * rp, parts - 1) * p.entries + c];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (i + k * rp < parts) f(e[k], c, (float)min(n - (int64_t)(i + k * rp) * p.rows, p.rows));
+        }
 }
 
 // f(first sample, workgroups) for launches of whole samples, the last samples first where `back`.

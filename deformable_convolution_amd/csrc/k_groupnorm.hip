@@ -226,11 +226,10 @@ __global__ __launch_bounds__(NT) void k_gn_join(GroupNormArgs a, GnParts p, cons
         const int g = (int)(job % a.G);
         const float2 *const v = part + b * p.parts * p.entries + (int64_t)g * per;
         float s = 0.0f, q = 0.0f;
-        each_entry<NT>(p, per, n, [&](int i, int c, float rows) { s += v[(int64_t)i * p.entries + c].x * rows; });
+        each_entry<NT>(p, v, per, n, [&](float2 e, int, float rows) { s += e.x * rows; });
         const float all = (float)n * (float)per;
         const float mean = n > 0 ? all_sum<NT>(s, red) / all : 0.0f;
-        each_entry<NT>(p, per, n, [&](int i, int c, float rows) {
-            const float2 e = v[(int64_t)i * p.entries + c];
+        each_entry<NT>(p, v, per, n, [&](float2 e, int, float rows) {
             const float d = e.x - mean;
             q += e.y + d * d * rows * (p.by_group ? (float)a.D : 1.0f);
         });
@@ -341,6 +340,8 @@ hipError_t run_held(const GroupNormArgs &a, const HeldPlan &p, hipStream_t strea
             hipLaunchKernelGGL((k_gn_held<T, N, R, kShuffle, ACT>), grid, block, p.lds, stream, a, p, first);
         else if (p.mode == kWhole)
             hipLaunchKernelGGL((k_gn_held<T, N, R, kWhole, ACT>), grid, block, p.lds, stream, a, p, first);
+        else if (p.mode == kOne)
+            hipLaunchKernelGGL((k_gn_held<T, N, R, kOne, ACT>), grid, block, p.lds, stream, a, p, first);
         else if constexpr (R <= 8)
             hipLaunchKernelGGL((k_gn_held<T, N, R, kMixed, ACT>), grid, block, p.lds, stream, a, p, first);
     }

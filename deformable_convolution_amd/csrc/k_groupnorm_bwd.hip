@@ -83,7 +83,7 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
             back(i, xh, u);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const bool own = MODE != kMixed || e >= t.skip;
+                const bool own = (MODE != kMixed && MODE != kOne) || e >= t.skip;
                 const float d = own ? u[e] : 0.0f, dx = own ? u[e] * xh[e] : 0.0f;
                 pb[e] += d;
                 pw[e] += dx;
@@ -267,8 +267,7 @@ __global__ __launch_bounds__(NT) void k_gn_join_back(GroupNormArgs a, GnParts p,
         const int g = (int)(job % a.G), per = p.by_group ? 1 : a.D;
         const float2 *const v = p.by_group ? groups + b * p.parts * a.G + g : part + b * p.parts * a.C + (int64_t)g * a.D;
         float s = 0.0f, q = 0.0f;
-        each_entry<NT>(p, per, n, [&](int i, int c, float) {
-            const float2 e = v[(int64_t)i * p.entries + c];
+        each_entry<NT>(p, v, per, n, [&](float2 e, int c, float) {
             const float w = a.w && !p.by_group ? T::ld((const E *)a.w, (int64_t)g * a.D + c) : 1.0f;
             s += e.x * w;
             q += e.y * w;
@@ -398,6 +397,8 @@ hipError_t run_held_back(const GroupNormArgs &a, const HeldPlan &p, hipStream_t 
         hipLaunchKernelGGL((k_gn_held_back<T, N, R, kShuffle, ACT>), grid, block, p.lds, stream, a, p, out);
     else if (p.mode == kWhole)
         hipLaunchKernelGGL((k_gn_held_back<T, N, R, kWhole, ACT>), grid, block, p.lds, stream, a, p, out);
+    else if (p.mode == kOne)
+        hipLaunchKernelGGL((k_gn_held_back<T, N, R, kOne, ACT>), grid, block, p.lds, stream, a, p, out);
     else
         hipLaunchKernelGGL((k_gn_held_back<T, N, R, kMixed, ACT>), grid, block, p.lds, stream, a, p, out);
     if (out) hipLaunchKernelGGL((k_gn_params<T>), dim3((a.C + 15) / 16), dim3(1024), 0, stream, out, (int64_t)p.grid_rows, a.C, a.gw, a.gb);

@@ -66,7 +66,8 @@ static void held_plan(const HeldPlan &p, int64_t B, int64_t S, int C, int G, int
           p.P * N < p.gs * D || p.gs * D < N || (int64_t)p.slabs * p.gs < G || (int64_t)(p.slabs - 1) * p.gs >= G || p.batches * p.nb < B ||
           (p.batches - 1) * p.nb >= B || p.nb * S * C * es > (int64_t)1 << 31 || p.lds > 64 * 1024 || (p.team & (p.team - 1)) || p.team < 1 ||
           p.team > 64 || p.grid_rows < 1 || p.grid_rows > p.batches;
-    if (p.mode != kMixed) bad = bad || D % N || p.gs * D != p.P * N;
+    if (p.mode == kShuffle || p.mode == kWhole) bad = bad || D % N || p.gs * D != p.P * N;
+    if (p.mode == kOne) bad = bad || p.gs != 1 || D < N || p.per != p.P;
     if (p.mode == kShuffle) bad = bad || p.rt != 1 || 64 % p.per || p.nb * p.P > p.nt || p.P % p.per;
     if (p.mode != kShuffle) bad = bad || p.lds < (size_t)tensors * (p.nt * (p.mode == kMixed ? N : 1) + p.nb * p.gs) * sizeof(float);
 }

@@ -35,7 +35,7 @@ SHAPES = [
     ((2, 5, 1), 1), ((2, 3, 6), 3), ((1, 4, 8), 8), ((2, 33, 64), 1), ((2, 33, 64), 8), ((2, 83, 512), 32), ((1, 1000, 48), 6),
     ((3, 257, 255), 17), ((2, 28, 28, 64), 8), ((2, 7, 9, 30), 5), ((1, 3000, 40), 4), ((2, 300, 1030), 10), ((1, 40, 2056), 8),
     ((1, 3, 5000), 5), ((2, 17, 12), 12), ((300, 2, 16), 2), ((1, 500, 3), 3), ((1, 500, 3), 1), ((4, 784, 96), 32), ((2, 64, 768), 96),
-    ((65, 5, 33), 11), ((1, 2000, 129), 3), ((2, 1, 40), 5), ((40, 9, 1), 1), ((1, 1, 17, 264), 33),
+    ((65, 5, 33), 11), ((1, 2000, 129), 3), ((2, 1, 40), 5), ((40, 9, 1), 1), ((1, 1, 17, 264), 33), ((70, 890), 1), ((5, 52, 578), 1), ((3, 200, 99), 3), ((2, 100, 510), 2),
 ]
 
 
@@ -164,7 +164,7 @@ def test_lengths(L, C, groups, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("shape,groups", [((4, 64), 4), ((2, 300, 48), 6), ((3, 257, 255), 17), ((1, 3000, 264), 1), ((2, 40, 2056), 8)])
+@pytest.mark.parametrize("shape,groups", [((4, 64), 4), ((2, 300, 48), 6), ((3, 257, 255), 17), ((1, 3000, 264), 1), ((2, 40, 2056), 8), ((3, 70, 198), 2)])
 def test_in_place_and_off_alignment(shape, groups, dtype):
     x, w, b, go = inputs(shape, dtype, 4)
     want, mean, rstd = sequence.group_norm(x, groups, w, b, activation="silu", with_stats=True)
