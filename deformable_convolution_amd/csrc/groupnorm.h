@@ -235,9 +235,9 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
 //
 // A sample's positions are cut into parts, the channels into tiles of at most 256
 // pieces: a workgroup's threads are rt rows of tp pieces, and a thread keeps its
-// channels over the part's positions.  The parts' statistics (of each group where
-// a tile holds all of them, else of each channel) go to the workspace and are
-// joined in order, by a kernel of its own or, where they are few, by every
+// channels over the part's positions.  The parts' statistics (of each group; where
+// no tile holds all of them of each channel first, which a kernel folds into
+// groups', a workgroup a part) go to the workspace and are joined in order, by a kernel of its own or, where they are few, by every
 // workgroup that needs them (8 x 16384 x 256 fp32 74 us, by a kernel 78; 2 x 65536 x
 // 128 bf16 31, 33); x is read again, the last part first.  Two workgroups a CU
 // in the first pass (four: 76, 34), up to four times as many in the second.
@@ -245,12 +245,11 @@ struct GnParts {
     int P, tp, tiles, rt, nt, parts;
     int64_t rows;     // positions of a part
     int split;        // workgroups of the second pass to a part
-    bool by_group;    // a part's statistics are kept for groups
+    bool by_group;    // a tile holds every group; else channels' statistics are folded into groups' first
     bool joined;      // the workgroups that need a sample's statistics join them themselves
-    int entries;      // of a part: G or C
     int team;         // lanes that add a group's values
     FastDiv by_tiles, by_parts, by_split, by_tp, by_rt, by_D;
-    size_t part_bytes, stat_bytes;
+    size_t channel_bytes, part_bytes, stat_bytes;  // the channels' statistics of all parts (folded), the groups', the joined ones
 };
 
 constexpr int64_t kMaxGrid = 1 << 21;  // workgroups of a launch (of at most 1024 threads)
@@ -276,15 +275,15 @@ inline GnParts plan_parts(int64_t B, int64_t S, int C, int G, int N, int esize, 
     p.rows = std::max<int64_t>(1, std::min((S + parts - 1) / parts, ((int64_t)1 << 31) / ((int64_t)C * esize)));
     p.parts = (int)std::max<int64_t>(1, (S + p.rows - 1) / p.rows);
     p.by_group = p.tiles == 1;
-    p.entries = p.by_group ? G : C;
-    p.joined = p.by_group && (int64_t)p.parts * G <= kJoinHere;
+    p.joined = (int64_t)p.parts * G <= kJoinHere;
     p.team = 64;
     while (p.team > 1 && p.team > p.nt / G) p.team /= 2;
     p.split = (int)std::max<int64_t>(1, std::min({(int64_t)4, p.rows / (8 * p.rt), kMaxGrid / ((int64_t)p.parts * p.tiles)}));
     p.by_split = make_fastdiv(p.split);
     p.by_tiles = make_fastdiv(p.tiles), p.by_parts = make_fastdiv(p.parts), p.by_tp = make_fastdiv(p.tp);
     p.by_rt = make_fastdiv(p.rt), p.by_D = make_fastdiv(C / G);
-    p.part_bytes = ((size_t)B * p.parts * p.entries * sizeof(float2) + 255) & ~(size_t)255;
+    p.channel_bytes = p.by_group ? 0 : ((size_t)B * p.parts * C * sizeof(float2) + 255) & ~(size_t)255;
+    p.part_bytes = ((size_t)B * p.parts * G * sizeof(float2) + 255) & ~(size_t)255;
     p.stat_bytes = ((size_t)B * G * sizeof(float2) + 255) & ~(size_t)255;
     return p;
 }
@@ -308,7 +307,7 @@ struct Place {
         tile = of_tile;
         b = first + s;
         part = (int)(q - s * p.parts);
-        lead = part == 0 && sub == 0;
+        lead = part == 0 && sub == 0 && tile == 0;
         const int each = ((int)p.rows + split - 1) / split;
         const int64_t begin = (int64_t)part * p.rows, until = min(begin + p.rows, a.S);
         const int64_t start = min(begin + (int64_t)sub * each, until), past = min(start + each, until);
@@ -347,25 +346,20 @@ __device__ __forceinline__ float all_sum(float v, float *red) {
     return v;
 }
 
-// f(statistics, entry, rows of the part) for every entry of a group's [parts][per]
-// at v, thread by thread, some loads at a time (3236 x 1808 fp32 in 16 groups, some
-// 200 parts of 113 channels each: 42 -> 35 us, gradients 44 -> 40).
+// f(statistics, rows of the part) for every part of a group at v, thread by
+// thread, some loads at a time.
 template <int NT, typename F>
-__device__ __forceinline__ void each_entry(const GnParts &p, const float2 *v, int per, int64_t n, F f) {
-    const int cols = per < NT ? per : NT, rp = NT / cols;
-    const int c0 = threadIdx.x % cols, p0 = threadIdx.x / cols;
+__device__ __forceinline__ void each_part(const GnParts &p, int G, const float2 *v, int64_t n, F f) {
     const int parts = (int)min((int64_t)p.parts, (n + p.rows - 1) / p.rows);  // that have rows
-    if (p0 >= rp) return;
     constexpr int U = 4;
-    for (int c = c0; c < per; c += cols)
-        for (int i = p0; i < parts; i += U * rp) {
-            float2 e[U];
+    for (int i = threadIdx.x; i < parts; i += U * NT) {
+        float2 e[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) e[k] = v[(int64_t)min(i + k * rp, parts - 1) * p.entries + c];
+        for (int k = 0; k < U; ++k) e[k] = v[(int64_t)min(i + k * NT, parts - 1) * G];
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (i + k * rp < parts) f(e[k], c, (float)min(n - (int64_t)(i + k * rp) * p.rows, p.rows));
-        }
+        for (int k = 0; k < U; ++k)
+            if (i + k * NT < parts) f(e[k], (float)min(n - (int64_t)(i + k * NT) * p.rows, p.rows));
+    }
 }
 
 // f(first sample, workgroups) for launches of whole samples, the last samples first where `back`.
@@ -392,6 +386,20 @@ __device__ __forceinline__ void fetch_parts(const GroupNormArgs &a, const GnPart
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = v[i];
     __syncthreads();
+}
+
+// f(statistics, channel) for those of a group's D channels that are a lane's, some loads at a time.
+template <typename F>
+__device__ __forceinline__ void each_channel(const GnParts &p, const float2 *v, int D, int lane, F f) {
+    constexpr int U = 8;
+    for (int i = lane; i < D; i += U * p.team) {
+        float2 e[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) e[k] = v[min(i + k * p.team, D - 1)];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i + k * p.team < D) f(e[k], i + k * p.team);
+    }
 }
 
 // f(group, lane of its team) for every group of a sample; a team's lanes share a wave.

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
 // that they do not start at the same distance in all channels of the memory, and
 // twice the workgroups: no faster); 13 x 4092 x 255 bf16: 11 us.
 template <typename T, int N>
-__global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts p, float2 *out, int64_t first) {
+__global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts p, float2 *channels_out, float2 *out, int64_t first) {
     using P = Piece<T, N>;
     using E = typename T::T;
     extern __shared__ float2 red[];  // [rt][tp][N], then of the channels
@@ -189,8 +189,9 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
         own[k] = make_float2(mu, q);
     }
     __syncthreads();
-    float2 *const o = out + (t.b * p.parts + t.part) * p.entries;
+    const int64_t row = t.b * p.parts + t.part;
     if (!p.by_group) {
+        float2 *const o = channels_out + row * a.C;
         for (int k = threadIdx.x; k < channels; k += blockDim.x) {
             const int piece = t.tile * p.tp + k / N, c = piece * N;
             if (piece >= p.P) continue;
@@ -198,6 +199,7 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
             if (k % N >= c - at) o[at + k % N] = own[k];
         }
     } else {
+        float2 *const o = out + row * a.G;
         // the last piece is moved back to end with the row
         auto of = [&](int c) { return own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c]; };
         each_group(a, p, [&](int g, int lane) {
@@ -215,23 +217,44 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
     }
 }
 
+// A part's groups from its channels.  (A workgroup a group for the channels of all
+// parts: 8479 x 1052 fp32 in 4 groups took 65 us, not 31; 300 x 5000 in one 103, not
+// 23, gradients 76, not 33.)
+__global__ __launch_bounds__(256) void k_gn_fold(GroupNormArgs a, GnParts p, const float2 *channels, float2 *out) {
+    const int64_t jobs = a.B * p.parts;
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int64_t b = job / p.parts, n = positions(a, b);
+        const float rows = (float)max(min(n - (job - b * p.parts) * p.rows, p.rows), (int64_t)0);
+        const float2 *const v = channels + job * a.C;
+        each_group(a, p, [&](int g, int lane) {
+            float mu = 0.0f, q = 0.0f;
+            const float2 *const of = v + (int64_t)g * a.D;
+            each_channel(p, of, a.D, lane, [&](float2 e, int) { mu += e.x; });
+            mu = team_sum(p, mu) / (float)a.D;
+            each_channel(p, of, a.D, lane, [&](float2 e, int) {
+                const float d = e.x - mu;
+                q += e.y + d * d * rows;
+            });
+            q = team_sum(p, q);
+            if (lane == 0) out[job * a.G + g] = make_float2(mu, q);
+        });
+    }
+}
+
 // A group's statistics from its parts'.
 template <int NT>
 __global__ __launch_bounds__(NT) void k_gn_join(GroupNormArgs a, GnParts p, const float2 *part, float2 *stat) {
     __shared__ float red[NT / 64];
     const int64_t jobs = a.B * a.G;
-    const int per = p.by_group ? 1 : a.D;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const int64_t b = job / a.G, n = positions(a, b);
-        const int g = (int)(job % a.G);
-        const float2 *const v = part + b * p.parts * p.entries + (int64_t)g * per;
+        const float2 *const v = part + b * p.parts * a.G + job % a.G;
         float s = 0.0f, q = 0.0f;
-        each_entry<NT>(p, v, per, n, [&](float2 e, int, float rows) { s += e.x * rows; });
-        const float all = (float)n * (float)per;
-        const float mean = n > 0 ? all_sum<NT>(s, red) / all : 0.0f;
-        each_entry<NT>(p, v, per, n, [&](float2 e, int, float rows) {
+        each_part<NT>(p, a.G, v, n, [&](float2 e, float rows) { s += e.x * rows; });
+        const float mean = n > 0 ? all_sum<NT>(s, red) / (float)n : 0.0f;
+        each_part<NT>(p, a.G, v, n, [&](float2 e, float rows) {
             const float d = e.x - mean;
-            q += e.y + d * d * rows * (p.by_group ? (float)a.D : 1.0f);
+            q += e.y + d * d * rows * (float)a.D;
         });
         const float var = n > 0 ? all_sum<NT>(q, red) / ((float)n * (float)a.D) : 0.0f;
         if (threadIdx.x == 0) {
@@ -361,13 +384,15 @@ hipError_t run(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
         }
     }
     const GnParts p = plan_parts(a.B, a.S, a.C, a.G, N, sizeof(typename T::T), num_cus);
-    float2 *const part = (float2 *)a.ws, *const stat = (float2 *)((char *)a.ws + p.part_bytes);
+    float2 *const channels = (float2 *)a.ws, *const part = (float2 *)((char *)a.ws + p.channel_bytes);
+    float2 *const stat = (float2 *)((char *)part + p.part_bytes);
     const size_t lds = (size_t)(p.rt + 1) * p.tp * N * sizeof(float2);
     by_samples(a.B, p, 1, false, [&](int64_t b, dim3 grid) {
-        hipLaunchKernelGGL((k_gn_part_stats<T, N>), grid, dim3(p.nt), lds, stream, a, p, part, b);
+        hipLaunchKernelGGL((k_gn_part_stats<T, N>), grid, dim3(p.nt), lds, stream, a, p, channels, part, b);
     });
+    if (!p.by_group) hipLaunchKernelGGL(k_gn_fold, dim3(grid_for(a.B * p.parts)), dim3(256), 0, stream, a, p, channels, part);
     if (!p.joined) {
-        if ((int64_t)p.parts * (p.by_group ? 1 : a.D) <= 256)
+        if (p.parts <= 256)
             hipLaunchKernelGGL((k_gn_join<64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, stat);
         else
             hipLaunchKernelGGL((k_gn_join<1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, stat);
@@ -385,7 +410,7 @@ size_t group_norm_workspace(int64_t B, int64_t S, int C, int G, int dtype, int n
     const int N = piece_size(C, dtype);
     if (plan_held(B, S, C, G, N, dtype == kF32 ? 4 : 2, 1, num_cus).R) return 0;
     const GnParts p = plan_parts(B, S, C, G, N, dtype == kF32 ? 4 : 2, num_cus);
-    return p.part_bytes + p.stat_bytes;
+    return p.channel_bytes + p.part_bytes + p.stat_bytes;
 }
 
 hipError_t launch_group_norm(const GroupNormArgs &a, int num_cus, hipStream_t stream) {

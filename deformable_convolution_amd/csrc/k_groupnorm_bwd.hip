@@ -256,22 +256,37 @@ __global__ __launch_bounds__(512) void k_gn_part_sums(GroupNormArgs a, GnParts p
         });
 }
 
-// mean u and mean(u xh) of a group.
-template <typename T, int NT>
-__global__ __launch_bounds__(NT) void k_gn_join_back(GroupNormArgs a, GnParts p, const float2 *part, const float2 *groups, float2 *stat) {
+// A part's groups from its channels.
+template <typename T>
+__global__ __launch_bounds__(256) void k_gn_fold_back(GroupNormArgs a, GnParts p, const float2 *channels, float2 *groups) {
     using E = typename T::T;
+    const int64_t jobs = a.B * p.parts;
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const float2 *const v = channels + job * a.C;
+        each_group(a, p, [&](int g, int lane) {
+            float u = 0.0f, ux = 0.0f;
+            const int64_t c0 = (int64_t)g * a.D;
+            each_channel(p, v + c0, a.D, lane, [&](float2 e, int i) {
+                const float w = a.w ? T::ld((const E *)a.w, c0 + i) : 1.0f;
+                u += e.x * w;
+                ux += e.y * w;
+            });
+            u = team_sum(p, u);
+            ux = team_sum(p, ux);
+            if (lane == 0) groups[job * a.G + g] = make_float2(u, ux);
+        });
+    }
+}
+
+// mean u and mean(u xh) of a group.
+template <int NT>
+__global__ __launch_bounds__(NT) void k_gn_join_back(GroupNormArgs a, GnParts p, const float2 *groups, float2 *stat) {
     __shared__ float red[NT / 64];
     const int64_t jobs = a.B * a.G;
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const int64_t b = job / a.G, n = positions(a, b);
-        const int g = (int)(job % a.G), per = p.by_group ? 1 : a.D;
-        const float2 *const v = p.by_group ? groups + b * p.parts * a.G + g : part + b * p.parts * a.C + (int64_t)g * a.D;
         float s = 0.0f, q = 0.0f;
-        each_entry<NT>(p, v, per, n, [&](float2 e, int c, float) {
-            const float w = a.w && !p.by_group ? T::ld((const E *)a.w, (int64_t)g * a.D + c) : 1.0f;
-            s += e.x * w;
-            q += e.y * w;
-        });
+        each_part<NT>(p, a.G, groups + b * p.parts * a.G + job % a.G, n, [&](float2 e, float) { s += e.x, q += e.y; });
         s = all_sum<NT>(s, red);
         q = all_sum<NT>(q, red);
         const float inv = n > 0 ? 1.0f / ((float)n * (float)a.D) : 0.0f;
@@ -386,7 +401,7 @@ struct BackBytes {
 };
 BackBytes back_bytes(int64_t B, int C, int G, const GnParts &p) {
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-    return {up((size_t)B * p.parts * C * sizeof(float2)), p.by_group ? up((size_t)B * p.parts * G * sizeof(float2)) : 0};
+    return {up((size_t)B * p.parts * C * sizeof(float2)), up((size_t)B * p.parts * G * sizeof(float2))};
 }
 
 template <typename T, int N, int R, int ACT>
@@ -424,11 +439,12 @@ hipError_t run_back(const GroupNormArgs &a, int num_cus, hipStream_t stream) {
         hipLaunchKernelGGL((k_gn_part_sums<T, N, ACT>), grid, dim3(p.nt), lds, stream, a, p, part, groups, b);
     });
     if (a.y && a.B > 0 && a.S > 0) {
+        if (!p.by_group) hipLaunchKernelGGL((k_gn_fold_back<T>), dim3(grid_for(a.B * p.parts)), dim3(256), 0, stream, a, p, part, groups);
         if (!p.joined) {
-            if ((int64_t)p.parts * (p.by_group ? 1 : a.D) <= 256)
-                hipLaunchKernelGGL((k_gn_join_back<T, 64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, part, groups, stat);
+            if (p.parts <= 256)
+                hipLaunchKernelGGL((k_gn_join_back<64>), dim3(grid_for(a.B * a.G)), dim3(64), 0, stream, a, p, groups, stat);
             else
-                hipLaunchKernelGGL((k_gn_join_back<T, 1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, part, groups, stat);
+                hipLaunchKernelGGL((k_gn_join_back<1024>), dim3(grid_for(a.B * a.G)), dim3(1024), 0, stream, a, p, groups, stat);
         }
         const size_t here = p.joined ? (size_t)a.G * (1 + p.parts) * sizeof(float2) : 0;
         by_samples(a.B, p, p.split, true, [&](int64_t b, dim3 grid) {

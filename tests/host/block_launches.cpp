@@ -75,7 +75,8 @@ static void held_plan(const HeldPlan &p, int64_t B, int64_t S, int C, int G, int
 static void part_plan(const GnParts &p, int64_t B, int64_t S, int C, int G, int N, int es) {
     bad = bad || p.rt < 1 || p.rt * p.tp > p.nt || p.nt > 512 || p.tiles * p.tp < p.P || (p.tiles - 1) * p.tp >= p.P || p.P * N < C ||
           p.parts * p.rows < S || (S > 0 && (p.parts - 1) * p.rows >= S) || p.rows * C * es > (int64_t)1 << 31 || p.split < 1 ||
-          p.part_bytes < (size_t)B * p.parts * p.entries * sizeof(float2) || p.stat_bytes < (size_t)B * G * sizeof(float2) ||
+          p.part_bytes < (size_t)B * p.parts * G * sizeof(float2) ||
+          (!p.by_group && p.channel_bytes < (size_t)B * p.parts * C * sizeof(float2)) || p.stat_bytes < (size_t)B * G * sizeof(float2) ||
           (p.joined && (size_t)G * (1 + p.parts) * sizeof(float2) > 64 * 1024) || (p.by_group && p.tiles != 1);
 }
 

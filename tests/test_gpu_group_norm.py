@@ -195,10 +195,9 @@ def test_in_place_and_off_alignment(shape, groups, dtype):
 
 # Samples too large to hold: with fewer parts' statistics than every workgroup joins itself and with more, channels in
 # several tiles, parts whose second pass is split, one and few channels.  K: 8 rows of a thread, the row-threads (253 of
-# 8 channels), then a part's channels and the parts over 64 lanes, or over 1024 threads (5 channels of each in 38
-# parts, 3 in 125).
+# 8 channels), then a part's channels and the parts over 64 lanes or more (5000 channels: 79 of a lane).
 PARTS = [((2, 5000, 64), 1, 100), ((2, 3000, 264), 3, 100), ((3, 1300, 512), 512, 192), ((2, 6000, 96), 96, 100),
-         ((1, 4100, 1030), 2, 300), ((1, 300, 5000), 1, 256), ((1, 2000, 2056), 1, 440), ((1, 30000, 8), 1, 320)]
+         ((1, 4100, 1030), 2, 100), ((1, 300, 5000), 1, 120), ((1, 2000, 2056), 1, 100), ((2, 700, 4104), 54, 100), ((1, 600, 4096), 512, 100), ((1, 30000, 8), 1, 320)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
