@@ -41,7 +41,8 @@ __device__ __forceinline__ int64_t positions(const GroupNormArgs &a, int64_t b) 
 // A workgroup holds the positions of nb samples times a slab of gs groups in
 // registers: x (and g) are read once.  Its threads are nb samples x rt rows x P
 // pieces of the slab's channels, R rows each (row t, t + rt, ...).  The mean is
-// taken first and the squares about it next, both from registers.
+// taken first, then the squares about it and what it leaves (a sum of differences,
+// which corrects both), all from registers.
 //
 // Samples that fit are held: against parts, which read twice, 32 x 784 x 512 fp32
 // takes 23 us (34), 4 x 4096 x 512 bf16 23 (29), 32768 rows of 1024 bf16 33
@@ -61,19 +62,20 @@ struct HeldPlan {
 enum Mode { kShuffle, kWhole, kOne, kMixed };
 
 // The sums of v over every group of a workgroup: [K] values for each of a
-// thread's NV groups.
-template <int N, int MODE, int K>
+// thread's NV groups, K up to 2.
+template <int N, int MODE>
 struct GroupSums {
     static constexpr int NV = MODE == kMixed ? N : 1;
-    float *red, *sums;
+    float *sums, *red;
     int np;
-    __device__ __forceinline__ GroupSums(const HeldPlan &p, float *lds) : red(lds), sums(lds + (size_t)p.nt * NV * K), np(p.nb * p.gs) {}
+    __device__ __forceinline__ GroupSums(const HeldPlan &p, float *lds) : sums(lds), red(lds + 2 * p.nb * p.gs), np(p.nb * p.gs) {}
     // channels: of the slab; slot: where the first of a thread's groups is among np (its sample's, for kMixed)
-    __device__ __forceinline__ void operator()(const HeldPlan &p, float (*v)[NV], int channels, int D, int slot, const int *of) {
+    template <int K>
+    __device__ __forceinline__ void operator()(const HeldPlan &p, float (&v)[K][NV], int channels, int D, int slot, const int *of) {
         if constexpr (MODE == kShuffle) {
+            for (int d = 1; d < p.per; d <<= 1)
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                for (int d = 1; d < p.per; d <<= 1) v[k][0] += __shfl_xor(v[k][0], d);
+                for (int k = 0; k < K; ++k) v[k][0] += __shfl_xor(v[k][0], d);
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -97,11 +99,12 @@ struct GroupSums {
 #pragma unroll
                     for (int k = 0; k < K; ++k) s[k] += red[(size_t)k * p.nt * NV + at];
                 }
+                for (int d = 1; d < p.team; d <<= 1)
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    for (int d = 1; d < p.team; d <<= 1) s[k] += __shfl_xor(s[k], d);
+                    for (int k = 0; k < K; ++k) s[k] += __shfl_xor(s[k], d);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
                     if (lane == 0) sums[k * np + g] = s[k];
-                }
             }
             __syncthreads();
 #pragma unroll
@@ -223,7 +226,7 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
     while (p.team > 1 && (p.team > p.nt / (p.nb * p.gs) || p.team / 2 >= p.rt * p.per)) p.team /= 2;
     p.by_P = make_fastdiv(p.P), p.by_rt = make_fastdiv(p.rt), p.by_per = make_fastdiv(p.per), p.by_gs = make_fastdiv(p.gs);
     p.by_D = make_fastdiv(D);
-    const size_t sums = (size_t)tensors * (p.nt * (p.mode == kMixed ? N : 1) + p.nb * p.gs) * sizeof(float);
+    const size_t sums = (size_t)2 * (p.nt * (p.mode == kMixed ? N : 1) + p.nb * p.gs) * sizeof(float);
     p.lds = tensors == 1 ? sums : std::max(sums, (size_t)p.nt * N * sizeof(float2));
     const int64_t rows = std::max<int64_t>(1, (8ll * num_cus + p.slabs - 1) / p.slabs);
     p.grid_rows = (int)std::min<int64_t>(p.batches, rows);

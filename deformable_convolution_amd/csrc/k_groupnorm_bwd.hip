@@ -22,7 +22,7 @@ __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan 
     const int slab = (int)(id % p.slabs), w0 = (int)(id / p.slabs);
     const HeldPlace<N, MODE> t(a, p, slab);
     constexpr int NV = HeldPlace<N, MODE>::NV;
-    GroupSums<N, MODE, 2> sum(p, lds);
+    GroupSums<N, MODE> sum(p, lds);
     float w[N], c[N], pw[N] = {}, pb[N] = {};
 #pragma unroll
     for (int e = 0; e < N; ++e) w[e] = 1.0f, c[e] = 0.0f;
