@@ -133,7 +133,8 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
 // A part's mean and squares about it: of kBatch rows at a time, from registers,
 // joined with those so far by (n, mean, M2) + (m, s, d): mean + (s - mean) m / (n +
 // m), M2 + d + (s - mean)^2 n m / (n + m); then over the row-threads and a group's
-// channels.  8 x 16384 x 256 fp32: 34 us, 3.9 TB/s (parts of 257 or 265 rows, so
+// channels.  Every mean, here and where parts are joined, is one of its terms plus the
+// mean of the differences from it: equal values have their own as mean.  8 x 16384 x 256 fp32: 34 us, 3.9 TB/s (parts of 257 or 265 rows, so
 // that they do not start at the same distance in all channels of the memory, and
 // twice the workgroups: no faster); 13 x 4092 x 255 bf16: 11 us.
 template <typename T, int N>
@@ -159,16 +160,17 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
         const int have = min(mine - i0, kBatch);
         const float m = (float)have, all = n + m, share = m / all;
         float s[N] = {}, d[N] = {};
+        if (i0 == 0) P::widen(raw[0], mean);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             float f[N];
             hold(raw[i]);
             P::widen(raw[i], f);
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e] += i < have ? f[e] : 0.0f;
+            for (int e = 0; e < N; ++e) s[e] += i < have ? f[e] - mean[e] : 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < N; ++e) s[e] = have == kBatch ? s[e] * (1.0f / kBatch) : s[e] / m;  // equal values have their own as mean
+        for (int e = 0; e < N; ++e) s[e] = mean[e] + (have == kBatch ? s[e] * (1.0f / kBatch) : s[e] / m);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             float f[N];
@@ -197,9 +199,10 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
     const float rows = (float)max(t.n, 1);
     float2 *const own = red + p.rt * channels;
     for (int k = threadIdx.x; k < channels; k += blockDim.x) {
+        const float m0 = red[k].x;
         float mu = 0.0f, q = 0.0f;
-        for (int i = 0; i < p.rt; ++i) mu += red[i * channels + k].x * (float)t.rows_of(p, i, t.n);
-        mu /= rows;
+        for (int i = 1; i < p.rt; ++i) mu += (red[i * channels + k].x - m0) * (float)t.rows_of(p, i, t.n);
+        mu = m0 + mu / rows;
         for (int i = 0; i < p.rt; ++i) {
             const float2 v = red[i * channels + k];
             const float d = v.x - mu;
@@ -222,9 +225,10 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
         // the last piece is moved back to end with the row
         auto of = [&](int c) { return own[c >= (p.P - 1) * N ? (p.P - 1) * N + c - (a.C - N) : c]; };
         each_group(a, p, [&](int g, int lane) {
+            const float m0 = of(g * a.D).x;
             float mu = 0.0f, q = 0.0f;
-            for (int i = lane; i < a.D; i += p.team) mu += of(g * a.D + i).x;
-            mu = team_sum(p, mu) / (float)a.D;
+            for (int i = lane; i < a.D; i += p.team) mu += of(g * a.D + i).x - m0;
+            mu = m0 + team_sum(p, mu) / (float)a.D;
             for (int i = lane; i < a.D; i += p.team) {
                 const float2 v = of(g * a.D + i);
                 const float d = v.x - mu;
@@ -246,10 +250,11 @@ __global__ __launch_bounds__(256) void k_gn_fold(GroupNormArgs a, GnParts p, con
         const float rows = (float)max(min(n - (job - b * p.parts) * p.rows, p.rows), (int64_t)0);
         const float2 *const v = channels + job * a.C;
         each_group(a, p, [&](int g, int lane) {
-            float mu = 0.0f, q = 0.0f;
             const float2 *const of = v + (int64_t)g * a.D;
-            each_channel(p, of, a.D, lane, [&](float2 e, int) { mu += e.x; });
-            mu = team_sum(p, mu) / (float)a.D;
+            const float m0 = of[0].x;
+            float mu = 0.0f, q = 0.0f;
+            each_channel(p, of, a.D, lane, [&](float2 e, int) { mu += e.x - m0; });
+            mu = m0 + team_sum(p, mu) / (float)a.D;
             each_channel(p, of, a.D, lane, [&](float2 e, int) {
                 const float d = e.x - mu;
                 q += e.y + d * d * rows;
@@ -268,9 +273,10 @@ __global__ __launch_bounds__(NT) void k_gn_join(GroupNormArgs a, GnParts p, cons
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const int64_t b = job / a.G, n = positions(a, b);
         const float2 *const v = part + b * p.parts * a.G + job % a.G;
+        const float m0 = v[0].x;
         float s = 0.0f, q = 0.0f;
-        each_part<NT>(p, a.G, v, n, [&](float2 e, float rows) { s += e.x * rows; });
-        const float mean = n > 0 ? all_sum<NT>(s, red) / (float)n : 0.0f;
+        each_part<NT>(p, a.G, v, n, [&](float2 e, float rows) { s += (e.x - m0) * rows; });
+        const float mean = n > 0 ? m0 + all_sum<NT>(s, red) / (float)n : 0.0f;
         each_part<NT>(p, a.G, v, n, [&](float2 e, float rows) {
             const float d = e.x - mean;
             q += e.y + d * d * rows * (float)a.D;
@@ -308,12 +314,13 @@ __global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts 
         float2 *const v = joined + a.G;
         fetch_parts(a, p, part, t.b, v);
         each_group(a, p, [&](int g, int lane) {
+            const float m0 = v[g].x;
             float s = 0.0f, q = 0.0f;
             for (int i = lane; i < p.parts; i += p.team) {
                 const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
-                if (rows > 0) s += v[i * a.G + g].x * (float)rows;
+                if (rows > 0) s += (v[i * a.G + g].x - m0) * (float)rows;
             }
-            const float mean = n > 0 ? team_sum(p, s) / (float)n : 0.0f;
+            const float mean = n > 0 ? m0 + team_sum(p, s) / (float)n : 0.0f;
             for (int i = lane; i < p.parts; i += p.team) {
                 const int64_t rows = min(n - (int64_t)i * p.rows, p.rows);
                 const float2 e = v[i * a.G + g];

@@ -23,6 +23,11 @@ VALUES = [0.1, 0.7, 1000.1, -37.3]
 # A group's lanes in one wave; several rows of whole pieces (up to 16 a thread); one odd group a slab; several odd groups.
 HELD = [((50, 512), 4), ((2, 784, 64), 4), ((4, 4096, 512), 32), ((70, 890), 1), ((3, 4092, 255), 17), ((3, 257, 255), 17), ((2, 100, 510), 34)]
 
+# Samples in parts: their statistics joined by every workgroup or by a kernel, every group in a tile or channels folded into
+# groups, one channel a group, parts that one workgroup reads in several batches.
+PARTS = [((2, 5000, 64), 1), ((2, 3000, 264), 3), ((3, 1300, 512), 512), ((2, 6000, 96), 96), ((1, 4100, 1030), 2), ((1, 300, 5000), 1),
+         ((2, 700, 4104), 54), ((1, 30000, 8), 1), ((520, 601, 36), 1), ((1, 16384, 257), 1)]
+
 
 def constant(shape, groups, value, dtype):
     """Every group of equal values, each another one."""
@@ -54,6 +59,13 @@ def check_equal(shape, groups, dtype):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape,groups", HELD)
 def test_held(shape, groups, dtype):
+    check_equal(shape, groups, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,groups", PARTS)
+def test_in_parts(shape, groups, dtype):
+    """Every mean is one of its terms and the mean of the differences from it, all of them 0."""
     check_equal(shape, groups, dtype)
 
 
