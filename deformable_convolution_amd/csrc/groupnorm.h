@@ -219,6 +219,18 @@ inline HeldPlan plan_held(int64_t B, int64_t S, int C, int G, int N, int esize, 
         return p;
     }
     p.nt = (p.nb * p.rt * p.P + 63) / 64 * 64;
+    // One odd group a slab whose rows are short runs of a line that other workgroups read too: forward (16 rows a thread)
+    // 3 x 7215 x 192 bf16 in 16 (24 bytes) 38 us, in parts 18, 64 x 4096 x 320 bf16 in 32 (20) 134, 110, 7 x 4741 x 80
+    // fp32 in 8 (40) 23, 17; of few threads not (40 x 2392 x 48 fp32 in 8: 19, 21).  Gradients 142 x 749 x 160 fp32 in 16
+    // (40) 122, 72, 472 x 1212 x 18 in 3 (24) 53, 43; of 44 bytes 32, 34.
+    const int64_t groups = p.batches * p.slabs;  // workgroups
+    const bool odd = !inside && p.gs == 1;
+    if (odd && D * esize < 44 && (tensors == 1 ? p.R == 16 && p.nt > 384 : p.R == 8 && groups > num_cus)) p.R = 0;
+    // And those of bf16, one workgroup a CU at a time, where most CUs would have none, or a few a second one: 14 x 1641 x
+    // 67 in 1 (14) 25 us, in parts 16; 70 x 194 x 516 in 1 24, 22; 150 of it 25.5, 35; 16 x 4092 x 510 in 17 (272) 57, 45;
+    // 36 x 554 x 1197 in 9 (324) 41, 50.
+    if (odd && tensors == 1 && N == 8 && p.R == 16 && p.nt > 512 && (5 * groups < 2 * num_cus || (groups > num_cus && 5 * groups < 6 * num_cus))) p.R = 0;
+    if (!p.R) return p;
     const int dn = inside ? D / N : D;
     p.mode = mixed ? kMixed : !inside ? kOne : p.rt == 1 && dn <= 64 && !(dn & (dn - 1)) ? kShuffle : kWhole;
     p.per = p.mode == kOne ? p.P : dn;
