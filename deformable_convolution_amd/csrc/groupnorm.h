@@ -44,9 +44,9 @@ __device__ __forceinline__ int64_t positions(const GroupNormArgs &a, int64_t b) 
 // taken first, then the squares about it and what it leaves (a sum of differences,
 // which corrects both), all from registers.
 //
-// Samples that fit are held: against parts, which read twice, 32 x 784 x 512 fp32
-// takes 23 us (34), 4 x 4096 x 512 bf16 23 (29), 32768 rows of 1024 bf16 33
-// (325), gradients 43 (55) and 52 (456).
+// Samples that fit are held (odd groups with exceptions, see plan_held): against
+// parts, which read twice, 32 x 784 x 512 fp32 takes 22 us (34), 4 x 4096 x 512 bf16
+// 21 (29), 32768 rows of 1024 bf16 33 (325), gradients 43 (55) and 48 to 52 (456).
 struct HeldPlan {
     int P, gs, slabs, rt, nb, nt, R;
     int64_t batches;       // of nb samples
@@ -58,7 +58,7 @@ struct HeldPlan {
 };
 // A group's lanes share a wave; a piece lies in one group; the slab is one group,
 // whose last piece repeats some of it (as if it were several, 11031 rows of 890
-// bf16 took 42 us, not 19; gradients 60, not 35); a piece may lie in several.
+// bf16 took 42 us, not 19; gradients 60, not 28); a piece may lie in several.
 enum Mode { kShuffle, kWhole, kOne, kMixed };
 
 // The sums of v over every group of a workgroup: [K] values for each of a

@@ -19,9 +19,10 @@ namespace {
 
 // All loads first, then the sums, the squares and the rows' results, each row
 // widened anew (hold() keeps the compiler from widening all of them at once, which
-// took twice the registers).  8 x 4096 x 512 bf16 in 32 groups: 25 us, 2.7 TB/s:
-// one workgroup a CU, whose reads, sums and writes follow one another; 32 x 784 x
-// 512 fp32 23 us, 4.5 TB/s; 32768 rows of 1024 bf16 33 us, 4.1 TB/s.
+// took twice the registers).  8 x 4096 x 512 bf16 in 32 groups: 24 us, 2.8 TB/s, the
+// vector unit busy for 54 % of it: one workgroup a CU, whose reads, sums and writes
+// follow one another; 32 x 784 x 512 fp32 22 us, 4.6 TB/s; 32768 rows of 1024 bf16 33
+// us, 4.1 TB/s.
 template <typename T, int N, int R, int MODE, int ACT>
 __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, int64_t first) {
     using P = Piece<T, N>;
@@ -134,9 +135,10 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
 // joined with those so far by (n, mean, M2) + (m, s, d): mean + (s - mean) m / (n +
 // m), M2 + d + (s - mean)^2 n m / (n + m); then over the row-threads and a group's
 // channels.  Every mean, here and where parts are joined, is one of its terms plus the
-// mean of the differences from it: equal values have their own as mean.  8 x 16384 x 256 fp32: 34 us, 3.9 TB/s (parts of 257 or 265 rows, so
-// that they do not start at the same distance in all channels of the memory, and
-// twice the workgroups: no faster); 13 x 4092 x 255 bf16: 11 us.
+// mean of the differences from it: equal values have their own as mean.  8 x 16384 x
+// 256 fp32: 34 us, 3.9 TB/s (parts of 257 or 265 rows, so that they do not start at
+// the same distance in all channels of the memory, and twice the workgroups: no
+// faster); 13 x 4092 x 255 bf16: 12 us.
 template <typename T, int N>
 __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts p, float2 *channels_out, float2 *out, int64_t first) {
     using P = Piece<T, N>;
@@ -293,7 +295,7 @@ __global__ __launch_bounds__(NT) void k_gn_join(GroupNormArgs a, GnParts p, cons
 
 // The second reading, the last samples and parts first: what the first pass read
 // last is in the last-level cache.  8 x 16384 x 256 fp32: 40 us, 6.7 TB/s; 13 x 4092
-// x 255 bf16, whose rows stand at odd addresses: 15 us, 2.9 TB/s.
+// x 255 bf16, whose rows stand at odd addresses: 16 us, 2.7 TB/s.
 template <typename T, int N, int ACT>
 __global__ __launch_bounds__(512) void k_gn_part_apply(GroupNormArgs a, GnParts p, const float2 *part, float2 *stat, int64_t first) {
     using P = Piece<T, N>;

@@ -12,7 +12,7 @@ namespace {
 // -> 42.8 us below), in bf16 z is formed anew.  32768 rows of 1024 bf16: 41 us, 4.9
 // TB/s; 32 x 784 x 512 fp32, silu: 43 us with the parameters' sums, 3.6 TB/s, where
 // eight rows a thread of both tensors leave four waves a SIMD; 512 x 49 x 1024 bf16,
-// silu: 68 us, 62 instructions an element.
+// silu: 66 us, 62 instructions an element.
 template <typename T, int N, int R, int MODE, int ACT>
 __global__ __launch_bounds__(512) void k_gn_held_back(GroupNormArgs a, HeldPlan p, float2 *out) {
     using P = Piece<T, N>;

@@ -605,7 +605,8 @@ __global__ __launch_bounds__(kLanes * kSlots) void k_rec_maps_back(RecurrenceArg
 // Both scans of a tile side by side: the states from the kept one ahead of the
 // tile, the gradients from its end.  Two waves a SIMD of 200 registers (fp32 228):
 // 8 x 16384 x 256 bf16 76 us, 4.4 TB/s, the vector unit busy for 60 % of it; 13 x
-// 4092 x 511 fp32, ragged, 109 us.
+// 4092 x 511 fp32, ragged, 109 us (of both passes, 152; 133 with 512 channels, whose
+// rows stand at even addresses).
 template <typename T, int N, int SL, bool ODD, bool BLEND>
 __global__ __launch_bounds__(kLanes * SL) void k_rec_walk_back(RecurrenceArgs a, Segments g) {
     __shared__ Ends<N, SL> ends[2][2];

@@ -651,7 +651,8 @@ int dc1d_group_norm(const dc1d_tensor *x, const dc1d_tensor *weight_or_null, con
  * zeros, and nothing that they or their grad_out hold reaches a gradient.
  * grad_x may be grad_out itself.  An empty x gives zero grad_weight and
  * grad_bias.  workspace: at least dc1d_group_norm_backward_workspace_bytes()
- * bytes, 256-byte aligned, when that is not 0 (partial sums).
+ * bytes, 256-byte aligned, when that is not 0 (partial sums; 8 bytes for every
+ * element of [N, C] where a group has more than 2048 fp32 or 4096 bf16 channels).
  */
 int dc1d_group_norm_backward_workspace_bytes(const dc1d_tensor *x, int64_t groups, int want_params, size_t *bytes_out);
 
