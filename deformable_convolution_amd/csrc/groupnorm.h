@@ -77,15 +77,20 @@ struct GroupSums {
 #pragma unroll
                 for (int k = 0; k < K; ++k) v[k][0] += __shfl_xor(v[k][0], d);
         } else {
+            using Sums = float __attribute__((ext_vector_type(K)));  // of one group, side by side: one access for both
+            Sums *const own = (Sums *)red, *const all_of = (Sums *)sums;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+            for (int e = 0; e < NV; ++e) {
+                Sums s;
 #pragma unroll
-                for (int e = 0; e < NV; ++e) red[((size_t)k * p.nt + threadIdx.x) * NV + e] = v[k][e];
+                for (int k = 0; k < K; ++k) s[k] = v[k][e];
+                own[threadIdx.x * NV + e] = s;
+            }
             __syncthreads();
             const int lane = threadIdx.x & (p.team - 1), all = p.rt * p.per, last = (channels + N - 1) / N - 1;
             for (int g = threadIdx.x / p.team; g < np; g += p.nt / p.team) {
                 const int sm = (int)fdiv(g, p.by_gs), first = (g - sm * p.gs) * p.per;
-                float s[K] = {};
+                Sums s = {};
                 for (int i = lane; i < all; i += p.team) {
                     const int r = (int)fdiv(i, p.by_per), j = first + i - r * p.per;
                     int at;
@@ -96,21 +101,20 @@ struct GroupSums {
                         at = j >= last * N ? last * N + j - (channels - N) : j;
                     }
                     at += (sm * p.rt + r) * p.P * NV;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) s[k] += red[(size_t)k * p.nt * NV + at];
+                    s += own[at];
                 }
                 for (int d = 1; d < p.team; d <<= 1)
 #pragma unroll
                     for (int k = 0; k < K; ++k) s[k] += __shfl_xor(s[k], d);
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (lane == 0) sums[k * np + g] = s[k];
+                if (lane == 0) all_of[g] = s;
             }
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+            for (int e = 0; e < NV; ++e) {
+                const Sums s = all_of[slot + (MODE == kMixed ? of[e] : 0)];
 #pragma unroll
-                for (int e = 0; e < NV; ++e) v[k][e] = sums[k * np + slot + (MODE == kMixed ? of[e] : 0)];
+                for (int k = 0; k < K; ++k) v[k][e] = s[k];
+            }
         }
     }
 };

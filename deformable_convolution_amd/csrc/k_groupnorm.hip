@@ -64,10 +64,10 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
         for (int e = 0; e < NV; ++e) hold(v[0][e]);
     }
     sum(p, v, t.channels, a.D, t.slot, t.of);
-    const float all = (float)n * (float)a.D;
+    const float inv = n > 0 ? 1.0f / ((float)n * (float)a.D) : 0.0f;
     float mean[NV], sq[2][NV] = {};
 #pragma unroll
-    for (int e = 0; e < NV; ++e) mean[e] = n > 0 ? v[0][e] / all : 0.0f;
+    for (int e = 0; e < NV; ++e) mean[e] = v[0][e] * inv;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         float f[N];
@@ -93,10 +93,10 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
     float r[NV];
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-        const float s = fabsf(sq[0][e]) < __builtin_inff() ? sq[0][e] : 0.0f, by = n > 0 ? s / all : 0.0f;
+        const float s = fabsf(sq[0][e]) < __builtin_inff() ? sq[0][e] : 0.0f, by = s * inv;
         const float left = sq[1][e] - s * by;
         mean[e] += by;
-        r[e] = n > 0 ? rsqrtf((left < 0.0f ? 0.0f : left) / all + a.eps) : 0.0f;
+        r[e] = n > 0 ? rsqrtf((left < 0.0f ? 0.0f : left) * inv + a.eps) : 0.0f;
     }
     if (!on) return;
     float w[N], c[N];
