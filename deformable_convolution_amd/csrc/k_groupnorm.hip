@@ -94,7 +94,7 @@ __global__ __launch_bounds__(1024) void k_gn_held(GroupNormArgs a, HeldPlan p, i
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
         const float s = fabsf(sq[0][e]) < __builtin_inff() ? sq[0][e] : 0.0f, by = s * inv;
-        const float left = sq[1][e] - s * by;
+        const float left = fmaf(-s, by, sq[1][e]);  // of infinite squares they, also where s by is past 32 bits
         mean[e] += by;
         r[e] = n > 0 ? rsqrtf((left < 0.0f ? 0.0f : left) * inv + a.eps) : 0.0f;
     }
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
         for (int e = 0; e < N; ++e) {
             const float v = s[e] - mean[e];
             mean[e] += v * share;
-            m2[e] += d[e] + v * v * n * share;
+            m2[e] += d[e] + v * (v * (n * share));  // 0 of no rows, also where v v is infinite
         }
         n = all;
     }
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(512) void k_gn_part_stats(GroupNormArgs a, GnParts 
         for (int i = 0; i < p.rt; ++i) {
             const float2 v = red[i * channels + k];
             const float d = v.x - mu;
-            q += v.y + d * d * (float)t.rows_of(p, i, t.n);
+            q += v.y + d * (d * (float)t.rows_of(p, i, t.n));
         }
         own[k] = make_float2(mu, q);
     }

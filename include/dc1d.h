@@ -620,7 +620,8 @@ int dc1d_attention_backward(const dc1d_strided *q, const dc1d_strided *k, const 
  *   activation  a dc1d_activation
  *
  * Positions past a sample's length give 0, whatever they hold; a sample of
- * length 0 has mean 0 and rstd 0.  y may be x itself (in place); otherwise
+ * length 0 has mean 0 and rstd 0.  Squares past fp32's range make the variance
+ * infinite and rstd 0.  y may be x itself (in place); otherwise
  * outputs must not overlap the inputs or each other.  eps is finite and not
  * negative; groups divides C.  An empty x is a no-op (with L = 0, mean and rstd
  * are 0).  workspace: at least dc1d_group_norm_workspace_bytes() bytes, 256-byte

@@ -93,3 +93,26 @@ def test_infinite_values_keep_their_mean(shape, groups):
     y[1].view(-1, shape[-1])[:, D:2 * D] = want[1].view(-1, shape[-1])[:, D:2 * D]
     mean[1, 1] = means[1, 1]
     assert torch.equal(y, want) and torch.equal(mean, means)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,groups", HELD + PARTS)
+def test_squares_past_32_bits(shape, groups, dtype):
+    """Values of 1e25, whose squares 32 bits do not hold: the variance is infinite, rstd 0 and y the bias, the mean as ever;
+    equal ones of 1e30 have their own as mean."""
+    g = torch.Generator().manual_seed(4)
+    b = torch.randn(shape[-1], generator=g).to(dtype).to(DEV)
+    lens = torch.full(shape[:1], shape[1] - 3, dtype=torch.int32, device=DEV) if len(shape) == 3 else None
+    n = shape[1] if lens is None else shape[1] - 3
+    part = (lambda t: t) if lens is None else (lambda t: t[:, :n])  # noqa: E731
+    spread = torch.randn(shape, generator=g)
+    for x in (spread * 1e25, (1 + 0.01 * spread) * 1e30):
+        x = x.to(dtype).to(DEV)
+        y, mean, rstd = sequence.group_norm(x, groups, None, b, lens=lens, with_stats=True)
+        v = part(x).double().view(shape[0], -1, groups, shape[-1] // groups)
+        assert not rstd.any() and torch.equal(part(y), part(b.expand(shape)))
+        top = v.abs().amax((1, 2, 3)).view(-1, 1)
+        assert ((mean.double() - v.mean((1, 3))).abs() <= 320 * U * top).all()  # 320: the most roundings of a shape in parts
+    x.fill_(1e30)
+    y, mean, rstd = sequence.group_norm(x, groups, None, b, lens=lens, with_stats=True)
+    assert (mean == x.view(-1)[0].float()).all() and torch.equal(part(y), part(b.expand(shape)))
